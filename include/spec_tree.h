@@ -77,8 +77,9 @@ typedef enum {
   SPEC_ERR_TIMEOUT = -9,         /* a bounded device-side wait ran out (never expected) */
   SPEC_ERR_PREFIX_RANGE = -10,   /* prefix_lens[b] < 0 or L_b + N_b > S_cap */
   SPEC_ERR_ALIGNMENT = -11,      /* a pointer is not 16-byte aligned */
-  SPEC_ERR_INDEX = -12           /* bounds-checked build only: a computed global index fell
+  SPEC_ERR_INDEX = -12,          /* bounds-checked build only: a computed global index fell
                                     outside its buffer; the access was skipped */
+  SPEC_ERR_NONFINITE = -13       /* a row to be quantised holds NaN or infinity */
 } spec_status;
 
 typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
@@ -306,6 +307,114 @@ int spec_kv_compact(void *k_cache, void *v_cache, int dtype, int B, int Hkv, int
                     const int32_t *prefix_lens, const int32_t *tree_offsets,
                     const int32_t *path_nodes, const int32_t *accept_len, int max_depth_plus1,
                     int32_t *new_prefix_lens, int32_t *status, void *stream);
+
+/*
+ * The 4-bit KV cache — spec_kv4_write, spec_kv4_read, spec_tree_attn_kv4 and
+ * spec_kv4_compact: the step's cache operations on keys and values held in
+ * 4 bits, 4.5 bits an element with their scales (D = 128), so that the
+ * attention of long prefixes reads 3.6 times fewer bytes than bf16.
+ *
+ *   kv_cache  [B][Hkv][S_cap][R] uint8, 16-byte aligned, R =
+ *             spec_kv4_record_bytes(D): 144 for D = 128, 80 for D = 64.
+ *
+ * One record holds the key and the value of one slot of one KV head:
+ *   bytes [0, D/2)        the key's codes, two per byte, dimension 2i in the
+ *                         low half of byte i
+ *   bytes [D/2, D)        the value's codes
+ *   bytes [D, D + D/16)   the key's scales, one per 16 dimensions
+ *   then D/16 bytes       the value's scales; zeros up to R
+ * A code has a sign bit (8), two exponent bits and a mantissa bit (e2m1):
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6.  A scale byte has five exponent bits (bias 15)
+ * and three mantissa bits: for byte c, e = c >> 3, m = c & 7, it stands for
+ * (1 + m/8) 2^(e-15), or m 2^-17 when e = 0.  An element is code x scale,
+ * which bfloat16 (and half) represent exactly.
+ *
+ * Quantisation of 16 elements x: scale = max|x| / 6 rounded to the nearest
+ * scale, at most 10240; each code is the one nearest to x / scale, at most 6
+ * in magnitude; ties go to the even code or byte, and every comparison is
+ * exact.  Magnitudes above 61440 therefore saturate, and a group whose
+ * largest magnitude is at most 3 x 2^-17 is stored as zeros.  The format
+ * holds no NaN or infinity; see spec_kv4_write.
+ */
+size_t spec_kv4_record_bytes(int D);   /* 0 when D is neither 64 nor 128 */
+
+/*
+ * spec_kv4_write — quantises dense rows into the cache.
+ *
+ * Row t of request b (offsets[b] <= t < offsets[b+1]) goes to slot
+ * start[b] + t - offsets[b] of every KV head: a prompt's keys and values
+ * from slot 0, or a tree's behind its prefix (offsets = tree_offsets, start
+ * = prefix_lens).  No other slot changes.
+ *
+ *   k, v      [T][Hkv][D]  dtype (SPEC_BF16 or SPEC_F32), 16-byte aligned, at
+ *             the given strides in elements between rows and between heads
+ *             (each a multiple of 16 bytes; the D elements of a head are
+ *             contiguous), so that rows may lie inside a fused projection
+ *   start     [B] int32, offsets [B+1] int32 (a request may have no rows; it
+ *             has no upper limit of rows)
+ *   T         rows of k and v; rows at or behind offsets[B] are ignored, T = 0
+ *             enqueues nothing
+ * Errors on the device: SPEC_ERR_TREE_TOO_LARGE (offsets outside [0, T] or
+ * decreasing) and SPEC_ERR_PREFIX_RANGE (a slot outside [0, S_cap)), for
+ * which the request's slots stay as they were; SPEC_ERR_NONFINITE (NaN or
+ * infinity among the rows), for which every group of 16 that holds one is
+ * stored as zeros and the others are written.
+ */
+int spec_kv4_write(const void *k, const void *v, int dtype, int B, int T, int Hkv, int D,
+                   int64_t k_row_stride, int64_t k_head_stride, int64_t v_row_stride,
+                   int64_t v_head_stride, void *kv_cache, int S_cap, const int32_t *start,
+                   const int32_t *offsets, int32_t *status, void *stream);
+
+/*
+ * spec_kv4_read — slots of the cache as dense rows, the inverse of
+ * spec_kv4_write with the same arguments: row t of k and v receives the
+ * elements of its slot, exactly.  Rows of k and v behind offsets[B], and
+ * those of a request in error, stay as they were.  A stride of 0 between
+ * several output rows or heads is SPEC_ERR_SHAPE.
+ */
+int spec_kv4_read(void *k, void *v, int dtype, int B, int T, int Hkv, int D, int64_t k_row_stride,
+                  int64_t k_head_stride, int64_t v_row_stride, int64_t v_head_stride,
+                  const void *kv_cache, int S_cap, const int32_t *start, const int32_t *offsets,
+                  int32_t *status, void *stream);
+
+/*
+ * spec_tree_attn_kv4 — spec_tree_attn_ex over the 4-bit cache, with an
+ * optional sliding window.
+ *
+ * q, o, the tree and the prefixes are those of spec_tree_attn_ex (mask, or
+ * parents when mask is NULL); a single new token per request is a tree of one
+ * node.  With window > 0, node i at depth d sits at position L_b + d, a prefix
+ * key j at position j and an ancestor at L_b + its depth; node i then sees a
+ * key of K(i) only if it lies less than `window` positions behind it (itself
+ * included), or at one of the first `sinks` positions.  Tiles of the cache
+ * that no node sees are not read.  window = 0 means no window (sinks is then
+ * ignored).
+ *
+ *   dtype        of q and o.  SPEC_BF16: softmax weights enter the product
+ *                with V as halves (11 significant bits), sums in fp32.
+ *                SPEC_F32: queries and weights as two halves each (22 bits).
+ *   Hq % Hkv == 0, Hq / Hkv at most 128, D 64 or 128
+ *   max_prefix   upper bound on every prefix_lens[b], sizes the key splits
+ *                (a larger value is safe, only slower)
+ * A row that sees no key (possible only with a mask that lacks the node
+ * itself) gets zeros.  Splits of the keys merge on chip; no workspace.
+ * Errors on the device: those of spec_tree_attn_ex.
+ */
+int spec_tree_attn_kv4(const void *q, const void *kv_cache, void *o, int dtype, int B, int T,
+                       int Hq, int Hkv, int D, int S_cap, int max_prefix,
+                       const int32_t *prefix_lens, const int32_t *tree_offsets,
+                       const uint32_t *mask, const int32_t *parents, float softmax_scale,
+                       int window, int sinks, int32_t *status, void *stream);
+
+/*
+ * spec_kv4_compact — spec_kv_compact on the 4-bit cache: the accepted path's
+ * records move behind the prefix as they are.  new_prefix_lens must not be
+ * prefix_lens itself (SPEC_ERR_SHAPE).
+ */
+int spec_kv4_compact(void *kv_cache, int B, int Hkv, int D, int S_cap, const int32_t *prefix_lens,
+                     const int32_t *tree_offsets, const int32_t *path_nodes,
+                     const int32_t *accept_len, int max_depth_plus1, int32_t *new_prefix_lens,
+                     int32_t *status, void *stream);
 
 /*
  * spec_tree_expand — one level of draft token-tree construction.

@@ -10,4 +10,5 @@ from .binding import (  # noqa: F401
     SpecError, load, lib_path, build_tree_mask, tree_attn, tree_attn_workspace_size,
     tree_verify, tree_verify_workspace_size, make_verify_workspace, kv_compact, tree_expand, tree_prune, status_string,
     philox_uniforms, tree_merge, STATUS,
+    kv4_record_bytes, make_kv4_cache, kv4_write, kv4_read, kv4_compact, tree_attn_kv4,
 )

@@ -25,6 +25,7 @@ STATUS = {
     -4: "SPEC_ERR_TREE_TOO_LARGE", -5: "SPEC_ERR_BAD_PARENT", -6: "SPEC_ERR_TOKEN_RANGE",
     -7: "SPEC_ERR_WORKSPACE", -8: "SPEC_ERR_CUDA", -9: "SPEC_ERR_TIMEOUT",
     -10: "SPEC_ERR_PREFIX_RANGE", -11: "SPEC_ERR_ALIGNMENT", -12: "SPEC_ERR_INDEX",
+    -13: "SPEC_ERR_NONFINITE",
 }
 SPEC_F32, SPEC_BF16 = 0, 1
 MAX_TREE_NODES = 128
@@ -71,6 +72,17 @@ def load():
     lib.spec_tree_verify_top_p.restype = I
     lib.spec_kv_compact.argtypes = [P, P, I, I, I, I, I, P, P, P, P, I, P, P, P]
     lib.spec_kv_compact.restype = I
+    I64 = ctypes.c_int64
+    lib.spec_kv4_record_bytes.argtypes = [I]
+    lib.spec_kv4_record_bytes.restype = SZ
+    lib.spec_kv4_write.argtypes = [P, P, I, I, I, I, I, I64, I64, I64, I64, P, I, P, P, P, P]
+    lib.spec_kv4_write.restype = I
+    lib.spec_kv4_read.argtypes = [P, P, I, I, I, I, I, I64, I64, I64, I64, P, I, P, P, P, P]
+    lib.spec_kv4_read.restype = I
+    lib.spec_kv4_compact.argtypes = [P, I, I, I, I, P, P, P, P, I, P, P, P]
+    lib.spec_kv4_compact.restype = I
+    lib.spec_tree_attn_kv4.argtypes = [P, P, P, I, I, I, I, I, I, I, I, P, P, P, P, F, I, I, P, P]
+    lib.spec_tree_attn_kv4.restype = I
     lib.spec_tree_expand.argtypes = [P, P, P, P, I, I, I, F, U64, P, P, P, P]
     lib.spec_tree_expand.restype = I
     lib.spec_tree_prune.argtypes = [P, P, P, P, I, I, P, P, P, P, P, P]
@@ -258,6 +270,161 @@ def kv_compact(k_cache, v_cache, prefix_lens, offsets, path_nodes, accept_len, s
                                _ptr(new_prefix_lens), _ptr(status), _stream(stream)),
            "spec_kv_compact")
     return new_prefix_lens
+
+
+# ---------------------------------------------------------------- 4-bit cache
+_KV4_DIMS = {144: 128, 80: 64}     # bytes of a slot record -> head dimension
+_DTYPES = {torch.bfloat16: SPEC_BF16, torch.float32: SPEC_F32}
+
+
+def kv4_record_bytes(D: int) -> int:
+    """Bytes of one slot (key and value of one KV head) of a 4-bit cache, 0 for
+    a head dimension it does not cover."""
+    return int(load().spec_kv4_record_bytes(int(D)))
+
+
+def make_kv4_cache(B, Hkv, S_cap, D, device="cuda"):
+    """An empty 4-bit cache: uint8 [B, Hkv, S_cap, kv4_record_bytes(D)]."""
+    R = kv4_record_bytes(D)
+    if R == 0:
+        raise ValueError(f"a 4-bit cache holds head dimensions 64 and 128, not {D}")
+    return torch.zeros((B, Hkv, S_cap, R), dtype=torch.uint8, device=device)
+
+
+def _kv4_cache(kv_cache):
+    """Checks a 4-bit cache; returns (device, B, Hkv, S_cap, D)."""
+    _dev(kv_cache, torch.uint8, "kv_cache")
+    if kv_cache.dim() != 4 or kv_cache.shape[3] not in _KV4_DIMS:
+        raise ValueError("kv_cache must be [B, Hkv, S_cap, kv4_record_bytes(D)]")
+    B, Hkv, S_cap, R = kv_cache.shape
+    dev = kv_cache.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"kv_cache is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev, B, Hkv, S_cap, _KV4_DIMS[R]
+
+
+def _i32(dev, t, shape, name):
+    if t.dtype != torch.int32 or t.device != dev:
+        raise TypeError(f"{name} must be torch.int32 on {dev}, got {t.dtype} on {t.device}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _dense_rows(dev, t, T, Hkv, D, name):
+    if t.device != dev:
+        raise TypeError(f"{name} must be on {dev}")
+    if t.dim() != 3 or t.shape != (T, Hkv, D) or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [{T}, {Hkv}, {D}] with its last dimension contiguous")
+    return t.stride(0), t.stride(1)
+
+
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+
+
+def kv4_write(k, v, kv_cache, start, offsets, status, stream=None):
+    """Quantises dense rows into the 4-bit cache.  k, v [T, Hkv, D] (bf16 or
+    fp32; rows and heads at any 16-byte stride); request b's rows
+    offsets[b] .. offsets[b+1] go to slots start[b] and up."""
+    lib = load()
+    dev, B, Hkv, S_cap, D = _kv4_cache(kv_cache)
+    dt = _DTYPES.get(k.dtype)
+    if dt is None or v.dtype != k.dtype:
+        raise TypeError("k and v must both be bfloat16 or float32")
+    T = k.shape[0]
+    ks, vs = _dense_rows(dev, k, T, Hkv, D, "k"), _dense_rows(dev, v, T, Hkv, D, "v")
+    _i32(dev, start, (B,), "start")
+    _i32(dev, offsets, (B + 1,), "offsets")
+    _i32(dev, status, (B,), "status")
+    _check(lib.spec_kv4_write(k.data_ptr(), v.data_ptr(), dt, B, T, Hkv, D, *ks, *vs, kv_cache.data_ptr(), S_cap,
+                              start.data_ptr(), offsets.data_ptr(), status.data_ptr(),
+                              _raw_stream(stream, dev)), "spec_kv4_write")
+
+
+def kv4_read(kv_cache, start, offsets, status, rows=None, dtype=torch.bfloat16, out=None, stream=None):
+    """Reads slots of the 4-bit cache back as dense rows, the inverse of
+    kv4_write: the first ``rows`` rows (offsets[-1] of them), or into
+    ``out`` = (k, v), whose rows behind the last request stay as they are.
+    Returns (k, v) [rows, Hkv, D]."""
+    lib = load()
+    dev, B, Hkv, S_cap, D = _kv4_cache(kv_cache)
+    if out is None:
+        if rows is None:
+            raise ValueError("kv4_read needs the number of rows, or out")
+        both = torch.empty((2, rows, Hkv, D), dtype=dtype, device=dev)
+        out = (both[0], both[1])
+    k, v = out
+    dt = _DTYPES.get(k.dtype)
+    if dt is None or v.dtype != k.dtype:
+        raise TypeError("rows are read as bfloat16 or float32")
+    T = k.shape[0]
+    ks, vs = _dense_rows(dev, k, T, Hkv, D, "k"), _dense_rows(dev, v, T, Hkv, D, "v")
+    _i32(dev, start, (B,), "start")
+    _i32(dev, offsets, (B + 1,), "offsets")
+    _i32(dev, status, (B,), "status")
+    _check(lib.spec_kv4_read(k.data_ptr(), v.data_ptr(), dt, B, T, Hkv, D, *ks, *vs, kv_cache.data_ptr(), S_cap,
+                             start.data_ptr(), offsets.data_ptr(), status.data_ptr(),
+                             _raw_stream(stream, dev)), "spec_kv4_read")
+    return out
+
+
+def kv4_compact(kv_cache, prefix_lens, offsets, path_nodes, accept_len, status,
+                new_prefix_lens=None, stream=None):
+    """kv_compact on a 4-bit cache (in place; records move as they are).
+    Returns the new prefix lengths (device int32 [B])."""
+    lib = load()
+    dev, B, Hkv, S_cap, D = _kv4_cache(kv_cache)
+    _i32(dev, prefix_lens, (B,), "prefix_lens")
+    _i32(dev, offsets, (B + 1,), "offsets")
+    _i32(dev, path_nodes, (B, path_nodes.shape[-1]), "path_nodes")
+    _i32(dev, accept_len, (B,), "accept_len")
+    _i32(dev, status, (B,), "status")
+    if new_prefix_lens is None:
+        new_prefix_lens = torch.empty_like(prefix_lens)
+    else:
+        _i32(dev, new_prefix_lens, (B,), "new_prefix_lens")
+    _check(lib.spec_kv4_compact(kv_cache.data_ptr(), B, Hkv, D, S_cap, prefix_lens.data_ptr(), offsets.data_ptr(),
+                                path_nodes.data_ptr(), accept_len.data_ptr(), path_nodes.shape[-1],
+                                new_prefix_lens.data_ptr(), status.data_ptr(),
+                                _raw_stream(stream, dev)), "spec_kv4_compact")
+    return new_prefix_lens
+
+
+def tree_attn_kv4(q, kv_cache, prefix_lens, offsets, mask, max_prefix, status, o=None,
+                  softmax_scale: float = 0.0, stream=None, parents=None, window: int = 0,
+                  sinks: int = 0):
+    """tree_attn over a 4-bit cache.  q [T, Hq, D] bf16 or fp32; with
+    ``window`` > 0 a node sees only keys less than ``window`` positions behind
+    it, and the first ``sinks`` positions; with ``mask=None`` the ancestor sets
+    come from ``parents``."""
+    lib = load()
+    dev, B, Hkv, S_cap, D = _kv4_cache(kv_cache)
+    dt = _DTYPES.get(q.dtype)
+    if dt is None:
+        raise TypeError("q must be bfloat16 or float32")
+    if q.device != dev or q.dim() != 3 or q.shape[2] != D or not q.is_contiguous():
+        raise ValueError(f"q must be contiguous [T, Hq, {D}] on {dev}")
+    T, Hq = q.shape[0], q.shape[1]
+    _i32(dev, prefix_lens, (B,), "prefix_lens")
+    _i32(dev, offsets, (B + 1,), "offsets")
+    _i32(dev, status, (B,), "status")
+    if mask is not None:
+        _i32(dev, mask, (T, 4), "mask")
+    elif parents is not None:
+        _i32(dev, parents, (T,), "parents")
+    else:
+        raise ValueError("tree_attn_kv4 needs a mask or the parent array")
+    if o is None:
+        o = torch.empty_like(q)
+    elif o.dtype != q.dtype or o.device != dev or o.shape != q.shape or not o.is_contiguous():
+        raise ValueError("o must be like q")
+    _check(lib.spec_tree_attn_kv4(q.data_ptr(), kv_cache.data_ptr(), o.data_ptr(), dt, B, T, Hq, Hkv, D, S_cap,
+                                  int(max_prefix), prefix_lens.data_ptr(), offsets.data_ptr(),
+                                  None if mask is None else mask.data_ptr(),
+                                  None if mask is not None else parents.data_ptr(), float(softmax_scale),
+                                  int(window), int(sinks), status.data_ptr(),
+                                  _raw_stream(stream, dev)), "spec_tree_attn_kv4")
+    return o
 
 
 def tree_expand(draft_logits, parent_scores, node_ids, requests, width: int, temperature: float,

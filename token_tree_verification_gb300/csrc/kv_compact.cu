@@ -7,8 +7,10 @@
 //
 // One CTA per (KV head, request): every accepted row of K and V is read into
 // shared memory first and written back after one barrier (a destination slot
-// may be the source of a later path entry), in 16-byte chunks.
-#include "common.cuh"
+// may be the source of a later path entry), in 16-byte chunks.  The 4-bit
+// cache is one array whose rows are the slots' records, so the same kernel
+// moves it (kv4.cuh).
+#include "kv4.cuh"
 
 namespace spec {
 
@@ -17,8 +19,9 @@ namespace {
 constexpr int kKvThreads = 256;
 
 struct KvArgs {
-  uint8_t *k, *v;
-  int es, B, H, D, S_cap, W;
+  uint8_t *k, *v;           // v: null when key and value share a row
+  int arrays, row_bytes;    // 2 (K and V) or 1
+  int B, H, S_cap, W;
   const int32_t *prefix, *offsets, *path, *accept;
   int32_t *new_prefix, *status;
 };
@@ -67,10 +70,10 @@ kv_compact_kernel(const KvArgs a) {
   if (!s_ok || acc == 0) return;
   const int L = s_L;
   const int32_t *pn = a.path + static_cast<size_t>(b) * a.W;
-  const int chunks = a.D * a.es / 16;                 // 16-byte chunks per row
-  const size_t row_bytes = static_cast<size_t>(a.D) * a.es;
+  const int chunks = a.row_bytes / 16;                // 16-byte chunks per row
+  const size_t row_bytes = static_cast<size_t>(a.row_bytes);
   const size_t head = (static_cast<size_t>(b) * a.H + h) * a.S_cap;
-  const int total = 2 * acc * chunks;
+  const int total = a.arrays * acc * chunks;
   for (int i = tid; i < total; i += kKvThreads) {
     const int kv = i / (acc * chunks), rem = i % (acc * chunks);
     const int j = rem / chunks, c = rem % chunks;
@@ -88,6 +91,32 @@ kv_compact_kernel(const KvArgs a) {
   }
 }
 
+// Checks shared by the dense and the 4-bit call, and the launch.
+int compact_rows(KvArgs args, int max_depth_plus1, void *stream) {
+  if (!args.prefix || !args.offsets || !args.path || !args.accept || !args.new_prefix || !args.status)
+    return SPEC_ERR_NULL;
+  if (args.B < 1 || args.H < 1 || args.S_cap < 1 || max_depth_plus1 < 1 ||
+      max_depth_plus1 > SPEC_MAX_TREE_NODES || args.B > 65535)
+    return SPEC_ERR_SHAPE;
+  if ((reinterpret_cast<uintptr_t>(args.k) & 15) || (reinterpret_cast<uintptr_t>(args.v) & 15))
+    return SPEC_ERR_ALIGNMENT;
+  // room for every row an accepted path can move (acc <= max_depth_plus1 - 1)
+  const size_t smem = static_cast<size_t>(args.arrays) * (max_depth_plus1 - 1) * args.row_bytes;
+  if (smem > 200 * 1024) return SPEC_ERR_SHAPE;
+  static std::atomic<size_t> granted[kMaxDevices];
+  if (smem > 48 * 1024 && !allow_dynamic_smem(kv_compact_kernel, smem, granted)) return SPEC_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(args.H), static_cast<unsigned>(args.B), 1);
+  cfg.blockDim = dim3(kKvThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  pdl_attribute(attr[0]);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_compact_kernel, args) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
 }  // namespace
 
 }  // namespace spec
@@ -103,39 +132,23 @@ extern "C" int spec_kv_compact(void *k_cache, void *v_cache, int dtype, int B, i
     return SPEC_ERR_NULL;
   if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_DTYPE;
   const int es = dtype == SPEC_F32 ? 4 : 2;
-  if (B < 1 || Hkv < 1 || S_cap < 1 || max_depth_plus1 < 1 || max_depth_plus1 > SPEC_MAX_TREE_NODES ||
-      D < 8 || (D * es) % 16 != 0 || B > 65535)
-    return SPEC_ERR_SHAPE;
-  if ((reinterpret_cast<uintptr_t>(k_cache) & 15) || (reinterpret_cast<uintptr_t>(v_cache) & 15))
-    return SPEC_ERR_ALIGNMENT;
-  KvArgs args;
-  args.k = static_cast<uint8_t *>(k_cache);
-  args.v = static_cast<uint8_t *>(v_cache);
-  args.es = es;
-  args.B = B;
-  args.H = Hkv;
-  args.D = D;
-  args.S_cap = S_cap;
-  args.W = max_depth_plus1;
-  args.prefix = prefix_lens;
-  args.offsets = tree_offsets;
-  args.path = path_nodes;
-  args.accept = accept_len;
-  args.new_prefix = new_prefix_lens;
-  args.status = status;
-  // room for every row an accepted path can move (acc <= max_depth_plus1 - 1)
-  const size_t smem = static_cast<size_t>(2) * (max_depth_plus1 - 1) * D * es;
-  if (smem > 200 * 1024) return SPEC_ERR_SHAPE;
-  static std::atomic<size_t> granted[kMaxDevices];
-  if (smem > 48 * 1024 && !allow_dynamic_smem(kv_compact_kernel, smem, granted)) return SPEC_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(Hkv), static_cast<unsigned>(B), 1);
-  cfg.blockDim = dim3(kKvThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  pdl_attribute(attr[0]);
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_compact_kernel, args) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  if (D < 8 || (D * es) % 16 != 0) return SPEC_ERR_SHAPE;
+  const KvArgs args = {static_cast<uint8_t *>(k_cache), static_cast<uint8_t *>(v_cache), 2, D * es, B, Hkv, S_cap,
+                       max_depth_plus1, prefix_lens, tree_offsets, path_nodes, accept_len, new_prefix_lens, status};
+  return compact_rows(args, max_depth_plus1, stream);
+}
+
+extern "C" int spec_kv4_compact(void *kv_cache, int B, int Hkv, int D, int S_cap,
+                                const int32_t *prefix_lens, const int32_t *tree_offsets,
+                                const int32_t *path_nodes, const int32_t *accept_len,
+                                int max_depth_plus1, int32_t *new_prefix_lens, int32_t *status,
+                                void *stream) {
+  using namespace spec;
+  if (!kv_cache) return SPEC_ERR_NULL;
+  if (D != 64 && D != 128) return SPEC_ERR_SHAPE;
+  // the CTAs of a request read its length while one of them writes the new one
+  if (new_prefix_lens && new_prefix_lens == prefix_lens) return SPEC_ERR_SHAPE;
+  const KvArgs args = {static_cast<uint8_t *>(kv_cache), nullptr, 1, kv4_record_bytes(D), B, Hkv, S_cap,
+                       max_depth_plus1, prefix_lens, tree_offsets, path_nodes, accept_len, new_prefix_lens, status};
+  return compact_rows(args, max_depth_plus1, stream);
 }

@@ -16,6 +16,7 @@ extern "C" const char *spec_status_string(int code) {
     case SPEC_ERR_PREFIX_RANGE: return "SPEC_ERR_PREFIX_RANGE: prefix does not fit the cache";
     case SPEC_ERR_ALIGNMENT: return "SPEC_ERR_ALIGNMENT: pointer not 16-byte aligned";
     case SPEC_ERR_INDEX: return "SPEC_ERR_INDEX: a computed index fell outside its buffer";
+    case SPEC_ERR_NONFINITE: return "SPEC_ERR_NONFINITE: a row to be quantised holds NaN or infinity";
     default: return "unknown spec_status";
   }
 }
