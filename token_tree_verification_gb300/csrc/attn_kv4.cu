@@ -6,145 +6,522 @@
 // and its ancestors; with a window w, of those only positions p_j > p_i - w or
 // p_j < sinks, where a prefix key's position is its slot and a tree node's is
 // the prefix length plus its depth.
-#include "attn_common.cuh"
-#include "kv4.cuh"
+#include <type_traits>
+
+#include "attn_kv4.cuh"
 
 namespace spec {
 
 namespace {
 
-struct Kv4AttnArgs {
-  AttnArgs a;          // k: the cache; v unused
-  int window, sinks;   // window 0: none
+// ---------------------------------------------------------------- mma.sync path
+// Few rows on each key: every warp decodes records in registers, straight into
+// the fragments of mma.m16n8k16, and no tile passes through shared memory
+// twice.  Both products are taken transposed, keys (then dimensions) along M
+// and rows along N, so that eight rows cost eight, not sixteen or 128:
+//   S^T = K Q^T   A: 16 keys x 16 dims of K,   B: 16 dims x 8 rows of Q
+//   O^T = V^T P^T A: 16 dims x 16 keys of V^T, B: 16 keys x 8 rows of P
+// The order of dims inside a contraction is free, so lane (g, t) = (lane / 4,
+// lane % 4) takes D/4 consecutive dims of key g as they lie in the record (one
+// 16-byte load at D = 128), and D/8 consecutive dims of each of its V keys.
+// S^T's accumulators hold (key g, rows 2t and 2t + 1); movmatrix turns a pair
+// of them into P's fragment (row g, keys 2t and 2t + 1).
+//
+// Which key of a group of 16 is fragment row n is free as well (one order for
+// both products).  kKeyOf spreads the loads over the banks: the record's
+// stride is 4 (D = 128: 36) or 20 words modulo 32, and with this order the
+// eight 16-byte pieces of K, or the sixteen 8-byte pieces of V, that go in one
+// pass hit 32 different banks.
+//
+// Each warp has a ring of its own, tiles of 32 keys brought by one bulk copy
+// each, so warps never wait for one another until the end.
+constexpr int kFewTile = 32;       // keys of a stage
+constexpr int kFewStages = 2;
+
+template <int D, int NT, int W, bool F32>
+struct FewCfg {
+  static constexpr int kWarps = W;
+  static constexpr int kRows = 8 * NT;
+  static constexpr int R = kv4_record_bytes(D);
+  static constexpr int kSteps = D / 16;               // k steps of S^T, m tiles of O^T
+  static constexpr int kParts = F32 ? 2 : 1;          // halves per fp32 query and weight
+  static constexpr bool kQInRegs = NT * kParts <= 2;
+  static constexpr int kStageBytes = kFewTile * R;
+  static constexpr int kRing = kWarps * kFewStages * kStageBytes;
+  static constexpr int kOStride = D + 4;
+  static constexpr int kMerge = kWarps * kRows * kOStride * 4;
+  static constexpr int kQBytes = kQInRegs ? 0 : kParts * kSteps * NT * 32 * 8;
+  static constexpr int kOffQ = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kOffRecv = kOffQ + kQBytes;    // what the peers of a cluster send
+  static constexpr int kSmem = kOffRecv + (kRows * D + 4 * kMaxSplits) * 4;
 };
 
-// What one row sees: prefix keys [0, sinks) and [first, L), and the tree nodes
-// in `tree`.
-struct RowKeys {
-  int sinks, first;
-  uint4 tree;
-};
-
-// A node's ancestors lie on one path, so the r-th lowest bit of its set is the
-// ancestor of depth r, and its own depth is the number of set bits less one.
-__device__ __forceinline__ RowKeys row_keys(uint4 m, int L, int window, int sinks) {
-  RowKeys r;
-  r.tree = m;
-  r.sinks = 0;
-  r.first = 0;
-  if (window == 0) return r;
-  const int depth = __popc(m.x) + __popc(m.y) + __popc(m.z) + __popc(m.w) - 1;
-  r.sinks = sinks;
-  r.first = max(0, L + depth - window + 1);
-  // ancestors of depth [sinks - L, depth - window] are out of sight
-  const int from = max(0, sinks - L), to = depth - window;
-  uint32_t *w = &r.tree.x;
-  int rank = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t left = w[i];
-    while (left && rank <= to) {
-      const uint32_t low = left & (0u - left);
-      if (rank >= from) w[i] &= ~low;
-      left ^= low;
-      ++rank;
-    }
-  }
-  return r;
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ bool row_sees(const RowKeys &r, int key, int L, int keys) {
-  if (key < L) return key < r.sinks || key >= r.first;
-  return key_visible(key, L, keys, r.tree);
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
-// ---------------------------------------------------------------- CUDA cores
-constexpr int kSimpleThreads = 128;
+// Key (0 .. 15) of fragment row n (0 .. 7); row n + 8 is the key after it.
+__device__ __forceinline__ int key_of(int n) {
+  const int t = n >> 1, o = n & 1;
+  return t < 2 ? 2 * t + 4 * o : 8 + 2 * t - 4 * o;
+}
 
-// One CTA per (node, query head), a key per thread and round.
-template <int D, typename E>
-__global__ void __launch_bounds__(kSimpleThreads)
-tree_attn_kv4_kernel(const Kv4AttnArgs p) {
-  constexpr int R = kv4_record_bytes(D);
+template <int D, int NT, int W, bool F32>
+__global__ void __launch_bounds__(32 * W, NT == 1 ? 16 / W : NT == 2 ? 2 : 1)
+tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
+  using C = FewCfg<D, NT, W, F32>;
+  constexpr int kFewWarps = W, kFewThreads = 32 * W;
+  using E = typename std::conditional<F32, float, __nv_bfloat16>::type;
+  constexpr int R = C::R, KS = C::kSteps, NP = C::kParts;
+  constexpr int kWords = D / 32;                  // code words of one lane's share of a key
   const AttnArgs &a = p.a;
-  __shared__ float qs[D];
-  __shared__ float ps[kSimpleThreads];
-  __shared__ float red[kSimpleThreads / 32];
-  const int h = blockIdx.x, t = blockIdx.y, tid = threadIdx.x;
-  if (h == 0 && t == 0)
-    for (int i = tid; i < a.B; i += kSimpleThreads) {
-      const ReqGeom r = request_geometry(a, i);
-      if (r.err) report(a.status, i, r.err);
-    }
-  const int b = find_request(a.offsets, a.B, t);
-  if (b < 0) return;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bar_full[kFewWarps][kFewStages];
+  __shared__ uint4 s_tree[C::kRows];
+  __shared__ int s_first[C::kRows];
+  __shared__ float s_m[kFewWarps][C::kRows], s_l[kFewWarps][C::kRows];
+  __shared__ float2 s_ml[kMaxSplits][C::kRows];
+  __shared__ int s_par[SPEC_MAX_TREE_NODES];
+  __shared__ int s_timeout;
+  const int CS = static_cast<int>(gridDim.x), split = static_cast<int>(blockIdx.x);
+  const int b = blockIdx.z / a.Hkv, g_kv = blockIdx.z % a.Hkv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+
+  pdl_trigger();
+  if (lane == 0) {
+    for (int s = 0; s < kFewStages; ++s) mbar_init(&bar_full[warp][s], 1);
+    fence_barrier_init();
+  }
+  if (tid == 0) s_timeout = 0;
+  __syncwarp();
+  pdl_wait();
+
   const ReqGeom G = request_geometry(a, b);
-  if (G.err) return;
-  const RowKeys see = row_keys(node_mask(a, G, b, t), G.L, p.window, p.sinks);
-  const E *q = static_cast<const E *>(a.q) + (static_cast<size_t>(t) * a.Hq + h) * D;
-  const uint8_t *kv = static_cast<const uint8_t *>(a.k) +
-                      (static_cast<size_t>(b) * a.Hkv + h / a.G) * a.S_cap * R;
-  if (tid < D) qs[tid] = static_cast<float>(q[tid]);
-  __syncthreads();
-  float m_run = -INFINITY, l_run = 0.f, acc = 0.f;
-  for (int c0 = 0; c0 < G.keys; c0 += kSimpleThreads) {
-    const int key = c0 + tid;
-    float sc = -INFINITY;
-    if (key < G.keys && row_sees(see, key, G.L, G.keys)) {
-      const uint8_t *rec = kv + static_cast<size_t>(key) * R;
-      float dot = 0.f;
-      for (int w = 0; w < D / 8; ++w) {
-        uint32_t x[4];
-        kv4_codes_to_half2(reinterpret_cast<const uint32_t *>(rec)[w], x);
-        const uint32_t s = kv4_scale_half2(rec[D + w / 2]);
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t y = mul_half2(x[i], s);
-          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&y));
-          dot = fmaf(qs[8 * w + 2 * i], f.x, dot);
-          dot = fmaf(qs[8 * w + 2 * i + 1], f.y, dot);
+  if (G.err) {      // the same for the whole cluster
+    if (tid == 0 && split == 0 && blockIdx.y == 0 && g_kv == 0) report(a.status, b, G.err);
+    return;
+  }
+  const TileList<kFewTile> tiles(G.L, G.keys, p.window, p.sinks);
+  const int per = (tiles.count + CS - 1) / CS;
+  const int t_end = min(tiles.count, (split + 1) * per);
+  const int t_begin = split * per + warp;             // this warp's tiles: t_begin, + kFewWarps, ...
+  const uint8_t *kv = static_cast<const uint8_t *>(a.k) + (static_cast<size_t>(b) * a.Hkv + g_kv) * a.S_cap * R;
+  uint8_t *ring = smem + warp * kFewStages * C::kStageBytes;
+
+  auto request = [&](int i, int st) {     // lane 0: tile i into stage st
+    const int key0 = tiles.key0(i);
+    const int n = min(kFewTile, G.keys - key0);
+    if (!range_in_bounds(key0, n, a.S_cap, a.status, b)) {
+      mbar_arrive(&bar_full[warp][st]);
+      return;
+    }
+    mbar_arrive_expect_tx(&bar_full[warp][st], static_cast<uint32_t>(n * R));
+    bulk_copy_g2s(smem_addr(ring + st * C::kStageBytes), kv + static_cast<size_t>(key0) * R,
+                  static_cast<uint32_t>(n * R), &bar_full[warp][st]);
+  };
+  // A cluster takes every gridDim.y-th block of its request's rows: the grid is
+  // sized by the mean number of rows, which the host knows, and a request with
+  // more than that takes more turns.
+  const int rows_total = G.n * a.G;
+  bool ok = true;
+  int st = 0, phase = 0;
+  for (int row0 = static_cast<int>(blockIdx.y) * C::kRows; row0 < rows_total;
+       row0 += static_cast<int>(gridDim.y) * C::kRows) {
+    const int rows_here = min(C::kRows, rows_total - row0);
+    if (CS > 1) cluster_arrive_relaxed();   // this CTA runs, and has read what it was sent before
+    if (lane == 0)
+      for (int s = 0; s < kFewStages; ++s)
+        if (t_begin + s * kFewWarps < t_end) request(t_begin + s * kFewWarps, (st + s) % kFewStages);
+
+    // ---- the rows: what each sees, and its query as halves
+    if (!a.mask && row0 == static_cast<int>(blockIdx.y) * C::kRows) {
+      for (int i = tid; i < G.n; i += kFewThreads)
+        s_par[i] = in_bounds(G.lo + i, a.T, a.status, b) ? __ldg(a.parents + G.lo + i) : -2;
+      __syncthreads();
+    }
+    if (tid < C::kRows) {
+      RowKeys see = {0, 0, make_uint4(0u, 0u, 0u, 0u)};
+      if (tid < rows_here) {
+        const int node = (row0 + tid) / a.G;
+        uint4 m = make_uint4(0u, 0u, 0u, 0u);
+        if (a.mask) {
+          if (in_bounds(G.lo + node, a.T, a.status, b)) m = clip_mask(__ldg(a.mask + G.lo + node), G.n);
+        } else {
+          bool bad = false;
+          m = ancestor_mask([&](int i) { return s_par[i]; }, node, &bad);
+          if (bad) report(a.status, b, SPEC_ERR_BAD_PARENT);
+        }
+        see = row_keys(m, G.L, p.window, p.sinks);
+      }
+      s_tree[tid] = see.tree;
+      s_first[tid] = see.first;
+    }
+    uint32_t qf[C::kQInRegs ? NP : 1][C::kQInRegs ? KS : 1][C::kQInRegs ? NT : 1][2];
+    uint2 *sq = reinterpret_cast<uint2 *>(smem + C::kOffQ);   // [part][step][tile][lane]
+    float c_row[NT][2];                                       // score factor of rows 2t, 2t + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = 8 * nt + g, node = (row0 + r) / a.G;
+      float x[D / 4];
+      const bool live = r < rows_here && in_bounds(G.lo + node, a.T, a.status, b);
+      const E *src = static_cast<const E *>(a.q) +
+                     (static_cast<size_t>(G.lo + node) * a.Hq + g_kv * a.G + (row0 + r) % a.G) * D + t * (D / 4);
+#pragma unroll
+      for (int c = 0; c < D / 4; c += 16 / static_cast<int>(sizeof(E))) {
+        const uint4 w = live ? __ldg(reinterpret_cast<const uint4 *>(src + c)) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (F32) {
+            x[c + e] = __uint_as_float(u[e]);
+          } else {
+            x[c + 2 * e] = __uint_as_float(u[e] << 16);
+            x[c + 2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+          }
         }
       }
-      sc = dot * a.scale_log2;
+      float top = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 4; ++c) top = fmaxf(top, fabsf(x[c]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int up = row_exponent(top);
+      const float grow = power_of_two(up);
+      const float c = a.scale_log2 * power_of_two(-up);
+      c_row[nt][0] = __shfl_sync(0xffffffffu, c, 8 * t);
+      c_row[nt][1] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int part = 0; part < NP; ++part) {
+          uint32_t h[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float y0 = x[4 * s + 2 * e] * grow, y1 = x[4 * s + 2 * e + 1] * grow;
+            h[e] = pack_half2(y0, y1);
+            if (part) {
+              const float2 f = unpack_half2(h[e]);
+              h[e] = pack_half2(y0 - f.x, y1 - f.y);
+            }
+          }
+          if constexpr (C::kQInRegs) {
+            qf[part][s][nt][0] = h[0];
+            qf[part][s][nt][1] = h[1];
+          } else if (nt % kFewWarps == warp) {      // NT <= 4: each tile of rows by one warp
+            sq[((part * KS + s) * NT + nt) * 32 + lane] = make_uint2(h[0], h[1]);
+          }
+        }
     }
-    float mx = sc;
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if ((tid & 31) == 0) red[tid >> 5] = mx;
     __syncthreads();
-    mx = red[0];
-    for (int w = 1; w < kSimpleThreads / 32; ++w) mx = fmaxf(mx, red[w]);
-    const float m_new = fmaxf(m_run, mx);
-    const float base = m_new == -INFINITY ? 0.f : m_new;
-    const float alpha = m_run == -INFINITY ? 0.f : exp2f(m_run - base);
-    const float w = exp2f(sc - base);
-    ps[tid] = w;
-    float sum = w;
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    __syncthreads();
-    if ((tid & 31) == 0) red[tid >> 5] = sum;
-    __syncthreads();
-    sum = 0.f;
-    for (int i = 0; i < kSimpleThreads / 32; ++i) sum += red[i];
-    l_run = l_run * alpha + sum;
-    m_run = m_new;
-    if (tid < D) {
-      float part = 0.f;
-      const int nk = min(kSimpleThreads, G.keys - c0);
-      for (int j = 0; j < nk; ++j) {
-        if (ps[j] == 0.f) continue;
-        const uint8_t *rec = kv + static_cast<size_t>(c0 + j) * R;
-        uint32_t x[4];
-        kv4_codes_to_half2(rec[D / 2 + tid / 2], x);
-        const uint32_t y = mul_half2(x[0], kv4_scale_half2(rec[D + D / 16 + tid / 16]));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&y));
-        part = fmaf(ps[j], tid & 1 ? f.y : f.x, part);
+
+    // ---- the keys
+    float o[NT][KS][4];
+    float m_ref[NT][2], nbase[NT][2], l_row[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < KS; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][j][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m_ref[nt][e] = -INFINITY;
+        nbase[nt][e] = kWeightLog2;
+        l_row[nt][e] = 0.f;
       }
-      acc = acc * alpha + part;
+    }
+    const int kn = key_of(g);                                 // this lane's K rows: kn, kn + 1
+    const int kv0 = key_of(2 * t), kv1 = key_of(2 * t + 1);   // its V keys: these and the ones after
+    for (int i = t_begin; i < t_end; i += kFewWarps) {
+      if (ok && !mbar_wait(&bar_full[warp][st], phase)) ok = false;
+      const int key0 = tiles.key0(i);
+      const uint8_t *tile = ring + st * C::kStageBytes;
+      float sc[2][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
+        uint32_t kw[2][kWords], ks[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint8_t *rec = tile + (16 * mt + kn + e) * R;
+          if constexpr (D == 128) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(rec + 16 * t);
+            kw[e][0] = w.x; kw[e][1] = w.y; kw[e][2] = w.z; kw[e][3] = w.w;
+            ks[e] = *reinterpret_cast<const uint16_t *>(rec + D + 2 * t);
+          } else {
+            const uint2 w = *reinterpret_cast<const uint2 *>(rec + 8 * t);
+            kw[e][0] = w.x; kw[e][1] = w.y;
+            ks[e] = rec[D + t];
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+          uint32_t h0[4], h1[4];
+          kv4_codes_to_half2(kw[0][w], h0);
+          kv4_codes_to_half2(kw[1][w], h1);
+          const uint32_t s0 = kv4_scale_half2(w < 2 ? ks[0] & 0xFFu : ks[0] >> 8);
+          const uint32_t s1 = kv4_scale_half2(w < 2 ? ks[1] & 0xFFu : ks[1] >> 8);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            h0[e] = mul_half2(h0[e], s0);
+            h1[e] = mul_half2(h1[e], s1);
+          }
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int part = 0; part < NP; ++part)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const int s = 2 * w + half;
+                uint2 q;
+                if constexpr (C::kQInRegs) q = make_uint2(qf[part][s][nt][0], qf[part][s][nt][1]);
+                else q = sq[((part * KS + s) * NT + nt) * 32 + lane];
+                mma_16816(sc[mt][nt], h0[2 * half], h1[2 * half], h0[2 * half + 1], h1[2 * half + 1], q.x, q.y);
+              }
+        }
+      }
+      // keys that some row may not see: the tree, and the window's borders
+      const bool whole = key0 + kFewTile <= G.L &&
+                         (p.window == 0 || key0 + kFewTile <= p.sinks || key0 >= G.L + G.n - p.window);
+      if (!whole) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 8 * nt + 2 * t + e;
+            const RowKeys see = {p.window ? p.sinks : 0, s_first[r], s_tree[r]};
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                if (!row_sees(see, key0 + 16 * mt + kn + k, G.L, G.keys)) sc[mt][nt][2 * k + e] = -INFINITY;
+          }
+      }
+      bool want = false;
+      float mx[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mx[nt][e] = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][2 + e]), fmaxf(sc[1][nt][e], sc[1][nt][2 + e])) * c_row[nt][e];
+          want |= mx[nt][e] > m_ref[nt][e] + kMoveLog2;
+        }
+      if (__any_sync(0xffffffffu, want)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float m = mx[nt][e];
+#pragma unroll
+            for (int x = 4; x < 32; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+            if (m > m_ref[nt][e] + kMoveLog2) {
+              m = ceilf(m);
+              const float alpha = exp2f(m_ref[nt][e] - m);    // 0 the first time
+              l_row[nt][e] *= alpha;
+#pragma unroll
+              for (int j = 0; j < KS; ++j) {
+                o[nt][j][e] *= alpha;
+                o[nt][j][2 + e] *= alpha;
+              }
+              m_ref[nt][e] = m;
+              nbase[nt][e] = kWeightLog2 - m;
+            }
+          }
+      }
+      // ---- weights, and their product with V
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t pf[NP][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float p0 = fast_exp2(fmaf(sc[mt][nt][2 * k], c_row[nt][0], nbase[nt][0]));
+            const float p1 = fast_exp2(fmaf(sc[mt][nt][2 * k + 1], c_row[nt][1], nbase[nt][1]));
+            l_row[nt][0] += p0;
+            l_row[nt][1] += p1;
+            const uint32_t h = pack_half2(p0, p1);
+            pf[0][nt][k] = movmatrix(h);
+            if constexpr (F32) {
+              const float2 f = unpack_half2(h);
+              pf[1][nt][k] = movmatrix(pack_half2(p0 - f.x, p1 - f.y));
+            }
+          }
+        // keys kv0, kv1 (k index 2t, 2t + 1), and the ones after them (+ 8)
+        uint32_t vw[4][D / 64];
+        uint32_t vs[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = 16 * mt + ((e & 1) ? kv1 : kv0) + (e >> 1);
+          const uint8_t *rec = tile + key * R;
+          if constexpr (D == 128) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(rec + D / 2 + 8 * g);
+            vw[e][0] = w.x; vw[e][1] = w.y;
+            vs[e] = rec[D + D / 16 + g];
+          } else {
+            vw[e][0] = *reinterpret_cast<const uint32_t *>(rec + D / 2 + 4 * g);
+            vs[e] = rec[D + D / 16 + g / 2];
+          }
+          if (!whole && key0 + key >= G.keys) vs[e] = 0u;   // slots that were not copied may hold anything
+        }
+        const uint32_t sa = (vs[0] << 7) | (vs[1] << 23), sb = (vs[2] << 7) | (vs[3] << 23);
+#pragma unroll
+        for (int w = 0; w < D / 64; ++w) {
+          uint32_t ae[4], ao[4], be[4], bo[4];   // even and odd dims of the first and second key pair
+          kv4_codes_to_half2((vw[0][w] & 0x0F0F0F0Fu) | ((vw[1][w] << 4) & 0xF0F0F0F0u), ae);
+          kv4_codes_to_half2(((vw[0][w] >> 4) & 0x0F0F0F0Fu) | (vw[1][w] & 0xF0F0F0F0u), ao);
+          kv4_codes_to_half2((vw[2][w] & 0x0F0F0F0Fu) | ((vw[3][w] << 4) & 0xF0F0F0F0u), be);
+          kv4_codes_to_half2(((vw[2][w] >> 4) & 0x0F0F0F0Fu) | (vw[3][w] & 0xF0F0F0F0u), bo);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t a0 = mul_half2(ae[e], sa), a1 = mul_half2(ao[e], sa);
+            const uint32_t a2 = mul_half2(be[e], sb), a3 = mul_half2(bo[e], sb);
+#pragma unroll
+            for (int part = 0; part < NP; ++part)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_16816(o[nt][4 * w + e], a0, a1, a2, a3, pf[part][nt][0], pf[part][nt][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0 && ok && i + kFewStages * kFewWarps < t_end) request(i + kFewStages * kFewWarps, st);
+      if (++st == kFewStages) {
+        st = 0;
+        phase ^= 1;
+      }
+    }
+    if (!ok && lane == 0) s_timeout = 1;
+
+    // ---- the warps' parts of each row, then the splits'
+    __syncthreads();     // every ring is read; no copy is in flight unless a wait ran out
+    const bool timed_out = s_timeout != 0;
+    if (timed_out && tid == 0) report(a.status, b, SPEC_ERR_TIMEOUT);
+    float *so = reinterpret_cast<float *>(smem);      // [warp][row][kOStride]
+    if (!timed_out) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * nt + 2 * t + e;
+          float l = l_row[nt][e];
+#pragma unroll
+          for (int x = 4; x < 32; x *= 2) l += __shfl_xor_sync(0xffffffffu, l, x);
+          if (g == 0) {
+            s_m[warp][r] = m_ref[nt][e];
+            s_l[warp][r] = l;
+          }
+          float *dst = so + (warp * C::kRows + r) * C::kOStride + (D / 8) * g;
+#pragma unroll
+          for (int j = 0; j < KS; ++j) *reinterpret_cast<float2 *>(dst + 2 * j) = make_float2(o[nt][j][e], o[nt][j][2 + e]);
+        }
     }
     __syncthreads();
+    auto out_row = [&](int r) -> E * {
+      const int node = (row0 + r) / a.G;
+      if (!in_bounds(G.lo + node, a.T, a.status, b)) return nullptr;
+      return static_cast<E *>(a.o) + (static_cast<size_t>(G.lo + node) * a.Hq + g_kv * a.G + (row0 + r) % a.G) * D;
+    };
+    if (!merge_rows<D, kFewWarps, C::kRows, kFewThreads, E>(
+            tid, CS, split, rows_here, timed_out, so, s_m, s_l, s_ml, reinterpret_cast<float4 *>(smem + C::kOffRecv),
+            [] { cluster_wait(); }, out_row))
+      return;
+    __syncthreads();    // all is read, before this CTA's next arrival says so and the ring is filled again
   }
-  if (tid < D)
-    static_cast<E *>(a.o)[(static_cast<size_t>(t) * a.Hq + h) * D + tid] =
-        static_cast<E>(l_run == 0.f ? 0.f : acc / l_run);
+}
+
+// A launch of `cs` splits (a cluster) of every unit, a unit being one block of
+// rows of one (request, KV head).
+template <int D, int NT, int W, bool F32>
+int launch_few(const Kv4AttnArgs &p, int blocks, int cs, void *stream) {
+  using C = FewCfg<D, NT, W, F32>;
+  auto kernel = tree_attn_kv4_few_kernel<D, NT, W, F32>;
+  static std::atomic<size_t> granted[kMaxDevices];
+  if (!allow_dynamic_smem(kernel, C::kSmem, granted)) return SPEC_ERR_CUDA;
+  if (cs > 8) {
+    static std::atomic<bool> wide[kMaxDevices];       // clusters beyond the portable 8
+    const int dev = current_device();
+    if (dev < 0) return SPEC_ERR_CUDA;
+    if (!wide[dev].load(std::memory_order_acquire)) {
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return SPEC_ERR_CUDA;
+      wide[dev].store(true, std::memory_order_release);
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cs, static_cast<unsigned>(blocks), static_cast<unsigned>(p.a.B * p.a.Hkv));
+  cfg.blockDim = dim3(32 * W, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  pdl_attribute(attr[1]);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+// Splits: while every warp keeps a tile, up to 8 as long as the CTAs stay
+// within two waves (about four CTAs of four warps per SM), and 16 only where 8
+// leave SMs without work.
+int few_splits(const Kv4AttnArgs &p, long long units, int max_prefix) {
+  long long keys = static_cast<long long>(max_prefix) + mean_nodes(p.a);
+  if (p.window) {
+    const long long near = static_cast<long long>(p.window) + p.sinks + mean_nodes(p.a) + 2 * kFewTile;
+    if (near < keys) keys = near;
+  }
+  const long long tiles = (keys + kFewTile - 1) / kFewTile;
+  const long long sms = sm_count();
+  int cs = 1;
+  while (cs < 8 && 2 * cs * units <= 8 * sms && tiles >= 8 * cs) cs *= 2;
+  if (cs == 8 && 8 * units < sms && tiles >= 64) cs = 16;
+  return cs;
+}
+
+template <int D, bool F32>
+int attn_few(const Kv4AttnArgs &p, int max_prefix, void *stream) {
+  const int rows = mean_nodes(p.a) * p.a.G;
+  const int per = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  const int blocks = (rows + per - 1) / per;
+  const long long pairs = static_cast<long long>(p.a.B) * p.a.Hkv;
+  if (pairs > 65535 || blocks > 65535) return SPEC_ERR_SHAPE;
+  const long long units = pairs * blocks;
+  const int cs = few_splits(p, units, max_prefix);
+  // eight warps instead of four where CTAs are few
+  if (per == 8)
+    return units * cs <= 2 * sm_count() ? launch_few<D, 1, 8, F32>(p, blocks, cs, stream)
+                                        : launch_few<D, 1, 4, F32>(p, blocks, cs, stream);
+  if constexpr (F32) {      // (bf16 has tensor-core kernels for more than 8 rows)
+    return per == 16 ? launch_few<D, 2, 4, F32>(p, blocks, cs, stream) : launch_few<D, 4, 4, F32>(p, blocks, cs, stream);
+  } else {
+    return SPEC_ERR_SHAPE;
+  }
+}
+
+// Which bf16 kernel: by the mean number of rows on each key (a request with
+// more takes more turns).
+template <int D>
+int attn_bf16(const Kv4AttnArgs &p, int max_prefix, void *stream) {
+  const int rows = mean_nodes(p.a) * p.a.G;
+  if (rows <= 8) return attn_few<D, false>(p, max_prefix, stream);
+  return rows <= 64 ? launch_kv4_tc(p, max_prefix, stream) : launch_kv4_rows(p, max_prefix, stream);
 }
 
 }  // namespace
@@ -188,14 +565,7 @@ extern "C" int spec_tree_attn_kv4(const void *q, const void *kv_cache, void *o, 
   // positions stay below S_cap: a window that large hides nothing
   p.window = window < S_cap ? window : S_cap;
   p.sinks = sinks < S_cap ? sinks : S_cap;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 grid(static_cast<unsigned>(Hq), static_cast<unsigned>(T), 1);
-  if (dtype == SPEC_BF16) {
-    if (D == 128) tree_attn_kv4_kernel<128, __nv_bfloat16><<<grid, kSimpleThreads, 0, st>>>(p);
-    else tree_attn_kv4_kernel<64, __nv_bfloat16><<<grid, kSimpleThreads, 0, st>>>(p);
-  } else {
-    if (D == 128) tree_attn_kv4_kernel<128, float><<<grid, kSimpleThreads, 0, st>>>(p);
-    else tree_attn_kv4_kernel<64, float><<<grid, kSimpleThreads, 0, st>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  if (dtype == SPEC_BF16)
+    return D == 128 ? attn_bf16<128>(p, max_prefix, stream) : attn_bf16<64>(p, max_prefix, stream);
+  return D == 128 ? attn_few<128, true>(p, max_prefix, stream) : attn_few<64, true>(p, max_prefix, stream);
 }

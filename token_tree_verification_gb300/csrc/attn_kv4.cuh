@@ -1,0 +1,267 @@
+// Pieces shared by the two kernels of tree attention over the 4-bit cache:
+// what a row sees, which tiles that takes, and the merge of the key splits.
+#pragma once
+
+#include "attn_common.cuh"
+#include "kv4.cuh"
+
+namespace spec {
+
+struct Kv4AttnArgs {
+  AttnArgs a;          // k: the cache; v unused
+  int window, sinks;   // window 0: none
+};
+
+// What one row sees: prefix keys [0, sinks) and [first, L), and the tree nodes
+// in `tree`.
+struct RowKeys {
+  int sinks, first;
+  uint4 tree;
+};
+
+// A node's ancestors lie on one path, so the r-th lowest bit of its set is the
+// ancestor of depth r, and its own depth is the number of set bits less one.
+__device__ __forceinline__ RowKeys row_keys(uint4 m, int L, int window, int sinks) {
+  RowKeys r;
+  r.tree = m;
+  r.sinks = 0;
+  r.first = 0;
+  if (window == 0) return r;
+  const int depth = max(0, __popc(m.x) + __popc(m.y) + __popc(m.z) + __popc(m.w) - 1);
+  r.sinks = sinks;
+  r.first = max(0, L + depth - window + 1);
+  // ancestors of depth [sinks - L, depth - window] are out of sight
+  const int from = max(0, sinks - L), to = depth - window;
+  uint32_t *w = &r.tree.x;
+  int rank = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t left = w[i];
+    while (left && rank <= to) {
+      const uint32_t low = left & (0u - left);
+      if (rank >= from) w[i] &= ~low;
+      left ^= low;
+      ++rank;
+    }
+  }
+  return r;
+}
+
+__device__ __forceinline__ bool row_sees(const RowKeys &r, int key, int L, int keys) {
+  if (key < L) return key < r.sinks || key >= r.first;
+  return key_visible(key, L, keys, r.tree);
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpack_half2(uint32_t x) {
+  return __half22float2(*reinterpret_cast<const __half2 *>(&x));
+}
+
+// Global to shared bulk copy (16-byte aligned, a multiple of 16 bytes),
+// completing on `bar`.
+__device__ __forceinline__ void bulk_copy_g2s(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_addr(bar))
+      : "memory");
+}
+
+template <typename E>
+__device__ __forceinline__ void store_row4(E *dst, float4 v) {
+  if constexpr (sizeof(E) == 4) {
+    *reinterpret_cast<float4 *>(dst) = v;
+  } else {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2 *>(dst) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+  }
+}
+
+// L2 prefetch of a run of global memory (16-byte aligned, a multiple of 16).
+__device__ __forceinline__ void bulk_prefetch_l2(const void *src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)
+               : "memory");
+}
+
+// mbar_wait for roles that wait long and often: the thread is suspended up to
+// 10 us a try instead of polling through the issue slots of the working warps.
+// (`bar` is a shared-memory address.)
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 10000;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+  for (uint32_t it = 0; it < kWaitLimitNs / 10000; ++it)
+    if (mbar_try(bar, parity)) return true;
+  return false;
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// A place in a ring of n stages and the phase of its barriers.
+template <int n>
+struct Ring {
+  uint32_t at = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if constexpr (n == 2) {
+      at ^= 1;
+      phase ^= at ^ 1;
+    } else if (++at == n) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// Which tiles of `TILE` keys a row block reads: all, or with a window those
+// that hold the first `sinks` slots, then those from the root's window on.
+template <int TILE>
+struct TileList {
+  int head, skip, count;
+  __device__ __forceinline__ TileList(int L, int keys, int window, int sinks) {
+    const int all = (keys + TILE - 1) / TILE;
+    head = 0;
+    skip = 0;
+    if (window > 0) {
+      head = (min(sinks, keys) + TILE - 1) / TILE;
+      const int from = max(0, L - window + 1) / TILE;
+      skip = max(0, from - head);
+    }
+    count = all - skip;
+  }
+  __device__ __forceinline__ int key0(int i) const { return (i < head ? i : i + skip) * TILE; }
+};
+
+// The weights' halves are scaled by 2^8 at the reference, a whole number at or
+// above the largest score so far, which moves only when a score passes it by
+// more than 7: they stay below 2^15 (a half ends at 2^16), and the row's
+// largest is at least 2^7, 2^32 times half the step of the smallest halves.
+// Whole references make 8 - m and the factors 2^(m - m') exact.
+constexpr float kWeightLog2 = 8.f;
+constexpr float kMoveLog2 = 7.f;
+
+constexpr int kMaxSplits = 16;
+
+// A row's query is taken as halves: scaled by 2^up so that its largest finite
+// element is near 2^13, which the score factor takes back.  (A row below
+// 2^-113 stays that much smaller: its scores vanish either way.)
+__device__ __forceinline__ int row_exponent(float top) {
+  return top > 0.f && top < INFINITY ? min(13 + 127 - (__float_as_int(top) >> 23), 126) : 0;
+}
+__device__ __forceinline__ float power_of_two(int e) { return __int_as_float((127 + e) << 23); }
+
+// Merge of a block's rows over the CTA's own parts and the cluster's splits,
+// and the output, by THREADS threads of the CTA (`tid` among them; any others
+// run the two cluster barriers of a split block, ready()'s and the one here)
+// with W parts per row in
+// so[W][ROWS][D + 4] (weighted sums), s_m[W][ROWS] (references) and
+// s_l[W][ROWS] (sums of weights), or with `timed_out`.  Without splits the
+// merged piece of four dims is the result; else it goes to the CTA of the
+// cluster that merges it (CTA q has pieces [q share, (q + 1) share)), and
+// every CTA gets each row's reference and sum: stores that nothing waits for.
+// ready() returns once every CTA's `recv` and `s_ml` may be written.  Returns
+// false when a CTA of the cluster timed out (nothing is written then).
+template <int D, int W, int ROWS, int THREADS, typename E, typename Ready, typename OutRow>
+__device__ __forceinline__ bool merge_rows(int tid, int CS, int split, int rows_here, bool timed_out, float *so,
+                                           const float (*s_m)[ROWS], const float (*s_l)[ROWS],
+                                           float2 (*s_ml)[ROWS], float4 *recv, Ready ready, OutRow out_row) {
+  constexpr int kStride = D + 4;
+  const int pieces = rows_here * (D / 4);
+  const int share = (pieces + CS - 1) / CS;
+  if (CS > 1) {
+    ready();
+    for (int i = tid; i < CS * rows_here; i += THREADS) {
+      const int r = i / CS, q = i % CS;
+      float M = s_m[0][r], L = 0.f;
+#pragma unroll
+      for (int w = 1; w < W; ++w) M = fmaxf(M, s_m[w][r]);
+      const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int w = 0; w < W; ++w) L = fmaf(exp2f(s_m[w][r] - base), s_l[w][r], L);
+      const uint32_t dst = peer_addr(&s_ml[split][r], q);
+      st_peer_f32(dst, timed_out ? INFINITY : M);
+      st_peer_f32(dst + 4, timed_out ? -1.f : L);      // no sum of weights is negative
+    }
+  }
+  auto finish = [&](int r, int c, float4 acc, float L) {
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    E *dst = out_row(r);
+    if (dst) store_row4(dst + c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+  };
+  for (int idx = tid; idx < pieces && !timed_out; idx += THREADS) {
+    const int r = idx / (D / 4), c = idx % (D / 4) * 4;
+    float4 acc;
+    float L;
+    if constexpr (W == 1) {
+      acc = *reinterpret_cast<const float4 *>(so + r * kStride + c);
+      L = s_l[0][r];
+    } else {
+      float M = s_m[0][r];
+#pragma unroll
+      for (int w = 1; w < W; ++w) M = fmaxf(M, s_m[w][r]);
+      const float base = M == -INFINITY ? 0.f : M;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      L = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float f = exp2f(s_m[w][r] - base);
+        const float4 v = *reinterpret_cast<const float4 *>(so + (w * ROWS + r) * kStride + c);
+        L = fmaf(f, s_l[w][r], L);
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+      }
+    }
+    if (CS > 1) st_peer_f32x4(peer_addr(recv + split * share + idx % share, idx / share), acc);
+    else finish(r, c, acc, L);
+  }
+  if (CS == 1) return !timed_out;
+  cluster_sync_all();
+  bool any_timeout = false;
+  for (int q = 0; q < CS; ++q) any_timeout |= s_ml[q][0].y < 0.f;
+  if (any_timeout) return false;      // every CTA of the cluster sees the same
+  for (int i = tid; i < min(share, pieces - split * share); i += THREADS) {
+    const int idx = split * share + i, r = idx / (D / 4), c = idx % (D / 4) * 4;
+    float M = -INFINITY;
+    for (int q = 0; q < CS; ++q) M = fmaxf(M, s_ml[q][r].x);
+    const float base = M == -INFINITY ? 0.f : M;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float L = 0.f;
+    for (int q = 0; q < CS; ++q) {
+      const float2 ml = s_ml[q][r];
+      const float f = exp2f(ml.x - base);
+      const float4 v = recv[q * share + i];
+      L = fmaf(f, ml.y, L);
+      acc.x = fmaf(f, v.x, acc.x);
+      acc.y = fmaf(f, v.y, acc.y);
+      acc.z = fmaf(f, v.z, acc.z);
+      acc.w = fmaf(f, v.w, acc.w);
+    }
+    finish(r, c, acc, L);
+  }
+  return true;
+}
+
+// The host does not know the requests' tree sizes; launches are sized by their
+// mean, rounded up.
+inline int mean_nodes(const AttnArgs &a) { return (a.T + a.B - 1) / a.B; }
+
+// The tensor-core paths, bf16 only: rows along N (attn_kv4_tc.cu) and along M
+// (attn_kv4_rows.cu).
+int launch_kv4_tc(const Kv4AttnArgs &p, int max_prefix, void *stream);
+int launch_kv4_rows(const Kv4AttnArgs &p, int max_prefix, void *stream);
+
+}  // namespace spec

@@ -1,0 +1,516 @@
+// Tree attention over the 4-bit KV cache on the 5th-generation tensor cores,
+// bf16 queries, for blocks of up to 128 rows of one KV head: large trees,
+// and trees with several query heads per KV head.
+//
+// With that many rows the products are bound by the softmax and the decoding,
+// not by what a row costs the tensor cores, so the rows lie along M here:
+//   S[rows][keys] = Q K^T   A = Q (shared memory),  B = K (keys x dims, shared memory, K-major)
+//   O[rows][dims] = P V     A = P (TMEM),           B = V (keys x dims, shared memory, MN-major)
+// A softmax thread then has one row, whose reference, sum and factor are
+// registers, and its weights go to TMEM as they are; decoded records serve 128
+// rows instead of 64.  (attn_kv4_tc.cu has the form for fewer rows, where the
+// cost is the decoding of each key.)
+//
+// One CTA = one split of the keys x one block of 128 rows x one (request, KV
+// head).  Warp roles:
+//   warp 0      brings tiles of 128 records, one bulk copy each
+//   warp 1      allocates TMEM and issues S_i into one of two TMEM buffers
+//   warp 2      issues O += P_i V_i
+//   warps 4-19  softmax: the four warps of a TMEM lane quarter hold the same 32
+//               rows, each 32 of the tile's 128 keys
+//   warps 20-23 decode keys, warps 24-27 values (one key per lane: loads of
+//               records 36 words apart and swizzled stores of rows 128 bytes
+//               apart are both free of bank conflicts)
+#include <type_traits>
+
+#include "attn_kv4_tc.cuh"
+
+namespace spec {
+
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kSoftFirst = 4;         // warps: four issuers, then the softmax, then the decoders
+constexpr int kSoftWarps = 16;
+constexpr int kDecodeFirst = kSoftFirst + kSoftWarps;
+constexpr int kDecodeWarps = 4;       // for keys, and as many for values
+constexpr int kThreads = 32 * (kDecodeFirst + 2 * kDecodeWarps);
+constexpr int kSoftThreads = 32 * kSoftWarps;
+constexpr int kPart = kTile / 4;      // keys of one softmax thread
+
+template <int D>
+struct Kv4Rows128 {
+  static constexpr int R = kv4_record_bytes(D);
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kBoxBytes = kTile * 128;             // 128 rows of 64 halves: Q, K and V alike
+  static constexpr int kOpBytes = kBoxes * kBoxBytes;
+  static constexpr int kRaw = D == 128 ? 3 : 5;             // stages of records
+  static constexpr int kRawBytes = kTile * R;
+  static constexpr int kOffK = 0;
+  static constexpr int kOffV = kOffK + 2 * kOpBytes;
+  static constexpr int kOffQ = kOffV + 2 * kOpBytes;
+  static constexpr int kOffRaw = kOffQ + kOpBytes;
+  // after the loop: the rows, the ones received, and their references and sums
+  static constexpr int kOffRecv = kRows * (D + 4) * 4;
+  static constexpr int kEnd = kOffRaw + kRaw * kRawBytes;
+  static constexpr int kOffMl = (kOffRecv + (kRows * D + 4 * kMaxSplits) * 4 + 15) / 16 * 16;
+  static constexpr int kMerge = kOffMl + kMaxSplits * kRows * 8;
+  static constexpr int kSmem = (kEnd > kMerge ? kEnd : kMerge) + 1024;
+  // TMEM: two S buffers, O, two P buffers (a pair of keys per column)
+  static constexpr uint32_t kColO = 2 * kTile, kColP = kColO + 128, kTmemCols = 512;
+  static_assert(kSmem <= 227 * 1024 - 8192, "shared memory budget");
+};
+
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// Which of the 32 keys from k0 on a row sees, as bits.
+__device__ __forceinline__ uint32_t sees32(const RowKeys &r, int k0, int L, int window) {
+  uint32_t prefix = low_bits(L - k0);
+  if (window) prefix &= low_bits(r.sinks - k0) | ~low_bits(r.first - k0);
+  const int o = k0 - L;            // first key's node
+  const uint4 m = r.tree;
+  if (o <= -32) return prefix;
+  if (o < 0) return prefix | (m.x << -o);
+  const int w = o >> 5;
+  const uint32_t lo = w == 0 ? m.x : w == 1 ? m.y : w == 2 ? m.z : w == 3 ? m.w : 0u;
+  const uint32_t hi = w == 0 ? m.y : w == 1 ? m.z : w == 2 ? m.w : 0u;
+  return __funnelshift_r(lo, hi, o & 31);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
+  using C = Kv4Rows128<D>;
+  constexpr int R = C::R, kRaw = C::kRaw;
+  const AttnArgs &a = p.a;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ struct {
+    uint64_t raw_full[kRaw], raw_empty[kRaw];
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t s_full[2], s_empty[2], p_full[2], o_done[2], q_full;
+  } bars;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_timeout;
+  __shared__ int s_par[SPEC_MAX_TREE_NODES];
+  __shared__ float s_c[kRows];                // a row's score factor
+  __shared__ float s_max[2][4][kRows];        // [tile parity][key part][row]
+  __shared__ float s_ref[1][kRows], s_sum[1][kRows];
+
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  const uint32_t sb = smem_addr(smem);
+  float2 (*s_ml)[kRows] = reinterpret_cast<float2 (*)[kRows]>(smem + C::kOffMl);
+  const uint32_t raw_full = smem_addr(bars.raw_full), raw_empty = smem_addr(bars.raw_empty);
+  const uint32_t s_full = smem_addr(bars.s_full), s_empty = smem_addr(bars.s_empty);
+  const uint32_t p_full = smem_addr(bars.p_full), o_done = smem_addr(bars.o_done);
+  const int CS = static_cast<int>(gridDim.x), split = static_cast<int>(blockIdx.x);
+  const int b = blockIdx.z / a.Hkv, g_kv = blockIdx.z % a.Hkv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  pdl_trigger();
+  if (tid == 0) {
+    for (int s = 0; s < kRaw; ++s) {
+      mbar_init(&bars.raw_full[s], 1);
+      mbar_init(&bars.raw_empty[s], 2 * kDecodeWarps);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars.k_full[s], kDecodeWarps);
+      mbar_init(&bars.v_full[s], kDecodeWarps);
+      mbar_init(&bars.k_empty[s], 1);
+      mbar_init(&bars.v_empty[s], 1);
+      mbar_init(&bars.s_full[s], 1);
+      mbar_init(&bars.s_empty[s], kSoftWarps);
+      mbar_init(&bars.p_full[s], kSoftWarps);
+      mbar_init(&bars.o_done[s], 1);
+    }
+    mbar_init(&bars.q_full, kSoftWarps);
+    fence_barrier_init();
+    s_timeout = 0;
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(&s_tmem, C::kTmemCols);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = s_tmem;
+  pdl_wait();
+
+  const ReqGeom G = request_geometry(a, b);
+  const int rows_total = G.err ? 0 : G.n * a.G;
+  if (G.err && tid == 0 && split == 0 && blockIdx.y == 0 && g_kv == 0) report(a.status, b, G.err);
+  const TileList<kTile> tiles(G.L, G.keys, p.window, p.sinks);
+  const int per = (tiles.count + CS - 1) / CS;
+  const int t0 = split * per;
+  const int ntiles = max(0, min(t0 + per, tiles.count) - t0);
+
+  // Each role runs the turns (row blocks) of this CTA on its own, its places
+  // in the rings going on from turn to turn, and meets the others at their
+  // ends, where the softmax warps merge the rows.  A wait that runs out clears
+  // ok: the role stops waiting, and all return after the turn.
+  bool ok = true;
+  auto turns = [&](auto &&work, auto &&finish) {
+    for (int row0 = static_cast<int>(blockIdx.y) * kRows; row0 < rows_total;
+         row0 += static_cast<int>(gridDim.y) * kRows) {
+      work(row0);
+      if (!ok) s_timeout = 1;
+      __syncwarp();
+      tc::fence_before_sync();
+      __syncthreads();
+      tc::fence_after_sync();
+      const bool done = finish(row0);
+      // (the next turn's operands take the staged rows' place)
+      __syncthreads();
+      if (!done) break;
+    }
+  };
+  // A split block's CTAs arrive twice at the cluster's barrier: when a thread's
+  // work on the turn is done (then peers may write here), and when the rows
+  // have been sent.
+  auto wait_merge = [&](int) {       // the other roles while rows are merged
+    if (CS == 1) return s_timeout == 0;
+    cluster_arrive_relaxed();
+    cluster_wait();
+    cluster_sync_all();
+    bool done = true;
+    for (int q = 0; q < CS; ++q) done &= !(s_ml[q][0].y < 0.f);
+    return done;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ records
+    const uint8_t *kv = static_cast<const uint8_t *>(a.k) + (static_cast<size_t>(b) * a.Hkv + g_kv) * a.S_cap * R;
+    Ring<kRaw> raw;
+    raw.phase = 1;      // every stage is free at first
+    auto tile = [&](int i, const uint8_t *&src, uint32_t &bytes) {
+      const int key0 = tiles.key0(t0 + i), count = min(kTile, G.keys - key0);
+      src = kv + static_cast<size_t>(key0) * R;
+      bytes = static_cast<uint32_t>(count * R);
+      return range_in_bounds(key0, count, a.S_cap, a.status, b);
+    };
+    turns([&](int) {
+      if (lane != 0) return;
+      const uint8_t *src;
+      uint32_t bytes;
+      for (int i = 0; i < ntiles && ok; ++i, raw.next()) {
+        ok = mbar_sleep(raw_empty + 8 * raw.at, raw.phase);
+        if (!ok) break;
+        if (tile(i, src, bytes)) {
+          mbar_arrive_expect_tx(&bars.raw_full[raw.at], bytes);
+          bulk_copy_g2s(sb + C::kOffRaw + raw.at * C::kRawBytes, src, bytes, &bars.raw_full[raw.at]);
+        } else {
+          mbar_arrive(&bars.raw_full[raw.at]);
+        }
+        // the stages alone do not cover HBM's latency
+        if (i + kRaw < ntiles && tile(i + kRaw, src, bytes)) bulk_prefetch_l2(src, bytes);
+      }
+    }, wait_merge);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ S = Q K^T
+    constexpr uint32_t id = tc::idesc_f16_f32(kRows, kTile, 0, 0);
+    const uint64_t qd0 = tc::smem_desc_sw128(sb + C::kOffQ, 16, 1024);
+    const uint64_t kd0 = tc::smem_desc_sw128(sb + C::kOffK, 16, 1024);
+    const uint32_t k_full = smem_addr(bars.k_full);
+    Ring<2> kr;
+    uint32_t q_phase = 0;
+    turns([&](int) {
+      if (ntiles == 0) return;
+      ok = mbar_sleep(smem_addr(&bars.q_full), q_phase);
+      q_phase ^= 1;
+      for (int i = 0; i < ntiles && ok; ++i, kr.next()) {
+        ok = mbar_sleep(s_empty + 8 * kr.at, kr.phase ^ 1) && mbar_sleep(k_full + 8 * kr.at, kr.phase);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint64_t kd = kd0 + static_cast<uint64_t>(kr.at * C::kOpBytes >> 4);
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t at = ((ks >> 2) * C::kBoxBytes + (ks & 3) * 32) >> 4;
+            tc::mma_bf16(tmem + kr.at * kTile, qd0 + at, kd + at, id, ks > 0);
+          }
+          tc::commit(&bars.s_full[kr.at]);
+          tc::commit(&bars.k_empty[kr.at]);
+        }
+        __syncwarp();
+      }
+    }, wait_merge);
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ O += P V
+    constexpr uint32_t id = tc::idesc_f16_f32(kRows, D, 0, 1);
+    const uint64_t vd0 = tc::smem_desc_sw128(sb + C::kOffV, C::kBoxBytes, 1024);
+    const uint32_t v_full = smem_addr(bars.v_full);
+    Ring<2> vr;
+    turns([&](int) {
+      for (int i = 0; i < ntiles && ok; ++i, vr.next()) {
+        ok = mbar_sleep(v_full + 8 * vr.at, vr.phase) && mbar_sleep(p_full + 8 * vr.at, vr.phase);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint64_t vd = vd0 + static_cast<uint64_t>(vr.at * C::kOpBytes >> 4);
+        const uint32_t pt = tmem + C::kColP + vr.at * (kTile / 2);
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            tc::mma_bf16_ts(tmem + C::kColO, pt + kk * 8, vd + (kk * 16 * 128 >> 4), id, (i | kk) != 0);
+          tc::commit(&bars.o_done[vr.at]);
+          tc::commit(&bars.v_empty[vr.at]);
+        }
+        __syncwarp();
+      }
+    }, wait_merge);
+  } else if (warp < kSoftFirst) {
+    turns([](int) {}, wait_merge);
+  } else if (warp >= kDecodeFirst) {
+    // ------------------------------------------------------------ decode
+    const bool of_v = warp >= kDecodeFirst + kDecodeWarps;
+    const int key = (warp & 3) * 32 + lane;
+    const uint32_t full = smem_addr(of_v ? bars.v_full : bars.k_full);
+    const uint32_t empty = smem_addr(of_v ? bars.v_empty : bars.k_empty);
+    const uint8_t *rec0 = smem + C::kOffRaw + key * R;
+    const uint32_t row = sb + (of_v ? C::kOffV : C::kOffK) + key * 128 + ((key & 7) << 4);
+    const int keys_left = G.keys - key;
+    Ring<kRaw> raw;
+    Ring<2> op;
+    turns([&](int) {
+      for (int i = 0; i < ntiles; ++i, raw.next(), op.next()) {
+        ok = ok && mbar_sleep(raw_full + 8 * raw.at, raw.phase);
+        const KeyCodes<D> codes(rec0 + raw.at * C::kRawBytes, of_v, tiles.key0(t0 + i) < keys_left);
+        ok = ok && mbar_sleep(empty + 8 * op.at, op.phase ^ 1);
+        const uint32_t dst = row + op.at * C::kOpBytes;
+        codes.decode([&](int g, const uint32_t(&h)[8]) { put_swizzled<C::kBoxBytes>(dst, g, h); });
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_at(full + 8 * op.at);
+          mbar_arrive_at(raw_empty + 8 * raw.at);
+        }
+      }
+    }, wait_merge);
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int quad = warp & 3, part = (warp - kSoftFirst) >> 2;
+    const int soft = tid - 32 * kSoftFirst;            // 0 .. 511
+    const int row = quad * 32 + lane;                  // and TMEM lane
+    const int group = 2 + quad;                        // named barrier of the quarter's four warps
+    const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    Ring<2> sr;
+    float sum = 0.f, ref = -INFINITY;
+    turns([&](int row0) {
+      const int rows_here = min(kRows, rows_total - row0);
+      const bool live = row < rows_here;
+      // ---- Q as halves: 8 dims of a row per thread and round; every load of
+      //      the set-up is under way before the first is used
+      constexpr int kPieces = D / 8, kRounds = kRows * kPieces / kSoftThreads;
+      uint4 x4[kRounds], m = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int rr = 0; rr < kRounds; ++rr) {
+        const int idx = rr * kSoftThreads + soft, r = idx / kPieces, c = idx % kPieces;
+        x4[rr] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows_here && in_bounds(G.lo + (row0 + r) / a.G, a.T, a.status, b))
+          x4[rr] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
+                                                         (static_cast<size_t>(G.lo + (row0 + r) / a.G) * a.Hq +
+                                                          g_kv * a.G + (row0 + r) % a.G) *
+                                                             D) +
+                         c);
+      }
+      const int node = (row0 + row) / a.G;
+      if (a.mask) {
+        if (live && in_bounds(G.lo + node, a.T, a.status, b)) m = __ldg(a.mask + G.lo + node);
+      } else if (row0 == static_cast<int>(blockIdx.y) * kRows) {
+        for (int i = soft; i < G.n; i += kSoftThreads)
+          s_par[i] = in_bounds(G.lo + i, a.T, a.status, b) ? __ldg(a.parents + G.lo + i) : -2;
+      }
+#pragma unroll
+      for (int rr = 0; rr < kRounds; ++rr) {
+        const int idx = rr * kSoftThreads + soft, r = idx / kPieces, c = idx % kPieces;
+        const uint32_t u[4] = {x4[rr].x, x4[rr].y, x4[rr].z, x4[rr].w};
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xFFFF0000u))));
+#pragma unroll
+        for (int k = 1; k < kPieces; k *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+        const int up = row_exponent(top);
+        const float grow = power_of_two(up);
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          h[e] = pack_half2(__uint_as_float(u[e] << 16) * grow, __uint_as_float(u[e] & 0xFFFF0000u) * grow);
+        st_shared_v4(sb + C::kOffQ + (c >> 3) * C::kBoxBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4), h[0], h[1], h[2],
+                     h[3]);
+        if (c == 0) s_c[r] = a.scale_log2 * power_of_two(-up);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_at(smem_addr(&bars.q_full));
+      named_bar_sync(1, kSoftThreads);
+      // ---- what this thread's row sees
+      if (a.mask) {
+        m = clip_mask(m, G.n);
+      } else if (live) {
+        bool bad = false;
+        m = ancestor_mask([&](int i) { return s_par[i]; }, node, &bad);
+        if (bad) report(a.status, b, SPEC_ERR_BAD_PARENT);
+      }
+      const RowKeys see = row_keys(m, G.L, p.window, p.sinks);
+      const float c = s_c[row];
+      ref = live ? -INFINITY : 0.f;           // rows of no node need no reference
+      sum = 0.f;
+      float shift = kWeightLog2;               // 8 - reference (8 while there is none)
+
+      for (int i = 0; i < ntiles; ++i, sr.next()) {
+        const int key0 = tiles.key0(t0 + i), k0 = key0 + part * kPart;
+        ok = ok && mbar_sleep(s_full + 8 * sr.at, sr.phase);
+        if (quad * 32 >= rows_here) {
+          // a quarter without rows: its lanes of P stay what they are, and so
+          // do its rows of O, which nothing reads
+          ok = ok && mbar_sleep(o_done + 8 * sr.at, sr.phase ^ 1);
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive_at(s_empty + 8 * sr.at);
+            mbar_arrive_at(p_full + 8 * sr.at);
+          }
+          continue;
+        }
+        __syncwarp();
+        tc::fence_after_sync();
+        float x[kPart];
+        tc::ld32(trow + sr.at * kTile + part * kPart, x);
+        tc::wait_ld();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(s_empty + 8 * sr.at);
+        // x = score - reference + 8, in powers of two
+#pragma unroll
+        for (int j = 0; j < kPart; j += 2) fma2(x[j], x[j + 1], c, c, shift, shift);
+        if (!(k0 + kPart <= G.L && (p.window == 0 || k0 + kPart <= p.sinks || k0 >= G.L + G.n - p.window))) {
+          const uint32_t sees = sees32(see, k0, G.L, p.window);
+#pragma unroll
+          for (int j = 0; j < kPart; ++j)
+            if (!((sees >> j) & 1u)) x[j] = -INFINITY;
+        }
+        float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int j = 4; j < kPart; ++j) top[j & 3] = fmaxf(top[j & 3], x[j]);
+        const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        s_max[sr.at][part][row] = most;
+        const bool fresh = ref == -INFINITY;
+        // the barrier makes every part's maximum visible, and says whether any
+        // row of the quarter moves its reference
+        if (named_bar_or(group, 128, fresh ? most > -INFINITY : most > kWeightLog2 + kMoveLog2)) {
+          const float mx = fmaxf(fmaxf(s_max[sr.at][0][row], s_max[sr.at][1][row]),
+                                 fmaxf(s_max[sr.at][2][row], s_max[sr.at][3][row]));
+          float factor = 1.f, by = 0.f;
+          if (mx > (fresh ? -INFINITY : kWeightLog2 + kMoveLog2)) {
+            by = ceilf(mx - kWeightLog2);
+            factor = fresh ? 0.f : exp2f(-by);
+            ref = (fresh ? 0.f : ref) + by;
+            shift -= by;
+          }
+          if (i > 0) {
+            // O holds the products of this turn's earlier tiles
+            ok = ok && mbar_sleep(o_done + 8 * (sr.at ^ 1), sr.phase ^ sr.at ^ 1);
+            __syncwarp();
+            tc::fence_after_sync();
+#pragma unroll
+            for (int j = 0; j < D / 4; j += 8) {
+              const uint32_t at = trow + C::kColO + part * (D / 4) + j;
+              float o[8];
+              tc::ld8(at, o);
+              tc::wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] *= factor;
+              tmem_st(at, o);
+            }
+            tc::wait_st();
+          }
+          sum *= factor;
+#pragma unroll
+          for (int j = 0; j < kPart; ++j) x[j] -= by;
+        }
+        // ---- weights; P's buffer is free once the product two tiles back is done
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int j = 0; j < kPart; ++j) x[j] = fast_exp2(x[j]);
+#pragma unroll
+        for (int j = 0; j < kPart; j += 2) add2(s0, s1, x[j], x[j + 1]);
+        sum += s0 + s1;
+        ok = ok && mbar_sleep(o_done + 8 * sr.at, sr.phase ^ 1);
+        __syncwarp();
+        tc::fence_after_sync();
+#pragma unroll
+        for (int q = 0; q < kPart / 16; ++q) {
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[e] = pack_half2(x[16 * q + 2 * e], x[16 * q + 2 * e + 1]);
+          tc::st8(trow + C::kColP + sr.at * (kTile / 2) + part * (kPart / 2) + 8 * q, h);
+        }
+        tc::wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(p_full + 8 * sr.at);
+      }
+      // ---- the block's rows out of TMEM.  Their place in shared memory is free
+      //      once the last product is done.
+      if (ntiles > 0) ok = ok && mbar_sleep(o_done + 8 * (sr.at ^ 1), sr.phase ^ sr.at ^ 1);
+      if (CS > 1) cluster_arrive_relaxed();
+      __syncwarp();
+      tc::fence_after_sync();
+      s_max[0][part][row] = sum;
+      if (!ok) s_timeout = 1;
+      named_bar_sync(1, kSoftThreads);
+      if (s_timeout == 0) {
+        if (part == 0) {
+          s_sum[0][row] = (s_max[0][0][row] + s_max[0][1][row]) + (s_max[0][2][row] + s_max[0][3][row]);
+          s_ref[0][row] = ntiles > 0 ? ref : -INFINITY;
+        }
+        const uint32_t so = sb + (row * (D + 4) + part * (D / 4)) * 4;
+#pragma unroll
+        for (int j = 0; j < D / 4; j += 8) {
+          float o[8] = {};
+          if (ntiles > 0) {
+            tc::ld8(trow + C::kColO + part * (D / 4) + j, o);
+            tc::wait_ld();
+          }
+#pragma unroll
+          for (int e = 0; e < 8; e += 4)
+            st_shared_v4(so + (j + e) * 4, __float_as_uint(o[e]), __float_as_uint(o[e + 1]), __float_as_uint(o[e + 2]),
+                         __float_as_uint(o[e + 3]));
+        }
+      }
+    }, [&](int row0) {
+      const bool timed_out = s_timeout != 0;
+      if (timed_out && soft == 0) report(a.status, b, SPEC_ERR_TIMEOUT);
+      auto out_row = [&](int r) -> __nv_bfloat16 * {
+        const int node = (row0 + r) / a.G;
+        if (!in_bounds(G.lo + node, a.T, a.status, b)) return nullptr;
+        return static_cast<__nv_bfloat16 *>(a.o) +
+               (static_cast<size_t>(G.lo + node) * a.Hq + g_kv * a.G + (row0 + r) % a.G) * D;
+      };
+      return merge_rows<D, 1, kRows, kSoftThreads, __nv_bfloat16>(
+          soft, CS, split, min(kRows, rows_total - row0), timed_out, reinterpret_cast<float *>(smem), s_ref, s_sum,
+          s_ml, reinterpret_cast<float4 *>(smem + C::kOffRecv), [] { cluster_wait(); }, out_row);
+    });
+  }
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc::tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+}  // namespace
+
+int launch_kv4_rows(const Kv4AttnArgs &p, int max_prefix, void *stream) {
+  const int blocks = (mean_nodes(p.a) * p.a.G + kRows - 1) / kRows;
+  static std::atomic<size_t> granted[2][kMaxDevices];
+  if (p.a.D == 128)
+    return launch_kv4_tiles(tree_attn_kv4_rows_kernel<128>, p, kThreads, Kv4Rows128<128>::kSmem, blocks, max_prefix,
+                            granted[0], stream);
+  return launch_kv4_tiles(tree_attn_kv4_rows_kernel<64>, p, kThreads, Kv4Rows128<64>::kSmem, blocks, max_prefix,
+                          granted[1], stream);
+}
+
+}  // namespace spec

@@ -1,0 +1,169 @@
+// Pieces shared by the two tensor-core kernels of tree attention over the
+// 4-bit cache: register budgets, packed arithmetic, and the decoding of a
+// tile's records.
+#pragma once
+
+#include "attn_kv4.cuh"
+#include "tcgen05.cuh"
+
+namespace spec {
+
+constexpr int kTile = 128;            // keys of a tile
+
+template <int regs>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(regs));
+}
+template <int regs>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(regs));
+}
+
+// Two fp32 at once.
+__device__ __forceinline__ void fma2(float &x0, float &x1, float c0, float c1, float n0, float n1) {
+  asm("{\n\t.reg .b64 x, c, n;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 c, {%2, %3};\n\tmov.b64 n, {%4, %5};\n\t"
+      "fma.rn.f32x2 x, x, c, n;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(c0), "f"(c1), "f"(n0), "f"(n1));
+}
+__device__ __forceinline__ void add2(float &x0, float &x1, float y0, float y1) {
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(y0), "f"(y1));
+}
+
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[32]) { tc::ld32(taddr, v); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[16]) { tc::ld16(taddr, v); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[8]) { tc::ld8(taddr, v); }
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&v)[8]) {
+  uint32_t u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(v[i]);
+  tc::st8(taddr, u);
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// Reduction of n values (n = 8, 16 or 32) over the warp's lanes: lane l returns
+// value l % n reduced over all of them.  Each round exchanges half of the
+// values with the lane across and keeps the other half.
+template <int n, typename Op>
+__device__ __forceinline__ float reduce_scatter(const float (&x)[n], int lane, Op op) {
+  float v[n];
+#pragma unroll
+  for (int i = 0; i < n; ++i) v[i] = x[i];
+#pragma unroll
+  for (int h = n / 2; h >= 1; h /= 2) {
+    const bool up = lane & h;
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const float give = up ? v[i] : v[i + h];
+      const float keep = up ? v[i + h] : v[i];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, h));
+    }
+  }
+#pragma unroll
+  for (int h = n; h < 32; h *= 2) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], h));
+  return v[0];
+}
+
+// One lane's key of a tile of records: its D codes and scales, from a stage
+// of the ring.  Slots at or behind the request's last may hold anything (they
+// were not copied): zeros stand for them.
+template <int D>
+struct KeyCodes {
+  uint4 code[D / 32];
+  uint32_t scale[D / 64];
+
+  __device__ __forceinline__ KeyCodes(const uint8_t *rec, bool of_v, bool live) {
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c)
+      code[c] = *reinterpret_cast<const uint4 *>(rec + (of_v ? D / 2 : 0) + 16 * c);
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      scale[c] = *reinterpret_cast<const uint32_t *>(rec + D + (of_v ? D / 16 : 0) + 4 * c);
+      if (!live) scale[c] = 0u;
+    }
+  }
+
+  // put(g, h): the 16 dims of group g as eight half pairs
+  template <typename Put>
+  __device__ __forceinline__ void decode(Put put) const {
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      const uint32_t word[4] = {code[c].x, code[c].y, code[c].z, code[c].w};
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {       // a group: two words
+        uint32_t h[8];
+        kv4_codes_to_half2(word[2 * q], *reinterpret_cast<uint32_t(*)[4]>(h));
+        kv4_codes_to_half2(word[2 * q + 1], *reinterpret_cast<uint32_t(*)[4]>(h + 4));
+        const uint32_t s = kv4_scale_half2(__byte_perm(scale[c / 2], 0, 0x4440 + 2 * (c & 1) + q));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = mul_half2(h[e], s);
+        put(2 * c + q, h);
+      }
+    }
+  }
+};
+
+// A group's place in a 128-byte-swizzled operand of [keys][64 dims] boxes:
+// `row` is the key's row of the first box with the key's swizzle in bits 4-6.
+template <int kBoxBytes>
+__device__ __forceinline__ void put_swizzled(uint32_t row, int g, const uint32_t (&h)[8]) {
+  const uint32_t at = row + (g >> 2) * kBoxBytes, piece = (g & 3) << 5;
+  st_shared_v4(at ^ piece, h[0], h[1], h[2], h[3]);
+  st_shared_v4(at ^ (piece + 16), h[4], h[5], h[6], h[7]);
+}
+
+// Launch of a kernel that takes one CTA per SM: `blocks` row blocks (the
+// grid's y) of every (request, KV head), and as many splits of the keys (a
+// cluster) as make waves x (tiles of a CTA + its set-up, first tile and merge,
+// in tiles) least.
+template <typename Kernel>
+int launch_kv4_tiles(Kernel kernel, const Kv4AttnArgs &p, int threads, size_t smem, int blocks, int max_prefix,
+                     std::atomic<size_t> *granted, void *stream) {
+  const AttnArgs &a = p.a;
+  if (!allow_dynamic_smem(kernel, smem, granted)) return SPEC_ERR_CUDA;
+  const int nodes = mean_nodes(a);
+  long long keys = static_cast<long long>(max_prefix) + nodes;
+  if (p.window) {
+    const long long near = static_cast<long long>(p.window) + p.sinks + nodes + 2 * kTile;
+    if (near < keys) keys = near;
+  }
+  const long long tiles = (keys + kTile - 1) / kTile;
+  const long long pairs = static_cast<long long>(a.B) * a.Hkv;
+  if (pairs > 65535 || blocks > 65535) return SPEC_ERR_SHAPE;
+  const long long units = pairs * blocks, slots = sm_count();
+  int cs = 1;
+  long long best = -1;
+  for (int c = 1; c <= 8; ++c) {
+    if (c > 1 && tiles < 2 * c) break;
+    const long long waves = (units * c + slots - 1) / slots;
+    const long long cost = waves * ((tiles + c - 1) / c + 8 + (c > 1 ? 2 : 0));
+    if (best < 0 || cost < best) {
+      best = cost;
+      cs = c;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cs, static_cast<unsigned>(blocks), static_cast<unsigned>(pairs));
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  pdl_attribute(attr[1]);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+}  // namespace spec
