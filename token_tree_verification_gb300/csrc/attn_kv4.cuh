@@ -80,12 +80,6 @@ __device__ __forceinline__ void store_row4(E *dst, float4 v) {
   }
 }
 
-// L2 prefetch of a run of global memory (16-byte aligned, a multiple of 16).
-__device__ __forceinline__ void bulk_prefetch_l2(const void *src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)
-               : "memory");
-}
-
 // mbar_wait for roles that wait long and often: the thread is suspended up to
 // 10 us a try instead of polling through the issue slots of the working warps.
 // (`bar` is a shared-memory address.)
@@ -105,6 +99,18 @@ __device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
   for (uint32_t it = 0; it < kWaitLimitNs / 10000; ++it)
     if (mbar_try(bar, parity)) return true;
   return false;
+}
+// Whether the phase is over, without waiting.
+__device__ __forceinline__ bool mbar_over(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
 }
 __device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");

@@ -14,10 +14,13 @@
 // One CTA = one split of the keys x one block of 128 rows x one (request, KV
 // head).  Warp roles:
 //   warp 0      brings tiles of 128 records, one bulk copy each
-//   warp 1      allocates TMEM and issues S_i into one of two TMEM buffers
-//   warp 2      issues O += P_i V_i
+//   warp 1      allocates TMEM and issues S_i, the two halves of its keys apart
+//   warp 2      issues O += P_i V_i, the halves apart
 //   warps 4-19  softmax: the four warps of a TMEM lane quarter hold the same 32
-//               rows, each 32 of the tile's 128 keys
+//               rows, each 32 of the tile's 128 keys.  The two warps of a half of
+//               the keys share references, sums and an O of their own, merged at
+//               the end like splits of the keys: the halves never wait for each
+//               other, and one's exponentials run beside the other's maxima
 //   warps 20-23 decode keys, warps 24-27 values (one key per lane: loads of
 //               records 36 words apart and swizzled stores of rows 128 bytes
 //               apart are both free of bank conflicts)
@@ -50,14 +53,15 @@ struct Kv4Rows128 {
   static constexpr int kOffV = kOffK + 2 * kOpBytes;
   static constexpr int kOffQ = kOffV + 2 * kOpBytes;
   static constexpr int kOffRaw = kOffQ + kOpBytes;
-  // after the loop: the rows, the ones received, and their references and sums
-  static constexpr int kOffRecv = kRows * (D + 4) * 4;
+  // after the loop: the rows of both halves, the ones received, and their
+  // references and sums
+  static constexpr int kOffRecv = 2 * kRows * (D + 4) * 4;
+  static constexpr int kOffMl = kOffRecv + (kRows * D + 4 * kMaxSplits) * 4;
   static constexpr int kEnd = kOffRaw + kRaw * kRawBytes;
-  static constexpr int kOffMl = (kOffRecv + (kRows * D + 4 * kMaxSplits) * 4 + 15) / 16 * 16;
   static constexpr int kMerge = kOffMl + kMaxSplits * kRows * 8;
   static constexpr int kSmem = (kEnd > kMerge ? kEnd : kMerge) + 1024;
-  // TMEM: two S buffers, O, two P buffers (a pair of keys per column)
-  static constexpr uint32_t kColO = 2 * kTile, kColP = kColO + 128, kTmemCols = 512;
+  // TMEM: S and O of both halves, two P buffers (a pair of keys per column)
+  static constexpr uint32_t kColO = kTile, kColP = kColO + 256, kTmemCols = 512;
   static_assert(kSmem <= 227 * 1024 - 8192, "shared memory budget");
 };
 
@@ -87,14 +91,14 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
   __shared__ struct {
     uint64_t raw_full[kRaw], raw_empty[kRaw];
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t s_full[2], s_empty[2], p_full[2], o_done[2], q_full;
+    uint64_t s_full[2], s_empty[2], p_full[2][2], o_done[2][2], q_full;     // [half], [half][tile parity]
   } bars;
   __shared__ uint32_t s_tmem;
   __shared__ int s_timeout;
   __shared__ int s_par[SPEC_MAX_TREE_NODES];
   __shared__ float s_c[kRows];                // a row's score factor
   __shared__ float s_max[2][4][kRows];        // [tile parity][key part][row]
-  __shared__ float s_ref[1][kRows], s_sum[1][kRows];
+  __shared__ float s_ref[2][kRows], s_sum[2][kRows];
 
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -119,9 +123,11 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
       mbar_init(&bars.k_empty[s], 1);
       mbar_init(&bars.v_empty[s], 1);
       mbar_init(&bars.s_full[s], 1);
-      mbar_init(&bars.s_empty[s], kSoftWarps);
-      mbar_init(&bars.p_full[s], kSoftWarps);
-      mbar_init(&bars.o_done[s], 1);
+      mbar_init(&bars.s_empty[s], kSoftWarps / 2);
+      for (int q = 0; q < 2; ++q) {
+        mbar_init(&bars.p_full[s][q], kSoftWarps / 2);
+        mbar_init(&bars.o_done[s][q], 1);
+      }
     }
     mbar_init(&bars.q_full, kSoftWarps);
     fence_barrier_init();
@@ -183,56 +189,53 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
     const uint8_t *kv = static_cast<const uint8_t *>(a.k) + (static_cast<size_t>(b) * a.Hkv + g_kv) * a.S_cap * R;
     Ring<kRaw> raw;
     raw.phase = 1;      // every stage is free at first
-    auto tile = [&](int i, const uint8_t *&src, uint32_t &bytes) {
-      const int key0 = tiles.key0(t0 + i), count = min(kTile, G.keys - key0);
-      src = kv + static_cast<size_t>(key0) * R;
-      bytes = static_cast<uint32_t>(count * R);
-      return range_in_bounds(key0, count, a.S_cap, a.status, b);
-    };
     turns([&](int) {
       if (lane != 0) return;
-      const uint8_t *src;
-      uint32_t bytes;
       for (int i = 0; i < ntiles && ok; ++i, raw.next()) {
         ok = mbar_sleep(raw_empty + 8 * raw.at, raw.phase);
         if (!ok) break;
-        if (tile(i, src, bytes)) {
+        const int key0 = tiles.key0(t0 + i), count = min(kTile, G.keys - key0);
+        const uint32_t bytes = static_cast<uint32_t>(count * R);
+        if (range_in_bounds(key0, count, a.S_cap, a.status, b)) {
           mbar_arrive_expect_tx(&bars.raw_full[raw.at], bytes);
-          bulk_copy_g2s(sb + C::kOffRaw + raw.at * C::kRawBytes, src, bytes, &bars.raw_full[raw.at]);
+          bulk_copy_g2s(sb + C::kOffRaw + raw.at * C::kRawBytes, kv + static_cast<size_t>(key0) * R, bytes,
+                        &bars.raw_full[raw.at]);
         } else {
           mbar_arrive(&bars.raw_full[raw.at]);
         }
-        // the stages alone do not cover HBM's latency
-        if (i + kRaw < ntiles && tile(i + kRaw, src, bytes)) bulk_prefetch_l2(src, bytes);
       }
     }, wait_merge);
   } else if (warp == 1) {
     // ------------------------------------------------------------ S = Q K^T
-    constexpr uint32_t id = tc::idesc_f16_f32(kRows, kTile, 0, 0);
+    constexpr uint32_t id = tc::idesc_f16_f32(kRows, kTile / 2, 0, 0);
     const uint64_t qd0 = tc::smem_desc_sw128(sb + C::kOffQ, 16, 1024);
     const uint64_t kd0 = tc::smem_desc_sw128(sb + C::kOffK, 16, 1024);
     const uint32_t k_full = smem_addr(bars.k_full);
     Ring<2> kr;
+    uint32_t phase = 0;        // of the S buffers: one per half
     uint32_t q_phase = 0;
     turns([&](int) {
       if (ntiles == 0) return;
       ok = mbar_sleep(smem_addr(&bars.q_full), q_phase);
       q_phase ^= 1;
-      for (int i = 0; i < ntiles && ok; ++i, kr.next()) {
-        ok = mbar_sleep(s_empty + 8 * kr.at, kr.phase ^ 1) && mbar_sleep(k_full + 8 * kr.at, kr.phase);
-        if (!ok) break;
-        tc::fence_after_sync();
-        const uint64_t kd = kd0 + static_cast<uint64_t>(kr.at * C::kOpBytes >> 4);
-        if (tc::elect_one()) {
+      for (int i = 0; i < ntiles && ok; ++i, kr.next(), phase ^= 1) {
+        ok = mbar_sleep(k_full + 8 * kr.at, kr.phase);
+        for (int half = 0; half < 2 && ok; ++half) {
+          ok = mbar_sleep(s_empty + 8 * half, phase ^ 1);
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint64_t kd = kd0 + static_cast<uint64_t>((kr.at * C::kOpBytes + half * (kTile / 2 * 128)) >> 4);
+          if (tc::elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t at = ((ks >> 2) * C::kBoxBytes + (ks & 3) * 32) >> 4;
-            tc::mma_bf16(tmem + kr.at * kTile, qd0 + at, kd + at, id, ks > 0);
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t at = ((ks >> 2) * C::kBoxBytes + (ks & 3) * 32) >> 4;
+              tc::mma_bf16(tmem + half * (kTile / 2), qd0 + at, kd + at, id, ks > 0);
+            }
+            tc::commit(&bars.s_full[half]);
+            if (half) tc::commit(&bars.k_empty[kr.at]);
           }
-          tc::commit(&bars.s_full[kr.at]);
-          tc::commit(&bars.k_empty[kr.at]);
+          __syncwarp();
         }
-        __syncwarp();
       }
     }, wait_merge);
   } else if (warp == 2) {
@@ -243,19 +246,22 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
     Ring<2> vr;
     turns([&](int) {
       for (int i = 0; i < ntiles && ok; ++i, vr.next()) {
-        ok = mbar_sleep(v_full + 8 * vr.at, vr.phase) && mbar_sleep(p_full + 8 * vr.at, vr.phase);
-        if (!ok) break;
-        tc::fence_after_sync();
-        const uint64_t vd = vd0 + static_cast<uint64_t>(vr.at * C::kOpBytes >> 4);
-        const uint32_t pt = tmem + C::kColP + vr.at * (kTile / 2);
-        if (tc::elect_one()) {
+        ok = mbar_sleep(v_full + 8 * vr.at, vr.phase);
+        for (int half = 0; half < 2 && ok; ++half) {
+          ok = mbar_sleep(p_full + 16 * half + 8 * vr.at, vr.phase);
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint64_t vd = vd0 + static_cast<uint64_t>((vr.at * C::kOpBytes + half * (kTile / 2 * 128)) >> 4);
+          const uint32_t pt = tmem + C::kColP + vr.at * (kTile / 2) + half * (kTile / 4);
+          if (tc::elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            tc::mma_bf16_ts(tmem + C::kColO, pt + kk * 8, vd + (kk * 16 * 128 >> 4), id, (i | kk) != 0);
-          tc::commit(&bars.o_done[vr.at]);
-          tc::commit(&bars.v_empty[vr.at]);
+            for (int kk = 0; kk < kTile / 32; ++kk)
+              tc::mma_bf16_ts(tmem + C::kColO + half * 128, pt + kk * 8, vd + (kk * 16 * 128 >> 4), id, (i | kk) != 0);
+            tc::commit(&bars.o_done[half][vr.at]);
+            if (half) tc::commit(&bars.v_empty[vr.at]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
     }, wait_merge);
   } else if (warp < kSoftFirst) {
@@ -290,10 +296,16 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
     // ------------------------------------------------------------ softmax
     const int quad = warp & 3, part = (warp - kSoftFirst) >> 2;
     const int soft = tid - 32 * kSoftFirst;            // 0 .. 511
+    const int half = part >> 1, sub = part & 1;
     const int row = quad * 32 + lane;                  // and TMEM lane
-    const int group = 2 + quad;                        // named barrier of the quarter's four warps
+    const int group = 2 + 2 * quad + half;             // named barrier of the two warps
     const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    Ring<2> sr;
+    const uint32_t s_col = trow + part * kPart, o_col = trow + C::kColO + half * 128 + sub * (D / 2);
+    const uint32_t p_col = trow + C::kColP + part * (kPart / 2);
+    const uint32_t s_full_h = s_full + 8 * half, s_empty_h = s_empty + 8 * half;
+    const uint32_t p_full_h = p_full + 16 * half, o_done_h = o_done + 16 * half;
+    Ring<2> sr;              // P's buffers, and the parity of the tile
+    uint32_t phase = 0;      // of the half's S
     float sum = 0.f, ref = -INFINITY;
     turns([&](int row0) {
       const int rows_here = min(kRows, rows_total - row0);
@@ -358,28 +370,17 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
       sum = 0.f;
       float shift = kWeightLog2;               // 8 - reference (8 while there is none)
 
-      for (int i = 0; i < ntiles; ++i, sr.next()) {
+      for (int i = 0; i < ntiles; ++i, sr.next(), phase ^= 1) {
         const int key0 = tiles.key0(t0 + i), k0 = key0 + part * kPart;
-        ok = ok && mbar_sleep(s_full + 8 * sr.at, sr.phase);
-        if (quad * 32 >= rows_here) {
-          // a quarter without rows: its lanes of P stay what they are, and so
-          // do its rows of O, which nothing reads
-          ok = ok && mbar_sleep(o_done + 8 * sr.at, sr.phase ^ 1);
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive_at(s_empty + 8 * sr.at);
-            mbar_arrive_at(p_full + 8 * sr.at);
-          }
-          continue;
-        }
+        ok = ok && mbar_sleep(s_full_h, phase);
         __syncwarp();
         tc::fence_after_sync();
         float x[kPart];
-        tc::ld32(trow + sr.at * kTile + part * kPart, x);
+        tc::ld32(s_col, x);
         tc::wait_ld();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive_at(s_empty + 8 * sr.at);
+        if (lane == 0) mbar_arrive_at(s_empty_h);
         // x = score - reference + 8, in powers of two
 #pragma unroll
         for (int j = 0; j < kPart; j += 2) fma2(x[j], x[j + 1], c, c, shift, shift);
@@ -389,17 +390,13 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
           for (int j = 0; j < kPart; ++j)
             if (!((sees >> j) & 1u)) x[j] = -INFINITY;
         }
-        float top[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-        for (int j = 4; j < kPart; ++j) top[j & 3] = fmaxf(top[j & 3], x[j]);
-        const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        const float most = max_of(x);
         s_max[sr.at][part][row] = most;
         const bool fresh = ref == -INFINITY;
-        // the barrier makes every part's maximum visible, and says whether any
-        // row of the quarter moves its reference
-        if (named_bar_or(group, 128, fresh ? most > -INFINITY : most > kWeightLog2 + kMoveLog2)) {
-          const float mx = fmaxf(fmaxf(s_max[sr.at][0][row], s_max[sr.at][1][row]),
-                                 fmaxf(s_max[sr.at][2][row], s_max[sr.at][3][row]));
+        // the barrier makes both warps' maxima visible, and says whether any of
+        // their rows moves its reference
+        if (named_bar_or(group, 64, fresh ? most > -INFINITY : most > kWeightLog2 + kMoveLog2)) {
+          const float mx = fmaxf(s_max[sr.at][2 * half][row], s_max[sr.at][2 * half + 1][row]);
           float factor = 1.f, by = 0.f;
           if (mx > (fresh ? -INFINITY : kWeightLog2 + kMoveLog2)) {
             by = ceilf(mx - kWeightLog2);
@@ -409,18 +406,17 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
           }
           if (i > 0) {
             // O holds the products of this turn's earlier tiles
-            ok = ok && mbar_sleep(o_done + 8 * (sr.at ^ 1), sr.phase ^ sr.at ^ 1);
+            ok = ok && mbar_sleep(o_done_h + 8 * (sr.at ^ 1), sr.phase ^ sr.at ^ 1);
             __syncwarp();
             tc::fence_after_sync();
 #pragma unroll
-            for (int j = 0; j < D / 4; j += 8) {
-              const uint32_t at = trow + C::kColO + part * (D / 4) + j;
+            for (int j = 0; j < D / 2; j += 8) {
               float o[8];
-              tc::ld8(at, o);
+              tc::ld8(o_col + j, o);
               tc::wait_ld();
 #pragma unroll
               for (int e = 0; e < 8; ++e) o[e] *= factor;
-              tmem_st(at, o);
+              tmem_st(o_col + j, o);
             }
             tc::wait_st();
           }
@@ -429,13 +425,14 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
           for (int j = 0; j < kPart; ++j) x[j] -= by;
         }
         // ---- weights; P's buffer is free once the product two tiles back is done
+        const bool room = mbar_over(o_done_h + 8 * sr.at, sr.phase ^ 1);
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int j = 0; j < kPart; ++j) x[j] = fast_exp2(x[j]);
 #pragma unroll
         for (int j = 0; j < kPart; j += 2) add2(s0, s1, x[j], x[j + 1]);
         sum += s0 + s1;
-        ok = ok && mbar_sleep(o_done + 8 * sr.at, sr.phase ^ 1);
+        ok = ok && (room || mbar_sleep(o_done_h + 8 * sr.at, sr.phase ^ 1));
         __syncwarp();
         tc::fence_after_sync();
 #pragma unroll
@@ -443,16 +440,16 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
           uint32_t h[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) h[e] = pack_half2(x[16 * q + 2 * e], x[16 * q + 2 * e + 1]);
-          tc::st8(trow + C::kColP + sr.at * (kTile / 2) + part * (kPart / 2) + 8 * q, h);
+          tc::st8(p_col + sr.at * (kTile / 2) + 8 * q, h);
         }
         tc::wait_st();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive_at(p_full + 8 * sr.at);
+        if (lane == 0) mbar_arrive_at(p_full_h + 8 * sr.at);
       }
       // ---- the block's rows out of TMEM.  Their place in shared memory is free
       //      once the last product is done.
-      if (ntiles > 0) ok = ok && mbar_sleep(o_done + 8 * (sr.at ^ 1), sr.phase ^ sr.at ^ 1);
+      if (ntiles > 0) ok = ok && mbar_sleep(o_done_h + 8 * (sr.at ^ 1), sr.phase ^ sr.at ^ 1);
       if (CS > 1) cluster_arrive_relaxed();
       __syncwarp();
       tc::fence_after_sync();
@@ -460,16 +457,16 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
       if (!ok) s_timeout = 1;
       named_bar_sync(1, kSoftThreads);
       if (s_timeout == 0) {
-        if (part == 0) {
-          s_sum[0][row] = (s_max[0][0][row] + s_max[0][1][row]) + (s_max[0][2][row] + s_max[0][3][row]);
-          s_ref[0][row] = ntiles > 0 ? ref : -INFINITY;
+        if (sub == 0) {
+          s_sum[half][row] = s_max[0][2 * half][row] + s_max[0][2 * half + 1][row];
+          s_ref[half][row] = ntiles > 0 ? ref : -INFINITY;
         }
-        const uint32_t so = sb + (row * (D + 4) + part * (D / 4)) * 4;
+        const uint32_t so = sb + ((half * kRows + row) * (D + 4) + sub * (D / 2)) * 4;
 #pragma unroll
-        for (int j = 0; j < D / 4; j += 8) {
+        for (int j = 0; j < D / 2; j += 8) {
           float o[8] = {};
           if (ntiles > 0) {
-            tc::ld8(trow + C::kColO + part * (D / 4) + j, o);
+            tc::ld8(o_col + j, o);
             tc::wait_ld();
           }
 #pragma unroll
@@ -487,7 +484,7 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
         return static_cast<__nv_bfloat16 *>(a.o) +
                (static_cast<size_t>(G.lo + node) * a.Hq + g_kv * a.G + (row0 + r) % a.G) * D;
       };
-      return merge_rows<D, 1, kRows, kSoftThreads, __nv_bfloat16>(
+      return merge_rows<D, 2, kRows, kSoftThreads, __nv_bfloat16>(
           soft, CS, split, min(kRows, rows_total - row0), timed_out, reinterpret_cast<float *>(smem), s_ref, s_sum,
           s_ml, reinterpret_cast<float4 *>(smem + C::kOffRecv), [] { cluster_wait(); }, out_row);
     });

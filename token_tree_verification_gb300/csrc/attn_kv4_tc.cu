@@ -199,27 +199,20 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
       const uint8_t *kv = static_cast<const uint8_t *>(a.k) + (static_cast<size_t>(b) * a.Hkv + g_kv) * a.S_cap * R;
       Ring<kRaw> raw;
       raw.phase = 1;      // every stage is free at first
-      auto tile = [&](int i, const uint8_t *&src, uint32_t &bytes) {
-        const int key0 = tiles.key0(t0 + i), count = min(kTile, G.keys - key0);
-        src = kv + static_cast<size_t>(key0) * R;
-        bytes = static_cast<uint32_t>(count * R);
-        return range_in_bounds(key0, count, a.S_cap, a.status, b);
-      };
       turns([&](int) {
         if (lane != 0) return;
-        const uint8_t *src;
-        uint32_t bytes;
         for (int i = 0; i < ntiles && ok; ++i, raw.next()) {
           ok = mbar_sleep(raw_empty + 8 * raw.at, raw.phase);
           if (!ok) break;
-          if (tile(i, src, bytes)) {
+          const int key0 = tiles.key0(t0 + i), count = min(kTile, G.keys - key0);
+          const uint32_t bytes = static_cast<uint32_t>(count * R);
+          if (range_in_bounds(key0, count, a.S_cap, a.status, b)) {
             mbar_arrive_expect_tx(&bars.raw_full[raw.at], bytes);
-            bulk_copy_g2s(sb + C::kOffRaw + raw.at * C::kRawBytes, src, bytes, &bars.raw_full[raw.at]);
+            bulk_copy_g2s(sb + C::kOffRaw + raw.at * C::kRawBytes, kv + static_cast<size_t>(key0) * R, bytes,
+                          &bars.raw_full[raw.at]);
           } else {
             mbar_arrive(&bars.raw_full[raw.at]);
           }
-          // the stages alone do not cover HBM's latency
-          if (i + kRaw < ntiles && tile(i + kRaw, src, bytes)) bulk_prefetch_l2(src, bytes);
         }
       }, wait_merge);
     } else if (warp == 1) {
@@ -453,10 +446,7 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
             if (!sees) x[j] = -INFINITY;
           }
         }
-        float top[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-        for (int j = 4; j < RP; ++j) top[j & 3] = fmaxf(top[j & 3], x[j]);
-        const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        const float most = max_of(x);
         if (named_bar_or(group, 128, unset || most > kWeightLog2 + kMoveLog2)) {
           // some reference moves (or is not there yet): the rows' maxima over
           // the tile's keys, new references, and what has been summed so far
@@ -506,11 +496,12 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
           }
         }
         // ---- weights; P's buffer is free once the parity's last product is done
+        const bool room = mbar_over(o_done + 8 * par, phase ^ 1);
 #pragma unroll
         for (int j = 0; j < RP; ++j) x[j] = fast_exp2(x[j]);
 #pragma unroll
         for (int j = 0; j < RP; j += 2) add2(sum[j], sum[j + 1], x[j], x[j + 1]);
-        ok = ok && mbar_sleep(o_done + 8 * par, phase ^ 1);
+        ok = ok && (room || mbar_sleep(o_done + 8 * par, phase ^ 1));
 #pragma unroll
         for (int c = 0; c < RP / 8; ++c)
           st_shared_v4(prow ^ (c << 4), pack_half2(x[8 * c], x[8 * c + 1]), pack_half2(x[8 * c + 2], x[8 * c + 3]),

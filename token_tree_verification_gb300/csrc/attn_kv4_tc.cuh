@@ -35,6 +35,23 @@ __device__ __forceinline__ void add2(float &x0, float &x1, float y0, float y1) {
       : "f"(y0), "f"(y1));
 }
 
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
+  return m;
+}
+// The largest of n values (NaN is passed over).
+template <int n>
+__device__ __forceinline__ float max_of(const float (&x)[n]) {
+  static_assert(n % 8 == 0, "pairs of four chains");
+  float m[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+  for (int j = 4; j + 4 < n; j += 8)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = max3(m[e], x[j + e], x[j + 4 + e]);
+  return max3(max3(m[0], m[1], x[n - 1]), max3(m[2], m[3], x[n - 2]), fmaxf(x[n - 3], x[n - 4]));
+}
+
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[32]) { tc::ld32(taddr, v); }
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[16]) { tc::ld16(taddr, v); }
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[8]) { tc::ld8(taddr, v); }
