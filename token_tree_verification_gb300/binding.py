@@ -292,34 +292,39 @@ def make_kv4_cache(B, Hkv, S_cap, D, device="cuda"):
 
 
 def _kv4_cache(kv_cache):
-    """Checks a 4-bit cache; returns (device, B, Hkv, S_cap, D)."""
-    _dev(kv_cache, torch.uint8, "kv_cache")
-    if kv_cache.dim() != 4 or kv_cache.shape[3] not in _KV4_DIMS:
-        raise ValueError("kv_cache must be [B, Hkv, S_cap, kv4_record_bytes(D)]")
+    """Checks a 4-bit cache; returns (device index, B, Hkv, S_cap, D)."""
+    index = kv_cache.get_device()
+    if index < 0 or kv_cache.dtype is not torch.uint8:
+        raise TypeError(f"kv_cache must be a CUDA tensor of torch.uint8, got {kv_cache.dtype} on {kv_cache.device}")
+    if kv_cache.dim() != 4 or kv_cache.shape[3] not in _KV4_DIMS or not kv_cache.is_contiguous():
+        raise ValueError("kv_cache must be contiguous [B, Hkv, S_cap, kv4_record_bytes(D)]")
+    if index != torch._C._cuda_getDevice():
+        raise ValueError(f"kv_cache is on cuda:{index}, the current device is cuda:{torch.cuda.current_device()}")
     B, Hkv, S_cap, R = kv_cache.shape
-    dev = kv_cache.device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"kv_cache is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
-    return dev, B, Hkv, S_cap, _KV4_DIMS[R]
+    return index, B, Hkv, S_cap, _KV4_DIMS[R]
 
 
-def _i32(dev, t, shape, name):
-    if t.dtype != torch.int32 or t.device != dev:
-        raise TypeError(f"{name} must be torch.int32 on {dev}, got {t.dtype} on {t.device}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}, got {tuple(t.shape)}")
+def _i32(index, n, **tensors):
+    """Checks int32 device arrays of n elements."""
+    for name, t in tensors.items():
+        if t.dtype is not torch.int32 or t.get_device() != index:
+            raise TypeError(f"{name} must be torch.int32 on cuda:{index}, got {t.dtype} on {t.device}")
+        if t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous with {n} elements, got {tuple(t.shape)}")
 
 
-def _dense_rows(dev, t, T, Hkv, D, name):
-    if t.device != dev:
-        raise TypeError(f"{name} must be on {dev}")
-    if t.dim() != 3 or t.shape != (T, Hkv, D) or t.stride(2) != 1:
+def _dense_rows(index, t, T, Hkv, D, name):
+    """Checks dense rows; returns their strides."""
+    if t.get_device() != index:
+        raise TypeError(f"{name} must be on cuda:{index}, got {t.device}")
+    row, head, one = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if one != 1 or tuple(t.shape) != (T, Hkv, D):
         raise ValueError(f"{name} must be [{T}, {Hkv}, {D}] with its last dimension contiguous")
-    return t.stride(0), t.stride(1)
+    return row, head
 
 
-def _raw_stream(stream, dev):
-    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+def _raw_stream(stream, index):
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def kv4_write(k, v, kv_cache, start, offsets, status, stream=None):
@@ -327,18 +332,20 @@ def kv4_write(k, v, kv_cache, start, offsets, status, stream=None):
     fp32; rows and heads at any 16-byte stride); request b's rows
     offsets[b] .. offsets[b+1] go to slots start[b] and up."""
     lib = load()
-    dev, B, Hkv, S_cap, D = _kv4_cache(kv_cache)
+    index, B, Hkv, S_cap, D = _kv4_cache(kv_cache)
     dt = _DTYPES.get(k.dtype)
-    if dt is None or v.dtype != k.dtype:
+    if dt is None or v.dtype is not k.dtype:
         raise TypeError("k and v must both be bfloat16 or float32")
     T = k.shape[0]
-    ks, vs = _dense_rows(dev, k, T, Hkv, D, "k"), _dense_rows(dev, v, T, Hkv, D, "v")
-    _i32(dev, start, (B,), "start")
-    _i32(dev, offsets, (B + 1,), "offsets")
-    _i32(dev, status, (B,), "status")
-    _check(lib.spec_kv4_write(k.data_ptr(), v.data_ptr(), dt, B, T, Hkv, D, *ks, *vs, kv_cache.data_ptr(), S_cap,
-                              start.data_ptr(), offsets.data_ptr(), status.data_ptr(),
-                              _raw_stream(stream, dev)), "spec_kv4_write")
+    ks0, ks1 = _dense_rows(index, k, T, Hkv, D, "k")
+    vs0, vs1 = _dense_rows(index, v, T, Hkv, D, "v")
+    _i32(index, B, start=start, status=status)
+    _i32(index, B + 1, offsets=offsets)
+    rc = lib.spec_kv4_write(k.data_ptr(), v.data_ptr(), dt, B, T, Hkv, D, ks0, ks1, vs0, vs1,
+                            kv_cache.data_ptr(), S_cap, start.data_ptr(), offsets.data_ptr(),
+                            status.data_ptr(), _raw_stream(stream, index))
+    if rc:
+        raise SpecError(rc, "spec_kv4_write")
 
 
 def kv4_read(kv_cache, start, offsets, status, rows=None, dtype=torch.bfloat16, out=None, stream=None):
@@ -347,25 +354,30 @@ def kv4_read(kv_cache, start, offsets, status, rows=None, dtype=torch.bfloat16, 
     ``out`` = (k, v), whose rows behind the last request stay as they are.
     Returns (k, v) [rows, Hkv, D]."""
     lib = load()
-    dev, B, Hkv, S_cap, D = _kv4_cache(kv_cache)
+    index, B, Hkv, S_cap, D = _kv4_cache(kv_cache)
     if out is None:
         if rows is None:
             raise ValueError("kv4_read needs the number of rows, or out")
-        both = torch.empty((2, rows, Hkv, D), dtype=dtype, device=dev)
-        out = (both[0], both[1])
-    k, v = out
+        k = torch.empty((rows, Hkv, D), dtype=dtype, device=kv_cache.device)
+        v = torch.empty_like(k)
+        T, ks0, ks1 = rows, Hkv * D, D
+        vs0, vs1 = ks0, ks1
+    else:
+        k, v = out
+        T = k.shape[0]
+        ks0, ks1 = _dense_rows(index, k, T, Hkv, D, "k")
+        vs0, vs1 = _dense_rows(index, v, T, Hkv, D, "v")
     dt = _DTYPES.get(k.dtype)
-    if dt is None or v.dtype != k.dtype:
+    if dt is None or v.dtype is not k.dtype:
         raise TypeError("rows are read as bfloat16 or float32")
-    T = k.shape[0]
-    ks, vs = _dense_rows(dev, k, T, Hkv, D, "k"), _dense_rows(dev, v, T, Hkv, D, "v")
-    _i32(dev, start, (B,), "start")
-    _i32(dev, offsets, (B + 1,), "offsets")
-    _i32(dev, status, (B,), "status")
-    _check(lib.spec_kv4_read(k.data_ptr(), v.data_ptr(), dt, B, T, Hkv, D, *ks, *vs, kv_cache.data_ptr(), S_cap,
-                             start.data_ptr(), offsets.data_ptr(), status.data_ptr(),
-                             _raw_stream(stream, dev)), "spec_kv4_read")
-    return out
+    _i32(index, B, start=start, status=status)
+    _i32(index, B + 1, offsets=offsets)
+    rc = lib.spec_kv4_read(k.data_ptr(), v.data_ptr(), dt, B, T, Hkv, D, ks0, ks1, vs0, vs1,
+                           kv_cache.data_ptr(), S_cap, start.data_ptr(), offsets.data_ptr(),
+                           status.data_ptr(), _raw_stream(stream, index))
+    if rc:
+        raise SpecError(rc, "spec_kv4_read")
+    return k, v
 
 
 def kv4_compact(kv_cache, prefix_lens, offsets, path_nodes, accept_len, status,
@@ -373,20 +385,20 @@ def kv4_compact(kv_cache, prefix_lens, offsets, path_nodes, accept_len, status,
     """kv_compact on a 4-bit cache (in place; records move as they are).
     Returns the new prefix lengths (device int32 [B])."""
     lib = load()
-    dev, B, Hkv, S_cap, D = _kv4_cache(kv_cache)
-    _i32(dev, prefix_lens, (B,), "prefix_lens")
-    _i32(dev, offsets, (B + 1,), "offsets")
-    _i32(dev, path_nodes, (B, path_nodes.shape[-1]), "path_nodes")
-    _i32(dev, accept_len, (B,), "accept_len")
-    _i32(dev, status, (B,), "status")
+    index, B, Hkv, S_cap, D = _kv4_cache(kv_cache)
+    W = path_nodes.shape[-1]
     if new_prefix_lens is None:
         new_prefix_lens = torch.empty_like(prefix_lens)
-    else:
-        _i32(dev, new_prefix_lens, (B,), "new_prefix_lens")
-    _check(lib.spec_kv4_compact(kv_cache.data_ptr(), B, Hkv, D, S_cap, prefix_lens.data_ptr(), offsets.data_ptr(),
-                                path_nodes.data_ptr(), accept_len.data_ptr(), path_nodes.shape[-1],
-                                new_prefix_lens.data_ptr(), status.data_ptr(),
-                                _raw_stream(stream, dev)), "spec_kv4_compact")
+    _i32(index, B, prefix_lens=prefix_lens, accept_len=accept_len, status=status,
+         new_prefix_lens=new_prefix_lens)
+    _i32(index, B + 1, offsets=offsets)
+    _i32(index, B * W, path_nodes=path_nodes)
+    rc = lib.spec_kv4_compact(kv_cache.data_ptr(), B, Hkv, D, S_cap, prefix_lens.data_ptr(),
+                              offsets.data_ptr(), path_nodes.data_ptr(), accept_len.data_ptr(), W,
+                              new_prefix_lens.data_ptr(), status.data_ptr(),
+                              _raw_stream(stream, index))
+    if rc:
+        raise SpecError(rc, "spec_kv4_compact")
     return new_prefix_lens
 
 
@@ -398,32 +410,34 @@ def tree_attn_kv4(q, kv_cache, prefix_lens, offsets, mask, max_prefix, status, o
     it, and the first ``sinks`` positions; with ``mask=None`` the ancestor sets
     come from ``parents``."""
     lib = load()
-    dev, B, Hkv, S_cap, D = _kv4_cache(kv_cache)
+    index, B, Hkv, S_cap, D = _kv4_cache(kv_cache)
     dt = _DTYPES.get(q.dtype)
     if dt is None:
         raise TypeError("q must be bfloat16 or float32")
-    if q.device != dev or q.dim() != 3 or q.shape[2] != D or not q.is_contiguous():
-        raise ValueError(f"q must be contiguous [T, Hq, {D}] on {dev}")
-    T, Hq = q.shape[0], q.shape[1]
-    _i32(dev, prefix_lens, (B,), "prefix_lens")
-    _i32(dev, offsets, (B + 1,), "offsets")
-    _i32(dev, status, (B,), "status")
+    if q.get_device() != index or q.dim() != 3 or q.shape[2] != D or not q.is_contiguous():
+        raise ValueError(f"q must be contiguous [T, Hq, {D}] on cuda:{index}")
+    T, Hq, _ = q.shape
+    _i32(index, B, prefix_lens=prefix_lens, status=status)
+    _i32(index, B + 1, offsets=offsets)
+    mask_ptr = parents_ptr = None
     if mask is not None:
-        _i32(dev, mask, (T, 4), "mask")
+        _i32(index, 4 * T, mask=mask)
+        mask_ptr = mask.data_ptr()
     elif parents is not None:
-        _i32(dev, parents, (T,), "parents")
+        _i32(index, T, parents=parents)
+        parents_ptr = parents.data_ptr()
     else:
         raise ValueError("tree_attn_kv4 needs a mask or the parent array")
     if o is None:
         o = torch.empty_like(q)
-    elif o.dtype != q.dtype or o.device != dev or o.shape != q.shape or not o.is_contiguous():
+    elif o.dtype is not q.dtype or o.get_device() != index or o.shape != q.shape or not o.is_contiguous():
         raise ValueError("o must be like q")
-    _check(lib.spec_tree_attn_kv4(q.data_ptr(), kv_cache.data_ptr(), o.data_ptr(), dt, B, T, Hq, Hkv, D, S_cap,
-                                  int(max_prefix), prefix_lens.data_ptr(), offsets.data_ptr(),
-                                  None if mask is None else mask.data_ptr(),
-                                  None if mask is not None else parents.data_ptr(), float(softmax_scale),
-                                  int(window), int(sinks), status.data_ptr(),
-                                  _raw_stream(stream, dev)), "spec_tree_attn_kv4")
+    rc = lib.spec_tree_attn_kv4(q.data_ptr(), kv_cache.data_ptr(), o.data_ptr(), dt, B, T, Hq, Hkv, D,
+                                S_cap, max_prefix, prefix_lens.data_ptr(), offsets.data_ptr(), mask_ptr,
+                                parents_ptr, softmax_scale, window, sinks, status.data_ptr(),
+                                _raw_stream(stream, index))
+    if rc:
+        raise SpecError(rc, "spec_tree_attn_kv4")
     return o
 
 

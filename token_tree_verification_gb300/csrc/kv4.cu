@@ -20,131 +20,244 @@ struct Kv4Args {
 // even, in exact arithmetic.  Every boundary between two scales is 6 x (a
 // number of at most 5 significant bits), which has at most 7, so amax may
 // first be cut to 12 significant bits with everything below folded into the
-// last one (that moves it across no boundary and onto none).  What is then no
-// tie stays 2^-12 away from one, far more than the product with 1/6 can err,
-// and rounding that product to 16 bits makes a true tie exact again.
+// last one (that moves it across no boundary and onto none; a bf16 has 8 to
+// begin with).  What is then no tie stays 2^-12 away from one, far more than
+// the product with 1/6 can err, and rounding that product to 16 bits makes a
+// true tie exact again.
+template <typename E>
 __device__ __forceinline__ uint32_t round_sticky(uint32_t bits) {
+  if constexpr (sizeof(E) == 2) return bits;
   return (bits & 0xFFFFF000u) | ((bits & 0xFFFu) ? 0x1000u : 0u);
 }
-__device__ __forceinline__ uint32_t snap16(uint32_t bits) { return (bits + 0x80u) & 0xFFFFFF00u; }
 
+template <typename E>
 __device__ __forceinline__ uint32_t scale_of(uint32_t amax_bits) {
-  const float x = __uint_as_float(round_sticky(amax_bits));
-  const uint32_t q = snap16(__float_as_uint(x * (1.0f / 6.0f)));
+  const float x = __uint_as_float(round_sticky<E>(amax_bits)) * (1.0f / 6.0f);
+  const uint32_t q = (__float_as_uint(x) + 0x80u) & 0xFFFFFF00u;
   const uint32_t normal = ((q + 0x7FFFFu + ((q >> 20) & 1u)) >> 20) - ((127u - 15u) << 3);
   const uint32_t small = static_cast<uint32_t>(__float2int_rn(__uint_as_float(q) * 131072.f));
   return min(q < 0x38800000u ? small : normal, kKv4MaxScale);   // 2^-14 parts the two
 }
 
+// The codes of two elements, x / scale rounded to the nearest with ties to
+// even, exactly.  The boundaries are multiples of 1/4; an element (12
+// significant bits) that is on none stays 2^-14 away from it, so its quotient
+// may be rounded to multiples of 2^-14 first: adding and taking away 768 does
+// that, and removes the 2^-21 by which the product with 1 / scale can err.  (A
+// zero keeps the element's sign.)
+__device__ __forceinline__ uint32_t codes_of(float x0, float x1, float inv) {
+  constexpr float kGrid = 768.f;
+  const float y0 = __fadd_rn(__fmaf_rn(x0, inv, kGrid), -kGrid), y1 = __fadd_rn(__fmaf_rn(x1, inv, kGrid), -kGrid);
+  uint32_t c;
+  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\tcvt.u32.u8 %0, t;\n\t}"
+      : "=r"(c)
+      : "f"(copysignf(y0, x0)), "f"(copysignf(y1, x1)));
+  return c;
+}
+
+// Eight elements of a row, 16-byte loads and stores.
+template <typename E>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = __ldg(reinterpret_cast<const uint4 *>(p)); }
+  __device__ __forceinline__ void clear() { v = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void floats(float (&x)[8]) const {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(u[i] << 16);
+      x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+  }
+};
+template <>
+struct Eight<float> {
+  uint4 v, w;
+  __device__ __forceinline__ void load(const float *p) {
+    v = __ldg(reinterpret_cast<const uint4 *>(p));
+    w = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+  }
+  __device__ __forceinline__ void clear() { v = w = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void floats(float (&x)[8]) const {
+    const uint32_t u[8] = {v.x, v.y, v.z, v.w, w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(u[i]);
+  }
+};
+
+// Where flattened row t * H + h lies, walked along consecutive rows: the
+// request is looked up again only when t leaves the present one's rows.
+struct RowWalk {
+  const Kv4Args &a;
+  uint32_t h;
+  int t, b;
+  Kv4Rows r;
+  __device__ __forceinline__ RowWalk(const Kv4Args &args, uint32_t row) : a(args) {
+    t = static_cast<int>(row / static_cast<uint32_t>(a.H));
+    h = row - static_cast<uint32_t>(t) * a.H;
+    look_up();
+  }
+  __device__ __forceinline__ void look_up() {
+    b = t < a.T ? find_request(a.offsets, a.B, t) : -1;
+    r = {0, 0, 0, 1};
+    if (b >= 0) r = kv4_rows(a.offsets, a.start, b, a.T, a.S_cap);
+  }
+  __device__ __forceinline__ bool valid() const {
+    return b >= 0 && !r.err && t < a.T && t >= r.lo && t < r.lo + r.n &&
+           in_bounds(r.start + (t - r.lo), a.S_cap, a.status, b);
+  }
+  template <int R>
+  __device__ __forceinline__ uint8_t *record() const {
+    return a.kv + ((static_cast<size_t>(b) * a.H + h) * a.S_cap + r.start + (t - r.lo)) * R;
+  }
+  __device__ __forceinline__ void advance(uint32_t rows) {
+    h += rows;
+    if (h < static_cast<uint32_t>(a.H)) return;
+    do {
+      h -= a.H;
+      ++t;
+    } while (h >= static_cast<uint32_t>(a.H));
+    if (b < 0 || t >= r.lo + r.n) look_up();
+  }
+};
+
+__device__ __forceinline__ void report_bad_rows(const Kv4Args &a) {
+  if (blockIdx.x != 0) return;
+  for (int b = threadIdx.x; b < a.B; b += kRowThreads) {
+    const Kv4Rows r = kv4_rows(a.offsets, a.start, b, a.T, a.S_cap);
+    if (r.err) report(a.status, b, r.err);
+  }
+}
+
 // One row (key and value of one request, head and slot) is 2 x D / 8 lanes of
-// eight dimensions each: a whole warp for D = 128, half of one for D = 64.
-template <int D, typename E>
+// eight dimensions each: a whole warp for D = 128, half of one for D = 64.  A
+// warp takes U consecutive rounds of rows with their loads under way at once;
+// both kernels are bound by HBM on long runs and by latency on short ones.
+template <int D, int U, typename E>
 __global__ void __launch_bounds__(kRowThreads)
 kv4_write_kernel(const Kv4Args a) {
   constexpr int kLanes = D / 4;                 // lanes of a row
+  constexpr int kSide = 32 / kLanes;            // rows of a warp side by side
   constexpr int R = kv4_record_bytes(D);
   const int tid = threadIdx.x, lane = tid & 31;
   const int sub = lane % kLanes;                // place within the row
   const bool is_v = sub >= kLanes / 2;
-  const int chunk = sub % (kLanes / 2);
+  const E *base = static_cast<const E *>(is_v ? a.v : a.k) + sub % (kLanes / 2) * 8;
+  const long long st = is_v ? a.v_st : a.k_st, sh = is_v ? a.v_sh : a.k_sh;
   pdl_trigger();
   pdl_wait();
-  if (blockIdx.x == 0)
-    for (int b = tid; b < a.B; b += kRowThreads) {
-      const Kv4Rows r = kv4_rows(a.offsets, a.start, b, a.T, a.S_cap);
-      if (r.err) report(a.status, b, r.err);
-    }
-  const long long rows = static_cast<long long>(a.T) * a.H;
-  const long long step = static_cast<long long>(gridDim.x) * (kRowThreads / kLanes);
-  for (long long w = (static_cast<long long>(blockIdx.x) * kRowThreads + tid - lane) / kLanes; w < rows; w += step) {
-    const long long row = w + lane / kLanes;
-    const int t = static_cast<int>(min(row, rows - 1) / a.H), h = static_cast<int>(min(row, rows - 1) % a.H);
-    const int b = find_request(a.offsets, a.B, t);
-    Kv4Rows r = {0, 0, 0, 1};
-    if (b >= 0) r = kv4_rows(a.offsets, a.start, b, a.T, a.S_cap);
-    // lanes without a row still take part in the shuffles below
-    const bool ok = row < rows && b >= 0 && !r.err && t >= r.lo && t < r.lo + r.n;
-    float x[8];
+  const uint32_t warp = (blockIdx.x * kRowThreads + tid) / 32;
+  RowWalk w(a, warp * (U * kSide) + lane / kLanes);
+  Eight<E> in[U];
+  uint8_t *rec[U];
+  int req[U];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    if (ok) {
-      const E *src = static_cast<const E *>(is_v ? a.v : a.k) +
-                     t * (is_v ? a.v_st : a.k_st) + h * (is_v ? a.v_sh : a.k_sh) + chunk * 8;
-      for (int i = 0; i < 8; ++i) x[i] = static_cast<float>(src[i]);
+  for (int u = 0; u < U; ++u) {
+    rec[u] = nullptr;
+    req[u] = w.b;
+    if (w.valid()) {
+      in[u].load(base + w.t * st + w.h * sh);
+      rec[u] = w.record<R>();
+    } else {
+      in[u].clear();
     }
+    if (u + 1 < U) w.advance(kSide);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float x[8];
+    in[u].floats(x);
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    const bool finite = top < 0x7F800000u;
-    if (!finite) report(a.status, b, SPEC_ERR_NONFINITE);
-    uint32_t byte = finite ? scale_of(top) : 0u;
-    const float inv = byte ? 1.0f / __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 7))) : 0.f;
+    if (top >= 0x7F800000u) {                   // NaN or infinity: the group becomes zeros
+      report(a.status, req[u], SPEC_ERR_NONFINITE);
+      top = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    }
+    uint32_t byte = scale_of<E>(top);
+    float inv = 0.f;
+    if (byte) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(__half2float(__ushort_as_half(byte << 7))));
     uint32_t codes = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float y[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float z = finite ? __uint_as_float(round_sticky(__float_as_uint(x[2 * i + e]))) * inv : 0.f;
-        y[e] = __uint_as_float(snap16(__float_as_uint(z)));
-      }
-      uint32_t c;
-      asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\tcvt.u32.u8 %0, t;\n\t}"
-          : "=r"(c)
-          : "f"(y[0]), "f"(y[1]));
-      codes |= c << (8 * i);
+      for (int e = 0; e < 2; ++e) y[e] = __uint_as_float(round_sticky<E>(__float_as_uint(x[2 * i + e])));
+      codes |= codes_of(y[0], y[1], inv) << (8 * i);
     }
     // scale bytes of four neighbouring groups to one word
     byte |= __shfl_down_sync(0xffffffffu, byte, 2) << 8;
     byte |= __shfl_down_sync(0xffffffffu, byte, 4) << 16;
-    if (ok && in_bounds(r.start + (t - r.lo), a.S_cap, a.status, b)) {
-      uint32_t *rec = reinterpret_cast<uint32_t *>(
-          a.kv + ((static_cast<size_t>(b) * a.H + h) * a.S_cap + r.start + (t - r.lo)) * R);
-      rec[sub] = codes;
-      if (sub % 8 == 0) rec[D / 4 + sub / 8] = byte;
-      if (D == 64 && sub % 8 == 4) rec[D / 4 + 2 + sub / 8] = 0u;
+    if (rec[u]) {
+      uint32_t *word = reinterpret_cast<uint32_t *>(rec[u]);
+      word[sub] = codes;
+      if (sub % 8 == 0) word[D / 4 + sub / 8] = byte;
+      if (D == 64 && sub % 8 == 4) word[D / 4 + 2 + sub / 8] = 0u;
     }
   }
+  report_bad_rows(a);
 }
 
-template <int D, typename E>
+template <int D, int U, typename E>
 __global__ void __launch_bounds__(kRowThreads)
 kv4_read_kernel(const Kv4Args a) {
   constexpr int kLanes = D / 4;
+  constexpr int kSide = 32 / kLanes;
   constexpr int R = kv4_record_bytes(D);
   const int tid = threadIdx.x, lane = tid & 31;
   const int sub = lane % kLanes;
   const bool is_v = sub >= kLanes / 2;
-  const int chunk = sub % (kLanes / 2);
+  E *base = static_cast<E *>(is_v ? a.v : a.k) + sub % (kLanes / 2) * 8;
+  const long long st = is_v ? a.v_st : a.k_st, sh = is_v ? a.v_sh : a.k_sh;
   pdl_trigger();
   pdl_wait();
-  if (blockIdx.x == 0)
-    for (int b = tid; b < a.B; b += kRowThreads) {
-      const Kv4Rows r = kv4_rows(a.offsets, a.start, b, a.T, a.S_cap);
-      if (r.err) report(a.status, b, r.err);
+  const uint32_t warp = (blockIdx.x * kRowThreads + tid) / 32;
+  RowWalk w(a, warp * (U * kSide) + lane / kLanes);
+  uint32_t code[U], scale[U];
+  E *dst[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    dst[u] = nullptr;
+    code[u] = scale[u] = 0u;
+    if (w.valid()) {
+      const uint8_t *rec = w.record<R>();
+      code[u] = __ldg(reinterpret_cast<const uint32_t *>(rec) + sub);
+      scale[u] = __ldg(rec + D + sub / 2);
+      dst[u] = base + w.t * st + w.h * sh;
     }
-  const long long rows = static_cast<long long>(a.T) * a.H;
-  const long long step = static_cast<long long>(gridDim.x) * (kRowThreads / kLanes);
-  for (long long row = (static_cast<long long>(blockIdx.x) * kRowThreads + tid) / kLanes; row < rows; row += step) {
-    const int t = static_cast<int>(row / a.H), h = static_cast<int>(row % a.H);
-    const int b = find_request(a.offsets, a.B, t);
-    if (b < 0) continue;
-    const Kv4Rows r = kv4_rows(a.offsets, a.start, b, a.T, a.S_cap);
-    if (r.err || t < r.lo || t >= r.lo + r.n || !in_bounds(r.start + (t - r.lo), a.S_cap, a.status, b)) continue;
-    const uint8_t *rec = a.kv + ((static_cast<size_t>(b) * a.H + h) * a.S_cap + r.start + (t - r.lo)) * R;
+    if (u + 1 < U) w.advance(kSide);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (!dst[u]) continue;
     uint32_t p[4];
-    kv4_codes_to_half2(__ldg(reinterpret_cast<const uint32_t *>(rec) + sub), p);
-    const uint32_t s = kv4_scale_half2(__ldg(rec + D + sub / 2));
-    E *dst = static_cast<E *>(is_v ? a.v : a.k) + t * (is_v ? a.v_st : a.k_st) +
-             h * (is_v ? a.v_sh : a.k_sh) + chunk * 8;
+    kv4_codes_to_half2(code[u], p);
+    const uint32_t s = kv4_scale_half2(scale[u]);
+    float2 f[4];
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t y = mul_half2(p[i], s);
-      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&y));
-      dst[2 * i] = static_cast<E>(f.x);
-      dst[2 * i + 1] = static_cast<E>(f.y);
+      f[i] = __half22float2(*reinterpret_cast<const __half2 *>(&y));
+    }
+    if constexpr (sizeof(E) == 4) {
+      reinterpret_cast<float4 *>(dst[u])[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+      reinterpret_cast<float4 *>(dst[u])[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+    } else {
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(f[i].x, f[i].y);
+        o[i] = *reinterpret_cast<const uint32_t *>(&v);
+      }
+      *reinterpret_cast<uint4 *>(dst[u]) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
+  report_bad_rows(a);
 }
 
 // Checks that both calls share.  Dense rows: 16-byte vectors, so every row
@@ -164,13 +277,9 @@ int check_rows(const void *k, const void *v, int dtype, int B, int T, int Hkv, i
 }
 
 template <typename Kernel>
-int launch_rows(Kernel kernel, const Kv4Args &args, int D, void *stream) {
-  const long long lanes = static_cast<long long>(args.T) * args.H * (D / 4);
-  if (lanes == 0) return SPEC_OK;
+int launch_rows(Kernel kernel, const Kv4Args &args, long long warps, void *stream) {
   cudaLaunchConfig_t cfg = {};
-  const long long blocks = (lanes + kRowThreads - 1) / kRowThreads;
-  const long long most = static_cast<long long>(sm_count()) * 8;
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks < most ? blocks : most), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>((warps * 32 + kRowThreads - 1) / kRowThreads), 1, 1);
   cfg.blockDim = dim3(kRowThreads, 1, 1);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
@@ -178,6 +287,30 @@ int launch_rows(Kernel kernel, const Kv4Args &args, int D, void *stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+// Four rounds of rows per warp where that still leaves every SM 32 warps, else
+// one, so that a tree's few rows spread over the GPU.
+template <bool kWrite, int D, typename E>
+int rows_by_size(const Kv4Args &args, void *stream) {
+  const long long rows = static_cast<long long>(args.T) * args.H, side = 32 / (D / 4);
+  if (rows == 0) return SPEC_OK;
+  if (rows > 0x7FFFFFFFll) return SPEC_ERR_SHAPE;      // rows are counted in 32 bits
+  const long long one = (rows + side - 1) / side, four = (one + 3) / 4;
+  if (four < 32ll * sm_count()) {
+    if constexpr (kWrite) return launch_rows(kv4_write_kernel<D, 1, E>, args, one, stream);
+    else return launch_rows(kv4_read_kernel<D, 1, E>, args, one, stream);
+  }
+  if constexpr (kWrite) return launch_rows(kv4_write_kernel<D, 4, E>, args, four, stream);
+  else return launch_rows(kv4_read_kernel<D, 4, E>, args, four, stream);
+}
+
+template <bool kWrite>
+int launch_by_type(const Kv4Args &args, int dtype, int D, void *stream) {
+  if (dtype == SPEC_BF16)
+    return D == 128 ? rows_by_size<kWrite, 128, __nv_bfloat16>(args, stream)
+                    : rows_by_size<kWrite, 64, __nv_bfloat16>(args, stream);
+  return D == 128 ? rows_by_size<kWrite, 128, float>(args, stream) : rows_by_size<kWrite, 64, float>(args, stream);
 }
 
 }  // namespace
@@ -198,11 +331,7 @@ extern "C" int spec_kv4_write(const void *k, const void *v, int dtype, int B, in
   if (rc != SPEC_OK) return rc;
   const Kv4Args args = {const_cast<void *>(k), const_cast<void *>(v), k_row_stride, k_head_stride, v_row_stride,
                         v_head_stride, static_cast<uint8_t *>(kv_cache), start, offsets, status, B, T, Hkv, S_cap};
-  if (dtype == SPEC_BF16)
-    return D == 128 ? launch_rows(kv4_write_kernel<128, __nv_bfloat16>, args, D, stream)
-                    : launch_rows(kv4_write_kernel<64, __nv_bfloat16>, args, D, stream);
-  return D == 128 ? launch_rows(kv4_write_kernel<128, float>, args, D, stream)
-                  : launch_rows(kv4_write_kernel<64, float>, args, D, stream);
+  return launch_by_type<true>(args, dtype, D, stream);
 }
 
 extern "C" int spec_kv4_read(void *k, void *v, int dtype, int B, int T, int Hkv, int D, int64_t k_row_stride,
@@ -217,9 +346,5 @@ extern "C" int spec_kv4_read(void *k, void *v, int dtype, int B, int T, int Hkv,
     return SPEC_ERR_SHAPE;
   const Kv4Args args = {k, v, k_row_stride, k_head_stride, v_row_stride, v_head_stride,
                         static_cast<uint8_t *>(const_cast<void *>(kv_cache)), start, offsets, status, B, T, Hkv, S_cap};
-  if (dtype == SPEC_BF16)
-    return D == 128 ? launch_rows(kv4_read_kernel<128, __nv_bfloat16>, args, D, stream)
-                    : launch_rows(kv4_read_kernel<64, __nv_bfloat16>, args, D, stream);
-  return D == 128 ? launch_rows(kv4_read_kernel<128, float>, args, D, stream)
-                  : launch_rows(kv4_read_kernel<64, float>, args, D, stream);
+  return launch_by_type<false>(args, dtype, D, stream);
 }

@@ -71,17 +71,4 @@ __device__ __forceinline__ Kv4Rows kv4_rows(const int32_t *offsets, const int32_
   return r;
 }
 
-// The request that owns row t (the same for the whole warp): the number of
-// requests that end at or before t, counted 32 at a time.  B when none does.
-__device__ __forceinline__ int find_request_warp(const int32_t *offsets, int B, int t, int lane) {
-  int count = 0;
-  for (int base = 0; base < B; base += 32) {
-    const bool ended = base + lane < B && __ldg(offsets + base + lane + 1) <= t;
-    const int here = __popc(__ballot_sync(0xffffffffu, ended));
-    count += here;
-    if (here < 32) break;
-  }
-  return count;
-}
-
 }  // namespace spec
