@@ -186,53 +186,62 @@ __device__ __forceinline__ bool merge_rows(int tid, int CS, int split, int rows_
   constexpr int kStride = D + 4;
   const int pieces = rows_here * (D / 4);
   const int share = (pieces + CS - 1) / CS;
-  if (CS > 1) {
-    ready();
-    for (int i = tid; i < CS * rows_here; i += THREADS) {
-      const int r = i / CS, q = i % CS;
-      float M = s_m[0][r], L = 0.f;
+  // the factors of a row's W parts, and its merged reference and sum
+  auto part_factors = [&](int r, float (&f)[W], float &M, float &L) {
+    M = s_m[0][r];
 #pragma unroll
-      for (int w = 1; w < W; ++w) M = fmaxf(M, s_m[w][r]);
-      const float base = M == -INFINITY ? 0.f : M;
+    for (int w = 1; w < W; ++w) M = fmaxf(M, s_m[w][r]);
+    const float base = M == -INFINITY ? 0.f : M;
+    L = 0.f;
 #pragma unroll
-      for (int w = 0; w < W; ++w) L = fmaf(exp2f(s_m[w][r] - base), s_l[w][r], L);
-      const uint32_t dst = peer_addr(&s_ml[split][r], q);
-      st_peer_f32(dst, timed_out ? INFINITY : M);
-      st_peer_f32(dst + 4, timed_out ? -1.f : L);      // no sum of weights is negative
+    for (int w = 0; w < W; ++w) {
+      f[w] = fast_exp2(s_m[w][r] - base);
+      L = fmaf(f[w], s_l[w][r], L);
     }
-  }
+  };
+  auto add_piece = [](float4 &acc, float f, float4 v) {
+    acc.x = fmaf(f, v.x, acc.x);
+    acc.y = fmaf(f, v.y, acc.y);
+    acc.z = fmaf(f, v.z, acc.z);
+    acc.w = fmaf(f, v.w, acc.w);
+  };
   auto finish = [&](int r, int c, float4 acc, float L) {
     const float inv = L == 0.f ? 0.f : 1.f / L;
     E *dst = out_row(r);
     if (dst) store_row4(dst + c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
   };
-  for (int idx = tid; idx < pieces && !timed_out; idx += THREADS) {
-    const int r = idx / (D / 4), c = idx % (D / 4) * 4;
-    float4 acc;
-    float L;
-    if constexpr (W == 1) {
-      acc = *reinterpret_cast<const float4 *>(so + r * kStride + c);
-      L = s_l[0][r];
-    } else {
-      float M = s_m[0][r];
+  float per_share = 0.f;
+  if (CS > 1) {
+    per_share = 1.f / static_cast<float>(share);
+    ready();
+    for (int i = tid; i < rows_here * kMaxSplits; i += THREADS) {
+      const int r = i / kMaxSplits, q = i % kMaxSplits;
+      if (q >= CS) continue;
+      float f[W], M, L;
+      part_factors(r, f, M, L);
+      const uint32_t dst = peer_addr(&s_ml[split][r], q);
+      st_peer_f32(dst, timed_out ? INFINITY : M);
+      st_peer_f32(dst + 4, timed_out ? -1.f : L);      // no sum of weights is negative
+    }
+  }
+  if (!timed_out) {
+#pragma unroll 2
+    for (int idx = tid; idx < pieces; idx += THREADS) {
+      const int r = idx / (D / 4), c = idx % (D / 4) * 4;
+      float f[W], M, L;
+      part_factors(r, f, M, L);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 1; w < W; ++w) M = fmaxf(M, s_m[w][r]);
-      const float base = M == -INFINITY ? 0.f : M;
-      acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      L = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float f = exp2f(s_m[w][r] - base);
-        const float4 v = *reinterpret_cast<const float4 *>(so + (w * ROWS + r) * kStride + c);
-        L = fmaf(f, s_l[w][r], L);
-        acc.x = fmaf(f, v.x, acc.x);
-        acc.y = fmaf(f, v.y, acc.y);
-        acc.z = fmaf(f, v.z, acc.z);
-        acc.w = fmaf(f, v.w, acc.w);
+      for (int w = 0; w < W; ++w)
+        add_piece(acc, f[w], *reinterpret_cast<const float4 *>(so + (w * ROWS + r) * kStride + c));
+      if (CS > 1) {
+        // (idx and share are far below 2^22: the quotient is exact)
+        const int q = static_cast<int>((static_cast<float>(idx) + 0.5f) * per_share);
+        st_peer_f32x4(peer_addr(recv + split * share + idx - q * share, q), acc);
+      } else {
+        finish(r, c, acc, L);
       }
     }
-    if (CS > 1) st_peer_f32x4(peer_addr(recv + split * share + idx % share, idx / share), acc);
-    else finish(r, c, acc, L);
   }
   if (CS == 1) return !timed_out;
   cluster_sync_all();
@@ -242,19 +251,17 @@ __device__ __forceinline__ bool merge_rows(int tid, int CS, int split, int rows_
   for (int i = tid; i < min(share, pieces - split * share); i += THREADS) {
     const int idx = split * share + i, r = idx / (D / 4), c = idx % (D / 4) * 4;
     float M = -INFINITY;
+#pragma unroll 4
     for (int q = 0; q < CS; ++q) M = fmaxf(M, s_ml[q][r].x);
     const float base = M == -INFINITY ? 0.f : M;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float L = 0.f;
+#pragma unroll 4
     for (int q = 0; q < CS; ++q) {
       const float2 ml = s_ml[q][r];
-      const float f = exp2f(ml.x - base);
-      const float4 v = recv[q * share + i];
+      const float f = fast_exp2(ml.x - base);
       L = fmaf(f, ml.y, L);
-      acc.x = fmaf(f, v.x, acc.x);
-      acc.y = fmaf(f, v.y, acc.y);
-      acc.z = fmaf(f, v.z, acc.z);
-      acc.w = fmaf(f, v.w, acc.w);
+      add_piece(acc, f, recv[q * share + i]);
     }
     finish(r, c, acc, L);
   }

@@ -96,6 +96,7 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
   __shared__ uint32_t s_tmem;
   __shared__ int s_timeout;
   __shared__ int s_par[SPEC_MAX_TREE_NODES];
+  __shared__ long long s_row[kRows];            // a row's first element of q and o
   __shared__ float s_c[kRows];                // a row's score factor
   __shared__ float s_max[2][4][kRows];        // [tile parity][key part][row]
   __shared__ float s_ref[2][kRows], s_sum[2][kRows];
@@ -350,7 +351,13 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
           h[e] = pack_half2(__uint_as_float(u[e] << 16) * grow, __uint_as_float(u[e] & 0xFFFF0000u) * grow);
         st_shared_v4(sb + C::kOffQ + (c >> 3) * C::kBoxBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4), h[0], h[1], h[2],
                      h[3]);
-        if (c == 0) s_c[r] = a.scale_log2 * power_of_two(-up);
+        if (c == 0) {
+          const int node_r = (row0 + r) / a.G;
+          s_c[r] = a.scale_log2 * power_of_two(-up);
+          s_row[r] = in_bounds(G.lo + node_r, a.T, a.status, b)
+                         ? (static_cast<long long>(G.lo + node_r) * a.Hq + g_kv * a.G + (row0 + r) - node_r * a.G) * D
+                         : -1;
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -426,11 +433,15 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
         }
         // ---- weights; P's buffer is free once the product two tiles back is done
         const bool room = mbar_over(o_done_h + 8 * sr.at, sr.phase ^ 1);
-        float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int j = 0; j < kPart; ++j) x[j] = fast_exp2(x[j]);
+        float s0 = x[0], s1 = x[1], s2 = x[2], s3 = x[3];
 #pragma unroll
-        for (int j = 0; j < kPart; j += 2) add2(s0, s1, x[j], x[j + 1]);
+        for (int j = 4; j < kPart; j += 4) {
+          add2(s0, s1, x[j], x[j + 1]);
+          add2(s2, s3, x[j + 2], x[j + 3]);
+        }
+        add2(s0, s1, s2, s3);
         sum += s0 + s1;
         ok = ok && (room || mbar_sleep(o_done_h + 8 * sr.at, sr.phase ^ 1));
         __syncwarp();
@@ -478,12 +489,7 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
     }, [&](int row0) {
       const bool timed_out = s_timeout != 0;
       if (timed_out && soft == 0) report(a.status, b, SPEC_ERR_TIMEOUT);
-      auto out_row = [&](int r) -> __nv_bfloat16 * {
-        const int node = (row0 + r) / a.G;
-        if (!in_bounds(G.lo + node, a.T, a.status, b)) return nullptr;
-        return static_cast<__nv_bfloat16 *>(a.o) +
-               (static_cast<size_t>(G.lo + node) * a.Hq + g_kv * a.G + (row0 + r) % a.G) * D;
-      };
+      auto out_row = [&](int r) { return s_row[r] < 0 ? nullptr : static_cast<__nv_bfloat16 *>(a.o) + s_row[r]; };
       return merge_rows<D, 2, kRows, kSoftThreads, __nv_bfloat16>(
           soft, CS, split, min(kRows, rows_total - row0), timed_out, reinterpret_cast<float *>(smem), s_ref, s_sum,
           s_ml, reinterpret_cast<float4 *>(smem + C::kOffRecv), [] { cluster_wait(); }, out_row);

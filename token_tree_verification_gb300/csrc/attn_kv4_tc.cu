@@ -97,6 +97,7 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
   __shared__ uint32_t s_tmem;
   __shared__ int s_timeout;
   __shared__ int s_par[SPEC_MAX_TREE_NODES];
+  __shared__ long long s_row[N];            // a row's first element of q and o
   __shared__ uint4 s_tree[N];
   __shared__ int s_first[N];
   __shared__ __align__(16) float s_c[N];           // a row's score factor
@@ -384,7 +385,13 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
           h[e] = pack_half2(__uint_as_float(u[e] << 16) * grow, __uint_as_float(u[e] & 0xFFFF0000u) * grow);
         st_shared_v4(sb + C::kOffQ + (c >> 3) * C::kQBoxBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4), h[0], h[1], h[2],
                      h[3]);
-        if (c == 0) s_c[r] = a.scale_log2 * power_of_two(-up);
+        if (c == 0) {
+          const int node_r = (row0 + r) / a.G;
+          s_c[r] = a.scale_log2 * power_of_two(-up);
+          s_row[r] = in_bounds(G.lo + node_r, a.T, a.status, b)
+                         ? (static_cast<long long>(G.lo + node_r) * a.Hq + g_kv * a.G + (row0 + r) - node_r * a.G) * D
+                         : -1;
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -547,12 +554,7 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
     }, [&](int row0) {
       const bool timed_out = s_timeout != 0;
       if (timed_out && soft == 0) report(a.status, b, SPEC_ERR_TIMEOUT);
-      auto out_row = [&](int r) -> __nv_bfloat16 * {
-        const int node = (row0 + r) / a.G;
-        if (!in_bounds(G.lo + node, a.T, a.status, b)) return nullptr;
-        return static_cast<__nv_bfloat16 *>(a.o) +
-               (static_cast<size_t>(G.lo + node) * a.Hq + g_kv * a.G + (row0 + r) % a.G) * D;
-      };
+      auto out_row = [&](int r) { return s_row[r] < 0 ? nullptr : static_cast<__nv_bfloat16 *>(a.o) + s_row[r]; };
       return merge_rows<D, 2, N, kSoftThreads, __nv_bfloat16>(
           soft, CS, split, min(N, rows_total - row0), timed_out, reinterpret_cast<float *>(smem), s_ref, s_sum, s_ml,
           reinterpret_cast<float4 *>(smem + C::kOffRecv), [] { cluster_wait(); }, out_row);

@@ -5,7 +5,7 @@ namespace spec {
 
 namespace {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 128;
 
 struct Kv4Args {
   void *k, *v;                              // dense rows [T][Hkv][D]
@@ -47,7 +47,9 @@ __device__ __forceinline__ uint32_t scale_of(uint32_t amax_bits) {
 // zero keeps the element's sign.)
 __device__ __forceinline__ uint32_t codes_of(float x0, float x1, float inv) {
   constexpr float kGrid = 768.f;
-  const float y0 = __fadd_rn(__fmaf_rn(x0, inv, kGrid), -kGrid), y1 = __fadd_rn(__fmaf_rn(x1, inv, kGrid), -kGrid);
+  float y0 = x0, y1 = x1;
+  fma2(y0, y1, inv, inv, kGrid, kGrid);
+  add2(y0, y1, -kGrid, -kGrid);
   uint32_t c;
   asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\tcvt.u32.u8 %0, t;\n\t}"
       : "=r"(c)
@@ -63,6 +65,12 @@ struct Eight<__nv_bfloat16> {
   uint4 v;
   __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = __ldg(reinterpret_cast<const uint4 *>(p)); }
   __device__ __forceinline__ void clear() { v = make_uint4(0u, 0u, 0u, 0u); }
+  // the largest magnitude, as the bits of a float
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+    return max(m << 16, m & 0xFFFF0000u);
+  }
   __device__ __forceinline__ void floats(float (&x)[8]) const {
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -80,6 +88,11 @@ struct Eight<float> {
     w = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
   }
   __device__ __forceinline__ void clear() { v = w = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t m = max(max(max(v.x & 0x7FFFFFFFu, v.y & 0x7FFFFFFFu), max(v.z & 0x7FFFFFFFu, v.w & 0x7FFFFFFFu)),
+                           max(max(w.x & 0x7FFFFFFFu, w.y & 0x7FFFFFFFu), max(w.z & 0x7FFFFFFFu, w.w & 0x7FFFFFFFu)));
+    return m;
+  }
   __device__ __forceinline__ void floats(float (&x)[8]) const {
     const uint32_t u[8] = {v.x, v.y, v.z, v.w, w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -87,39 +100,46 @@ struct Eight<float> {
   }
 };
 
-// Where flattened row t * H + h lies, walked along consecutive rows: the
-// request is looked up again only when t leaves the present one's rows.
+// A walk along consecutive flattened rows t * H + h: the dense row's offset and
+// the record move on by strides within a token's heads; the request is looked
+// up again only when t leaves the present one's rows.
+template <int R>
 struct RowWalk {
   const Kv4Args &a;
-  uint32_t h;
-  int t, b;
+  long long st, sh, dense;       // element strides, and offset of the present row
+  uint8_t *rec;
+  int h, t, b;
+  bool ok;                        // the row belongs to a request without error
   Kv4Rows r;
-  __device__ __forceinline__ RowWalk(const Kv4Args &args, uint32_t row) : a(args) {
+
+  __device__ __forceinline__ RowWalk(const Kv4Args &args, long long row_stride, long long head_stride, uint32_t row)
+      : a(args), st(row_stride), sh(head_stride) {
     t = static_cast<int>(row / static_cast<uint32_t>(a.H));
-    h = row - static_cast<uint32_t>(t) * a.H;
+    h = static_cast<int>(row - static_cast<uint32_t>(t) * a.H);
     look_up();
   }
   __device__ __forceinline__ void look_up() {
     b = t < a.T ? find_request(a.offsets, a.B, t) : -1;
     r = {0, 0, 0, 1};
     if (b >= 0) r = kv4_rows(a.offsets, a.start, b, a.T, a.S_cap);
+    place();
   }
-  __device__ __forceinline__ bool valid() const {
-    return b >= 0 && !r.err && t < a.T && t >= r.lo && t < r.lo + r.n &&
-           in_bounds(r.start + (t - r.lo), a.S_cap, a.status, b);
+  __device__ __forceinline__ void place() {
+    dense = t * st + h * sh;
+    ok = b >= 0 && !r.err && t < r.lo + r.n && in_bounds(r.start + (t - r.lo), a.S_cap, a.status, b);
+    rec = a.kv + ((static_cast<size_t>(max(b, 0)) * a.H + h) * a.S_cap + r.start + (t - r.lo)) * R;
   }
-  template <int R>
-  __device__ __forceinline__ uint8_t *record() const {
-    return a.kv + ((static_cast<size_t>(b) * a.H + h) * a.S_cap + r.start + (t - r.lo)) * R;
-  }
-  __device__ __forceinline__ void advance(uint32_t rows) {
+  __device__ __forceinline__ void advance(int rows) {
     h += rows;
-    if (h < static_cast<uint32_t>(a.H)) return;
+    dense += rows * sh;
+    rec += static_cast<size_t>(rows) * a.S_cap * R;
+    if (h < a.H) return;
     do {
       h -= a.H;
       ++t;
-    } while (h >= static_cast<uint32_t>(a.H));
+    } while (h >= a.H);
     if (b < 0 || t >= r.lo + r.n) look_up();
+    else place();
   }
 };
 
@@ -133,11 +153,12 @@ __device__ __forceinline__ void report_bad_rows(const Kv4Args &a) {
 
 // One row (key and value of one request, head and slot) is 2 x D / 8 lanes of
 // eight dimensions each: a whole warp for D = 128, half of one for D = 64.  A
-// warp takes U consecutive rounds of rows with their loads under way at once;
-// both kernels are bound by HBM on long runs and by latency on short ones.
+// warp walks `rounds` x U x (32 / lanes of a row) consecutive rows, U rounds of
+// loads under way at once.  Both kernels are bound by HBM on long runs; on
+// short ones by the chain of look-ups in front of the first load.
 template <int D, int U, typename E>
 __global__ void __launch_bounds__(kRowThreads)
-kv4_write_kernel(const Kv4Args a) {
+kv4_write_kernel(const Kv4Args a, int rounds) {
   constexpr int kLanes = D / 4;                 // lanes of a row
   constexpr int kSide = 32 / kLanes;            // rows of a warp side by side
   constexpr int R = kv4_record_bytes(D);
@@ -145,59 +166,53 @@ kv4_write_kernel(const Kv4Args a) {
   const int sub = lane % kLanes;                // place within the row
   const bool is_v = sub >= kLanes / 2;
   const E *base = static_cast<const E *>(is_v ? a.v : a.k) + sub % (kLanes / 2) * 8;
-  const long long st = is_v ? a.v_st : a.k_st, sh = is_v ? a.v_sh : a.k_sh;
   pdl_trigger();
   pdl_wait();
   const uint32_t warp = (blockIdx.x * kRowThreads + tid) / 32;
-  RowWalk w(a, warp * (U * kSide) + lane / kLanes);
-  Eight<E> in[U];
-  uint8_t *rec[U];
-  int req[U];
+  RowWalk<R> w(a, is_v ? a.v_st : a.k_st, is_v ? a.v_sh : a.k_sh,
+               warp * static_cast<uint32_t>(rounds * U * kSide) + lane / kLanes);
+  for (int round = 0; round < rounds; ++round) {
+    Eight<E> in[U];
+    uint32_t *rec[U];
+    int req[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    rec[u] = nullptr;
-    req[u] = w.b;
-    if (w.valid()) {
-      in[u].load(base + w.t * st + w.h * sh);
-      rec[u] = w.record<R>();
-    } else {
-      in[u].clear();
+    for (int u = 0; u < U; ++u) {
+      rec[u] = w.ok ? reinterpret_cast<uint32_t *>(w.rec) : nullptr;
+      req[u] = w.b;
+      if (w.ok) in[u].load(base + w.dense);
+      else in[u].clear();
+      w.advance(kSide);
     }
-    if (u + 1 < U) w.advance(kSide);
-  }
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    float x[8];
-    in[u].floats(x);
-    uint32_t top = 0;
+    for (int u = 0; u < U; ++u) {
+      uint32_t top = in[u].top();
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      if (top >= 0x7F800000u) {                 // NaN or infinity: the group becomes zeros
+        report(a.status, req[u], SPEC_ERR_NONFINITE);
+        top = 0;
+        in[u].clear();
+      }
+      uint32_t byte = scale_of<E>(top);
+      float inv = 0.f;
+      if (byte) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(__half2float(__ushort_as_half(byte << 7))));
+      float x[8];
+      in[u].floats(x);
+      uint32_t codes = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    if (top >= 0x7F800000u) {                   // NaN or infinity: the group becomes zeros
-      report(a.status, req[u], SPEC_ERR_NONFINITE);
-      top = 0;
+      for (int i = 0; i < 4; ++i) {
+        float y[2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    }
-    uint32_t byte = scale_of<E>(top);
-    float inv = 0.f;
-    if (byte) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(__half2float(__ushort_as_half(byte << 7))));
-    uint32_t codes = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float y[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) y[e] = __uint_as_float(round_sticky<E>(__float_as_uint(x[2 * i + e])));
-      codes |= codes_of(y[0], y[1], inv) << (8 * i);
-    }
-    // scale bytes of four neighbouring groups to one word
-    byte |= __shfl_down_sync(0xffffffffu, byte, 2) << 8;
-    byte |= __shfl_down_sync(0xffffffffu, byte, 4) << 16;
-    if (rec[u]) {
-      uint32_t *word = reinterpret_cast<uint32_t *>(rec[u]);
-      word[sub] = codes;
-      if (sub % 8 == 0) word[D / 4 + sub / 8] = byte;
-      if (D == 64 && sub % 8 == 4) word[D / 4 + 2 + sub / 8] = 0u;
+        for (int e = 0; e < 2; ++e) y[e] = __uint_as_float(round_sticky<E>(__float_as_uint(x[2 * i + e])));
+        codes |= codes_of(y[0], y[1], inv) << (8 * i);
+      }
+      // scale bytes of four neighbouring groups to one word
+      byte |= __shfl_down_sync(0xffffffffu, byte, 2) << 8;
+      byte |= __shfl_down_sync(0xffffffffu, byte, 4) << 16;
+      if (rec[u]) {
+        rec[u][sub] = codes;
+        if (sub % 8 == 0) rec[u][D / 4 + sub / 8] = byte;
+        if (D == 64 && sub % 8 == 4) rec[u][D / 4 + 2 + sub / 8] = 0u;
+      }
     }
   }
   report_bad_rows(a);
@@ -205,7 +220,7 @@ kv4_write_kernel(const Kv4Args a) {
 
 template <int D, int U, typename E>
 __global__ void __launch_bounds__(kRowThreads)
-kv4_read_kernel(const Kv4Args a) {
+kv4_read_kernel(const Kv4Args a, int rounds) {
   constexpr int kLanes = D / 4;
   constexpr int kSide = 32 / kLanes;
   constexpr int R = kv4_record_bytes(D);
@@ -213,48 +228,48 @@ kv4_read_kernel(const Kv4Args a) {
   const int sub = lane % kLanes;
   const bool is_v = sub >= kLanes / 2;
   E *base = static_cast<E *>(is_v ? a.v : a.k) + sub % (kLanes / 2) * 8;
-  const long long st = is_v ? a.v_st : a.k_st, sh = is_v ? a.v_sh : a.k_sh;
   pdl_trigger();
   pdl_wait();
   const uint32_t warp = (blockIdx.x * kRowThreads + tid) / 32;
-  RowWalk w(a, warp * (U * kSide) + lane / kLanes);
-  uint32_t code[U], scale[U];
-  E *dst[U];
+  RowWalk<R> w(a, is_v ? a.v_st : a.k_st, is_v ? a.v_sh : a.k_sh,
+               warp * static_cast<uint32_t>(rounds * U * kSide) + lane / kLanes);
+  for (int round = 0; round < rounds; ++round) {
+    uint32_t code[U], scale[U];
+    E *dst[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    dst[u] = nullptr;
-    code[u] = scale[u] = 0u;
-    if (w.valid()) {
-      const uint8_t *rec = w.record<R>();
-      code[u] = __ldg(reinterpret_cast<const uint32_t *>(rec) + sub);
-      scale[u] = __ldg(rec + D + sub / 2);
-      dst[u] = base + w.t * st + w.h * sh;
+    for (int u = 0; u < U; ++u) {
+      dst[u] = w.ok ? base + w.dense : nullptr;
+      code[u] = scale[u] = 0u;
+      if (w.ok) {
+        code[u] = __ldg(reinterpret_cast<const uint32_t *>(w.rec) + sub);
+        scale[u] = __ldg(w.rec + D + sub / 2);
+      }
+      w.advance(kSide);
     }
-    if (u + 1 < U) w.advance(kSide);
-  }
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (!dst[u]) continue;
-    uint32_t p[4];
-    kv4_codes_to_half2(code[u], p);
-    const uint32_t s = kv4_scale_half2(scale[u]);
-    float2 f[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t y = mul_half2(p[i], s);
-      f[i] = __half22float2(*reinterpret_cast<const __half2 *>(&y));
-    }
-    if constexpr (sizeof(E) == 4) {
-      reinterpret_cast<float4 *>(dst[u])[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-      reinterpret_cast<float4 *>(dst[u])[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
-    } else {
-      uint32_t o[4];
+    for (int u = 0; u < U; ++u) {
+      if (!dst[u]) continue;
+      uint32_t p[4];
+      kv4_codes_to_half2(code[u], p);
+      const uint32_t s = kv4_scale_half2(scale[u]);
+      float2 f[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(f[i].x, f[i].y);
-        o[i] = *reinterpret_cast<const uint32_t *>(&v);
+        const uint32_t y = mul_half2(p[i], s);
+        f[i] = __half22float2(*reinterpret_cast<const __half2 *>(&y));
       }
-      *reinterpret_cast<uint4 *>(dst[u]) = make_uint4(o[0], o[1], o[2], o[3]);
+      if constexpr (sizeof(E) == 4) {
+        reinterpret_cast<float4 *>(dst[u])[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+        reinterpret_cast<float4 *>(dst[u])[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+      } else {
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 v = __floats2bfloat162_rn(f[i].x, f[i].y);
+          o[i] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+        *reinterpret_cast<uint4 *>(dst[u]) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
     }
   }
   report_bad_rows(a);
@@ -277,7 +292,7 @@ int check_rows(const void *k, const void *v, int dtype, int B, int T, int Hkv, i
 }
 
 template <typename Kernel>
-int launch_rows(Kernel kernel, const Kv4Args &args, long long warps, void *stream) {
+int launch_rows(Kernel kernel, const Kv4Args &args, long long warps, int rounds, void *stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((warps * 32 + kRowThreads - 1) / kRowThreads), 1, 1);
   cfg.blockDim = dim3(kRowThreads, 1, 1);
@@ -286,23 +301,27 @@ int launch_rows(Kernel kernel, const Kv4Args &args, long long warps, void *strea
   pdl_attribute(attr[0]);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, args, rounds) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
-// Four rounds of rows per warp where that still leaves every SM 32 warps, else
-// one, so that a tree's few rows spread over the GPU.
+// One round of rows per warp while that leaves every SM at most 32 warps, so
+// that a tree's few rows spread over the GPU; beyond, U rounds at once, and as
+// many turns of them as make kWaves waves of 32 warps on every SM.
 template <bool kWrite, int D, typename E>
 int rows_by_size(const Kv4Args &args, void *stream) {
+  constexpr int U = 2, kWaves = 4;
   const long long rows = static_cast<long long>(args.T) * args.H, side = 32 / (D / 4);
   if (rows == 0) return SPEC_OK;
   if (rows > 0x7FFFFFFFll) return SPEC_ERR_SHAPE;      // rows are counted in 32 bits
-  const long long one = (rows + side - 1) / side, four = (one + 3) / 4;
-  if (four < 32ll * sm_count()) {
-    if constexpr (kWrite) return launch_rows(kv4_write_kernel<D, 1, E>, args, one, stream);
-    else return launch_rows(kv4_read_kernel<D, 1, E>, args, one, stream);
+  const long long one = (rows + side - 1) / side, wave = 32ll * sm_count();
+  if (one <= wave) {
+    if constexpr (kWrite) return launch_rows(kv4_write_kernel<D, 1, E>, args, one, 1, stream);
+    else return launch_rows(kv4_read_kernel<D, 1, E>, args, one, 1, stream);
   }
-  if constexpr (kWrite) return launch_rows(kv4_write_kernel<D, 4, E>, args, four, stream);
-  else return launch_rows(kv4_read_kernel<D, 4, E>, args, four, stream);
+  const long long rounds = (one + U * kWaves * wave - 1) / (U * kWaves * wave);
+  const long long warps = (one + U * rounds - 1) / (U * rounds);
+  if constexpr (kWrite) return launch_rows(kv4_write_kernel<D, U, E>, args, warps, static_cast<int>(rounds), stream);
+  else return launch_rows(kv4_read_kernel<D, U, E>, args, warps, static_cast<int>(rounds), stream);
 }
 
 template <bool kWrite>

@@ -52,6 +52,22 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+// Two fp32 at once.
+__device__ __forceinline__ void fma2(float &x0, float &x1, float c0, float c1, float n0, float n1) {
+  asm("{\n\t.reg .b64 x, c, n;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 c, {%2, %3};\n\tmov.b64 n, {%4, %5};\n\t"
+      "fma.rn.f32x2 x, x, c, n;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(c0), "f"(c1), "f"(n0), "f"(n1));
+}
+__device__ __forceinline__ void add2(float &x0, float &x1, float y0, float y1) {
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(y0), "f"(y1));
+}
+
 // Rows of a ragged batch against the cache: request b's rows are
 // [offsets[b], offsets[b+1]) and its row i belongs to slot start[b] + i.
 struct Kv4Rows {
