@@ -65,6 +65,16 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same onto zero.
+__device__ __forceinline__ void mma_16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -150,23 +160,11 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
         s_par[i] = in_bounds(G.lo + i, a.T, a.status, b) ? __ldg(a.parents + G.lo + i) : -2;
       __syncthreads();
     }
-    if (tid < C::kRows) {
-      RowKeys see = {0, 0, make_uint4(0u, 0u, 0u, 0u)};
-      if (tid < rows_here) {
-        const int node = (row0 + tid) / a.G;
-        uint4 m = make_uint4(0u, 0u, 0u, 0u);
-        if (a.mask) {
-          if (in_bounds(G.lo + node, a.T, a.status, b)) m = clip_mask(__ldg(a.mask + G.lo + node), G.n);
-        } else {
-          bool bad = false;
-          m = ancestor_mask([&](int i) { return s_par[i]; }, node, &bad);
-          if (bad) report(a.status, b, SPEC_ERR_BAD_PARENT);
-        }
-        see = row_keys(m, G.L, p.window, p.sinks);
-      }
-      s_tree[tid] = see.tree;
-      s_first[tid] = see.first;
-    }
+    // (the mask's load is under way while the queries are taken)
+    uint4 row_mask = make_uint4(0u, 0u, 0u, 0u);
+    const int row_node = (row0 + tid) / a.G;
+    if (a.mask && tid < rows_here && in_bounds(G.lo + row_node, a.T, a.status, b))
+      row_mask = __ldg(a.mask + G.lo + row_node);
     uint32_t qf[C::kQInRegs ? NP : 1][C::kQInRegs ? KS : 1][C::kQInRegs ? NT : 1][2];
     uint2 *sq = reinterpret_cast<uint2 *>(smem + C::kOffQ);   // [part][step][tile][lane]
     float c_row[NT][2];                                       // score factor of rows 2t, 2t + 1
@@ -223,6 +221,18 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
           }
         }
     }
+    if (tid < C::kRows) {
+      if (a.mask) {
+        row_mask = clip_mask(row_mask, G.n);
+      } else if (tid < rows_here) {
+        bool bad = false;
+        row_mask = ancestor_mask([&](int i) { return s_par[i]; }, row_node, &bad);
+        if (bad) report(a.status, b, SPEC_ERR_BAD_PARENT);
+      }
+      const RowKeys see = row_keys(row_mask, G.L, p.window, p.sinks);
+      s_tree[tid] = see.tree;
+      s_first[tid] = see.first;
+    }
     __syncthreads();
 
     // ---- the keys
@@ -250,10 +260,6 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
       float sc[2][NT][4];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
         uint32_t kw[2][kWords], ks[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -290,7 +296,10 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
                 uint2 q;
                 if constexpr (C::kQInRegs) q = make_uint2(qf[part][s][nt][0], qf[part][s][nt][1]);
                 else q = sq[((part * KS + s) * NT + nt) * 32 + lane];
-                mma_16816(sc[mt][nt], h0[2 * half], h1[2 * half], h0[2 * half + 1], h1[2 * half + 1], q.x, q.y);
+                if (s == 0 && part == 0)
+                  mma_16816_first(sc[mt][nt], h0[0], h1[0], h0[1], h1[1], q.x, q.y);
+                else
+                  mma_16816(sc[mt][nt], h0[2 * half], h1[2 * half], h0[2 * half + 1], h1[2 * half + 1], q.x, q.y);
               }
         }
       }
@@ -478,9 +487,12 @@ int launch_few(const Kv4AttnArgs &p, int blocks, int cs, void *stream) {
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
-// Splits: while every warp keeps a tile, up to 8 as long as the CTAs stay
-// within two waves (about four CTAs of four warps per SM), and 16 only where 8
-// leave SMs without work.
+// Splits of the keys, by the time they are expected to take.  Measured at
+// D = 128, up to 8 rows: a warp alone on its scheduler takes 1.0 us per tile
+// of 32 keys, and 0.47 us x (CTAs of four warps per SM) once the SM's issue
+// slots are shared; set-up, first tile and output take 3 us, the merge of
+// splits 1.5 us, overlapped with other CTAs' work beyond the four that are
+// resident.  16 splits only where 8 leave SMs without work.
 int few_splits(const Kv4AttnArgs &p, long long units, int max_prefix) {
   long long keys = static_cast<long long>(max_prefix) + mean_nodes(p.a);
   if (p.window) {
@@ -489,10 +501,20 @@ int few_splits(const Kv4AttnArgs &p, long long units, int max_prefix) {
   }
   const long long tiles = (keys + kFewTile - 1) / kFewTile;
   const long long sms = sm_count();
-  int cs = 1;
-  while (cs < 8 && 2 * cs * units <= 8 * sms && tiles >= 8 * cs) cs *= 2;
-  if (cs == 8 && 8 * units < sms && tiles >= 64) cs = 16;
-  return cs;
+  int best = 1;
+  double least = 0;
+  for (int cs = 1; cs <= 8 && (cs == 1 || tiles >= 4 * cs); cs *= 2) {
+    const double per_sm = static_cast<double>((units * cs + sms - 1) / sms);
+    const double per_tile = 0.47 * per_sm > 1.0 ? 0.47 * per_sm : 1.0;
+    const double fixed = (cs > 1 ? 4.5 : 3.0) * (per_sm > 4 ? per_sm / 4 : 1.0);
+    const double us = static_cast<double>((tiles + 4 * cs - 1) / (4 * cs)) * per_tile + fixed;
+    if (cs == 1 || us < least) {
+      least = us;
+      best = cs;
+    }
+  }
+  if (best == 8 && 8 * units < sms && tiles >= 64) best = 16;
+  return best;
 }
 
 template <int D, bool F32>
