@@ -354,7 +354,7 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
         if (c == 0) {
           const int node_r = (row0 + r) / a.G;
           s_c[r] = a.scale_log2 * power_of_two(-up);
-          s_row[r] = in_bounds(G.lo + node_r, a.T, a.status, b)
+          s_row[r] = r < rows_here && in_bounds(G.lo + node_r, a.T, a.status, b)
                          ? (static_cast<long long>(G.lo + node_r) * a.Hq + g_kv * a.G + (row0 + r) - node_r * a.G) * D
                          : -1;
         }
@@ -508,12 +508,12 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
 
 int launch_kv4_rows(const Kv4AttnArgs &p, int max_prefix, void *stream) {
   const int blocks = (mean_nodes(p.a) * p.a.G + kRows - 1) / kRows;
-  static std::atomic<size_t> granted[2][kMaxDevices];
+  static TileLaunch state[2];
   if (p.a.D == 128)
     return launch_kv4_tiles(tree_attn_kv4_rows_kernel<128>, p, kThreads, Kv4Rows128<128>::kSmem, blocks, max_prefix,
-                            granted[0], stream);
+                            &state[0], stream);
   return launch_kv4_tiles(tree_attn_kv4_rows_kernel<64>, p, kThreads, Kv4Rows128<64>::kSmem, blocks, max_prefix,
-                          granted[1], stream);
+                          &state[1], stream);
 }
 
 }  // namespace spec

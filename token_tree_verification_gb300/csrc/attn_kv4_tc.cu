@@ -388,7 +388,7 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
         if (c == 0) {
           const int node_r = (row0 + r) / a.G;
           s_c[r] = a.scale_log2 * power_of_two(-up);
-          s_row[r] = in_bounds(G.lo + node_r, a.T, a.status, b)
+          s_row[r] = r < rows_here && in_bounds(G.lo + node_r, a.T, a.status, b)
                          ? (static_cast<long long>(G.lo + node_r) * a.Hq + g_kv * a.G + (row0 + r) - node_r * a.G) * D
                          : -1;
         }
@@ -571,9 +571,9 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
 
 template <int D, int N>
 int launch_tc(const Kv4AttnArgs &p, int max_prefix, void *stream) {
-  static std::atomic<size_t> granted[kMaxDevices];
+  static TileLaunch state;
   const int blocks = (mean_nodes(p.a) * p.a.G + N - 1) / N;
-  return launch_kv4_tiles(tree_attn_kv4_tc_kernel<D, N>, p, kTcThreads, Kv4Tc<D, N>::kSmem, blocks, max_prefix, granted,
+  return launch_kv4_tiles(tree_attn_kv4_tc_kernel<D, N>, p, kTcThreads, Kv4Tc<D, N>::kSmem, blocks, max_prefix, &state,
                           stream);
 }
 

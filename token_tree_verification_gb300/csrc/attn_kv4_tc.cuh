@@ -124,12 +124,20 @@ __device__ __forceinline__ void put_swizzled(uint32_t row, int g, const uint32_t
 // Launch of a kernel that takes one CTA per SM: `blocks` row blocks (the
 // grid's y) of every (request, KV head), and as many splits of the keys (a
 // cluster) as make waves x (tiles of a CTA + its set-up, first tile and merge,
-// in tiles) least.
+// in tiles) least.  Of clusters of 16 only about four run at once (eight of
+// them took twice the time of four, and longer than eight clusters of 8), so
+// they serve up to four units: 64-node trees on 4 KV heads behind 30000 keys
+// take 25.5 us with 16 splits and 37.7 us with 8.
+struct TileLaunch {
+  std::atomic<size_t> granted[kMaxDevices];
+  std::atomic<bool> wide[kMaxDevices];
+};
+
 template <typename Kernel>
 int launch_kv4_tiles(Kernel kernel, const Kv4AttnArgs &p, int threads, size_t smem, int blocks, int max_prefix,
-                     std::atomic<size_t> *granted, void *stream) {
+                     TileLaunch *state, void *stream) {
   const AttnArgs &a = p.a;
-  if (!allow_dynamic_smem(kernel, smem, granted)) return SPEC_ERR_CUDA;
+  if (!allow_dynamic_smem(kernel, smem, state->granted)) return SPEC_ERR_CUDA;
   const int nodes = mean_nodes(a);
   long long keys = static_cast<long long>(max_prefix) + nodes;
   if (p.window) {
@@ -139,16 +147,26 @@ int launch_kv4_tiles(Kernel kernel, const Kv4AttnArgs &p, int threads, size_t sm
   const long long tiles = (keys + kTile - 1) / kTile;
   const long long pairs = static_cast<long long>(a.B) * a.Hkv;
   if (pairs > 65535 || blocks > 65535) return SPEC_ERR_SHAPE;
-  const long long units = pairs * blocks, slots = sm_count();
+  const long long units = pairs * blocks, sms = sm_count();
   int cs = 1;
   long long best = -1;
-  for (int c = 1; c <= 8; ++c) {
+  for (int c = 1; c <= 16; c = c == 8 ? 16 : c + 1) {
     if (c > 1 && tiles < 2 * c) break;
+    const long long slots = c > 8 ? sms * 64 / 152 : sms;
     const long long waves = (units * c + slots - 1) / slots;
     const long long cost = waves * ((tiles + c - 1) / c + 8 + (c > 1 ? 2 : 0));
     if (best < 0 || cost < best) {
       best = cost;
       cs = c;
+    }
+  }
+  if (cs > 8) {
+    const int dev = current_device();
+    if (dev < 0) return SPEC_ERR_CUDA;
+    if (!state->wide[dev].load(std::memory_order_acquire)) {
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return SPEC_ERR_CUDA;
+      state->wide[dev].store(true, std::memory_order_release);
     }
   }
   cudaLaunchConfig_t cfg = {};
