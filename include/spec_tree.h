@@ -353,7 +353,7 @@ size_t spec_kv4_record_bytes(int D);   /* 0 when D is neither 64 nor 128 */
  *   start     [B] int32, offsets [B+1] int32 (a request may have no rows; it
  *             has no upper limit of rows)
  *   T         rows of k and v; rows at or behind offsets[B] are ignored, T = 0
- *             enqueues nothing
+ *             enqueues nothing (k and v may then be NULL); T x Hkv below 2^31
  * Errors on the device: SPEC_ERR_TREE_TOO_LARGE (offsets outside [0, T] or
  * decreasing) and SPEC_ERR_PREFIX_RANGE (a slot outside [0, S_cap)), for
  * which the request's slots stay as they were; SPEC_ERR_NONFINITE (NaN or

@@ -184,11 +184,20 @@ SHAPES = [  # D, Hq, Hkv, prefixes, nodes
     (128, 1, 1, [0], [1]), (64, 1, 1, [1], [1]), (128, 4, 4, [15, 16, 17], [1, 1, 1]), (64, 8, 1, [63, 64, 65, 0], [2, 1, 3, 5]),
     (128, 8, 1, [300], [1]), (128, 3, 1, [129, 5], [7, 40]), (128, 10, 2, [33], [13]), (64, 4, 2, [700, 20, 0], [64, 33, 16]),
     (128, 2, 2, [1000], [128]), (128, 16, 2, [250, 511], [128, 3]), (64, 32, 1, [90], [11]), (128, 128, 1, [70], [3]),
-    (128, 5, 1, [4000], [26]), (128, 32, 32, [2048], [9]), (64, 2, 1, [20000], [2])]
+    (128, 5, 1, [4000], [26]), (128, 32, 32, [2048], [9]), (64, 2, 1, [20000], [2]),
+    # 48 and 64 rows on a key
+    (128, 4, 1, [600], [12]), (64, 16, 2, [10, 300], [8, 8]), (128, 2, 2, [1500], [64]),
+    # splits into 16, for one row block
+    (128, 1, 1, [9000], [20]), (64, 2, 2, [9000], [90])]
+
+RAGGED = [  # one request with many more rows than the mean, which its CTAs take in turns
+    (128, 2, 2, [3000, 10, 5, 2000], [1, 1, 1, 20]), (128, 1, 1, [1900, 2000], [1, 60]),
+    (64, 2, 1, [3000, 3, 0], [128, 1, 1]), (128, 8, 2, [40, 2, 300, 1, 0], [1, 1, 128, 1, 1]),
+    (64, 1, 1, [0, 0, 0, 1500], [1, 1, 1, 100])]
 
 
 @DTYPES
-@pytest.mark.parametrize("D,Hq,Hkv,L,n", SHAPES)
+@pytest.mark.parametrize("D,Hq,Hkv,L,n", SHAPES + RAGGED)
 @pytest.mark.parametrize("window,sinks", [(0, 0), (50, 3), (1, 0)], ids=["all", "window", "self"])
 def test_attention(dtype, D, Hq, Hkv, L, n, window, sinks):
     rng = np.random.default_rng(Hq * 7 + L[0] + n[0])
@@ -280,6 +289,73 @@ def test_attention_reports_and_leaves_a_request_in_error(dtype):
     st = zeros_status(3)
     o = ttv.tree_attn_kv4(q, rec, i32([20, 30, 5]), i32([0, 8, 16, 24]), None, 40, st, parents=i32(bad))
     assert st.tolist() == [0, -5, 0] and torch.equal(o[:8], good[:8]) and torch.equal(o[16:], good[16:])
+
+
+@DTYPES
+def test_many_requests_and_empty_ones(dtype):
+    """300 requests of 0 to 3 rows: offsets longer than a block, looked up from any row."""
+    rng = np.random.default_rng(20)
+    B, H, D, cap = 300, 2, 64, 12
+    n = rng.integers(0, 4, B)
+    n[:2], n[-1] = 0, 0
+    off, start = np.concatenate([[0], np.cumsum(n)]), rng.integers(0, 9, B)
+    T = int(off[-1])
+    k, v = (torch.from_numpy(rng.standard_normal((T, H, D)).astype(np.float32)).to(dtype) for _ in range(2))
+    cache, st = ttv.make_kv4_cache(B, H, cap, D), zeros_status(B)
+    ttv.kv4_write(k.cuda(), v.cuda(), cache, i32(start), i32(off), st)
+    want = np.zeros(cache.shape, np.uint8)
+    kv4.write(want, k.float().numpy(), v.float().numpy(), start, off)
+    np.testing.assert_array_equal(cache.cpu().numpy(), want)
+    kk, _ = ttv.kv4_read(cache, i32(start), i32(off), st, rows=T, dtype=dtype)
+    np.testing.assert_array_equal(kk.double().cpu().numpy(), kv4.read(want, D, start, off)[0])
+    # no rows at all: nothing is launched
+    none = torch.empty((0, H, D), dtype=dtype, device="cuda")
+    ttv.kv4_write(none, none, cache, i32(start), torch.zeros(B + 1, dtype=torch.int32, device="cuda"), st)
+    assert ttv.kv4_read(cache, i32(start), torch.zeros(B + 1, dtype=torch.int32, device="cuda"), st, rows=0)[0].shape[0] == 0
+    np.testing.assert_array_equal(cache.cpu().numpy(), want)
+    assert not st.any()
+
+
+def test_long_runs_of_rows():
+    """Enough rows that a warp walks several turns of them, over tokens, heads and requests."""
+    rng = np.random.default_rng(21)
+    for D, H, n in ((128, 3, [9000, 0, 4321]), (64, 32, [1, 2500])):
+        off = np.concatenate([[0], np.cumsum(n)])
+        T, start = int(off[-1]), [3] * len(n)
+        k, v = (torch.from_numpy(rng.standard_normal((T, H, D)).astype(np.float32)).to(BF16) for _ in range(2))
+        cache, st = ttv.make_kv4_cache(len(n), H, max(n) + 4, D), zeros_status(len(n))
+        ttv.kv4_write(k.cuda(), v.cuda(), cache, i32(start), i32(off), st)
+        want = np.zeros(cache.shape, np.uint8)
+        kv4.write(want, k.float().numpy(), v.float().numpy(), start, off)
+        np.testing.assert_array_equal(cache.cpu().numpy(), want)
+        kk, vv = ttv.kv4_read(cache, i32(start), i32(off), st, rows=T, dtype=F32)
+        for got, ref in zip((kk, vv), kv4.read(want, D, start, off)):
+            np.testing.assert_array_equal(got.double().cpu().numpy(), ref)
+        assert not st.any()
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own outputs, while the other runs."""
+    rng = np.random.default_rng(22)
+    L, n, D = [900, 2000], [1, 40], 128
+    cache = torch.from_numpy(random_records(rng, (2, 4, 2050), D)).cuda()
+    q = [torch.from_numpy(rng.standard_normal((c, 8, D)).astype(np.float32)).to(BF16).cuda() for c in (2, 80, 256)]
+    batches = []
+    for x in q:
+        c = x.shape[0] // 2
+        par = random_tree(rng, c) + random_tree(rng, c)
+        batches.append((x, i32(L), i32([0, c, 2 * c]), i32(par), zeros_status(2)))
+    cache = torch.cat([cache, cache], 2)[:, :, :2200].contiguous()
+    call = lambda x, lens, off, par, st: ttv.tree_attn_kv4(x, cache, lens, off, None, 2000, st, parents=par)  # noqa: E731
+    ref = [call(*b) for b in batches]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for i in range(24):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append((i % 3, call(*batches[i % 3])))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, ref[j]) for j, o in got)
+    assert not any(b[4].any() for b in batches)
 
 
 def test_cache_offsets_beyond_32_bits():

@@ -274,6 +274,7 @@ def kv_compact(k_cache, v_cache, prefix_lens, offsets, path_nodes, accept_len, s
 
 # ---------------------------------------------------------------- 4-bit cache
 _KV4_DIMS = {144: 128, 80: 64}     # bytes of a slot record -> head dimension
+_I32 = torch.int32
 _DTYPES = {torch.bfloat16: SPEC_BF16, torch.float32: SPEC_F32}
 
 
@@ -304,13 +305,18 @@ def _kv4_cache(kv_cache):
     return index, B, Hkv, S_cap, _KV4_DIMS[R]
 
 
-def _i32(index, n, **tensors):
-    """Checks int32 device arrays of n elements."""
-    for name, t in tensors.items():
-        if t.dtype is not torch.int32 or t.get_device() != index:
-            raise TypeError(f"{name} must be torch.int32 on cuda:{index}, got {t.dtype} on {t.device}")
-        if t.numel() != n or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous with {n} elements, got {tuple(t.shape)}")
+def _not_i32(index, n, t, name):
+    """The error of a tensor that is not n contiguous int32 on the device."""
+    if t.dtype is not torch.int32 or t.get_device() != index:
+        return TypeError(f"{name} must be torch.int32 on cuda:{index}, got {t.dtype} on {t.device}")
+    return ValueError(f"{name} must be contiguous with {n} elements, got {tuple(t.shape)}")
+
+
+def _i32(index, n, t, name):
+    """The pointer of a device array of n int32."""
+    if t.dtype is _I32 and t.get_device() == index and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
+    raise _not_i32(index, n, t, name)
 
 
 def _dense_rows(index, t, T, Hkv, D, name):
@@ -339,11 +345,10 @@ def kv4_write(k, v, kv_cache, start, offsets, status, stream=None):
     T = k.shape[0]
     ks0, ks1 = _dense_rows(index, k, T, Hkv, D, "k")
     vs0, vs1 = _dense_rows(index, v, T, Hkv, D, "v")
-    _i32(index, B, start=start, status=status)
-    _i32(index, B + 1, offsets=offsets)
     rc = lib.spec_kv4_write(k.data_ptr(), v.data_ptr(), dt, B, T, Hkv, D, ks0, ks1, vs0, vs1,
-                            kv_cache.data_ptr(), S_cap, start.data_ptr(), offsets.data_ptr(),
-                            status.data_ptr(), _raw_stream(stream, index))
+                            kv_cache.data_ptr(), S_cap, _i32(index, B, start, "start"),
+                            _i32(index, B + 1, offsets, "offsets"), _i32(index, B, status, "status"),
+                            _raw_stream(stream, index))
     if rc:
         raise SpecError(rc, "spec_kv4_write")
 
@@ -370,11 +375,10 @@ def kv4_read(kv_cache, start, offsets, status, rows=None, dtype=torch.bfloat16, 
     dt = _DTYPES.get(k.dtype)
     if dt is None or v.dtype is not k.dtype:
         raise TypeError("rows are read as bfloat16 or float32")
-    _i32(index, B, start=start, status=status)
-    _i32(index, B + 1, offsets=offsets)
     rc = lib.spec_kv4_read(k.data_ptr(), v.data_ptr(), dt, B, T, Hkv, D, ks0, ks1, vs0, vs1,
-                           kv_cache.data_ptr(), S_cap, start.data_ptr(), offsets.data_ptr(),
-                           status.data_ptr(), _raw_stream(stream, index))
+                           kv_cache.data_ptr(), S_cap, _i32(index, B, start, "start"),
+                           _i32(index, B + 1, offsets, "offsets"), _i32(index, B, status, "status"),
+                           _raw_stream(stream, index))
     if rc:
         raise SpecError(rc, "spec_kv4_read")
     return k, v
@@ -389,14 +393,12 @@ def kv4_compact(kv_cache, prefix_lens, offsets, path_nodes, accept_len, status,
     W = path_nodes.shape[-1]
     if new_prefix_lens is None:
         new_prefix_lens = torch.empty_like(prefix_lens)
-    _i32(index, B, prefix_lens=prefix_lens, accept_len=accept_len, status=status,
-         new_prefix_lens=new_prefix_lens)
-    _i32(index, B + 1, offsets=offsets)
-    _i32(index, B * W, path_nodes=path_nodes)
-    rc = lib.spec_kv4_compact(kv_cache.data_ptr(), B, Hkv, D, S_cap, prefix_lens.data_ptr(),
-                              offsets.data_ptr(), path_nodes.data_ptr(), accept_len.data_ptr(), W,
-                              new_prefix_lens.data_ptr(), status.data_ptr(),
-                              _raw_stream(stream, index))
+    rc = lib.spec_kv4_compact(kv_cache.data_ptr(), B, Hkv, D, S_cap, _i32(index, B, prefix_lens, "prefix_lens"),
+                              _i32(index, B + 1, offsets, "offsets"),
+                              _i32(index, B * W, path_nodes, "path_nodes"),
+                              _i32(index, B, accept_len, "accept_len"), W,
+                              _i32(index, B, new_prefix_lens, "new_prefix_lens"),
+                              _i32(index, B, status, "status"), _raw_stream(stream, index))
     if rc:
         raise SpecError(rc, "spec_kv4_compact")
     return new_prefix_lens
@@ -417,15 +419,11 @@ def tree_attn_kv4(q, kv_cache, prefix_lens, offsets, mask, max_prefix, status, o
     if q.get_device() != index or q.dim() != 3 or q.shape[2] != D or not q.is_contiguous():
         raise ValueError(f"q must be contiguous [T, Hq, {D}] on cuda:{index}")
     T, Hq, _ = q.shape
-    _i32(index, B, prefix_lens=prefix_lens, status=status)
-    _i32(index, B + 1, offsets=offsets)
     mask_ptr = parents_ptr = None
     if mask is not None:
-        _i32(index, 4 * T, mask=mask)
-        mask_ptr = mask.data_ptr()
+        mask_ptr = _i32(index, 4 * T, mask, "mask")
     elif parents is not None:
-        _i32(index, T, parents=parents)
-        parents_ptr = parents.data_ptr()
+        parents_ptr = _i32(index, T, parents, "parents")
     else:
         raise ValueError("tree_attn_kv4 needs a mask or the parent array")
     if o is None:
@@ -433,9 +431,9 @@ def tree_attn_kv4(q, kv_cache, prefix_lens, offsets, mask, max_prefix, status, o
     elif o.dtype is not q.dtype or o.get_device() != index or o.shape != q.shape or not o.is_contiguous():
         raise ValueError("o must be like q")
     rc = lib.spec_tree_attn_kv4(q.data_ptr(), kv_cache.data_ptr(), o.data_ptr(), dt, B, T, Hq, Hkv, D,
-                                S_cap, max_prefix, prefix_lens.data_ptr(), offsets.data_ptr(), mask_ptr,
-                                parents_ptr, softmax_scale, window, sinks, status.data_ptr(),
-                                _raw_stream(stream, index))
+                                S_cap, max_prefix, _i32(index, B, prefix_lens, "prefix_lens"),
+                                _i32(index, B + 1, offsets, "offsets"), mask_ptr, parents_ptr, softmax_scale,
+                                window, sinks, _i32(index, B, status, "status"), _raw_stream(stream, index))
     if rc:
         raise SpecError(rc, "spec_tree_attn_kv4")
     return o

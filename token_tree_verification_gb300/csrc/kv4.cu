@@ -280,7 +280,7 @@ kv4_read_kernel(const Kv4Args a, int rounds) {
 int check_rows(const void *k, const void *v, int dtype, int B, int T, int Hkv, int D,
                long long k_st, long long k_sh, long long v_st, long long v_sh, const void *kv, int S_cap,
                const int32_t *start, const int32_t *offsets, const int32_t *status) {
-  if (!k || !v || !kv || !start || !offsets || !status) return SPEC_ERR_NULL;
+  if (((!k || !v) && T != 0) || !kv || !start || !offsets || !status) return SPEC_ERR_NULL;
   if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_DTYPE;
   if (B < 1 || T < 0 || Hkv < 1 || S_cap < 1 || (D != 64 && D != 128)) return SPEC_ERR_SHAPE;
   const int es = dtype == SPEC_F32 ? 4 : 2;
