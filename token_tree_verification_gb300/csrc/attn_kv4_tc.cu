@@ -18,15 +18,16 @@
 //   warp 1      allocates TMEM and issues S^T_i as soon as tile i's keys
 //               are decoded and the parity's S^T has been read
 //   warp 2      issues O^T += V_i^T P_i^T
-//   warps 4-19  softmax: a key per TMEM lane, so four warps for the keys of a
-//               tile; two such groups (half of the rows each) for even tiles
-//               and two for odd ones.  The sums of weights stay in registers,
-//               one per row, until the end
-//   warps 20-23 decode keys into TMEM, warps 24-27 values into shared memory
-//               (128-byte swizzle): one key per lane, so that a warp's 16-byte
-//               loads (records 36 words apart) and stores (rows 128 bytes
-//               apart, swizzled) are both free of bank conflicts.  Keys in TMEM
-//               spare shared memory the decoded K twice, written and read
+//   then        softmax: a key per TMEM lane, so four warps for the keys of a
+//               tile; for more than 16 rows two such groups (half of the rows
+//               each) for even tiles and two for odd ones, else one each.  The sums of
+//               weights stay in registers, one per row, until the end
+//   then        decoders, four warps per operand (two such sets, which take
+//               turns, for up to 16 rows): keys into TMEM, values into shared
+//               memory (128-byte swizzle), one key per lane, so that a warp's
+//               16-byte loads (records 36 words apart) and stores (rows 128
+//               bytes apart, swizzled) are both free of bank conflicts.  Keys in
+//               TMEM spare shared memory the decoded K twice, written and read
 // A chain of eight MMAs takes about 850 cycles from issue to its barrier, a
 // tile's two chains and its softmax about 3000, so what counts is how many
 // tiles are under way: three decoded, two in the softmax.
@@ -39,21 +40,28 @@ namespace spec {
 namespace {
 
 constexpr int kSoftFirst = 4;         // warps: four issuers, then the softmax, then the decoders
-constexpr int kSoftWarps = 16;
-constexpr int kDecodeFirst = kSoftFirst + kSoftWarps;
-constexpr int kDecodeWarps = 4;       // for keys, and as many for values
-constexpr int kTcThreads = 32 * (kDecodeFirst + 2 * kDecodeWarps);
-constexpr int kSoftThreads = 32 * kSoftWarps;
-// Registers: 28 warps launch with 72 a thread; the softmax takes 88, the
-// decoders keep 56 and the issuers 40: 16 x 88 + 8 x 56 + 4 x 40 = 28 x 72.
-constexpr int kSoftRegs = 88, kDecodeRegs = 56, kIssueRegs = 40;
-static_assert(kSoftWarps * kSoftRegs + 2 * kDecodeWarps * kDecodeRegs + kSoftFirst * kIssueRegs <=
-                  kTcThreads / 32 * 72,
-              "register split");
+constexpr int kDecodeWarps = 4;       // of one set, for keys, and as many for values
+constexpr int kTcThreads = 32 * 28;
+// Registers: 28 warps launch with 72 a thread; sixteen softmax warps take 88
+// (eight: 120), the decoders keep 56 and the issuers 40.
+constexpr int kDecodeRegs = 56, kIssueRegs = 40;
 constexpr int kOps = 3;               // decoded K tiles (TMEM), decoded V tiles (shared memory)
 
 template <int D, int N>
 struct Kv4Tc {
+  // 32 and 64 rows: the softmax bounds, so two groups share a tile's rows; 16:
+  // the decoding does, and two sets of decoders take turns.  (32 heads x 8
+  // requests behind 8192: 16 rows 84 -> 76 us with two sets; 32 rows 92 us with
+  // two softmax groups, 100 us with two sets.)
+  static constexpr int kHalves = N == 16 ? 1 : 2;
+  static constexpr int kSets = N == 16 ? 2 : 1;
+  static constexpr int kSoftWarps = 8 * kHalves, kSoftThreads = 32 * kSoftWarps;
+  static constexpr int kDecodeFirst = kSoftFirst + kSoftWarps;
+  static constexpr int kSoftRegs = kHalves == 2 ? 88 : 120;
+  static_assert(kDecodeFirst + 2 * kSets * kDecodeWarps == kTcThreads / 32, "warps");
+  static_assert(kSoftWarps * kSoftRegs + 2 * kSets * kDecodeWarps * kDecodeRegs + kSoftFirst * kIssueRegs <=
+                    kTcThreads / 32 * 72,
+                "register split");
   static constexpr int R = kv4_record_bytes(D);
   static constexpr int kBoxes = D / 64;
   static constexpr int kBoxBytes = kTile * 128;             // 128 rows of 64 halves
@@ -69,7 +77,7 @@ struct Kv4Tc {
   static constexpr int kOffQ = kOffP + 2 * kPBytes;
   static constexpr int kOffRaw = kOffQ + kQBytes;
   static constexpr int kSmem = kOffRaw + kRaw * kRawBytes + 1024;
-  static constexpr int kRowsPer = N / 2;                    // rows of one softmax thread
+  static constexpr int kRowsPer = N / kHalves;              // rows of one softmax thread
   // TMEM: S^T and O^T of even and odd tiles, K tiles (a pair of dims per column)
   static constexpr uint32_t kColO = 2 * N;
   static constexpr uint32_t kColK = 4 * N;
@@ -86,7 +94,8 @@ template <int D, int N>
 __global__ void __launch_bounds__(kTcThreads, 1)
 tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
   using C = Kv4Tc<D, N>;
-  constexpr int R = C::R, RP = C::kRowsPer, kRaw = C::kRaw;
+  constexpr int R = C::R, RP = C::kRowsPer, kRaw = C::kRaw, kSets = C::kSets;
+  constexpr int kSoftWarps = C::kSoftWarps, kSoftThreads = C::kSoftThreads, kDecodeFirst = C::kDecodeFirst;
   const AttnArgs &a = p.a;
   extern __shared__ uint8_t smem_raw[];
   __shared__ struct {
@@ -279,6 +288,7 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
   } else if (warp >= kDecodeFirst) {
     // ------------------------------------------------------------ decode
     give_registers<kDecodeRegs>();
+    const int set = ((warp - kDecodeFirst) / kDecodeWarps) % kSets;
     auto decode = [&](auto of_v) {
       constexpr bool kV = decltype(of_v)::value;
       const int key = (warp & 3) * 32 + lane;               // and the warp's TMEM lanes
@@ -293,8 +303,10 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
       Ring<kRaw> raw;
       Ring<kOps> op;
       op.phase = 1;
+      int turn_of = 0;           // the set whose tile the rings are at
       turns([&](int) {
-        for (int i = 0; i < ntiles; ++i, raw.next(), op.next()) {
+        for (int i = 0; i < ntiles; ++i, raw.next(), op.next(), turn_of ^= kSets - 1) {
+          if (turn_of != set) continue;
           ok = ok && mbar_sleep(raw_full + 8 * raw.at, raw.phase);
           const KeyCodes<D> key_codes(rec0 + raw.at * C::kRawBytes, kV, tiles.key0(t0 + i) < keys_left);
           ok = ok && mbar_sleep(empty + 8 * op.at, op.phase);
@@ -321,17 +333,17 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
         }
       }, wait_merge);
     };
-    if (warp >= kDecodeFirst + kDecodeWarps) decode(std::true_type{});
+    if (warp >= kDecodeFirst + kSets * kDecodeWarps) decode(std::true_type{});
     else decode(std::false_type{});
   } else {
     // ------------------------------------------------------------ softmax
-    // Four groups of four warps: two for even tiles and two for odd ones (the
-    // chain S^T, weights, product of one tile then runs beside that of the
-    // next), each with half of the rows.  The parities keep references, sums
-    // and O^T of their own, merged at the end like splits of the keys.
-    take_registers<kSoftRegs>();
-    const int w = warp - kSoftFirst, quad = warp & 3, half = (w >> 2) & 1, par = w >> 3;
-    const int soft = tid - 32 * kSoftFirst;            // 0 .. 511
+    // Groups of four warps: one or two (each with half of the rows) for even
+    // tiles and as many for odd ones, so that the chain S^T, weights, product of
+    // one tile runs beside that of the next.  The parities keep references,
+    // sums and O^T of their own, merged at the end like splits of the keys.
+    take_registers<C::kSoftRegs>();
+    const int w = warp - kSoftFirst, quad = warp & 3, half = (w >> 2) % C::kHalves, par = w / (4 * C::kHalves);
+    const int soft = tid - 32 * kSoftFirst;            // 0 .. kSoftThreads - 1
     const int r0 = half * RP, group = 2 + (w >> 2);    // first row; named barrier of the group
     const int key_lane = quad * 32 + lane;             // key of a tile, and TMEM lane
     // this key's row of P, swizzled over its 128, 64 or 32 bytes
