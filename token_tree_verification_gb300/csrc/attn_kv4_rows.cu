@@ -4,8 +4,8 @@
 //
 // With that many rows the products are bound by the softmax and the decoding,
 // not by what a row costs the tensor cores, so the rows lie along M here:
-//   S[rows][keys] = Q K^T   A = Q (shared memory),  B = K (keys x dims, shared memory, K-major)
-//   O[rows][dims] = P V     A = P (TMEM),           B = V (keys x dims, shared memory, MN-major)
+//   S[rows][keys] = Q K^T   A = Q (TMEM),  B = K (keys x dims, shared memory, K-major)
+//   O[rows][dims] = P V     A = P (TMEM),  B = V (keys x dims, shared memory, MN-major)
 // A softmax thread then has one row, whose reference, sum and factor are
 // registers, and its weights go to TMEM as they are; decoded records serve 128
 // rows instead of 64.  (attn_kv4_tc.cu has the form for fewer rows, where the
@@ -14,8 +14,8 @@
 // One CTA = one split of the keys x one block of 128 rows x one (request, KV
 // head).  Warp roles:
 //   warp 0      brings tiles of 128 records, one bulk copy each
-//   warp 1      allocates TMEM and issues S_i, the two halves of its keys apart
-//   warp 2      issues O += P_i V_i, the halves apart
+//   warp 1      allocates TMEM and issues S_i
+//   warp 2      issues O += P_i V_i, the two halves of the tile's keys apart
 //   warps 4-19  softmax: the four warps of a TMEM lane quarter hold the same 32
 //               rows, each 32 of the tile's 128 keys.  The two warps of a half of
 //               the keys share references, sums and an O of their own, merged at
@@ -24,6 +24,10 @@
 //   warps 20-23 decode keys, warps 24-27 values (one key per lane: loads of
 //               records 36 words apart and swizzled stores of rows 128 bytes
 //               apart are both free of bank conflicts)
+// What passes through shared memory comes next to the softmax in cost: 36 KB of
+// records in and out, 64 KB of decoded operands in and 64 KB out per tile, 1300
+// cycles at 128 bytes each.  (Q as a shared-memory operand, read for each half
+// of the keys, added 64 KB.)
 #include <type_traits>
 
 #include "attn_kv4_tc.cuh"
@@ -45,14 +49,13 @@ template <int D>
 struct Kv4Rows128 {
   static constexpr int R = kv4_record_bytes(D);
   static constexpr int kBoxes = D / 64;
-  static constexpr int kBoxBytes = kTile * 128;             // 128 rows of 64 halves: Q, K and V alike
+  static constexpr int kBoxBytes = kTile * 128;             // 128 rows of 64 halves, K and V alike
   static constexpr int kOpBytes = kBoxes * kBoxBytes;
-  static constexpr int kRaw = D == 128 ? 3 : 5;             // stages of records
+  static constexpr int kRaw = 4;                            // stages of records
   static constexpr int kRawBytes = kTile * R;
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kOffK + 2 * kOpBytes;
-  static constexpr int kOffQ = kOffV + 2 * kOpBytes;
-  static constexpr int kOffRaw = kOffQ + kOpBytes;
+  static constexpr int kOffRaw = kOffV + 2 * kOpBytes;
   // after the loop: the rows of both halves, the ones received, and their
   // references and sums
   static constexpr int kOffRecv = 2 * kRows * (D + 4) * 4;
@@ -60,8 +63,8 @@ struct Kv4Rows128 {
   static constexpr int kEnd = kOffRaw + kRaw * kRawBytes;
   static constexpr int kMerge = kOffMl + kMaxSplits * kRows * 8;
   static constexpr int kSmem = (kEnd > kMerge ? kEnd : kMerge) + 1024;
-  // TMEM: S and O of both halves, two P buffers (a pair of keys per column)
-  static constexpr uint32_t kColO = kTile, kColP = kColO + 256, kTmemCols = 512;
+  // TMEM: S, O of both halves, P (a pair of keys per column), Q (a pair of dims)
+  static constexpr uint32_t kColO = kTile, kColP = kColO + 256, kColQ = kColP + kTile / 2, kTmemCols = 512;
   static_assert(kSmem <= 227 * 1024 - 8192, "shared memory budget");
 };
 
@@ -91,14 +94,13 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
   __shared__ struct {
     uint64_t raw_full[kRaw], raw_empty[kRaw];
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t s_full[2], s_empty[2], p_full[2][2], o_done[2][2], q_full;     // [half], [half][tile parity]
+    uint64_t s_full, s_empty[2], p_full[2], o_done[2], q_full;     // [half of the keys]
   } bars;
   __shared__ uint32_t s_tmem;
   __shared__ int s_timeout;
   __shared__ int s_par[SPEC_MAX_TREE_NODES];
   __shared__ long long s_row[kRows];            // a row's first element of q and o
-  __shared__ float s_c[kRows];                // a row's score factor
-  __shared__ float s_max[2][4][kRows];        // [tile parity][key part][row]
+  __shared__ float s_max[2][4][kRows];        // [tile parity][part][row]
   __shared__ float s_ref[2][kRows], s_sum[2][kRows];
 
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -106,7 +108,7 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
   const uint32_t sb = smem_addr(smem);
   float2 (*s_ml)[kRows] = reinterpret_cast<float2 (*)[kRows]>(smem + C::kOffMl);
   const uint32_t raw_full = smem_addr(bars.raw_full), raw_empty = smem_addr(bars.raw_empty);
-  const uint32_t s_full = smem_addr(bars.s_full), s_empty = smem_addr(bars.s_empty);
+  const uint32_t s_full = smem_addr(&bars.s_full), s_empty = smem_addr(bars.s_empty);
   const uint32_t p_full = smem_addr(bars.p_full), o_done = smem_addr(bars.o_done);
   const int CS = static_cast<int>(gridDim.x), split = static_cast<int>(blockIdx.x);
   const int b = blockIdx.z / a.Hkv, g_kv = blockIdx.z % a.Hkv;
@@ -123,13 +125,11 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
       mbar_init(&bars.v_full[s], kDecodeWarps);
       mbar_init(&bars.k_empty[s], 1);
       mbar_init(&bars.v_empty[s], 1);
-      mbar_init(&bars.s_full[s], 1);
       mbar_init(&bars.s_empty[s], kSoftWarps / 2);
-      for (int q = 0; q < 2; ++q) {
-        mbar_init(&bars.p_full[s][q], kSoftWarps / 2);
-        mbar_init(&bars.o_done[s][q], 1);
-      }
+      mbar_init(&bars.p_full[s], kSoftWarps / 2);
+      mbar_init(&bars.o_done[s], 1);
     }
+    mbar_init(&bars.s_full, 1);
     mbar_init(&bars.q_full, kSoftWarps);
     fence_barrier_init();
     s_timeout = 0;
@@ -208,35 +208,31 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
     }, wait_merge);
   } else if (warp == 1) {
     // ------------------------------------------------------------ S = Q K^T
-    constexpr uint32_t id = tc::idesc_f16_f32(kRows, kTile / 2, 0, 0);
-    const uint64_t qd0 = tc::smem_desc_sw128(sb + C::kOffQ, 16, 1024);
+    constexpr uint32_t id = tc::idesc_f16_f32(kRows, kTile, 0, 0);
     const uint64_t kd0 = tc::smem_desc_sw128(sb + C::kOffK, 16, 1024);
     const uint32_t k_full = smem_addr(bars.k_full);
     Ring<2> kr;
-    uint32_t phase = 0;        // of the S buffers: one per half
+    uint32_t phase = 1;        // of the S buffer: free at first
     uint32_t q_phase = 0;
     turns([&](int) {
       if (ntiles == 0) return;
       ok = mbar_sleep(smem_addr(&bars.q_full), q_phase);
       q_phase ^= 1;
       for (int i = 0; i < ntiles && ok; ++i, kr.next(), phase ^= 1) {
-        ok = mbar_sleep(k_full + 8 * kr.at, kr.phase);
-        for (int half = 0; half < 2 && ok; ++half) {
-          ok = mbar_sleep(s_empty + 8 * half, phase ^ 1);
-          if (!ok) break;
-          tc::fence_after_sync();
-          const uint64_t kd = kd0 + static_cast<uint64_t>((kr.at * C::kOpBytes + half * (kTile / 2 * 128)) >> 4);
-          if (tc::elect_one()) {
+        ok = mbar_sleep(k_full + 8 * kr.at, kr.phase) && mbar_sleep(s_empty, phase) && mbar_sleep(s_empty + 8, phase);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint64_t kd = kd0 + static_cast<uint64_t>(kr.at * C::kOpBytes >> 4);
+        if (tc::elect_one()) {
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-              const uint32_t at = ((ks >> 2) * C::kBoxBytes + (ks & 3) * 32) >> 4;
-              tc::mma_bf16(tmem + half * (kTile / 2), qd0 + at, kd + at, id, ks > 0);
-            }
-            tc::commit(&bars.s_full[half]);
-            if (half) tc::commit(&bars.k_empty[kr.at]);
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t at = ((ks >> 2) * C::kBoxBytes + (ks & 3) * 32) >> 4;
+            tc::mma_bf16_ts(tmem, tmem + C::kColQ + ks * 8, kd + at, id, ks > 0);
           }
-          __syncwarp();
+          tc::commit(&bars.s_full);
+          tc::commit(&bars.k_empty[kr.at]);
         }
+        __syncwarp();
       }
     }, wait_merge);
   } else if (warp == 2) {
@@ -245,20 +241,21 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
     const uint64_t vd0 = tc::smem_desc_sw128(sb + C::kOffV, C::kBoxBytes, 1024);
     const uint32_t v_full = smem_addr(bars.v_full);
     Ring<2> vr;
+    uint32_t phase = 0;        // of P
     turns([&](int) {
-      for (int i = 0; i < ntiles && ok; ++i, vr.next()) {
+      for (int i = 0; i < ntiles && ok; ++i, vr.next(), phase ^= 1) {
         ok = mbar_sleep(v_full + 8 * vr.at, vr.phase);
         for (int half = 0; half < 2 && ok; ++half) {
-          ok = mbar_sleep(p_full + 16 * half + 8 * vr.at, vr.phase);
+          ok = mbar_sleep(p_full + 8 * half, phase);
           if (!ok) break;
           tc::fence_after_sync();
           const uint64_t vd = vd0 + static_cast<uint64_t>((vr.at * C::kOpBytes + half * (kTile / 2 * 128)) >> 4);
-          const uint32_t pt = tmem + C::kColP + vr.at * (kTile / 2) + half * (kTile / 4);
+          const uint32_t pt = tmem + C::kColP + half * (kTile / 4);
           if (tc::elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kTile / 32; ++kk)
               tc::mma_bf16_ts(tmem + C::kColO + half * 128, pt + kk * 8, vd + (kk * 16 * 128 >> 4), id, (i | kk) != 0);
-            tc::commit(&bars.o_done[half][vr.at]);
+            tc::commit(&bars.o_done[half]);
             if (half) tc::commit(&bars.v_empty[vr.at]);
           }
           __syncwarp();
@@ -303,66 +300,54 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
     const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t s_col = trow + part * kPart, o_col = trow + C::kColO + half * 128 + sub * (D / 2);
     const uint32_t p_col = trow + C::kColP + part * (kPart / 2);
-    const uint32_t s_full_h = s_full + 8 * half, s_empty_h = s_empty + 8 * half;
-    const uint32_t p_full_h = p_full + 16 * half, o_done_h = o_done + 16 * half;
-    Ring<2> sr;              // P's buffers, and the parity of the tile
-    uint32_t phase = 0;      // of the half's S
+    const uint32_t s_empty_h = s_empty + 8 * half, p_full_h = p_full + 8 * half, o_done_h = o_done + 8 * half;
+    uint32_t phase = 0;      // of S, P and the products: flips with every tile
     float sum = 0.f, ref = -INFINITY;
     turns([&](int row0) {
       const int rows_here = min(kRows, rows_total - row0);
       const bool live = row < rows_here;
-      // ---- Q as halves: 8 dims of a row per thread and round; every load of
-      //      the set-up is under way before the first is used
-      constexpr int kPieces = D / 8, kRounds = kRows * kPieces / kSoftThreads;
-      uint4 x4[kRounds], m = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-      for (int rr = 0; rr < kRounds; ++rr) {
-        const int idx = rr * kSoftThreads + soft, r = idx / kPieces, c = idx % kPieces;
-        x4[rr] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows_here && in_bounds(G.lo + (row0 + r) / a.G, a.T, a.status, b))
-          x4[rr] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
-                                                         (static_cast<size_t>(G.lo + (row0 + r) / a.G) * a.Hq +
-                                                          g_kv * a.G + (row0 + r) % a.G) *
-                                                             D) +
-                         c);
-      }
+      // ---- Q as halves: this thread's row, a quarter of its dims.  Every load
+      //      of the set-up is under way before the first is used.
       const int node = (row0 + row) / a.G;
+      const bool mine = live && in_bounds(G.lo + node, a.T, a.status, b);
+      const long long first = (static_cast<long long>(G.lo + node) * a.Hq + g_kv * a.G + (row0 + row) - node * a.G) * D;
+      const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + first + part * (D / 4));
+      uint4 x4[D / 32], m = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) x4[c] = mine ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
       if (a.mask) {
-        if (live && in_bounds(G.lo + node, a.T, a.status, b)) m = __ldg(a.mask + G.lo + node);
+        if (mine) m = __ldg(a.mask + G.lo + node);
       } else if (row0 == static_cast<int>(blockIdx.y) * kRows) {
         for (int i = soft; i < G.n; i += kSoftThreads)
           s_par[i] = in_bounds(G.lo + i, a.T, a.status, b) ? __ldg(a.parents + G.lo + i) : -2;
       }
+      if (part == 0) s_row[row] = mine ? first : -1;
+      float top = 0.f;
 #pragma unroll
-      for (int rr = 0; rr < kRounds; ++rr) {
-        const int idx = rr * kSoftThreads + soft, r = idx / kPieces, c = idx % kPieces;
-        const uint32_t u[4] = {x4[rr].x, x4[rr].y, x4[rr].z, x4[rr].w};
-        float top = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xFFFF0000u))));
-#pragma unroll
-        for (int k = 1; k < kPieces; k *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-        const int up = row_exponent(top);
-        const float grow = power_of_two(up);
-        uint32_t h[4];
+      for (int c = 0; c < D / 32; ++c) {
+        const uint32_t u[4] = {x4[c].x, x4[c].y, x4[c].z, x4[c].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          h[e] = pack_half2(__uint_as_float(u[e] << 16) * grow, __uint_as_float(u[e] & 0xFFFF0000u) * grow);
-        st_shared_v4(sb + C::kOffQ + (c >> 3) * C::kBoxBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4), h[0], h[1], h[2],
-                     h[3]);
-        if (c == 0) {
-          const int node_r = (row0 + r) / a.G;
-          s_c[r] = a.scale_log2 * power_of_two(-up);
-          s_row[r] = r < rows_here && in_bounds(G.lo + node_r, a.T, a.status, b)
-                         ? (static_cast<long long>(G.lo + node_r) * a.Hq + g_kv * a.G + (row0 + r) - node_r * a.G) * D
-                         : -1;
-        }
+          top = max3(top, fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xFFFF0000u)));
       }
-      fence_proxy_async_smem();
+      s_max[0][part][row] = top;
+      named_bar_sync(1, kSoftThreads);
+      const int up = row_exponent(fmaxf(fmaxf(s_max[0][0][row], s_max[0][1][row]), fmaxf(s_max[0][2][row], s_max[0][3][row])));
+      const float grow = power_of_two(up), c = a.scale_log2 * power_of_two(-up);
+#pragma unroll
+      for (int q = 0; q < D / 64; ++q) {
+        uint32_t h[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t u = (&x4[2 * q + (e >> 2)].x)[e & 3];
+          h[e] = pack_half2(__uint_as_float(u << 16) * grow, __uint_as_float(u & 0xFFFF0000u) * grow);
+        }
+        tc::st8(trow + C::kColQ + part * (D / 8) + 8 * q, h);
+      }
+      tc::wait_st();
+      tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive_at(smem_addr(&bars.q_full));
-      named_bar_sync(1, kSoftThreads);
       // ---- what this thread's row sees
       if (a.mask) {
         m = clip_mask(m, G.n);
@@ -372,14 +357,13 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
         if (bad) report(a.status, b, SPEC_ERR_BAD_PARENT);
       }
       const RowKeys see = row_keys(m, G.L, p.window, p.sinks);
-      const float c = s_c[row];
       ref = live ? -INFINITY : 0.f;           // rows of no node need no reference
       sum = 0.f;
       float shift = kWeightLog2;               // 8 - reference (8 while there is none)
 
-      for (int i = 0; i < ntiles; ++i, sr.next(), phase ^= 1) {
+      for (int i = 0; i < ntiles; ++i, phase ^= 1) {
         const int key0 = tiles.key0(t0 + i), k0 = key0 + part * kPart;
-        ok = ok && mbar_sleep(s_full_h, phase);
+        ok = ok && mbar_sleep(s_full, phase);
         __syncwarp();
         tc::fence_after_sync();
         float x[kPart];
@@ -398,12 +382,12 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
             if (!((sees >> j) & 1u)) x[j] = -INFINITY;
         }
         const float most = max_of(x);
-        s_max[sr.at][part][row] = most;
+        s_max[phase][part][row] = most;
         const bool fresh = ref == -INFINITY;
         // the barrier makes both warps' maxima visible, and says whether any of
         // their rows moves its reference
         if (named_bar_or(group, 64, fresh ? most > -INFINITY : most > kWeightLog2 + kMoveLog2)) {
-          const float mx = fmaxf(s_max[sr.at][2 * half][row], s_max[sr.at][2 * half + 1][row]);
+          const float mx = fmaxf(s_max[phase][2 * half][row], s_max[phase][2 * half + 1][row]);
           float factor = 1.f, by = 0.f;
           if (mx > (fresh ? -INFINITY : kWeightLog2 + kMoveLog2)) {
             by = ceilf(mx - kWeightLog2);
@@ -413,7 +397,7 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
           }
           if (i > 0) {
             // O holds the products of this turn's earlier tiles
-            ok = ok && mbar_sleep(o_done_h + 8 * (sr.at ^ 1), sr.phase ^ sr.at ^ 1);
+            ok = ok && mbar_sleep(o_done_h, phase ^ 1);
             __syncwarp();
             tc::fence_after_sync();
 #pragma unroll
@@ -431,8 +415,8 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
 #pragma unroll
           for (int j = 0; j < kPart; ++j) x[j] -= by;
         }
-        // ---- weights; P's buffer is free once the product two tiles back is done
-        const bool room = mbar_over(o_done_h + 8 * sr.at, sr.phase ^ 1);
+        // ---- weights; their place is free once the last tile's product is done
+        const bool room = mbar_over(o_done_h, phase ^ 1);
 #pragma unroll
         for (int j = 0; j < kPart; ++j) x[j] = fast_exp2(x[j]);
         float s0 = x[0], s1 = x[1], s2 = x[2], s3 = x[3];
@@ -443,7 +427,7 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
         }
         add2(s0, s1, s2, s3);
         sum += s0 + s1;
-        ok = ok && (room || mbar_sleep(o_done_h + 8 * sr.at, sr.phase ^ 1));
+        ok = ok && (room || mbar_sleep(o_done_h, phase ^ 1));
         __syncwarp();
         tc::fence_after_sync();
 #pragma unroll
@@ -451,16 +435,16 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
           uint32_t h[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) h[e] = pack_half2(x[16 * q + 2 * e], x[16 * q + 2 * e + 1]);
-          tc::st8(p_col + sr.at * (kTile / 2) + 8 * q, h);
+          tc::st8(p_col + 8 * q, h);
         }
         tc::wait_st();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive_at(p_full_h + 8 * sr.at);
+        if (lane == 0) mbar_arrive_at(p_full_h);
       }
       // ---- the block's rows out of TMEM.  Their place in shared memory is free
       //      once the last product is done.
-      if (ntiles > 0) ok = ok && mbar_sleep(o_done_h + 8 * (sr.at ^ 1), sr.phase ^ sr.at ^ 1);
+      if (ntiles > 0) ok = ok && mbar_sleep(o_done_h, phase ^ 1);
       if (CS > 1) cluster_arrive_relaxed();
       __syncwarp();
       tc::fence_after_sync();
