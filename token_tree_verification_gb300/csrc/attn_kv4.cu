@@ -538,12 +538,16 @@ int attn_few(const Kv4AttnArgs &p, int max_prefix, void *stream) {
 }
 
 // Which bf16 kernel: by the mean number of rows on each key (a request with
-// more takes more turns).
+// more takes more turns).  Measured, 32 heads x 8 requests behind 8192: 8 rows
+// take 59 us in mma.sync and 75 us on tcgen05 with the rows along N, 9 rows 75
+// us there; 32 rows 94 us along N and 149 us along M; 64 rows 138 us along N (in
+// a form for 64) and 144 us along M, but one such tree behind 2048 15.4 and
+// 14.5 us, so that form was dropped.
 template <int D>
 int attn_bf16(const Kv4AttnArgs &p, int max_prefix, void *stream) {
   const int rows = mean_nodes(p.a) * p.a.G;
   if (rows <= 8) return attn_few<D, false>(p, max_prefix, stream);
-  return rows <= 64 ? launch_kv4_tc(p, max_prefix, stream) : launch_kv4_rows(p, max_prefix, stream);
+  return rows <= 32 ? launch_kv4_tc(p, max_prefix, stream) : launch_kv4_rows(p, max_prefix, stream);
 }
 
 }  // namespace

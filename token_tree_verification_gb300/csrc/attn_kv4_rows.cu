@@ -14,8 +14,8 @@
 // One CTA = one split of the keys x one block of 128 rows x one (request, KV
 // head).  Warp roles:
 //   warp 0      brings tiles of 128 records, one bulk copy each
-//   warp 1      allocates TMEM and issues S_i
-//   warp 2      issues O += P_i V_i, the two halves of the tile's keys apart
+//   warp 1      allocates TMEM and issues S_i, the two halves of the tile's keys apart
+//   warp 2      issues O += P_i V_i, the halves apart
 //   warps 4-19  softmax: the four warps of a TMEM lane quarter hold the same 32
 //               rows, each 32 of the tile's 128 keys.  The two warps of a half of
 //               the keys share references, sums and an O of their own, merged at
@@ -51,7 +51,7 @@ struct Kv4Rows128 {
   static constexpr int kBoxes = D / 64;
   static constexpr int kBoxBytes = kTile * 128;             // 128 rows of 64 halves, K and V alike
   static constexpr int kOpBytes = kBoxes * kBoxBytes;
-  static constexpr int kRaw = 4;                            // stages of records
+  static constexpr int kRaw = 3;                            // stages of records
   static constexpr int kRawBytes = kTile * R;
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kOffK + 2 * kOpBytes;
@@ -94,7 +94,7 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
   __shared__ struct {
     uint64_t raw_full[kRaw], raw_empty[kRaw];
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t s_full, s_empty[2], p_full[2], o_done[2], q_full;     // [half of the keys]
+    uint64_t s_full[2], s_empty[2], p_full[2], o_done[2], q_full;     // [half of the keys]
   } bars;
   __shared__ uint32_t s_tmem;
   __shared__ int s_timeout;
@@ -108,7 +108,7 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
   const uint32_t sb = smem_addr(smem);
   float2 (*s_ml)[kRows] = reinterpret_cast<float2 (*)[kRows]>(smem + C::kOffMl);
   const uint32_t raw_full = smem_addr(bars.raw_full), raw_empty = smem_addr(bars.raw_empty);
-  const uint32_t s_full = smem_addr(&bars.s_full), s_empty = smem_addr(bars.s_empty);
+  const uint32_t s_full = smem_addr(bars.s_full), s_empty = smem_addr(bars.s_empty);
   const uint32_t p_full = smem_addr(bars.p_full), o_done = smem_addr(bars.o_done);
   const int CS = static_cast<int>(gridDim.x), split = static_cast<int>(blockIdx.x);
   const int b = blockIdx.z / a.Hkv, g_kv = blockIdx.z % a.Hkv;
@@ -125,11 +125,11 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
       mbar_init(&bars.v_full[s], kDecodeWarps);
       mbar_init(&bars.k_empty[s], 1);
       mbar_init(&bars.v_empty[s], 1);
+      mbar_init(&bars.s_full[s], 1);
       mbar_init(&bars.s_empty[s], kSoftWarps / 2);
       mbar_init(&bars.p_full[s], kSoftWarps / 2);
       mbar_init(&bars.o_done[s], 1);
     }
-    mbar_init(&bars.s_full, 1);
     mbar_init(&bars.q_full, kSoftWarps);
     fence_barrier_init();
     s_timeout = 0;
@@ -208,7 +208,7 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
     }, wait_merge);
   } else if (warp == 1) {
     // ------------------------------------------------------------ S = Q K^T
-    constexpr uint32_t id = tc::idesc_f16_f32(kRows, kTile, 0, 0);
+    constexpr uint32_t id = tc::idesc_f16_f32(kRows, kTile / 2, 0, 0);
     const uint64_t kd0 = tc::smem_desc_sw128(sb + C::kOffK, 16, 1024);
     const uint32_t k_full = smem_addr(bars.k_full);
     Ring<2> kr;
@@ -219,20 +219,23 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
       ok = mbar_sleep(smem_addr(&bars.q_full), q_phase);
       q_phase ^= 1;
       for (int i = 0; i < ntiles && ok; ++i, kr.next(), phase ^= 1) {
-        ok = mbar_sleep(k_full + 8 * kr.at, kr.phase) && mbar_sleep(s_empty, phase) && mbar_sleep(s_empty + 8, phase);
-        if (!ok) break;
-        tc::fence_after_sync();
-        const uint64_t kd = kd0 + static_cast<uint64_t>(kr.at * C::kOpBytes >> 4);
-        if (tc::elect_one()) {
+        ok = mbar_sleep(k_full + 8 * kr.at, kr.phase);
+        for (int half = 0; half < 2 && ok; ++half) {
+          ok = mbar_sleep(s_empty + 8 * half, phase);
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint64_t kd = kd0 + static_cast<uint64_t>((kr.at * C::kOpBytes + half * (kTile / 2 * 128)) >> 4);
+          if (tc::elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t at = ((ks >> 2) * C::kBoxBytes + (ks & 3) * 32) >> 4;
-            tc::mma_bf16_ts(tmem, tmem + C::kColQ + ks * 8, kd + at, id, ks > 0);
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t at = ((ks >> 2) * C::kBoxBytes + (ks & 3) * 32) >> 4;
+              tc::mma_bf16_ts(tmem + half * (kTile / 2), tmem + C::kColQ + ks * 8, kd + at, id, ks > 0);
+            }
+            tc::commit(&bars.s_full[half]);
+            if (half) tc::commit(&bars.k_empty[kr.at]);
           }
-          tc::commit(&bars.s_full);
-          tc::commit(&bars.k_empty[kr.at]);
+          __syncwarp();
         }
-        __syncwarp();
       }
     }, wait_merge);
   } else if (warp == 2) {
@@ -300,7 +303,8 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
     const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t s_col = trow + part * kPart, o_col = trow + C::kColO + half * 128 + sub * (D / 2);
     const uint32_t p_col = trow + C::kColP + part * (kPart / 2);
-    const uint32_t s_empty_h = s_empty + 8 * half, p_full_h = p_full + 8 * half, o_done_h = o_done + 8 * half;
+    const uint32_t s_full_h = s_full + 8 * half, s_empty_h = s_empty + 8 * half, p_full_h = p_full + 8 * half,
+                   o_done_h = o_done + 8 * half;
     uint32_t phase = 0;      // of S, P and the products: flips with every tile
     float sum = 0.f, ref = -INFINITY;
     turns([&](int row0) {
@@ -363,7 +367,7 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
 
       for (int i = 0; i < ntiles; ++i, phase ^= 1) {
         const int key0 = tiles.key0(t0 + i), k0 = key0 + part * kPart;
-        ok = ok && mbar_sleep(s_full, phase);
+        ok = ok && mbar_sleep(s_full_h, phase);
         __syncwarp();
         tc::fence_after_sync();
         float x[kPart];

@@ -49,10 +49,10 @@ constexpr int kOps = 3;               // decoded K tiles (TMEM), decoded V tiles
 
 template <int D, int N>
 struct Kv4Tc {
-  // 32 and 64 rows: the softmax bounds, so two groups share a tile's rows; 16:
-  // the decoding does, and two sets of decoders take turns.  (32 heads x 8
-  // requests behind 8192: 16 rows 84 -> 76 us with two sets; 32 rows 92 us with
-  // two softmax groups, 100 us with two sets.)
+  // 32 rows: the softmax bounds, so two groups share a tile's rows; 16: the
+  // decoding does, and two sets of decoders take turns.  (32 heads x 8 requests
+  // behind 8192: 16 rows 84 -> 76 us with two sets; 32 rows 92 us with two
+  // softmax groups, 100 us with two sets.)
   static constexpr int kHalves = N == 16 ? 1 : 2;
   static constexpr int kSets = N == 16 ? 2 : 1;
   static constexpr int kSoftWarps = 8 * kHalves, kSoftThreads = 32 * kSoftWarps;
@@ -71,7 +71,7 @@ struct Kv4Tc {
   static constexpr int kPPitch = N * 2;                     // a key's weights: their own swizzle width
   static constexpr int kPBytes = kTile * kPPitch;
   static constexpr int kRawBytes = kTile * R;
-  static constexpr int kRaw = N == 64 ? 3 : 5;              // stages of records, as many as fit
+  static constexpr int kRaw = 5;                            // stages of records
   static constexpr int kOffV = 0;
   static constexpr int kOffP = kOffV + kOps * kOpBytes;
   static constexpr int kOffQ = kOffP + 2 * kPBytes;
@@ -346,8 +346,8 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
     const int soft = tid - 32 * kSoftFirst;            // 0 .. kSoftThreads - 1
     const int r0 = half * RP, group = 2 + (w >> 2);    // first row; named barrier of the group
     const int key_lane = quad * 32 + lane;             // key of a tile, and TMEM lane
-    // this key's row of P, swizzled over its 128, 64 or 32 bytes
-    const int swz = N == 64 ? key_lane & 7 : N == 32 ? (key_lane >> 1) & 3 : (key_lane >> 2) & 1;
+    // this key's row of P, swizzled over its 64 or 32 bytes
+    const int swz = N == 32 ? (key_lane >> 1) & 3 : (key_lane >> 2) & 1;
     const uint32_t prow =
         sb + C::kOffP + par * C::kPBytes + key_lane * C::kPPitch + (((half * (RP / 8)) ^ swz) << 4);
     const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
@@ -592,9 +592,7 @@ int launch_tc(const Kv4AttnArgs &p, int max_prefix, void *stream) {
 template <int D>
 int by_rows(const Kv4AttnArgs &p, int max_prefix, void *stream) {
   const int rows = mean_nodes(p.a) * p.a.G;
-  if (rows <= 16) return launch_tc<D, 16>(p, max_prefix, stream);
-  if (rows <= 32) return launch_tc<D, 32>(p, max_prefix, stream);
-  return launch_tc<D, 64>(p, max_prefix, stream);
+  return rows <= 16 ? launch_tc<D, 16>(p, max_prefix, stream) : launch_tc<D, 32>(p, max_prefix, stream);
 }
 
 }  // namespace

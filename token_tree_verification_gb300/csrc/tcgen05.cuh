@@ -55,13 +55,13 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
   return d;
 }
 
-// An MN-major operand of 64, 32 or 16 16-bit elements along M/N, rows of K
-// packed one after another and swizzled over their own width (128, 64 or 32
-// bytes: layouts 2, 4 and 6); the stride offset is that of 8 rows.
+// An MN-major operand of 32 or 16 16-bit elements along M/N, rows of K packed
+// one after another and swizzled over their own width (64 or 32 bytes: layouts
+// 4 and 6); the stride offset is that of 8 rows.
 template <int N>
 __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
-  static_assert(N == 64 || N == 32 || N == 16, "one swizzle atom wide");
-  constexpr uint64_t layout = N == 64 ? 2 : N == 32 ? 4 : 6;
+  static_assert(N == 32 || N == 16, "one swizzle atom wide");
+  constexpr uint64_t layout = N == 32 ? 4 : 6;
   return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>(1) << 16 |
          static_cast<uint64_t>(8 * N * 2 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | layout << 61;
 }
