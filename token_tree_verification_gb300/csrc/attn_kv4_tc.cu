@@ -108,6 +108,7 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
   __shared__ int s_par[SPEC_MAX_TREE_NODES];
   __shared__ long long s_row[N];            // a row's first element of q and o
   __shared__ uint4 s_tree[N];
+  __shared__ uint32_t s_sees[SPEC_MAX_TREE_NODES];     // the rows that see a tree node, as bits
   __shared__ int s_first[N];
   __shared__ __align__(16) float s_c[N];           // a row's score factor
   // per parity of the tiles: 8 - the row's reference, the last move of it
@@ -427,6 +428,13 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
         }
       }
       named_bar_sync(1, kSoftThreads);
+      // the rows' sets turned round, a word of rows for every node
+      for (int u = w; u < G.n; u += kSoftWarps) {
+        const bool sees = lane < N && (reinterpret_cast<const uint32_t *>(&s_tree[lane % N])[u >> 5] >> (u & 31)) & 1u;
+        const uint32_t rows = __ballot_sync(0xffffffffu, sees);
+        if (lane == 0) s_sees[u] = rows;
+      }
+      named_bar_sync(1, kSoftThreads);
 
       float sum[RP];
 #pragma unroll
@@ -456,14 +464,18 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
                            (p.window == 0 || key0 + kTile <= p.sinks || key0 >= G.L + G.n - p.window);
         if (!whole) {
           const int key = key0 + key_lane, up = key - G.L;       // node of a tree key
+          uint32_t sees = 0u;                                    // rows of this thread that see the key
+          if (up >= 0) {
+            if (key < G.keys) sees = s_sees[up] >> r0;
+          } else if (p.window == 0 || key < p.sinks) {
+            sees = ~0u;
+          } else {
 #pragma unroll
-          for (int j = 0; j < RP; ++j) {
-            bool sees;
-            if (up < 0) sees = p.window == 0 || key < p.sinks || key >= s_first[r0 + j];
-            else sees = key < G.keys &&
-                        (reinterpret_cast<const uint32_t *>(&s_tree[r0 + j])[(up >> 5) & 3] >> (up & 31)) & 1u;
-            if (!sees) x[j] = -INFINITY;
+            for (int j = 0; j < RP; ++j) sees |= key >= s_first[r0 + j] ? 1u << j : 0u;
           }
+#pragma unroll
+          for (int j = 0; j < RP; ++j)
+            if (!((sees >> j) & 1u)) x[j] = -INFINITY;
         }
         const float most = max_of(x);
         if (named_bar_or(group, 128, unset || most > kWeightLog2 + kMoveLog2)) {
