@@ -356,9 +356,11 @@ size_t spec_kv4_record_bytes(int D);   /* 0 when D is neither 64 nor 128 */
  *             enqueues nothing (k and v may then be NULL); T x Hkv below 2^31
  * Errors on the device: SPEC_ERR_TREE_TOO_LARGE (offsets outside [0, T] or
  * decreasing) and SPEC_ERR_PREFIX_RANGE (a slot outside [0, S_cap)), for
- * which the request's slots stay as they were; SPEC_ERR_NONFINITE (NaN or
- * infinity among the rows), for which every group of 16 that holds one is
- * stored as zeros and the others are written.
+ * which the request's slots stay as they were (a row's request is found by
+ * bisection: with malformed offsets, rows of other requests may be left out
+ * too, never misplaced); SPEC_ERR_NONFINITE (NaN or infinity among the rows),
+ * for which every group of 16 that holds one is stored as zeros and the
+ * others are written.
  */
 int spec_kv4_write(const void *k, const void *v, int dtype, int B, int T, int Hkv, int D,
                    int64_t k_row_stride, int64_t k_head_stride, int64_t v_row_stride,
@@ -386,14 +388,17 @@ int spec_kv4_read(void *k, void *v, int dtype, int B, int T, int Hkv, int D, int
  * node.  With window > 0, node i at depth d sits at position L_b + d, a prefix
  * key j at position j and an ancestor at L_b + its depth; node i then sees a
  * key of K(i) only if it lies less than `window` positions behind it (itself
- * included), or at one of the first `sinks` positions.  Tiles of the cache
- * that no node sees are not read.  window = 0 means no window (sinks is then
- * ignored).
+ * included), or at one of the first `sinks` positions.  window = 0 means no
+ * window (sinks is then ignored).  Prefix slots that the window hides from
+ * every node may hold anything, like the slots behind the tree; tiles of such
+ * slots are not read.  Every other slot holds a record as spec_kv4_write
+ * stores them.
  *
  *   dtype        of q and o.  SPEC_BF16: softmax weights enter the product
  *                with V as halves (11 significant bits), sums in fp32.
  *                SPEC_F32: queries and weights as two halves each (22 bits).
- *   Hq % Hkv == 0, Hq / Hkv at most 128, D 64 or 128
+ *   Hq % Hkv == 0, Hq / Hkv at most 128, D 64 or 128, B x Hkv at most 65535,
+ *   S_cap at most 2^31 - 1025
  *   max_prefix   upper bound on every prefix_lens[b], sizes the key splits
  *                (a larger value is safe, only slower)
  * A row that sees no key (possible only with a mask that lacks the node

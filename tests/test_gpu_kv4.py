@@ -153,10 +153,12 @@ def test_a_request_in_error_changes_nothing(off, start, codes):
 
 
 # ------------------------------------------------------------------ attention
-def check_attn(q, rec, L, off, parents, window=0, sinks=0, masks="mask", scale=0.0, max_prefix=None):
+def check_attn(q, rec, L, off, parents, window=0, sinks=0, masks="mask", scale=0.0, max_prefix=None,
+               stored=None):
+    """`stored`: what the cache holds where that is not what the rows see of it, `rec`."""
     dtype, D = q.dtype, q.shape[2]
     st = zeros_status(len(L))
-    args = (q.cuda(), torch.from_numpy(rec).cuda(), i32(L), i32(off))
+    args = (q.cuda(), torch.from_numpy(rec if stored is None else stored).cuda(), i32(L), i32(off))
     par = i32(parents)
     mask = ttv.build_tree_mask(par, i32(off), st)[0] if masks == "mask" else None
     o = ttv.tree_attn_kv4(*args, mask, int(max(L)) if max_prefix is None else max_prefix, st, softmax_scale=scale,
@@ -225,6 +227,23 @@ def test_windows_that_cut_the_tree_and_the_tiles(dtype, window, sinks, chain):
     parents = sum((random_tree(rng, c, chain) for c in n), [])
     q = torch.from_numpy(rng.standard_normal((off[-1], 6, D)).astype(np.float32)).to(dtype)
     check_attn(q, rec, L, off, parents, window, sinks)
+
+
+@DTYPES
+@pytest.mark.parametrize("Hq,n", [(2, [1, 3, 2]), (4, [6, 8, 1]), (4, [16, 13, 1]), (8, [40, 5, 22])])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (30, 5), (129, 64)])
+def test_slots_behind_the_window_may_hold_anything(dtype, Hq, n, window, sinks):
+    rng = np.random.default_rng(Hq + window)
+    L, D = [500, 70, 263], 128
+    off = np.concatenate([[0], np.cumsum(n)])
+    rec = random_records(rng, (3, 1, 560), D)
+    stored = rec.copy()
+    for b, (a, c) in enumerate(zip(L, n)):
+        stored[b, :, sinks:max(sinks, a - window + 1)] = 255      # the root's window begins at a - window + 1
+        stored[b, :, a + c:] = 255
+    parents = sum((random_tree(rng, c) for c in n), [])
+    q = torch.from_numpy(rng.standard_normal((off[-1], Hq, D)).astype(np.float32)).to(dtype)
+    check_attn(q, rec, L, off, parents, window, sinks, stored=stored)
 
 
 @DTYPES
@@ -356,6 +375,21 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     assert all(torch.equal(o, ref[j]) for j, o in got)
     assert not any(b[4].any() for b in batches)
+
+
+def test_as_many_rows_as_can_be_counted():
+    """2^31 - 1 rows (one, broadcast), all but three of them behind the last request."""
+    rng = np.random.default_rng(22)
+    T, D, cap = 2 ** 31 - 1, 64, 8
+    k = torch.from_numpy(rng.standard_normal((1, 1, D)).astype(np.float32)).to(BF16)
+    before = rng.integers(0, 256, (2, 1, cap, kv4.record_bytes(D)), dtype=np.uint8)
+    cache, st = torch.from_numpy(before).cuda(), zeros_status(2)
+    wide = k.cuda().expand(T, 1, D)
+    ttv.kv4_write(wide, wide, cache, i32([4, 1]), i32([0, 2, 3]), st)
+    three = k.float().expand(3, 1, D).numpy()
+    kv4.write(before, three, three, [4, 1], [0, 2, 3])
+    np.testing.assert_array_equal(cache.cpu().numpy(), before)
+    assert st.tolist() == [0, 0]
 
 
 def test_cache_offsets_beyond_32_bits():

@@ -118,7 +118,8 @@ def test_refusals_before_any_launch(lib):
         assert attn(**{name: None}) == -1, name
     assert attn(dtype=5) == -3
     for bad in (dict(B=0), dict(T=0), dict(T=129), dict(Hq=3), dict(Hq=258), dict(H=0), dict(D=80), dict(S=0),
-                dict(mp=-1), dict(window=-1), dict(sinks=-1)):
+                dict(mp=-1), dict(window=-1), dict(sinks=-1), dict(S=2 ** 31 - 1024), dict(B=32768, H=2),
+                dict(B=2 ** 31 - 1, T=2 ** 31 - 1, H=1)):
         assert attn(**bad) == -2, bad
     for name in ("q", "kv", "o", "mask"):
         assert attn(**{name: P(0x1004)}) == -11, name

@@ -28,7 +28,7 @@ namespace {
 // of them into P's fragment (row g, keys 2t and 2t + 1).
 //
 // Which key of a group of 16 is fragment row n is free as well (one order for
-// both products).  kKeyOf spreads the loads over the banks: the record's
+// both products).  key_of spreads the loads over the banks: the record's
 // stride is 4 (D = 128: 36) or 20 words modulo 32, and with this order the
 // eight 16-byte pieces of K, or the sixteen 8-byte pieces of V, that go in one
 // pass hit 32 different banks.
@@ -256,7 +256,21 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
     for (int i = t_begin; i < t_end; i += kFewWarps) {
       if (ok && !mbar_wait(&bar_full[warp][st], phase)) ok = false;
       const int key0 = tiles.key0(i);
-      const uint8_t *tile = ring + st * C::kStageBytes;
+      uint8_t *tile = ring + st * C::kStageBytes;
+      // keys that some row may not see: the tree, and the window's borders.  Those
+      // that none sees lose their value scales where they lie (a test at each use
+      // took 5% more time of long prefixes).
+      const bool whole = key0 + kFewTile <= G.L &&
+                         (p.window == 0 || key0 + kFewTile <= p.sinks || key0 >= G.L + G.n - p.window);
+      if (!whole) {
+        if (!LiveKeys(G.L, G.keys, p.window, p.sinks)(key0 + lane)) {
+          uint32_t *scales = reinterpret_cast<uint32_t *>(tile + lane * R + D + D / 16);
+#pragma unroll
+          for (int e = 0; e < D / 64; ++e) scales[e] = 0u;
+        }
+        fence_proxy_async_smem();       // before the stage's next copy
+        __syncwarp();
+      }
       float sc[2][NT][4];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
@@ -303,9 +317,6 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
               }
         }
       }
-      // keys that some row may not see: the tree, and the window's borders
-      const bool whole = key0 + kFewTile <= G.L &&
-                         (p.window == 0 || key0 + kFewTile <= p.sinks || key0 >= G.L + G.n - p.window);
       if (!whole) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -385,7 +396,6 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
             vw[e][0] = *reinterpret_cast<const uint32_t *>(rec + D / 2 + 4 * g);
             vs[e] = rec[D + D / 16 + g / 2];
           }
-          if (!whole && key0 + key >= G.keys) vs[e] = 0u;   // slots that were not copied may hold anything
         }
         const uint32_t sa = (vs[0] << 7) | (vs[1] << 23), sb = (vs[2] << 7) | (vs[3] << 23);
 #pragma unroll
@@ -520,22 +530,22 @@ int few_splits(const Kv4AttnArgs &p, long long units, int max_prefix) {
 template <int D, bool F32>
 int attn_few(const Kv4AttnArgs &p, int max_prefix, void *stream) {
   const int rows = mean_nodes(p.a) * p.a.G;
-  const int per = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  // (bf16 has other kernels for more than 8 rows)
+  const int per = !F32 || rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
   const int blocks = (rows + per - 1) / per;
-  const long long pairs = static_cast<long long>(p.a.B) * p.a.Hkv;
-  if (pairs > 65535 || blocks > 65535) return SPEC_ERR_SHAPE;
-  const long long units = pairs * blocks;
+  const long long units = static_cast<long long>(p.a.B) * p.a.Hkv * blocks;
   const int cs = few_splits(p, units, max_prefix);
-  // eight warps instead of four where CTAs are few
-  if (per == 8)
-    return units * cs <= 2 * sm_count() ? launch_few<D, 1, 8, F32>(p, blocks, cs, stream)
-                                        : launch_few<D, 1, 4, F32>(p, blocks, cs, stream);
-  if constexpr (F32) {      // (bf16 has tensor-core kernels for more than 8 rows)
-    return per == 16 ? launch_few<D, 2, 4, F32>(p, blocks, cs, stream) : launch_few<D, 4, 4, F32>(p, blocks, cs, stream);
-  } else {
-    return SPEC_ERR_SHAPE;
+  if constexpr (F32) {
+    if (per == 16) return launch_few<D, 2, 4, F32>(p, blocks, cs, stream);
+    if (per == 32) return launch_few<D, 4, 4, F32>(p, blocks, cs, stream);
   }
+  // eight warps instead of four where CTAs are few
+  return units * cs <= 2 * sm_count() ? launch_few<D, 1, 8, F32>(p, blocks, cs, stream)
+                                      : launch_few<D, 1, 4, F32>(p, blocks, cs, stream);
 }
+
+// Slots, and the ends of the tiles that hold them, are counted in 32 bits.
+constexpr int kMaxSlots = 0x7FFFFFFF - 1024;
 
 // Which bf16 kernel: by the mean number of rows on each key (a request with
 // more takes more turns).  Measured, 32 heads x 8 requests behind 8192: 8 rows
@@ -567,6 +577,7 @@ extern "C" int spec_tree_attn_kv4(const void *q, const void *kv_cache, void *o, 
       Hq / Hkv > 128 || S_cap < 1 || max_prefix < 0 || window < 0 || sinks < 0)
     return SPEC_ERR_SHAPE;
   if (D != 64 && D != 128) return SPEC_ERR_SHAPE;
+  if (S_cap > kMaxSlots || static_cast<long long>(B) * Hkv > 65535) return SPEC_ERR_SHAPE;
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(kv_cache) | reinterpret_cast<uintptr_t>(o) |
        reinterpret_cast<uintptr_t>(mask)) & 15)
     return SPEC_ERR_ALIGNMENT;

@@ -1,4 +1,4 @@
-// Pieces shared by the two kernels of tree attention over the 4-bit cache:
+// Pieces shared by the three kernels of tree attention over the 4-bit cache:
 // what a row sees, which tiles that takes, and the merge of the key splits.
 #pragma once
 
@@ -51,6 +51,21 @@ __device__ __forceinline__ bool row_sees(const RowKeys &r, int key, int L, int k
   if (key < L) return key < r.sinks || key >= r.first;
   return key_visible(key, L, keys, r.tree);
 }
+
+// The slots that some row may see.  The others in a tile, behind the last or left
+// behind by the window, may hold anything, and their values are taken as zeros:
+// a weight of zero does not hide a NaN.
+struct LiveKeys {
+  int from, sinks;
+  uint32_t span;         // keys from `from` on
+  __device__ __forceinline__ LiveKeys(int L, int keys, int window, int sinks_)
+      : from(window ? max(0, L - window + 1) : 0), sinks(window ? min(sinks_, keys) : 0) {
+    span = static_cast<uint32_t>(keys - from);
+  }
+  __device__ __forceinline__ bool operator()(int key) const {
+    return static_cast<uint32_t>(key - from) < span || key < sinks;
+  }
+};
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -270,7 +285,7 @@ __device__ __forceinline__ bool merge_rows(int tid, int CS, int split, int rows_
 
 // The host does not know the requests' tree sizes; launches are sized by their
 // mean, rounded up.
-inline int mean_nodes(const AttnArgs &a) { return (a.T + a.B - 1) / a.B; }
+inline int mean_nodes(const AttnArgs &a) { return 1 + (a.T - 1) / a.B; }
 
 // The tensor-core paths, bf16 only: rows along N (attn_kv4_tc.cu) and along M
 // (attn_kv4_rows.cu).

@@ -275,13 +275,13 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
     const uint32_t empty = smem_addr(of_v ? bars.v_empty : bars.k_empty);
     const uint8_t *rec0 = smem + C::kOffRaw + key * R;
     const uint32_t row = sb + (of_v ? C::kOffV : C::kOffK) + key * 128 + ((key & 7) << 4);
-    const int keys_left = G.keys - key;
+    const LiveKeys live(G.L, G.keys, p.window, p.sinks);
     Ring<kRaw> raw;
     Ring<2> op;
     turns([&](int) {
       for (int i = 0; i < ntiles; ++i, raw.next(), op.next()) {
         ok = ok && mbar_sleep(raw_full + 8 * raw.at, raw.phase);
-        const KeyCodes<D> codes(rec0 + raw.at * C::kRawBytes, of_v, tiles.key0(t0 + i) < keys_left);
+        const KeyCodes<D> codes(rec0 + raw.at * C::kRawBytes, of_v, live(tiles.key0(t0 + i) + key));
         ok = ok && mbar_sleep(empty + 8 * op.at, op.phase ^ 1);
         const uint32_t dst = row + op.at * C::kOpBytes;
         codes.decode([&](int g, const uint32_t(&h)[8]) { put_swizzled<C::kBoxBytes>(dst, g, h); });

@@ -300,7 +300,7 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
       // K: the key's TMEM lane, 8 columns per 16 dims
       const uint32_t row = sb + C::kOffV + key * 128 + ((key & 7) << 4);
       const uint32_t col = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::kColK;
-      const int keys_left = G.keys - key;
+      const LiveKeys live(G.L, G.keys, p.window, p.sinks);
       Ring<kRaw> raw;
       Ring<kOps> op;
       op.phase = 1;
@@ -309,7 +309,7 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
         for (int i = 0; i < ntiles; ++i, raw.next(), op.next(), turn_of ^= kSets - 1) {
           if (turn_of != set) continue;
           ok = ok && mbar_sleep(raw_full + 8 * raw.at, raw.phase);
-          const KeyCodes<D> key_codes(rec0 + raw.at * C::kRawBytes, kV, tiles.key0(t0 + i) < keys_left);
+          const KeyCodes<D> key_codes(rec0 + raw.at * C::kRawBytes, kV, live(tiles.key0(t0 + i) + key));
           ok = ok && mbar_sleep(empty + 8 * op.at, op.phase);
           if constexpr (!kV) {
             __syncwarp();
@@ -447,7 +447,7 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
         __syncwarp();
         tc::fence_after_sync();
         float x[RP];
-        tmem_ld(s_col, x);
+        tc::ld16(s_col, x);
         tc::wait_ld();
         tc::fence_before_sync();
         __syncwarp();

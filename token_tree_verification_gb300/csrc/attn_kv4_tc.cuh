@@ -36,9 +36,6 @@ __device__ __forceinline__ float max_of(const float (&x)[n]) {
   return max3(max3(m[0], m[1], x[n - 1]), max3(m[2], m[3], x[n - 2]), fmaxf(x[n - 3], x[n - 4]));
 }
 
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[32]) { tc::ld32(taddr, v); }
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[16]) { tc::ld16(taddr, v); }
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[8]) { tc::ld8(taddr, v); }
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&v)[8]) {
   uint32_t u[8];
 #pragma unroll
@@ -50,7 +47,7 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t x, uint32_t
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-// Reduction of n values (n = 8, 16 or 32) over the warp's lanes: lane l returns
+// Reduction of n values (a power of two) over the warp's lanes: lane l returns
 // value l % n reduced over all of them.  Each round exchanges half of the
 // values with the lane across and keeps the other half.
 template <int n, typename Op>
@@ -74,8 +71,7 @@ __device__ __forceinline__ float reduce_scatter(const float (&x)[n], int lane, O
 }
 
 // One lane's key of a tile of records: its D codes and scales, from a stage
-// of the ring.  Slots at or behind the request's last may hold anything (they
-// were not copied): zeros stand for them.
+// of the ring; zeros for one that is not live.
 template <int D>
 struct KeyCodes {
   uint4 code[D / 32];
@@ -146,7 +142,6 @@ int launch_kv4_tiles(Kernel kernel, const Kv4AttnArgs &p, int threads, size_t sm
   }
   const long long tiles = (keys + kTile - 1) / kTile;
   const long long pairs = static_cast<long long>(a.B) * a.Hkv;
-  if (pairs > 65535 || blocks > 65535) return SPEC_ERR_SHAPE;
   const long long units = pairs * blocks, sms = sm_count();
   int cs = 1;
   long long best = -1;

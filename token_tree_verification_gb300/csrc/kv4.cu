@@ -108,26 +108,28 @@ struct RowWalk {
   const Kv4Args &a;
   long long st, sh, dense;       // element strides, and offset of the present row
   uint8_t *rec;
-  int h, t, b;
+  int h, b;
+  uint32_t t;                     // (the last warps' walks may end behind 2^31)
   bool ok;                        // the row belongs to a request without error
   Kv4Rows r;
 
   __device__ __forceinline__ RowWalk(const Kv4Args &args, long long row_stride, long long head_stride, uint32_t row)
       : a(args), st(row_stride), sh(head_stride) {
-    t = static_cast<int>(row / static_cast<uint32_t>(a.H));
-    h = static_cast<int>(row - static_cast<uint32_t>(t) * a.H);
+    t = row / static_cast<uint32_t>(a.H);
+    h = static_cast<int>(row - t * static_cast<uint32_t>(a.H));
     look_up();
   }
   __device__ __forceinline__ void look_up() {
-    b = t < a.T ? find_request(a.offsets, a.B, t) : -1;
+    b = t < static_cast<uint32_t>(a.T) ? find_request(a.offsets, a.B, static_cast<int>(t)) : -1;
     r = {0, 0, 0, 1};
     if (b >= 0) r = kv4_rows(a.offsets, a.start, b, a.T, a.S_cap);
     place();
   }
   __device__ __forceinline__ void place() {
+    const int i = static_cast<int>(t) - r.lo;        // of the request's rows
     dense = t * st + h * sh;
-    ok = b >= 0 && !r.err && t < r.lo + r.n && in_bounds(r.start + (t - r.lo), a.S_cap, a.status, b);
-    rec = a.kv + ((static_cast<size_t>(max(b, 0)) * a.H + h) * a.S_cap + r.start + (t - r.lo)) * R;
+    ok = b >= 0 && !r.err && i < r.n && in_bounds(r.start + i, a.S_cap, a.status, b);
+    rec = a.kv + ((static_cast<size_t>(max(b, 0)) * a.H + h) * a.S_cap + r.start + i) * R;
   }
   __device__ __forceinline__ void advance(int rows) {
     h += rows;
@@ -138,7 +140,7 @@ struct RowWalk {
       h -= a.H;
       ++t;
     } while (h >= a.H);
-    if (b < 0 || t >= r.lo + r.n) look_up();
+    if (b < 0 || static_cast<int>(t) - r.lo >= r.n) look_up();
     else place();
   }
 };
