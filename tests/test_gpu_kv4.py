@@ -377,6 +377,33 @@ def test_two_streams_at_once():
     assert not any(b[4].any() for b in batches)
 
 
+def test_outputs_made_for_a_call_on_another_stream():
+    """An output dropped while its call is under way on another stream is not handed out again before."""
+    rng = np.random.default_rng(23)
+    cache, n = torch.from_numpy(random_records(rng, (1, 8, 9000), 128)).cuda(), 9000
+    start, off, st = i32([0]), i32([0, n]), zeros_status(1)
+    side = torch.cuda.Stream()
+    ref = ttv.kv4_read(cache, start, off, st, rows=n)
+    q = torch.from_numpy(rng.standard_normal((1, 8, 128)).astype(np.float32)).to(BF16).cuda()
+    want = ttv.tree_attn_kv4(q, cache, i32([n - 1]), i32([0, 1]), None, n, st, parents=i32([-1]))
+    lens, one, par = i32([n - 1]), i32([0, 1]), i32([-1])
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for _ in range(3):
+            k, v = ttv.kv4_read(cache, start, off, st, rows=n, stream=side)
+            o = ttv.tree_attn_kv4(q, cache, lens, one, None, n, st, parents=par, stream=side)
+            addresses = {k.data_ptr(), v.data_ptr(), o.data_ptr()}
+            del k, v, o
+            fresh = [torch.empty_like(ref[0]), torch.empty_like(ref[1]), torch.empty_like(want)]
+            busy = not side.query()
+            assert not (busy and addresses & {x.data_ptr() for x in fresh})
+        side.synchronize()
+    k, v = ttv.kv4_read(cache, start, off, st, rows=n, stream=side)
+    o = ttv.tree_attn_kv4(q, cache, lens, one, None, n, st, parents=par, stream=side)
+    side.synchronize()
+    assert torch.equal(k, ref[0]) and torch.equal(v, ref[1]) and torch.equal(o, want) and st.tolist() == [0]
+
+
 def test_as_many_rows_as_can_be_counted():
     """2^31 - 1 rows (one, broadcast), all but three of them behind the last request."""
     rng = np.random.default_rng(22)

@@ -274,7 +274,13 @@ def kv_compact(k_cache, v_cache, prefix_lens, offsets, path_nodes, accept_len, s
 
 # ---------------------------------------------------------------- 4-bit cache
 _KV4_DIMS = {144: 128, 80: 64}     # bytes of a slot record -> head dimension
-_I32 = torch.int32
+_U8, _I32 = torch.uint8, torch.int32
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+# A new tensor (shape, strides, dtype) on the current device.  Outputs of a few
+# microseconds' work are made by it: torch.empty goes through the dispatcher,
+# 4.2 us beside a launch on a Grace core in place of 1.6 us.
+_empty = torch._C._dynamo.guards._empty_strided_cuda
 _DTYPES = {torch.bfloat16: SPEC_BF16, torch.float32: SPEC_F32}
 
 
@@ -294,15 +300,19 @@ def make_kv4_cache(B, Hkv, S_cap, D, device="cuda"):
 
 def _kv4_cache(kv_cache):
     """Checks a 4-bit cache; returns (device index, B, Hkv, S_cap, D)."""
-    index = kv_cache.get_device()
-    if index < 0 or kv_cache.dtype is not torch.uint8:
-        raise TypeError(f"kv_cache must be a CUDA tensor of torch.uint8, got {kv_cache.dtype} on {kv_cache.device}")
-    if kv_cache.dim() != 4 or kv_cache.shape[3] not in _KV4_DIMS or not kv_cache.is_contiguous():
-        raise ValueError("kv_cache must be contiguous [B, Hkv, S_cap, kv4_record_bytes(D)]")
-    if index != torch._C._cuda_getDevice():
-        raise ValueError(f"kv_cache is on cuda:{index}, the current device is cuda:{torch.cuda.current_device()}")
-    B, Hkv, S_cap, R = kv_cache.shape
-    return index, B, Hkv, S_cap, _KV4_DIMS[R]
+    index, shape = kv_cache.get_device(), kv_cache.shape
+    D = _KV4_DIMS.get(shape[3]) if len(shape) == 4 else None
+    if D is None or kv_cache.dtype is not _U8 or index != _current_device() or not kv_cache.is_contiguous():
+        raise _not_a_cache(kv_cache, index)
+    return index, shape[0], shape[1], shape[2], D
+
+
+def _not_a_cache(kv_cache, index):
+    if index < 0 or kv_cache.dtype is not _U8:
+        return TypeError(f"kv_cache must be a CUDA tensor of torch.uint8, got {kv_cache.dtype} on {kv_cache.device}")
+    if index != _current_device():
+        return ValueError(f"kv_cache is on cuda:{index}, the current device is cuda:{_current_device()}")
+    return ValueError("kv_cache must be contiguous [B, Hkv, S_cap, kv4_record_bytes(D)]")
 
 
 def _not_i32(index, n, t, name):
@@ -330,14 +340,14 @@ def _dense_rows(index, t, T, Hkv, D, name):
 
 
 def _raw_stream(stream, index):
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    return _current_stream(index) if stream is None else stream.cuda_stream
 
 
 def kv4_write(k, v, kv_cache, start, offsets, status, stream=None):
     """Quantises dense rows into the 4-bit cache.  k, v [T, Hkv, D] (bf16 or
     fp32; rows and heads at any 16-byte stride); request b's rows
     offsets[b] .. offsets[b+1] go to slots start[b] and up."""
-    lib = load()
+    lib = _lib or load()
     index, B, Hkv, S_cap, D = _kv4_cache(kv_cache)
     dt = _DTYPES.get(k.dtype)
     if dt is None or v.dtype is not k.dtype:
@@ -358,15 +368,18 @@ def kv4_read(kv_cache, start, offsets, status, rows=None, dtype=torch.bfloat16, 
     kv4_write: the first ``rows`` rows (offsets[-1] of them), or into
     ``out`` = (k, v), whose rows behind the last request stay as they are.
     Returns (k, v) [rows, Hkv, D]."""
-    lib = load()
+    lib = _lib or load()
     index, B, Hkv, S_cap, D = _kv4_cache(kv_cache)
     if out is None:
         if rows is None:
             raise ValueError("kv4_read needs the number of rows, or out")
-        k = torch.empty((rows, Hkv, D), dtype=dtype, device=kv_cache.device)
-        v = torch.empty_like(k)
         T, ks0, ks1 = rows, Hkv * D, D
         vs0, vs1 = ks0, ks1
+        k = _empty((T, Hkv, D), (ks0, ks1, 1), dtype)
+        v = _empty((T, Hkv, D), (ks0, ks1, 1), dtype)
+        if stream is not None:       # made for the current stream, used on another
+            k.record_stream(stream)
+            v.record_stream(stream)
     else:
         k, v = out
         T = k.shape[0]
@@ -388,11 +401,13 @@ def kv4_compact(kv_cache, prefix_lens, offsets, path_nodes, accept_len, status,
                 new_prefix_lens=None, stream=None):
     """kv_compact on a 4-bit cache (in place; records move as they are).
     Returns the new prefix lengths (device int32 [B])."""
-    lib = load()
+    lib = _lib or load()
     index, B, Hkv, S_cap, D = _kv4_cache(kv_cache)
     W = path_nodes.shape[-1]
     if new_prefix_lens is None:
-        new_prefix_lens = torch.empty_like(prefix_lens)
+        new_prefix_lens = _empty((B,), (1,), _I32)
+        if stream is not None:
+            new_prefix_lens.record_stream(stream)
     rc = lib.spec_kv4_compact(kv_cache.data_ptr(), B, Hkv, D, S_cap, _i32(index, B, prefix_lens, "prefix_lens"),
                               _i32(index, B + 1, offsets, "offsets"),
                               _i32(index, B * W, path_nodes, "path_nodes"),
@@ -411,7 +426,7 @@ def tree_attn_kv4(q, kv_cache, prefix_lens, offsets, mask, max_prefix, status, o
     ``window`` > 0 a node sees only keys less than ``window`` positions behind
     it, and the first ``sinks`` positions; with ``mask=None`` the ancestor sets
     come from ``parents``."""
-    lib = load()
+    lib = _lib or load()
     index, B, Hkv, S_cap, D = _kv4_cache(kv_cache)
     dt = _DTYPES.get(q.dtype)
     if dt is None:
@@ -427,7 +442,9 @@ def tree_attn_kv4(q, kv_cache, prefix_lens, offsets, mask, max_prefix, status, o
     else:
         raise ValueError("tree_attn_kv4 needs a mask or the parent array")
     if o is None:
-        o = torch.empty_like(q)
+        o = _empty((T, Hq, D), (Hq * D, D, 1), q.dtype)
+        if stream is not None:
+            o.record_stream(stream)
     elif o.dtype is not q.dtype or o.get_device() != index or o.shape != q.shape or not o.is_contiguous():
         raise ValueError("o must be like q")
     rc = lib.spec_tree_attn_kv4(q.data_ptr(), kv_cache.data_ptr(), o.data_ptr(), dt, B, T, Hq, Hkv, D,
