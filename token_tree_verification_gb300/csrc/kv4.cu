@@ -156,14 +156,23 @@ __device__ __forceinline__ void report_bad_rows(const Kv4Args &a) {
 // One row (key and value of one request, head and slot) is 2 x D / 8 lanes of
 // eight dimensions each: a whole warp for D = 128, half of one for D = 64.  A
 // warp walks `rounds` x U x (32 / lanes of a row) consecutive rows, U rounds of
-// loads under way at once.  Both kernels are bound by HBM on long runs; on
-// short ones by the chain of look-ups in front of the first load.
+// loads under way at once, and for 16-bit rows the next ones too (kAhead; fp32
+// rows, twice the registers, are faster without: 43.8 us in place of 46.6 for
+// 220 MB).
+//
+// A short run (64 rows of 32 heads: 2.5 us) is bound by the chain of look-ups in
+// front of its first load.  A long one: 269 MB of bf16 rows and records (51200
+// rows of 8 heads, D = 128) take 59.8 us, 4.5 TB/s, 0.66 of what a copy reaches;
+// the conversions' instructions keep the issue slots and the integer pipe about
+// two thirds busy.  Reading writes twice what it computes: 153 MB in 27.8 us, 5.5
+// TB/s, 0.81 of a copy.
 template <int D, int U, typename E>
 __global__ void __launch_bounds__(kRowThreads)
 kv4_write_kernel(const Kv4Args a, int rounds) {
   constexpr int kLanes = D / 4;                 // lanes of a row
   constexpr int kSide = 32 / kLanes;            // rows of a warp side by side
   constexpr int R = kv4_record_bytes(D);
+  constexpr bool kAhead = sizeof(E) == 2;
   const int tid = threadIdx.x, lane = tid & 31;
   const int sub = lane % kLanes;                // place within the row
   const bool is_v = sub >= kLanes / 2;
@@ -173,18 +182,32 @@ kv4_write_kernel(const Kv4Args a, int rounds) {
   const uint32_t warp = (blockIdx.x * kRowThreads + tid) / 32;
   RowWalk<R> w(a, is_v ? a.v_st : a.k_st, is_v ? a.v_sh : a.k_sh,
                warp * static_cast<uint32_t>(rounds * U * kSide) + lane / kLanes);
+  Eight<E> next[U];
+  uint32_t *next_rec[U];
+  int next_req[U];
+  auto load = [&] {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      next_rec[u] = w.ok ? reinterpret_cast<uint32_t *>(w.rec) : nullptr;
+      next_req[u] = w.b;
+      if (w.ok) next[u].load(base + w.dense);
+      else next[u].clear();
+      w.advance(kSide);
+    }
+  };
+  if (kAhead) load();
   for (int round = 0; round < rounds; ++round) {
+    if (!kAhead) load();
     Eight<E> in[U];
     uint32_t *rec[U];
     int req[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      rec[u] = w.ok ? reinterpret_cast<uint32_t *>(w.rec) : nullptr;
-      req[u] = w.b;
-      if (w.ok) in[u].load(base + w.dense);
-      else in[u].clear();
-      w.advance(kSide);
+      in[u] = next[u];
+      rec[u] = next_rec[u];
+      req[u] = next_req[u];
     }
+    if (kAhead && round + 1 < rounds) load();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       uint32_t top = in[u].top();
@@ -235,19 +258,31 @@ kv4_read_kernel(const Kv4Args a, int rounds) {
   const uint32_t warp = (blockIdx.x * kRowThreads + tid) / 32;
   RowWalk<R> w(a, is_v ? a.v_st : a.k_st, is_v ? a.v_sh : a.k_sh,
                warp * static_cast<uint32_t>(rounds * U * kSide) + lane / kLanes);
+  uint32_t next_code[U], next_scale[U];
+  E *next_dst[U];
+  auto load = [&] {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      next_dst[u] = w.ok ? base + w.dense : nullptr;
+      next_code[u] = next_scale[u] = 0u;
+      if (w.ok) {
+        next_code[u] = __ldg(reinterpret_cast<const uint32_t *>(w.rec) + sub);
+        next_scale[u] = __ldg(w.rec + D + sub / 2);
+      }
+      w.advance(kSide);
+    }
+  };
+  load();
   for (int round = 0; round < rounds; ++round) {
     uint32_t code[U], scale[U];
     E *dst[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      dst[u] = w.ok ? base + w.dense : nullptr;
-      code[u] = scale[u] = 0u;
-      if (w.ok) {
-        code[u] = __ldg(reinterpret_cast<const uint32_t *>(w.rec) + sub);
-        scale[u] = __ldg(w.rec + D + sub / 2);
-      }
-      w.advance(kSide);
+      dst[u] = next_dst[u];
+      code[u] = next_code[u];
+      scale[u] = next_scale[u];
     }
+    if (round + 1 < rounds) load();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (!dst[u]) continue;
@@ -308,10 +343,12 @@ int launch_rows(Kernel kernel, const Kv4Args &args, long long warps, int rounds,
 
 // One round of rows per warp while that leaves every SM at most 32 warps, so
 // that a tree's few rows spread over the GPU; beyond, U rounds at once, and as
-// many turns of them as make kWaves waves of 32 warps on every SM.
+// many turns of them as make kWaves waves of 32 warps on every SM.  U by
+// registers: reading bf16 rows takes 27.8 us with 4 and 30.6 with 2, fp32 rows
+// 35.5 and 32.6; writing 69.7 and 59.9.
 template <bool kWrite, int D, typename E>
 int rows_by_size(const Kv4Args &args, void *stream) {
-  constexpr int U = 2, kWaves = 4;
+  constexpr int U = !kWrite && sizeof(E) == 2 ? 4 : 2, kWaves = 4;
   const long long rows = static_cast<long long>(args.T) * args.H, side = 32 / (D / 4);
   if (rows == 0) return SPEC_OK;
   if (rows > 0x7FFFFFFFll) return SPEC_ERR_SHAPE;      // rows are counted in 32 bits
