@@ -329,6 +329,17 @@ def _i32(index, n, t, name):
     raise _not_i32(index, n, t, name)
 
 
+def _per_request(index, B, first, offsets, status, name):
+    """The pointers of the arrays that every call takes: B int32, the B + 1
+    offsets and the B status words."""
+    if (first.dtype is _I32 and offsets.dtype is _I32 and status.dtype is _I32
+            and first.get_device() == offsets.get_device() == status.get_device() == index
+            and first.numel() == status.numel() == B and offsets.numel() == B + 1
+            and first.is_contiguous() and offsets.is_contiguous() and status.is_contiguous()):
+        return first.data_ptr(), offsets.data_ptr(), status.data_ptr()
+    return _i32(index, B, first, name), _i32(index, B + 1, offsets, "offsets"), _i32(index, B, status, "status")
+
+
 def _dense_rows(index, t, T, Hkv, D, name):
     """Checks dense rows; returns their strides."""
     if t.get_device() != index:
@@ -337,10 +348,6 @@ def _dense_rows(index, t, T, Hkv, D, name):
     if one != 1 or tuple(t.shape) != (T, Hkv, D):
         raise ValueError(f"{name} must be [{T}, {Hkv}, {D}] with its last dimension contiguous")
     return row, head
-
-
-def _raw_stream(stream, index):
-    return _current_stream(index) if stream is None else stream.cuda_stream
 
 
 def kv4_write(k, v, kv_cache, start, offsets, status, stream=None):
@@ -355,10 +362,10 @@ def kv4_write(k, v, kv_cache, start, offsets, status, stream=None):
     T = k.shape[0]
     ks0, ks1 = _dense_rows(index, k, T, Hkv, D, "k")
     vs0, vs1 = _dense_rows(index, v, T, Hkv, D, "v")
-    rc = lib.spec_kv4_write(k.data_ptr(), v.data_ptr(), dt, B, T, Hkv, D, ks0, ks1, vs0, vs1,
-                            kv_cache.data_ptr(), S_cap, _i32(index, B, start, "start"),
-                            _i32(index, B + 1, offsets, "offsets"), _i32(index, B, status, "status"),
-                            _raw_stream(stream, index))
+    start, offsets, status = _per_request(index, B, start, offsets, status, "start")
+    rc = lib.spec_kv4_write(k.data_ptr(), v.data_ptr(), dt, B, T, Hkv, D, ks0, ks1, vs0, vs1, kv_cache.data_ptr(),
+                            S_cap, start, offsets, status,
+                            _current_stream(index) if stream is None else stream.cuda_stream)
     if rc:
         raise SpecError(rc, "spec_kv4_write")
 
@@ -388,10 +395,10 @@ def kv4_read(kv_cache, start, offsets, status, rows=None, dtype=torch.bfloat16, 
     dt = _DTYPES.get(k.dtype)
     if dt is None or v.dtype is not k.dtype:
         raise TypeError("rows are read as bfloat16 or float32")
-    rc = lib.spec_kv4_read(k.data_ptr(), v.data_ptr(), dt, B, T, Hkv, D, ks0, ks1, vs0, vs1,
-                           kv_cache.data_ptr(), S_cap, _i32(index, B, start, "start"),
-                           _i32(index, B + 1, offsets, "offsets"), _i32(index, B, status, "status"),
-                           _raw_stream(stream, index))
+    start, offsets, status = _per_request(index, B, start, offsets, status, "start")
+    rc = lib.spec_kv4_read(k.data_ptr(), v.data_ptr(), dt, B, T, Hkv, D, ks0, ks1, vs0, vs1, kv_cache.data_ptr(),
+                           S_cap, start, offsets, status,
+                           _current_stream(index) if stream is None else stream.cuda_stream)
     if rc:
         raise SpecError(rc, "spec_kv4_read")
     return k, v
@@ -408,12 +415,12 @@ def kv4_compact(kv_cache, prefix_lens, offsets, path_nodes, accept_len, status,
         new_prefix_lens = _empty((B,), (1,), _I32)
         if stream is not None:
             new_prefix_lens.record_stream(stream)
-    rc = lib.spec_kv4_compact(kv_cache.data_ptr(), B, Hkv, D, S_cap, _i32(index, B, prefix_lens, "prefix_lens"),
-                              _i32(index, B + 1, offsets, "offsets"),
+    prefix, offsets, status = _per_request(index, B, prefix_lens, offsets, status, "prefix_lens")
+    rc = lib.spec_kv4_compact(kv_cache.data_ptr(), B, Hkv, D, S_cap, prefix, offsets,
                               _i32(index, B * W, path_nodes, "path_nodes"),
                               _i32(index, B, accept_len, "accept_len"), W,
-                              _i32(index, B, new_prefix_lens, "new_prefix_lens"),
-                              _i32(index, B, status, "status"), _raw_stream(stream, index))
+                              _i32(index, B, new_prefix_lens, "new_prefix_lens"), status,
+                              _current_stream(index) if stream is None else stream.cuda_stream)
     if rc:
         raise SpecError(rc, "spec_kv4_compact")
     return new_prefix_lens
@@ -447,10 +454,10 @@ def tree_attn_kv4(q, kv_cache, prefix_lens, offsets, mask, max_prefix, status, o
             o.record_stream(stream)
     elif o.dtype is not q.dtype or o.get_device() != index or o.shape != q.shape or not o.is_contiguous():
         raise ValueError("o must be like q")
-    rc = lib.spec_tree_attn_kv4(q.data_ptr(), kv_cache.data_ptr(), o.data_ptr(), dt, B, T, Hq, Hkv, D,
-                                S_cap, max_prefix, _i32(index, B, prefix_lens, "prefix_lens"),
-                                _i32(index, B + 1, offsets, "offsets"), mask_ptr, parents_ptr, softmax_scale,
-                                window, sinks, _i32(index, B, status, "status"), _raw_stream(stream, index))
+    prefix, offsets, status = _per_request(index, B, prefix_lens, offsets, status, "prefix_lens")
+    rc = lib.spec_tree_attn_kv4(q.data_ptr(), kv_cache.data_ptr(), o.data_ptr(), dt, B, T, Hq, Hkv, D, S_cap,
+                                max_prefix, prefix, offsets, mask_ptr, parents_ptr, softmax_scale, window, sinks,
+                                status, _current_stream(index) if stream is None else stream.cuda_stream)
     if rc:
         raise SpecError(rc, "spec_tree_attn_kv4")
     return o

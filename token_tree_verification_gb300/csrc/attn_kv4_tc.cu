@@ -19,9 +19,9 @@
 //               are decoded and the parity's S^T has been read
 //   warp 2      issues O^T += V_i^T P_i^T
 //   then        softmax: a key per TMEM lane, so four warps for the keys of a
-//               tile; for more than 16 rows two such groups (half of the rows
-//               each) for even tiles and two for odd ones, else one each.  The sums of
-//               weights stay in registers, one per row, until the end
+//               tile; for more than 16 rows two such groups (half of the
+//               rows each) for even tiles and two for odd ones, else one each.
+//               The sums of weights stay in registers, one per row, until the end
 //   then        decoders, four warps per operand (two such sets, which take
 //               turns, for up to 16 rows): keys into TMEM, values into shared
 //               memory (128-byte swizzle), one key per lane, so that a warp's
@@ -31,6 +31,13 @@
 // A chain of eight MMAs takes about 850 cycles from issue to its barrier, a
 // tile's two chains and its softmax about 3000, so what counts is how many
 // tiles are under way: three decoded, two in the softmax.
+//
+// What bounds it, 32 rows, D = 128: about 1140 cycles a tile, of them 970 of
+// shared-memory traffic (records in and out, V's operand in and out, P), issue
+// slots 60% busy, the tensor pipe 28%.  8 requests x 32 heads behind 8192 keys:
+// 32 rows 91 us, 16 rows 74 us (278 MB, 3.8 TB/s); with a window of 4096 behind
+// 32768 61 us, in two waves of CTAs of which each spends about 10 us on its
+// set-up, first tile and output.
 #include <type_traits>
 
 #include "attn_kv4_tc.cuh"
@@ -106,11 +113,11 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
   __shared__ uint32_t s_tmem;
   __shared__ int s_timeout;
   __shared__ int s_par[SPEC_MAX_TREE_NODES];
-  __shared__ long long s_row[N];            // a row's first element of q and o
+  __shared__ long long s_row[N];                       // a row's first element of o
   __shared__ uint4 s_tree[N];
   __shared__ uint32_t s_sees[SPEC_MAX_TREE_NODES];     // the rows that see a tree node, as bits
   __shared__ int s_first[N];
-  __shared__ __align__(16) float s_c[N];           // a row's score factor
+  __shared__ __align__(16) float s_c[N];               // a row's score factor
   // per parity of the tiles: 8 - the row's reference, the last move of it
   // (factor of the old sums, shift of the scores), the reference, the sum of
   // weights, and the parts of maxima and sums that the four lane quarters hold
@@ -430,7 +437,8 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
       named_bar_sync(1, kSoftThreads);
       // the rows' sets turned round, a word of rows for every node
       for (int u = w; u < G.n; u += kSoftWarps) {
-        const bool sees = lane < N && (reinterpret_cast<const uint32_t *>(&s_tree[lane % N])[u >> 5] >> (u & 31)) & 1u;
+        const uint32_t *tree = reinterpret_cast<const uint32_t *>(&s_tree[lane % N]);
+        const bool sees = lane < N && ((tree[u >> 5] >> (u & 31)) & 1u);
         const uint32_t rows = __ballot_sync(0xffffffffu, sees);
         if (lane == 0) s_sees[u] = rows;
       }

@@ -163,8 +163,8 @@ __device__ __forceinline__ void report_bad_rows(const Kv4Args &a) {
 // A short run (64 rows of 32 heads: 2.5 us) is bound by the chain of look-ups in
 // front of its first load.  A long one: 269 MB of bf16 rows and records (51200
 // rows of 8 heads, D = 128) take 59.8 us, 4.5 TB/s, 0.66 of what a copy reaches;
-// the conversions' instructions keep the issue slots and the integer pipe about
-// two thirds busy.  Reading writes twice what it computes: 153 MB in 27.8 us, 5.5
+// the conversions' instructions keep the issue slots three quarters and the
+// integer pipe two thirds busy.  Reading writes twice what it computes: 153 MB in 27.8 us, 5.5
 // TB/s, 0.81 of a copy.
 template <int D, int U, typename E>
 __global__ void __launch_bounds__(kRowThreads)
