@@ -8,6 +8,50 @@
 
 namespace spec {
 
+namespace tc {
+
+// An MN-major operand of 32 or 16 16-bit elements along M/N, rows of K packed
+// one after another and swizzled over their own width (64 or 32 bytes: layouts
+// 4 and 6); the stride offset is that of 8 rows.
+template <int N>
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
+  static_assert(N == 32 || N == 16, "one swizzle atom wide");
+  constexpr uint64_t layout = N == 32 ? 4 : 6;
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>(1) << 16 |
+         static_cast<uint64_t>(8 * N * 2 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | layout << 61;
+}
+
+// idesc_bf16_f32 for half-precision A and B (format 0): kind::f16 takes both
+// operands in bf16 or both in half, as the descriptor says, so the bf16 MMAs
+// serve for halves too.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int b_mn) {
+  return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+         ((static_cast<uint32_t>(N) >> 3) << 17) | ((static_cast<uint32_t>(M) >> 4) << 24);
+}
+
+// One lane of a converged warp (the same one every time).  A warp that loops
+// as a whole, with only the MMAs themselves under this branch, keeps its
+// descriptors in uniform registers: an M = 128, N = 16 MMA then issues every 18
+// cycles, N = 64 every 33 (the tensor cores' own rate), against 46 for both
+// from a loop that a single lane runs.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+__device__ __forceinline__ void ld8(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+}  // namespace tc
+
 constexpr int kTile = 128;            // keys of a tile
 
 template <int regs>

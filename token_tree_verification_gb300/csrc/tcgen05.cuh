@@ -55,17 +55,6 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
   return d;
 }
 
-// An MN-major operand of 32 or 16 16-bit elements along M/N, rows of K packed
-// one after another and swizzled over their own width (64 or 32 bytes: layouts
-// 4 and 6); the stride offset is that of 8 rows.
-template <int N>
-__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
-  static_assert(N == 32 || N == 16, "one swizzle atom wide");
-  constexpr uint64_t layout = N == 32 ? 4 : 6;
-  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>(1) << 16 |
-         static_cast<uint64_t>(8 * N * 2 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | layout << 61;
-}
-
 // Instruction descriptor for kind::f16 with bf16 A/B and an fp32 accumulator.
 //   [4,6) D format (1 = f32)  [7,10) A format (1 = bf16)  [10,13) B format
 //   [15] A major (0 = K, 1 = MN)  [16] B major  [17,23) N >> 3  [24,29) M >> 4
@@ -75,14 +64,7 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int a_mn, in
          ((static_cast<uint32_t>(M) >> 4) << 24);
 }
 
-// The same for half-precision A and B (format 0).
-__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int b_mn) {
-  return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
-         ((static_cast<uint32_t>(N) >> 3) << 17) | ((static_cast<uint32_t>(M) >> 4) << 24);
-}
-
-// D[tmem] (+)= A[smem] * B[smem]; issued by a single thread (kind::f16: both
-// operands bf16, or both half, as the instruction descriptor says).
+// D[tmem] (+)= A[smem] * B[smem]; issued by a single thread.
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                          uint32_t idesc, bool accumulate) {
   asm volatile(
@@ -103,17 +85,6 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
       : "memory");
-}
-
-// One lane of a converged warp (the same one every time).  A warp that loops
-// as a whole, with only the MMAs themselves under this branch, keeps its
-// descriptors in uniform registers: an M = 128, N = 16 MMA then issues every 18
-// cycles, N = 64 every 33 (the tensor cores' own rate), against 46 for both
-// from a loop that a single lane runs.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
-  return r != 0;
 }
 
 // Arrive once on `bar` when every MMA this thread issued so far has completed.
@@ -155,16 +126,6 @@ __device__ __forceinline__ void ld16(uint32_t taddr, float (&v)[16]) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-__device__ __forceinline__ void ld8(uint32_t taddr, float (&v)[8]) {
-  uint32_t r[8];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr)
-               : "memory");
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 __device__ __forceinline__ void st32(uint32_t taddr, const float (&v)[32]) {
