@@ -34,7 +34,7 @@
 //
 // What bounds it, 32 rows, D = 128: about 1140 cycles a tile, of them 970 of
 // shared-memory traffic (records in and out, V's operand in and out, P), issue
-// slots 60% busy, the tensor pipe 28%.  8 requests x 32 heads behind 8192 keys:
+// slots 63% busy, the tensor pipe 15%.  8 requests x 32 heads behind 8192 keys:
 // 32 rows 91 us, 16 rows 74 us (278 MB, 3.8 TB/s); with a window of 4096 behind
 // 32768 61 us, in two waves of CTAs of which each spends about 10 us on its
 // set-up, first tile and output.
