@@ -50,6 +50,12 @@ constexpr int kDecodeWarps = 4;       // for keys, and as many for values
 constexpr int kThreads = 32 * (kDecodeFirst + 2 * kDecodeWarps);
 constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr int kPart = kTile / 4;      // keys of one softmax thread
+// Registers: 28 warps launch with 72 a thread; the softmax warps take 88, the
+// decoders keep 56 and the issuers 40.
+constexpr int kSoftRegs = 88, kDecodeRegs = 56, kIssueRegs = 40;
+static_assert(kSoftWarps * kSoftRegs + 2 * kDecodeWarps * kDecodeRegs + kSoftFirst * kIssueRegs <=
+                  (kSoftFirst + kSoftWarps + 2 * kDecodeWarps) * 72,
+              "register split");
 
 template <int D>
 struct Kv4Rows128 {
@@ -191,90 +197,95 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
     return done;
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ records
-    const uint8_t *kv = static_cast<const uint8_t *>(a.k) + (static_cast<size_t>(b) * a.Hkv + g_kv) * a.S_cap * R;
-    Ring<kRaw> raw;
-    raw.phase = 1;      // every stage is free at first
-    turns([&](int) {
-      if (lane != 0) return;
-      for (int i = 0; i < ntiles && ok; ++i, raw.next()) {
-        ok = mbar_sleep(raw_empty + 8 * raw.at, raw.phase);
-        if (!ok) break;
-        const int key0 = tiles.key0(t0 + i), count = min(kTile, G.keys - key0);
-        const uint32_t bytes = static_cast<uint32_t>(count * R);
-        if (range_in_bounds(key0, count, a.S_cap, a.status, b)) {
-          mbar_arrive_expect_tx(&bars.raw_full[raw.at], bytes);
-          bulk_copy_g2s(sb + C::kOffRaw + raw.at * C::kRawBytes, kv + static_cast<size_t>(key0) * R, bytes,
-                        &bars.raw_full[raw.at]);
-        } else {
-          mbar_arrive(&bars.raw_full[raw.at]);
-        }
-      }
-    }, wait_merge);
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ S = Q K^T
-    constexpr uint32_t id = tc::idesc_f16_f32(kRows, kTile / 2, 0, 0);
-    const uint64_t kd0 = tc::smem_desc_sw128(sb + C::kOffK, 16, 1024);
-    const uint32_t k_full = smem_addr(bars.k_full);
-    Ring<2> kr;
-    uint32_t phase = 1;        // of the S buffer: free at first
-    uint32_t q_phase = 0;
-    turns([&](int) {
-      if (ntiles == 0) return;
-      ok = mbar_sleep(smem_addr(&bars.q_full), q_phase);
-      q_phase ^= 1;
-      for (int i = 0; i < ntiles && ok; ++i, kr.next(), phase ^= 1) {
-        ok = mbar_sleep(k_full + 8 * kr.at, kr.phase);
-        for (int half = 0; half < 2 && ok; ++half) {
-          ok = mbar_sleep(s_empty + 8 * half, phase);
+  // (each group of four warps has one register budget)
+  if (warp < kSoftFirst) {
+    give_registers<kIssueRegs>();
+    if (warp == 0) {
+      // ------------------------------------------------------------ records
+      const uint8_t *kv = static_cast<const uint8_t *>(a.k) + (static_cast<size_t>(b) * a.Hkv + g_kv) * a.S_cap * R;
+      Ring<kRaw> raw;
+      raw.phase = 1;      // every stage is free at first
+      turns([&](int) {
+        if (lane != 0) return;
+        for (int i = 0; i < ntiles && ok; ++i, raw.next()) {
+          ok = mbar_sleep(raw_empty + 8 * raw.at, raw.phase);
           if (!ok) break;
-          tc::fence_after_sync();
-          const uint64_t kd = kd0 + static_cast<uint64_t>((kr.at * C::kOpBytes + half * (kTile / 2 * 128)) >> 4);
-          if (tc::elect_one()) {
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-              const uint32_t at = ((ks >> 2) * C::kBoxBytes + (ks & 3) * 32) >> 4;
-              tc::mma_bf16_ts(tmem + half * (kTile / 2), tmem + C::kColQ + ks * 8, kd + at, id, ks > 0);
+          const int key0 = tiles.key0(t0 + i), count = min(kTile, G.keys - key0);
+          const uint32_t bytes = static_cast<uint32_t>(count * R);
+          if (range_in_bounds(key0, count, a.S_cap, a.status, b)) {
+            mbar_arrive_expect_tx(&bars.raw_full[raw.at], bytes);
+            bulk_copy_g2s(sb + C::kOffRaw + raw.at * C::kRawBytes, kv + static_cast<size_t>(key0) * R, bytes,
+                          &bars.raw_full[raw.at]);
+          } else {
+            mbar_arrive(&bars.raw_full[raw.at]);
+          }
+        }
+      }, wait_merge);
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ S = Q K^T
+      constexpr uint32_t id = tc::idesc_f16_f32(kRows, kTile / 2, 0, 0);
+      const uint64_t kd0 = tc::smem_desc_sw128(sb + C::kOffK, 16, 1024);
+      const uint32_t k_full = smem_addr(bars.k_full);
+      Ring<2> kr;
+      uint32_t phase = 1;        // of the S buffer: free at first
+      uint32_t q_phase = 0;
+      turns([&](int) {
+        if (ntiles == 0) return;
+        ok = mbar_sleep(smem_addr(&bars.q_full), q_phase);
+        q_phase ^= 1;
+        for (int i = 0; i < ntiles && ok; ++i, kr.next(), phase ^= 1) {
+          ok = mbar_sleep(k_full + 8 * kr.at, kr.phase);
+          for (int half = 0; half < 2 && ok; ++half) {
+            ok = mbar_sleep(s_empty + 8 * half, phase);
+            if (!ok) break;
+            tc::fence_after_sync();
+            const uint64_t kd = kd0 + static_cast<uint64_t>((kr.at * C::kOpBytes + half * (kTile / 2 * 128)) >> 4);
+            if (tc::elect_one()) {
+  #pragma unroll
+              for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t at = ((ks >> 2) * C::kBoxBytes + (ks & 3) * 32) >> 4;
+                tc::mma_bf16_ts(tmem + half * (kTile / 2), tmem + C::kColQ + ks * 8, kd + at, id, ks > 0);
+              }
+              tc::commit(&bars.s_full[half]);
+              if (half) tc::commit(&bars.k_empty[kr.at]);
             }
-            tc::commit(&bars.s_full[half]);
-            if (half) tc::commit(&bars.k_empty[kr.at]);
+            __syncwarp();
           }
-          __syncwarp();
         }
-      }
-    }, wait_merge);
-  } else if (warp == 2) {
-    // ------------------------------------------------------------ O += P V
-    constexpr uint32_t id = tc::idesc_f16_f32(kRows, D, 0, 1);
-    const uint64_t vd0 = tc::smem_desc_sw128(sb + C::kOffV, C::kBoxBytes, 1024);
-    const uint32_t v_full = smem_addr(bars.v_full);
-    Ring<2> vr;
-    uint32_t phase = 0;        // of P
-    turns([&](int) {
-      for (int i = 0; i < ntiles && ok; ++i, vr.next(), phase ^= 1) {
-        ok = mbar_sleep(v_full + 8 * vr.at, vr.phase);
-        for (int half = 0; half < 2 && ok; ++half) {
-          ok = mbar_sleep(p_full + 8 * half, phase);
-          if (!ok) break;
-          tc::fence_after_sync();
-          const uint64_t vd = vd0 + static_cast<uint64_t>((vr.at * C::kOpBytes + half * (kTile / 2 * 128)) >> 4);
-          const uint32_t pt = tmem + C::kColP + half * (kTile / 4);
-          if (tc::elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < kTile / 32; ++kk)
-              tc::mma_bf16_ts(tmem + C::kColO + half * 128, pt + kk * 8, vd + (kk * 16 * 128 >> 4), id, (i | kk) != 0);
-            tc::commit(&bars.o_done[half]);
-            if (half) tc::commit(&bars.v_empty[vr.at]);
+      }, wait_merge);
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ O += P V
+      constexpr uint32_t id = tc::idesc_f16_f32(kRows, D, 0, 1);
+      const uint64_t vd0 = tc::smem_desc_sw128(sb + C::kOffV, C::kBoxBytes, 1024);
+      const uint32_t v_full = smem_addr(bars.v_full);
+      Ring<2> vr;
+      uint32_t phase = 0;        // of P
+      turns([&](int) {
+        for (int i = 0; i < ntiles && ok; ++i, vr.next(), phase ^= 1) {
+          ok = mbar_sleep(v_full + 8 * vr.at, vr.phase);
+          for (int half = 0; half < 2 && ok; ++half) {
+            ok = mbar_sleep(p_full + 8 * half, phase);
+            if (!ok) break;
+            tc::fence_after_sync();
+            const uint64_t vd = vd0 + static_cast<uint64_t>((vr.at * C::kOpBytes + half * (kTile / 2 * 128)) >> 4);
+            const uint32_t pt = tmem + C::kColP + half * (kTile / 4);
+            if (tc::elect_one()) {
+  #pragma unroll
+              for (int kk = 0; kk < kTile / 32; ++kk)
+                tc::mma_bf16_ts(tmem + C::kColO + half * 128, pt + kk * 8, vd + (kk * 16 * 128 >> 4), id, (i | kk) != 0);
+              tc::commit(&bars.o_done[half]);
+              if (half) tc::commit(&bars.v_empty[vr.at]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
-      }
-    }, wait_merge);
-  } else if (warp < kSoftFirst) {
-    turns([](int) {}, wait_merge);
+      }, wait_merge);
+    } else {
+      turns([](int) {}, wait_merge);
+    }
   } else if (warp >= kDecodeFirst) {
     // ------------------------------------------------------------ decode
+    give_registers<kDecodeRegs>();
     const bool of_v = warp >= kDecodeFirst + kDecodeWarps;
     const int key = (warp & 3) * 32 + lane;
     const uint32_t full = smem_addr(of_v ? bars.v_full : bars.k_full);
@@ -301,6 +312,7 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
     }, wait_merge);
   } else {
     // ------------------------------------------------------------ softmax
+    take_registers<kSoftRegs>();
     const int quad = warp & 3, part = (warp - kSoftFirst) >> 2;
     const int soft = tid - 32 * kSoftFirst;            // 0 .. 511
     const int half = part >> 1, sub = part & 1;
