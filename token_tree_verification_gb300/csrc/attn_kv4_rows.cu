@@ -409,6 +409,26 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
         const float most = max_of(x);
         s_max[phase][part][row] = most;
         const bool fresh = ref == -INFINITY;
+        // ---- weights at the present reference, which hardly ever moves: the
+        //      exponentials wait neither for the maxima nor for the other warp
+        uint32_t h[kPart / 16][8];
+        float tile_sum;
+        auto weigh = [&] {
+          float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+          for (int j = 0; j < kPart; j += 4) {
+            const float p0 = fast_exp2(x[j]), p1 = fast_exp2(x[j + 1]);
+            const float p2 = fast_exp2(x[j + 2]), p3 = fast_exp2(x[j + 3]);
+            add2(s0, s1, p0, p1);
+            add2(s2, s3, p2, p3);
+            h[j / 16][j / 2 % 8] = pack_half2(p0, p1);
+            h[j / 16][j / 2 % 8 + 1] = pack_half2(p2, p3);
+          }
+          add2(s0, s1, s2, s3);
+          tile_sum = s0 + s1;
+        };
+        weigh();
+        const bool room = mbar_over(o_done_h, phase ^ 1);
         // the barrier makes both warps' maxima visible, and says whether any of
         // their rows moves its reference
         if (named_bar_or(group, 64, fresh ? most > -INFINITY : most > kWeightLog2 + kMoveLog2)) {
@@ -439,29 +459,15 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
           sum *= factor;
 #pragma unroll
           for (int j = 0; j < kPart; ++j) x[j] -= by;
+          weigh();
         }
-        // ---- weights; their place is free once the last tile's product is done
-        const bool room = mbar_over(o_done_h, phase ^ 1);
-#pragma unroll
-        for (int j = 0; j < kPart; ++j) x[j] = fast_exp2(x[j]);
-        float s0 = x[0], s1 = x[1], s2 = x[2], s3 = x[3];
-#pragma unroll
-        for (int j = 4; j < kPart; j += 4) {
-          add2(s0, s1, x[j], x[j + 1]);
-          add2(s2, s3, x[j + 2], x[j + 3]);
-        }
-        add2(s0, s1, s2, s3);
-        sum += s0 + s1;
+        sum += tile_sum;
+        // ---- their place is free once the last tile's product is done
         ok = ok && (room || mbar_sleep(o_done_h, phase ^ 1));
         __syncwarp();
         tc::fence_after_sync();
 #pragma unroll
-        for (int q = 0; q < kPart / 16; ++q) {
-          uint32_t h[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) h[e] = pack_half2(x[16 * q + 2 * e], x[16 * q + 2 * e + 1]);
-          tc::st8(p_col + 8 * q, h);
-        }
+        for (int q = 0; q < kPart / 16; ++q) tc::st8(p_col + 8 * q, h[q]);
         tc::wait_st();
         tc::fence_before_sync();
         __syncwarp();
