@@ -8,7 +8,7 @@
 //   O[rows][dims] = P V     A = P (TMEM),  B = V (keys x dims, shared memory, MN-major)
 // A softmax thread then has one row, whose reference, sum and factor are
 // registers, and its weights go to TMEM as they are; decoded records serve 128
-// rows instead of 64.  (attn_kv4_tc.cu has the form for fewer rows, where the
+// rows instead of 32.  (attn_kv4_tc.cu has the form for fewer rows, where the
 // cost is the decoding of each key.)
 //
 // One CTA = one split of the keys x one block of 128 rows x one (request, KV
@@ -16,24 +16,28 @@
 //   warp 0      brings tiles of 128 records, one bulk copy each
 //   warp 1      allocates TMEM and issues S_i, the two halves of the tile's keys apart
 //   warp 2      issues O += P_i V_i, the halves apart
-//   warps 4-19  softmax: the four warps of a TMEM lane quarter hold the same 32
-//               rows, each 32 of the tile's 128 keys.  The two warps of a half of
-//               the keys share references, sums and an O of their own, merged at
-//               the end like splits of the keys: the halves never wait for each
-//               other, and one's exponentials run beside the other's maxima
-//   warps 20-23 decode keys, warps 24-27 values (one key per lane: loads of
-//               records 36 words apart and swizzled stores of rows 128 bytes
-//               apart are both free of bank conflicts)
+//   warps 4-11  softmax: a TMEM lane quarter's two warps hold the same 32 rows, each
+//               one half of the tile's keys, with references, sums and an O of its
+//               own, merged at the end like splits of the keys: no warp waits for
+//               another.  A tile's weights are taken at the reference that the row
+//               has; the rare tile that moves it reads S again
+//   warps 12-15 decode keys, warps 16-19 values (one key per lane: loads of records
+//               36 words apart and swizzled stores of rows 128 bytes apart are both
+//               free of bank conflicts); with the softmax warps they merge the rows
+// (Sixteen softmax warps, a quarter of the keys each, met at a barrier per tile
+// that two of them shared: 142 us for the 128-node trees below, 129 at D = 64.
+// Warps whose rows are no node's go along: leaving the work out took 2% longer.)
 // What passes through shared memory comes next to the softmax in cost: 36 KB of
 // records in and out, 64 KB of decoded operands in and 64 KB out per tile, 1300
 // cycles at 128 bytes each.  (Q as a shared-memory operand, read for each half
 // of the keys, added 64 KB.)
 //
 // Measured, D = 128: 4 requests x 8 KV heads x 1024 rows behind 8192 keys take
-// 158 us, 0.88 PFLOP/s, 0.46 of the measured bf16 rate (issue slots 70% busy, the
-// tensor pipe 45%; 256 CTAs are two waves on 152 SMs, of which the second is two
-// thirds full).  A tree of 64 nodes on 32 heads behind 2048 keys, five tiles a
-// CTA: 14.4 us, nearly all latency (set-up 3, first tile 2, loop 4, merge 3).
+// 136 us, 1.03 PFLOP/s, 0.54 of the measured bf16 rate (256 CTAs are two waves on
+// 152 SMs, of which the second is two thirds full; with all arithmetic taken out
+// the copies, products and waits alone take 100 us), at D = 64 122 us.  A tree of
+// 64 nodes on 32 heads behind 2048 keys, five tiles a CTA: 13.9 us, nearly all
+// latency (set-up 3, first tile 2, loop 4, merge 3).
 #include <type_traits>
 
 #include "attn_kv4_tc.cuh"
@@ -44,17 +48,18 @@ namespace {
 
 constexpr int kRows = 128;
 constexpr int kSoftFirst = 4;         // warps: four issuers, then the softmax, then the decoders
-constexpr int kSoftWarps = 16;
+constexpr int kSoftWarps = 8;
 constexpr int kDecodeFirst = kSoftFirst + kSoftWarps;
 constexpr int kDecodeWarps = 4;       // for keys, and as many for values
 constexpr int kThreads = 32 * (kDecodeFirst + 2 * kDecodeWarps);
 constexpr int kSoftThreads = 32 * kSoftWarps;
-constexpr int kPart = kTile / 4;      // keys of one softmax thread
-// Registers: 28 warps launch with 72 a thread; the softmax warps take 88, the
-// decoders keep 56 and the issuers 40.
-constexpr int kSoftRegs = 88, kDecodeRegs = 56, kIssueRegs = 40;
+constexpr int kHalf = kTile / 2;      // keys of one softmax thread
+constexpr int kMergeThreads = kSoftThreads + 32 * 2 * kDecodeWarps;     // softmax and decoders
+// Registers: 20 warps launch with 96 a thread; the softmax warps take 152, the
+// decoders keep 64 and the issuers 40.
+constexpr int kSoftRegs = 152, kDecodeRegs = 64, kIssueRegs = 40;
 static_assert(kSoftWarps * kSoftRegs + 2 * kDecodeWarps * kDecodeRegs + kSoftFirst * kIssueRegs <=
-                  (kSoftFirst + kSoftWarps + 2 * kDecodeWarps) * 72,
+                  (kSoftFirst + kSoftWarps + 2 * kDecodeWarps) * 96,
               "register split");
 
 template <int D>
@@ -63,7 +68,7 @@ struct Kv4Rows128 {
   static constexpr int kBoxes = D / 64;
   static constexpr int kBoxBytes = kTile * 128;             // 128 rows of 64 halves, K and V alike
   static constexpr int kOpBytes = kBoxes * kBoxBytes;
-  static constexpr int kRaw = 3;                            // stages of records
+  static constexpr int kRaw = 2;                            // stages of records (3: 140 us in place of 136)
   static constexpr int kRawBytes = kTile * R;
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kOffK + 2 * kOpBytes;
@@ -112,7 +117,7 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
   __shared__ int s_timeout;
   __shared__ int s_par[SPEC_MAX_TREE_NODES];
   __shared__ long long s_row[kRows];          // a row's first element of o
-  __shared__ float s_max[2][4][kRows];        // [tile parity][part][row]
+  __shared__ float s_top[2][kRows];           // [half of the dims][row]: largest magnitude of q
   __shared__ float s_ref[2][kRows], s_sum[2][kRows];
 
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -195,6 +200,16 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
     bool done = true;
     for (int q = 0; q < CS; ++q) done &= !(s_ml[q][0].y < 0.f);
     return done;
+  };
+
+  // The softmax warps' rows, staged, and the decoders' hands.
+  auto merge = [&](int row0, int thread) {
+    const bool timed_out = s_timeout != 0;
+    if (timed_out && thread == 0) report(a.status, b, SPEC_ERR_TIMEOUT);
+    auto out_row = [&](int r) { return s_row[r] < 0 ? nullptr : static_cast<__nv_bfloat16 *>(a.o) + s_row[r]; };
+    return merge_rows<D, 2, kRows, kMergeThreads, __nv_bfloat16>(
+        thread, CS, split, min(kRows, rows_total - row0), timed_out, reinterpret_cast<float *>(smem), s_ref, s_sum,
+        s_ml, reinterpret_cast<float4 *>(smem + C::kOffRecv), [] { cluster_wait(); }, out_row);
   };
 
   // (each group of four warps has one register budget)
@@ -309,65 +324,64 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
           mbar_arrive_at(raw_empty + 8 * raw.at);
         }
       }
-    }, wait_merge);
+    }, [&](int row0) {
+      if (CS > 1) cluster_arrive_relaxed();
+      return merge(row0, tid - 32 * kSoftFirst);
+    });
   } else {
     // ------------------------------------------------------------ softmax
     take_registers<kSoftRegs>();
-    const int quad = warp & 3, part = (warp - kSoftFirst) >> 2;
-    const int soft = tid - 32 * kSoftFirst;            // 0 .. 511
-    const int half = part >> 1, sub = part & 1;
+    const int quad = warp & 3, half = (warp - kSoftFirst) >> 2;
+    const int soft = tid - 32 * kSoftFirst;            // 0 .. 255
     const int row = quad * 32 + lane;                  // and TMEM lane
-    const int group = 2 + 2 * quad + half;             // named barrier of the two warps
     const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t s_col = trow + part * kPart, o_col = trow + C::kColO + half * 128 + sub * (D / 2);
-    const uint32_t p_col = trow + C::kColP + part * (kPart / 2);
+    const uint32_t s_col = trow + half * kHalf, o_col = trow + C::kColO + half * 128;
+    const uint32_t p_col = trow + C::kColP + half * (kHalf / 2);
     const uint32_t s_full_h = s_full + 8 * half, s_empty_h = s_empty + 8 * half, p_full_h = p_full + 8 * half,
                    o_done_h = o_done + 8 * half;
     uint32_t phase = 0;      // of S, P and the products: flips with every tile
-    float sum = 0.f, ref = -INFINITY;
     turns([&](int row0) {
       const int rows_here = min(kRows, rows_total - row0);
       const bool live = row < rows_here;
-      // ---- Q as halves: this thread's row, a quarter of its dims.  Every load
-      //      of the set-up is under way before the first is used.
+      // ---- Q as halves: this thread's row, half of its dims.  Every load of
+      //      the set-up is under way before the first is used.
       const int node = (row0 + row) / a.G;
       const bool mine = live && in_bounds(G.lo + node, a.T, a.status, b);
       const long long first =
           (static_cast<long long>(G.lo + node) * a.Hq + g_kv * a.G + (row0 + row) - node * a.G) * D;
       const uint4 *src =
-          reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + first + part * (D / 4));
-      uint4 x4[D / 32], m = make_uint4(0u, 0u, 0u, 0u);
+          reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + first + half * (D / 2));
+      uint4 x4[D / 16], m = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) x4[c] = mine ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+      for (int c = 0; c < D / 16; ++c) x4[c] = mine ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
       if (a.mask) {
         if (mine) m = __ldg(a.mask + G.lo + node);
       } else if (row0 == static_cast<int>(blockIdx.y) * kRows) {
         for (int i = soft; i < G.n; i += kSoftThreads)
           s_par[i] = in_bounds(G.lo + i, a.T, a.status, b) ? __ldg(a.parents + G.lo + i) : -2;
       }
-      if (part == 0) s_row[row] = mine ? first : -1;
+      if (half == 0) s_row[row] = mine ? first : -1;
       float top = 0.f;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < D / 16; ++c) {
         const uint32_t u[4] = {x4[c].x, x4[c].y, x4[c].z, x4[c].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           top = max3(top, fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xFFFF0000u)));
       }
-      s_max[0][part][row] = top;
+      s_top[half][row] = top;
       named_bar_sync(1, kSoftThreads);
-      top = fmaxf(fmaxf(s_max[0][0][row], s_max[0][1][row]), fmaxf(s_max[0][2][row], s_max[0][3][row]));
-      const int up = row_exponent(top);
+      const int up = row_exponent(fmaxf(s_top[0][row], s_top[1][row]));
       const float grow = power_of_two(up), c = a.scale_log2 * power_of_two(-up);
 #pragma unroll
-      for (int q = 0; q < D / 64; ++q) {
+      for (int q = 0; q < D / 32; ++q) {
         uint32_t h[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const uint32_t u = (&x4[2 * q + (e >> 2)].x)[e & 3];
           h[e] = pack_half2(__uint_as_float(u << 16) * grow, __uint_as_float(u & 0xFFFF0000u) * grow);
         }
-        tc::st8(trow + C::kColQ + part * (D / 8) + 8 * q, h);
+        tc::st8(trow + C::kColQ + half * (D / 4) + 8 * q, h);
       }
       tc::wait_st();
       tc::fence_before_sync();
@@ -382,60 +396,59 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
         if (bad) report(a.status, b, SPEC_ERR_BAD_PARENT);
       }
       const RowKeys see = row_keys(m, G.L, p.window, p.sinks);
-      ref = live ? -INFINITY : 0.f;           // rows of no node need no reference
-      sum = 0.f;
+      float ref = live ? -INFINITY : 0.f;      // rows of no node need no reference
+      float sum = 0.f;
       float shift = kWeightLog2;               // 8 - reference (8 while there is none)
 
       for (int i = 0; i < ntiles; ++i, phase ^= 1) {
-        const int key0 = tiles.key0(t0 + i), k0 = key0 + part * kPart;
+        const int key0 = tiles.key0(t0 + i), k0 = key0 + half * kHalf;
+        const bool whole = k0 + kHalf <= G.L && (p.window == 0 || k0 + kHalf <= p.sinks || k0 >= G.L + G.n - p.window);
         ok = ok && mbar_sleep(s_full_h, phase);
         __syncwarp();
         tc::fence_after_sync();
-        float x[kPart];
-        tc::ld32(s_col, x);
-        tc::wait_ld();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_at(s_empty_h);
-        // x = score - reference + 8, in powers of two
-#pragma unroll
-        for (int j = 0; j < kPart; j += 2) fma2(x[j], x[j + 1], c, c, shift, shift);
-        if (!(k0 + kPart <= G.L && (p.window == 0 || k0 + kPart <= p.sinks || k0 >= G.L + G.n - p.window))) {
-          const uint32_t sees = sees32(see, k0, G.L, p.window);
-#pragma unroll
-          for (int j = 0; j < kPart; ++j)
-            if (!((sees >> j) & 1u)) x[j] = -INFINITY;
-        }
-        const float most = max_of(x);
-        s_max[phase][part][row] = most;
-        const bool fresh = ref == -INFINITY;
-        // ---- weights at the present reference, which hardly ever moves: the
-        //      exponentials wait neither for the maxima nor for the other warp
-        uint32_t h[kPart / 16][8];
-        float tile_sum;
+        // The tile's weights at the present reference and their sum, and the
+        // largest score - reference + 8, in powers of two.  (S is read again when
+        // the reference moves, which it hardly ever does.)
+        uint32_t h[kHalf / 16][8];
+        float tile_sum, most;
         auto weigh = [&] {
+          float x[2][32];
+          tc::ld32(s_col, x[0]);
+          tc::ld32(s_col + 32, x[1]);
+          tc::wait_ld();
           float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+          most = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < kPart; j += 4) {
-            const float p0 = fast_exp2(x[j]), p1 = fast_exp2(x[j + 1]);
-            const float p2 = fast_exp2(x[j + 2]), p3 = fast_exp2(x[j + 3]);
-            add2(s0, s1, p0, p1);
-            add2(s2, s3, p2, p3);
-            h[j / 16][j / 2 % 8] = pack_half2(p0, p1);
-            h[j / 16][j / 2 % 8 + 1] = pack_half2(p2, p3);
+          for (int part = 0; part < 2; ++part) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) fma2(x[part][j], x[part][j + 1], c, c, shift, shift);
+            if (!whole) {
+              const uint32_t sees = sees32(see, k0 + 32 * part, G.L, p.window);
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!((sees >> j) & 1u)) x[part][j] = -INFINITY;
+            }
+            most = fmaxf(most, max_of(x[part]));
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              const float p0 = fast_exp2(x[part][j]), p1 = fast_exp2(x[part][j + 1]);
+              const float p2 = fast_exp2(x[part][j + 2]), p3 = fast_exp2(x[part][j + 3]);
+              add2(s0, s1, p0, p1);
+              add2(s2, s3, p2, p3);
+              h[2 * part + j / 16][j / 2 % 8] = pack_half2(p0, p1);
+              h[2 * part + j / 16][j / 2 % 8 + 1] = pack_half2(p2, p3);
+            }
           }
           add2(s0, s1, s2, s3);
           tile_sum = s0 + s1;
         };
         weigh();
-        const bool room = mbar_over(o_done_h, phase ^ 1);
-        // the barrier makes both warps' maxima visible, and says whether any of
-        // their rows moves its reference
-        if (named_bar_or(group, 64, fresh ? most > -INFINITY : most > kWeightLog2 + kMoveLog2)) {
-          const float mx = fmaxf(s_max[phase][2 * half][row], s_max[phase][2 * half + 1][row]);
-          float factor = 1.f, by = 0.f;
-          if (mx > (fresh ? -INFINITY : kWeightLog2 + kMoveLog2)) {
-            by = ceilf(mx - kWeightLog2);
+        const bool fresh = ref == -INFINITY;
+        const bool moves = most > (fresh ? -INFINITY : kWeightLog2 + kMoveLog2);
+        if (__any_sync(0xffffffffu, moves)) {
+          float factor = 1.f;
+          if (moves) {
+            const float by = ceilf(most - kWeightLog2);
             factor = fresh ? 0.f : exp2f(-by);
             ref = (fresh ? 0.f : ref) + by;
             shift -= by;
@@ -445,8 +458,8 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
             ok = ok && mbar_sleep(o_done_h, phase ^ 1);
             __syncwarp();
             tc::fence_after_sync();
-#pragma unroll
-            for (int j = 0; j < D / 2; j += 8) {
+#pragma unroll 1
+            for (int j = 0; j < D; j += 8) {
               float o[8];
               tc::ld8(o_col + j, o);
               tc::wait_ld();
@@ -457,58 +470,50 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
             tc::wait_st();
           }
           sum *= factor;
-#pragma unroll
-          for (int j = 0; j < kPart; ++j) x[j] -= by;
           weigh();
         }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(s_empty_h);
         sum += tile_sum;
-        // ---- their place is free once the last tile's product is done
-        ok = ok && (room || mbar_sleep(o_done_h, phase ^ 1));
+        // ---- the weights' place is free once the last tile's product is done (most
+        //      often it is: the test spares the wait's 115 cycles)
+        ok = ok && (mbar_over(o_done_h, phase ^ 1) || mbar_sleep(o_done_h, phase ^ 1));
         __syncwarp();
         tc::fence_after_sync();
 #pragma unroll
-        for (int q = 0; q < kPart / 16; ++q) tc::st8(p_col + 8 * q, h[q]);
+        for (int q = 0; q < kHalf / 16; ++q) tc::st8(p_col + 8 * q, h[q]);
         tc::wait_st();
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive_at(p_full_h);
       }
       // ---- the block's rows out of TMEM.  Their place in shared memory is free
-      //      once the last product is done.
+      //      once the last products of both halves are done.
       if (ntiles > 0) ok = ok && mbar_sleep(o_done_h, phase ^ 1);
       if (CS > 1) cluster_arrive_relaxed();
       __syncwarp();
       tc::fence_after_sync();
-      s_max[0][part][row] = sum;
       if (!ok) s_timeout = 1;
       named_bar_sync(1, kSoftThreads);
       if (s_timeout == 0) {
-        if (sub == 0) {
-          s_sum[half][row] = s_max[0][2 * half][row] + s_max[0][2 * half + 1][row];
-          s_ref[half][row] = ntiles > 0 ? ref : -INFINITY;
-        }
-        const uint32_t so = sb + ((half * kRows + row) * (D + 4) + sub * (D / 2)) * 4;
+        s_sum[half][row] = sum;
+        s_ref[half][row] = ntiles > 0 ? ref : -INFINITY;
+        const uint32_t so = sb + (half * kRows + row) * (D + 4) * 4;
 #pragma unroll
-        for (int j = 0; j < D / 2; j += 8) {
-          float o[8] = {};
+        for (int j = 0; j < D; j += 32) {
+          float o[32] = {};
           if (ntiles > 0) {
-            tc::ld8(o_col + j, o);
+            tc::ld32(o_col + j, o);
             tc::wait_ld();
           }
 #pragma unroll
-          for (int e = 0; e < 8; e += 4)
+          for (int e = 0; e < 32; e += 4)
             st_shared_v4(so + (j + e) * 4, __float_as_uint(o[e]), __float_as_uint(o[e + 1]), __float_as_uint(o[e + 2]),
                          __float_as_uint(o[e + 3]));
         }
       }
-    }, [&](int row0) {
-      const bool timed_out = s_timeout != 0;
-      if (timed_out && soft == 0) report(a.status, b, SPEC_ERR_TIMEOUT);
-      auto out_row = [&](int r) { return s_row[r] < 0 ? nullptr : static_cast<__nv_bfloat16 *>(a.o) + s_row[r]; };
-      return merge_rows<D, 2, kRows, kSoftThreads, __nv_bfloat16>(
-          soft, CS, split, min(kRows, rows_total - row0), timed_out, reinterpret_cast<float *>(smem), s_ref, s_sum,
-          s_ml, reinterpret_cast<float4 *>(smem + C::kOffRecv), [] { cluster_wait(); }, out_row);
-    });
+    }, [&](int row0) { return merge(row0, soft); });
   }
   __syncwarp();
   tc::fence_before_sync();
