@@ -349,6 +349,20 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
           mx[nt][e] = fmaxf(m0, m1) * c_row[nt][e];
           want |= mx[nt][e] > m_ref[nt][e] + kMoveLog2;
         }
+      // The weights, in fp32 calls at the present references, which hardly ever
+      // move, before the vote on them (16 rows, 256 units behind 4096: 65.7 -> 62.8
+      // us; bf16 calls have little to overlap: 178 -> 180 us on long prefixes)
+      float pw[2][NT][4];
+      auto weigh = [&] {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              pw[mt][nt][e] = fast_exp2(fmaf(sc[mt][nt][e], c_row[nt][e & 1], nbase[nt][e & 1]));
+      };
+      if (F32) weigh();
       if (__any_sync(0xffffffffu, want)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -370,7 +384,9 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
               nbase[nt][e] = kWeightLog2 - m;
             }
           }
+        if (F32) weigh();
       }
+      if (!F32) weigh();
       // ---- weights, and their product with V
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
@@ -379,8 +395,7 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float p0 = fast_exp2(fmaf(sc[mt][nt][2 * k], c_row[nt][0], nbase[nt][0]));
-            const float p1 = fast_exp2(fmaf(sc[mt][nt][2 * k + 1], c_row[nt][1], nbase[nt][1]));
+            const float p0 = pw[mt][nt][2 * k], p1 = pw[mt][nt][2 * k + 1];
             l_row[nt][0] += p0;
             l_row[nt][1] += p1;
             const uint32_t h = pack_half2(p0, p1);
@@ -560,9 +575,8 @@ constexpr int kMaxSlots = 0x7FFFFFFF - 1024;
 // Which bf16 kernel: by the mean number of rows on each key (a request with
 // more takes more turns).  Measured, 32 heads x 8 requests behind 8192: 8 rows
 // take 59 us in mma.sync and 75 us on tcgen05 with the rows along N, 9 rows 75
-// us there; 32 rows 94 us along N and 149 us along M; 64 rows 138 us along N (in
-// a form for 64) and 144 us along M, but one such tree behind 2048 15.4 and
-// 14.5 us, so that form was dropped.
+// us there; 32 rows 91 us along N and 121 us along M, 33 rows 121 us along M.  (A
+// form for 64 rows along N took 138 us for 64, 123 us along M.)
 template <int D>
 int attn_bf16(const Kv4AttnArgs &p, int max_prefix, void *stream) {
   const int rows = mean_nodes(p.a) * p.a.G;
