@@ -344,10 +344,11 @@ def _dense_rows(index, t, T, Hkv, D, name):
     """Checks dense rows; returns their strides."""
     if t.get_device() != index:
         raise TypeError(f"{name} must be on cuda:{index}, got {t.device}")
-    row, head, one = t.stride() if t.dim() == 3 else (0, 0, 0)
-    if one != 1 or tuple(t.shape) != (T, Hkv, D):
-        raise ValueError(f"{name} must be [{T}, {Hkv}, {D}] with its last dimension contiguous")
-    return row, head
+    if t.shape == (T, Hkv, D):
+        row, head, one = t.stride()
+        if one == 1:
+            return row, head
+    raise ValueError(f"{name} must be [{T}, {Hkv}, {D}] with its last dimension contiguous")
 
 
 def kv4_write(k, v, kv_cache, start, offsets, status, stream=None):
@@ -438,9 +439,10 @@ def tree_attn_kv4(q, kv_cache, prefix_lens, offsets, mask, max_prefix, status, o
     dt = _DTYPES.get(q.dtype)
     if dt is None:
         raise TypeError("q must be bfloat16 or float32")
-    if q.get_device() != index or q.dim() != 3 or q.shape[2] != D or not q.is_contiguous():
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != D or q.get_device() != index or not q.is_contiguous():
         raise ValueError(f"q must be contiguous [T, Hq, {D}] on cuda:{index}")
-    T, Hq, _ = q.shape
+    T, Hq, _ = shape
     mask_ptr = parents_ptr = None
     if mask is not None:
         mask_ptr = _i32(index, 4 * T, mask, "mask")
