@@ -57,9 +57,9 @@ constexpr int kHalf = kTile / 2;      // keys of one softmax thread
 constexpr int kMergeThreads = kSoftThreads + 32 * 2 * kDecodeWarps;     // softmax and decoders
 // Registers: 20 warps launch with 96 a thread; the softmax warps take 152, the
 // decoders keep 64 and the issuers 40.
-constexpr int kSoftRegs = 152, kDecodeRegs = 64, kIssueRegs = 40;
+constexpr int kLaunchRegs = 96, kSoftRegs = 152, kDecodeRegs = 64, kIssueRegs = 40;
 static_assert(kSoftWarps * kSoftRegs + 2 * kDecodeWarps * kDecodeRegs + kSoftFirst * kIssueRegs <=
-                  (kSoftFirst + kSoftWarps + 2 * kDecodeWarps) * 96,
+                  (kSoftFirst + kSoftWarps + 2 * kDecodeWarps) * kLaunchRegs,
               "register split");
 
 template <int D>
@@ -530,10 +530,10 @@ int launch_kv4_rows(const Kv4AttnArgs &p, int max_prefix, void *stream) {
   const int blocks = (mean_nodes(p.a) * p.a.G + kRows - 1) / kRows;
   static TileLaunch state[2];
   if (p.a.D == 128)
-    return launch_kv4_tiles(tree_attn_kv4_rows_kernel<128>, p, kThreads, Kv4Rows128<128>::kSmem, blocks, max_prefix,
-                            &state[0], stream);
-  return launch_kv4_tiles(tree_attn_kv4_rows_kernel<64>, p, kThreads, Kv4Rows128<64>::kSmem, blocks, max_prefix,
-                          &state[1], stream);
+    return launch_kv4_tiles(tree_attn_kv4_rows_kernel<128>, p, kThreads, kLaunchRegs, Kv4Rows128<128>::kSmem, blocks,
+                            max_prefix, &state[0], stream);
+  return launch_kv4_tiles(tree_attn_kv4_rows_kernel<64>, p, kThreads, kLaunchRegs, Kv4Rows128<64>::kSmem, blocks,
+                          max_prefix, &state[1], stream);
 }
 
 }  // namespace spec

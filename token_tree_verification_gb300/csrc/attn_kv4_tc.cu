@@ -51,7 +51,7 @@ constexpr int kDecodeWarps = 4;       // of one set, for keys, and as many for v
 constexpr int kTcThreads = 32 * 28;
 // Registers: 28 warps launch with 72 a thread; sixteen softmax warps take 88
 // (eight: 120), the decoders keep 56 and the issuers 40.
-constexpr int kDecodeRegs = 56, kIssueRegs = 40;
+constexpr int kLaunchRegs = 72, kDecodeRegs = 56, kIssueRegs = 40;
 constexpr int kOps = 3;               // decoded K tiles (TMEM), decoded V tiles (shared memory)
 
 template <int D, int N>
@@ -67,7 +67,7 @@ struct Kv4Tc {
   static constexpr int kSoftRegs = kHalves == 2 ? 88 : 120;
   static_assert(kDecodeFirst + 2 * kSets * kDecodeWarps == kTcThreads / 32, "warps");
   static_assert(kSoftWarps * kSoftRegs + 2 * kSets * kDecodeWarps * kDecodeRegs + kSoftFirst * kIssueRegs <=
-                    kTcThreads / 32 * 72,
+                    kTcThreads / 32 * kLaunchRegs,
                 "register split");
   static constexpr int R = kv4_record_bytes(D);
   static constexpr int kBoxes = D / 64;
@@ -605,8 +605,8 @@ template <int D, int N>
 int launch_tc(const Kv4AttnArgs &p, int max_prefix, void *stream) {
   static TileLaunch state;
   const int blocks = (mean_nodes(p.a) * p.a.G + N - 1) / N;
-  return launch_kv4_tiles(tree_attn_kv4_tc_kernel<D, N>, p, kTcThreads, Kv4Tc<D, N>::kSmem, blocks, max_prefix, &state,
-                          stream);
+  return launch_kv4_tiles(tree_attn_kv4_tc_kernel<D, N>, p, kTcThreads, kLaunchRegs, Kv4Tc<D, N>::kSmem, blocks,
+                          max_prefix, &state, stream);
 }
 
 template <int D>

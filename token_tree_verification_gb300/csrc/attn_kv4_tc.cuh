@@ -170,14 +170,27 @@ __device__ __forceinline__ void put_swizzled(uint32_t row, int g, const uint32_t
 // take 25.5 us with 16 splits and 37.7 us with 8.
 struct TileLaunch {
   std::atomic<size_t> granted[kMaxDevices];
-  std::atomic<bool> wide[kMaxDevices];
+  std::atomic<bool> fits[kMaxDevices], wide[kMaxDevices];
 };
 
+// Whether the kernel was compiled to launch with the registers that its roles
+// divide: with fewer, the roles that take more would wait for ever.
 template <typename Kernel>
-int launch_kv4_tiles(Kernel kernel, const Kv4AttnArgs &p, int threads, size_t smem, int blocks, int max_prefix,
-                     TileLaunch *state, void *stream) {
+bool has_registers(Kernel kernel, int regs, int dev, TileLaunch *state) {
+  if (state->fits[dev].load(std::memory_order_acquire)) return true;
+  cudaFuncAttributes f;
+  if (cudaFuncGetAttributes(&f, kernel) != cudaSuccess || f.numRegs < regs) return false;
+  state->fits[dev].store(true, std::memory_order_release);
+  return true;
+}
+
+template <typename Kernel>
+int launch_kv4_tiles(Kernel kernel, const Kv4AttnArgs &p, int threads, int regs, size_t smem, int blocks,
+                     int max_prefix, TileLaunch *state, void *stream) {
   const AttnArgs &a = p.a;
-  if (!allow_dynamic_smem(kernel, smem, state->granted)) return SPEC_ERR_CUDA;
+  const int dev = current_device();
+  if (dev < 0 || !has_registers(kernel, regs, dev, state) || !allow_dynamic_smem(kernel, smem, state->granted))
+    return SPEC_ERR_CUDA;
   const int nodes = mean_nodes(a);
   long long keys = static_cast<long long>(max_prefix) + nodes;
   if (p.window) {
@@ -200,8 +213,6 @@ int launch_kv4_tiles(Kernel kernel, const Kv4AttnArgs &p, int threads, size_t sm
     }
   }
   if (cs > 8) {
-    const int dev = current_device();
-    if (dev < 0) return SPEC_ERR_CUDA;
     if (!state->wide[dev].load(std::memory_order_acquire)) {
       if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return SPEC_ERR_CUDA;
