@@ -377,6 +377,23 @@ def test_two_streams_at_once():
     assert not any(b[4].any() for b in batches)
 
 
+@pytest.mark.parametrize("G", [1, 12, 24, 40])
+def test_as_many_requests_and_heads_as_a_launch_takes(G):
+    """65535 (request, head) pairs, a tile of keys each, against calls for a few of the requests."""
+    rng = np.random.default_rng(24)
+    B, H, D, cap = 257, 255, 64, 6
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    cache = torch.randint(0, 256, (B, H, cap, 80), dtype=torch.uint8, device="cuda", generator=gen)
+    cache[..., D:D + D // 8] = torch.randint(92, 107, (B, H, cap, D // 8), dtype=torch.uint8, device="cuda", generator=gen)
+    q = torch.randn((B, H * G, D), device="cuda", generator=gen).to(BF16)
+    L, off, par, st = i32(rng.integers(0, cap, B)), i32(np.arange(B + 1)), i32([-1] * B), zeros_status(B)
+    o = ttv.tree_attn_kv4(q, cache, L, off, None, cap, st, parents=par)
+    for b in (0, 128, 254):
+        few = ttv.tree_attn_kv4(q[b:b + 3], cache[b:b + 3], L[b:b + 3], off[:4], None, cap, st[:3], parents=par[:3])
+        assert torch.equal(o[b:b + 3], few)
+    assert not st.any()
+
+
 def test_outputs_made_for_a_call_on_another_stream():
     """An output dropped while its call is under way on another stream is not handed out again before."""
     rng = np.random.default_rng(23)
