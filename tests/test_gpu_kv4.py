@@ -303,6 +303,9 @@ def test_attention_reports_and_leaves_a_request_in_error(dtype):
         assert torch.equal(o[:8], good[:8])
         if codes[1] == -10:
             assert (o[8:16] == 9.0).all() and torch.equal(o[16:], good[16:]) and st.tolist() == codes
+    st = zeros_status(3)
+    ttv.tree_attn_kv4(q, rec, i32([20, 2 ** 31 - 1, 5]), i32([0, 8, 16, 24]), None, 40, st, parents=i32(parents))
+    assert st.tolist() == [0, -10, 0]
     bad = list(parents)
     bad[10] = 5
     st = zeros_status(3)
@@ -484,6 +487,10 @@ def test_compact_moves_records_as_the_oracle_moves_rows():
     before = cache.clone()
     newp = ttv.kv4_compact(cache, i32([2, 2, 36, 2]), i32([0, 6, 12, 18, 24]), path, i32([2, 1, 1, 9]), st)
     assert st.tolist() == [-5, -5, -10, -4] and newp.tolist() == [2, 2, 36, 2] and torch.equal(cache, before)
+    # a prefix whose sum with the tree passes 2^31
+    st = zeros_status(4)
+    ttv.kv4_compact(cache, i32([2, 2 ** 31 - 1, 2 ** 31 - 6, 2]), i32([0, 6, 12, 18, 24]), i32([[0, 1, -1, -1]] * 4), i32([1] * 4), st)
+    assert st.tolist() == [0, -10, -10, 0] and torch.equal(cache, before)
 
 
 def step_inputs(seed, B, Hq, Hkv, D, n, V, steps):

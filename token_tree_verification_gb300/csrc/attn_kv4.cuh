@@ -67,6 +67,13 @@ struct LiveKeys {
   }
 };
 
+// request_geometry, for any prefix length.
+__device__ __forceinline__ ReqGeom kv4_geometry(const AttnArgs &a, int b) {
+  ReqGeom G = request_geometry(a, b);
+  if (!G.err && G.L > a.S_cap - G.n) G.err = SPEC_ERR_PREFIX_RANGE;     // (L + n may pass 2^31)
+  return G;
+}
+
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);

@@ -42,7 +42,7 @@ kv_compact_kernel(const KvArgs a) {
       acc = __ldg(a.accept + b);
       const int32_t *pn = a.path + static_cast<size_t>(b) * a.W;
       int err = 0;
-      if (L < 0 || L + n > a.S_cap) {
+      if (L < 0 || static_cast<long long>(L) + n > a.S_cap) {
         err = SPEC_ERR_PREFIX_RANGE;
       } else if (acc < 0 || acc + 1 > a.W) {
         err = SPEC_ERR_TREE_TOO_LARGE;
