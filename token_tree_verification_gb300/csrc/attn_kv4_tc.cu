@@ -78,7 +78,13 @@ struct Kv4Tc {
   static constexpr int kPPitch = N * 2;                     // a key's weights: their own swizzle width
   static constexpr int kPBytes = kTile * kPPitch;
   static constexpr int kRawBytes = kTile * R;
-  static constexpr int kRaw = 5;                            // stages of records
+  // Stages of records (32 rows: 4 take 61.0 us for the window below, 5 61.9; 16
+  // rows: 75.4 and 73.5 us).  A set of decoders that skips the other's tiles must
+  // not meet a stage whose last copy it cannot know to be over, or the phase that
+  // it waits for would be taken for the one before the last: either the stage's
+  // last tile was its own, or it was consumed when the set's last tile was written.
+  static constexpr int kRaw = N == 16 ? 5 : 4;
+  static_assert(kSets == 1 || kRaw % kSets == 0 || kRaw >= kOps + kSets, "stages of records");
   static constexpr int kOffV = 0;
   static constexpr int kOffP = kOffV + kOps * kOpBytes;
   static constexpr int kOffQ = kOffP + 2 * kPBytes;

@@ -29,7 +29,6 @@ namespace spec {
 
 __host__ __device__ constexpr int kv4_record_bytes(int D) { return (D + D / 8 + 15) / 16 * 16; }
 
-constexpr int kKv4Group = 16;              // dimensions that share a scale
 constexpr uint32_t kKv4MaxScale = 0xE2;    // 10240: 6 x 10240 is the largest value, a finite half
 
 // Eight codes (one word, dimension 0 in the lowest nibble) as four half pairs.
