@@ -527,8 +527,15 @@ int launch_few(const Kv4AttnArgs &p, int blocks, int cs, void *stream) {
 // of 32 keys, and 0.47 us x (CTAs of four warps per SM) once the SM's issue
 // slots are shared; set-up, first tile and output take 3 us, the merge of
 // splits 1.5 us, overlapped with other CTAs' work beyond the four that are
-// resident.  16 splits only where 8 leave SMs without work.
-int few_splits(const Kv4AttnArgs &p, long long units, int max_prefix) {
+// resident.
+//
+// 16 splits only where 8 leave SMs without work.  Clusters of 16 find room on
+// fewer SMs: about twelve run at once with up to 16 rows, four with 32; more of
+// them take a second turn, which only long prefixes repay.  (One token, units
+// behind keys: 4 behind 32000 13.1 us in place of 20.6, 12 behind 8000 9.0 for
+// 10.0, 16 behind 8000 14.7 for 11.9, 16 behind 32000 30.2 for 32.4; fp32, 32
+// rows: 4 behind 8000 17.9 for 25.1, 8 behind 2048 20.0 for 15.5.)
+int few_splits(const Kv4AttnArgs &p, int rows, long long units, int max_prefix) {
   long long keys = static_cast<long long>(max_prefix) + mean_nodes(p.a);
   if (p.window) {
     const long long near = static_cast<long long>(p.window) + p.sinks + mean_nodes(p.a) + 2 * kFewTile;
@@ -548,7 +555,8 @@ int few_splits(const Kv4AttnArgs &p, long long units, int max_prefix) {
       best = cs;
     }
   }
-  if (best == 8 && 8 * units < sms && tiles >= 64) best = 16;
+  const int at_once = rows <= 16 ? 12 : 4;
+  if (best == 8 && 8 * units < sms && tiles >= 64 && (units <= at_once || tiles >= 1000)) best = 16;
   return best;
 }
 
@@ -559,7 +567,7 @@ int attn_few(const Kv4AttnArgs &p, int max_prefix, void *stream) {
   const int per = !F32 || rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
   const int blocks = (rows + per - 1) / per;
   const long long units = static_cast<long long>(p.a.B) * p.a.Hkv * blocks;
-  const int cs = few_splits(p, units, max_prefix);
+  const int cs = few_splits(p, per, units, max_prefix);
   if constexpr (F32) {
     if (per == 16) return launch_few<D, 2, 4, F32>(p, blocks, cs, stream);
     if (per == 32) return launch_few<D, 4, 4, F32>(p, blocks, cs, stream);
