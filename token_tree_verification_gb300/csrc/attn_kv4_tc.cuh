@@ -161,16 +161,11 @@ __device__ __forceinline__ void put_swizzled(uint32_t row, int g, const uint32_t
   st_shared_v4(at ^ (piece + 16), h[4], h[5], h[6], h[7]);
 }
 
-// Launch of a kernel that takes one CTA per SM: `blocks` row blocks (the
-// grid's y) of every (request, KV head), and as many splits of the keys (a
-// cluster) as make waves x (tiles of a CTA + its set-up, first tile and merge,
-// in tiles) least.  Of clusters of 16 only about four run at once (eight of
-// them took twice the time of four, and longer than eight clusters of 8), so
-// they serve up to four units: 64-node trees on 4 KV heads behind 30000 keys
-// take 25.5 us with 16 splits and 37.7 us with 8.
+// What a launch keeps of its kernel, per device.
 struct TileLaunch {
   std::atomic<size_t> granted[kMaxDevices];
-  std::atomic<bool> fits[kMaxDevices], wide[kMaxDevices];
+  std::atomic<bool> fits[kMaxDevices];
+  std::atomic<int> at_once[kMaxDevices][kMaxSplits + 1];    // clusters of each size that run at once, plus one
 };
 
 // Whether the kernel was compiled to launch with the registers that its roles
@@ -180,10 +175,48 @@ bool has_registers(Kernel kernel, int regs, int dev, TileLaunch *state) {
   if (state->fits[dev].load(std::memory_order_acquire)) return true;
   cudaFuncAttributes f;
   if (cudaFuncGetAttributes(&f, kernel) != cudaSuccess || f.numRegs < regs) return false;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return false;
   state->fits[dev].store(true, std::memory_order_release);
   return true;
 }
 
+inline void cluster_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], int cs, int threads,
+                           size_t smem) {
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  pdl_attribute(attr[1]);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+}
+
+// Clusters of `cs` CTAs that run at once: fewer than SMs / cs, since a cluster
+// stays within one of the GPU's groups of SMs.
+template <typename Kernel>
+int clusters_at_once(Kernel kernel, int cs, int threads, size_t smem, int dev, TileLaunch *state) {
+  const int known = state->at_once[dev][cs].load(std::memory_order_relaxed);
+  if (known) return known - 1;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cluster_config(cfg, attr, cs, threads, smem);
+  cfg.gridDim = dim3(cs, 1, 1);
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 0) n = 0;
+  state->at_once[dev][cs].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+// Launch of a kernel that takes one CTA per SM: `blocks` row blocks (the grid's
+// y) of every (request, KV head), and as many splits of the keys (a cluster) as
+// make waves x (tiles of a CTA + its set-up, first tile and merge, in tiles)
+// least.  (24 and 64 rows behind 4000 keys, by splits: 19 units 11.8 and 14.9 us
+// with 6, 19.6 and 24.7 with 8, of which 19 do not run at once; 40 units 15.2 and
+// 19.3 with 3, 24.4 and 31.4 with 4; 6 units behind 500 9.0 and 11.1 with 2, 9.3
+// and 12.3 without.)
 template <typename Kernel>
 int launch_kv4_tiles(Kernel kernel, const Kv4AttnArgs &p, int threads, int regs, size_t smem, int blocks,
                      int max_prefix, TileLaunch *state, void *stream) {
@@ -199,39 +232,25 @@ int launch_kv4_tiles(Kernel kernel, const Kv4AttnArgs &p, int threads, int regs,
   }
   const long long tiles = (keys + kTile - 1) / kTile;
   const long long pairs = static_cast<long long>(a.B) * a.Hkv;
-  const long long units = pairs * blocks, sms = sm_count();
+  const long long units = pairs * blocks;
   int cs = 1;
   long long best = -1;
-  for (int c = 1; c <= 16; c = c == 8 ? 16 : c + 1) {
+  for (int c = 1; c <= kMaxSplits; c = c == 8 ? kMaxSplits : c + 1) {
     if (c > 1 && tiles < 2 * c) break;
-    const long long slots = c > 8 ? sms * 64 / 152 : sms;
-    const long long waves = (units * c + slots - 1) / slots;
-    const long long cost = waves * ((tiles + c - 1) / c + 8 + (c > 1 ? 2 : 0));
+    const int slots = clusters_at_once(kernel, c, threads, smem, dev, state);
+    if (slots < 1) continue;
+    const long long waves = (units + slots - 1) / slots;
+    const long long cost = waves * (2 * ((tiles + c - 1) / c) + (c > 1 ? 19 : 16));     // in half tiles
     if (best < 0 || cost < best) {
       best = cost;
       cs = c;
     }
   }
-  if (cs > 8) {
-    if (!state->wide[dev].load(std::memory_order_acquire)) {
-      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-        return SPEC_ERR_CUDA;
-      state->wide[dev].store(true, std::memory_order_release);
-    }
-  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cs, static_cast<unsigned>(blocks), static_cast<unsigned>(pairs));
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cs;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  pdl_attribute(attr[1]);
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cluster_config(cfg, attr, cs, threads, smem);
+  cfg.gridDim = dim3(cs, static_cast<unsigned>(blocks), static_cast<unsigned>(pairs));
+  cfg.stream = static_cast<cudaStream_t>(stream);
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
