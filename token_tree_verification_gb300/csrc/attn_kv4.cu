@@ -488,93 +488,109 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
   }
 }
 
+// Up to 8 rows: eight warps a CTA where CTAs are few, else four.
+inline bool few_narrow(long long units, int cs) { return units * cs > 2 * sm_count(); }
+
+template <int D, int NT, int W, bool F32>
+struct FewKernel {
+  static KernelState state;
+};
+template <int D, int NT, int W, bool F32>
+KernelState FewKernel<D, NT, W, F32>::state;
+
 // A launch of `cs` splits (a cluster) of every unit, a unit being one block of
 // rows of one (request, KV head).
 template <int D, int NT, int W, bool F32>
-int launch_few(const Kv4AttnArgs &p, int blocks, int cs, void *stream) {
+int launch_few(const Kv4AttnArgs &p, int blocks, int cs, int dev, void *stream) {
   using C = FewCfg<D, NT, W, F32>;
   auto kernel = tree_attn_kv4_few_kernel<D, NT, W, F32>;
-  static std::atomic<size_t> granted[kMaxDevices];
-  if (!allow_dynamic_smem(kernel, C::kSmem, granted)) return SPEC_ERR_CUDA;
-  if (cs > 8) {
-    static std::atomic<bool> wide[kMaxDevices];       // clusters beyond the portable 8
-    const int dev = current_device();
-    if (dev < 0) return SPEC_ERR_CUDA;
-    if (!wide[dev].load(std::memory_order_acquire)) {
-      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-        return SPEC_ERR_CUDA;
-      wide[dev].store(true, std::memory_order_release);
-    }
-  }
+  if (!allow_clusters(kernel, C::kSmem, dev, &FewKernel<D, NT, W, F32>::state)) return SPEC_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cs, static_cast<unsigned>(blocks), static_cast<unsigned>(p.a.B * p.a.Hkv));
-  cfg.blockDim = dim3(32 * W, 1, 1);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cs;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  pdl_attribute(attr[1]);
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cluster_config(cfg, attr, cs, 32 * W, C::kSmem);
+  cfg.gridDim = dim3(cs, static_cast<unsigned>(blocks), static_cast<unsigned>(p.a.B * p.a.Hkv));
+  cfg.stream = static_cast<cudaStream_t>(stream);
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
-// Splits of the keys, by the time they are expected to take.  Measured at
-// D = 128, up to 8 rows: a warp alone on its scheduler takes 1.0 us per tile
-// of 32 keys, and 0.47 us x (CTAs of four warps per SM) once the SM's issue
-// slots are shared; set-up, first tile and output take 3 us, the merge of
-// splits 1.5 us, overlapped with other CTAs' work beyond the four that are
-// resident.
+// Splits of the keys, by the time they are expected to take, fitted to forced
+// splits of 3 to 200 units behind 500 to 32000 keys.
 //
-// 16 splits only where 8 leave SMs without work.  Clusters of 16 find room on
-// fewer SMs: about twelve run at once with up to 16 rows, four with 32; more of
-// them take a second turn, which only long prefixes repay.  (One token, units
-// behind keys: 4 behind 32000 13.1 us in place of 20.6, 12 behind 8000 9.0 for
-// 10.0, 16 behind 8000 14.7 for 11.9, 16 behind 32000 30.2 for 32.4; fp32, 32
-// rows: 4 behind 8000 17.9 for 25.1, 8 behind 2048 20.0 for 15.5.)
-int few_splits(const Kv4AttnArgs &p, int rows, long long units, int max_prefix) {
+// Fewer units than SMs: a warp's tile of 32 keys takes kTile[0] us while an SM has
+// one CTA of W warps, kTile[1] where two fill it; clusters of three and more are
+// placed unevenly, so that the step between the two begins early.  kFixed: set-up,
+// first tile and output, without and with a merge of splits.  (One token, 8 query
+// heads, 40 and 76 units behind 4000 keys 12.3 -> 10.8 and 19.9 -> 15.5 us against
+// a plan for evenly filled SMs; 16 fp32 rows, 40 units 28.3 -> 18.8.)
+//
+// More units: CTAs follow one another, and what counts is the SM's issue slots,
+// 0.47 us a tile and CTA of four warps.
+template <int D, int NT, bool F32>
+int few_splits(const Kv4AttnArgs &p, long long units, int max_prefix, int dev) {
+  constexpr int W = NT == 1 ? 8 : 4;
+  using C = FewCfg<D, NT, W, F32>;
+  auto kernel = tree_attn_kv4_few_kernel<D, NT, W, F32>;
+  KernelState *state = &FewKernel<D, NT, W, F32>::state;
+  if (!allow_clusters(kernel, C::kSmem, dev, state)) return 0;
+  constexpr double kTile[2] = {NT == 1 ? 1.0 : NT == 2 ? 1.2 : 1.9, NT == 1 ? 1.88 : NT == 2 ? 2.0 : 3.5};
+  constexpr double kFixed[2] = {NT == 1 ? 4.4 : NT == 2 ? 4.4 : 10.0, NT == 1 ? 5.2 : NT == 2 ? 6.5 : 11.8};
   long long keys = static_cast<long long>(max_prefix) + mean_nodes(p.a);
   if (p.window) {
     const long long near = static_cast<long long>(p.window) + p.sinks + mean_nodes(p.a) + 2 * kFewTile;
     if (near < keys) keys = near;
   }
-  const long long tiles = (keys + kFewTile - 1) / kFewTile;
-  const long long sms = sm_count();
+  const long long tiles = (keys + kFewTile - 1) / kFewTile, sms = sm_count();
   int best = 1;
-  double least = 0;
-  for (int cs = 1; cs <= 8 && (cs == 1 || tiles >= 4 * cs); cs *= 2) {
-    const double per_sm = static_cast<double>((units * cs + sms - 1) / sms);
-    const double per_tile = 0.47 * per_sm > 1.0 ? 0.47 * per_sm : 1.0;
-    const double fixed = (cs > 1 ? 4.5 : 3.0) * (per_sm > 4 ? per_sm / 4 : 1.0);
-    const double us = static_cast<double>((tiles + 4 * cs - 1) / (4 * cs)) * per_tile + fixed;
-    if (cs == 1 || us < least) {
+  double least = -1;
+  for (const int cs : {1, 2, 3, 4, 6, 8, 16}) {
+    if (cs > 1 && tiles < 4 * cs) break;
+    double us;
+    if (units < sms) {
+      const int at_once = clusters_at_once(kernel, cs, 32 * W, C::kSmem, dev, state);     // two CTAs on an SM
+      if (at_once < 1) continue;
+      const bool narrow = NT == 1 && few_narrow(units, cs);      // CTAs of half the warps
+      const int warps = cs * (narrow ? W / 2 : W);
+      const double fill = static_cast<double>(units) / (narrow ? at_once : 0.5 * at_once);     // 2: full
+      const double step = cs <= 2 ? (fill > 1 ? 1.0 : 0.0) : fill < 0.4 ? 0.0 : fill > 1 ? 1.0 : (fill - 0.4) / 0.6;
+      const double waves = fill <= 2 ? 1.0 : ceil(0.5 * fill);
+      us = waves * (static_cast<double>((tiles + warps - 1) / warps) * (kTile[0] + step * (kTile[1] - kTile[0])) +
+                    kFixed[cs > 1]);
+    } else {
+      if (cs > 8 || cs % 3 == 0) continue;       // (200 units: 35.6 us with 3 splits, 33.0 with 1 or 2)
+      const double per_sm = static_cast<double>((units * cs + sms - 1) / sms);
+      const double per_tile = 0.47 * per_sm > 1.0 ? 0.47 * per_sm : 1.0;
+      const double fixed = (cs > 1 ? 4.5 : 3.0) * (per_sm > 4 ? per_sm / 4 : 1.0);
+      us = static_cast<double>((tiles + 4 * cs - 1) / (4 * cs)) * per_tile + fixed;
+    }
+    if (least < 0 || us < least) {
       least = us;
       best = cs;
     }
   }
-  const int at_once = rows <= 16 ? 12 : 4;
-  if (best == 8 && 8 * units < sms && tiles >= 64 && (units <= at_once || tiles >= 1000)) best = 16;
   return best;
+}
+
+template <int D, int NT, bool F32>
+int split_few(const Kv4AttnArgs &p, int blocks, int max_prefix, void *stream) {
+  const int dev = current_device();
+  if (dev < 0) return SPEC_ERR_CUDA;
+  const long long units = static_cast<long long>(p.a.B) * p.a.Hkv * blocks;
+  const int cs = few_splits<D, NT, F32>(p, units, max_prefix, dev);
+  if (cs < 1) return SPEC_ERR_CUDA;
+  if constexpr (NT == 1)
+    return few_narrow(units, cs) ? launch_few<D, 1, 4, F32>(p, blocks, cs, dev, stream)
+                                 : launch_few<D, 1, 8, F32>(p, blocks, cs, dev, stream);
+  else return launch_few<D, NT, 4, F32>(p, blocks, cs, dev, stream);
 }
 
 template <int D, bool F32>
 int attn_few(const Kv4AttnArgs &p, int max_prefix, void *stream) {
   const int rows = mean_nodes(p.a) * p.a.G;
-  // (bf16 has other kernels for more than 8 rows)
-  const int per = !F32 || rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-  const int blocks = (rows + per - 1) / per;
-  const long long units = static_cast<long long>(p.a.B) * p.a.Hkv * blocks;
-  const int cs = few_splits(p, per, units, max_prefix);
-  if constexpr (F32) {
-    if (per == 16) return launch_few<D, 2, 4, F32>(p, blocks, cs, stream);
-    if (per == 32) return launch_few<D, 4, 4, F32>(p, blocks, cs, stream);
+  if constexpr (F32) {      // (bf16 has other kernels for more than 8 rows)
+    if (rows > 16) return split_few<D, 4, true>(p, (rows + 31) / 32, max_prefix, stream);
+    if (rows > 8) return split_few<D, 2, true>(p, 1, max_prefix, stream);
   }
-  // eight warps instead of four where CTAs are few
-  return units * cs <= 2 * sm_count() ? launch_few<D, 1, 8, F32>(p, blocks, cs, stream)
-                                      : launch_few<D, 1, 4, F32>(p, blocks, cs, stream);
+  return split_few<D, 1, F32>(p, 1, max_prefix, stream);
 }
 
 // Slots, and the ends of the tiles that hold them, are counted in 32 bits.

@@ -294,6 +294,53 @@ __device__ __forceinline__ bool merge_rows(int tid, int CS, int split, int rows_
 // mean, rounded up.
 inline int mean_nodes(const AttnArgs &a) { return 1 + (a.T - 1) / a.B; }
 
+// What the launches keep of a kernel, per device.
+struct KernelState {
+  std::atomic<size_t> granted[kMaxDevices];
+  std::atomic<bool> wide[kMaxDevices], fits[kMaxDevices];
+  std::atomic<int> at_once[kMaxDevices][kMaxSplits + 1];    // clusters of each size that run at once, plus one
+};
+
+// Allows the kernel its shared memory, and clusters beyond the portable 8.
+template <typename Kernel>
+bool allow_clusters(Kernel kernel, size_t smem, int dev, KernelState *state) {
+  if (!allow_dynamic_smem(kernel, smem, state->granted)) return false;
+  if (state->wide[dev].load(std::memory_order_acquire)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return false;
+  state->wide[dev].store(true, std::memory_order_release);
+  return true;
+}
+
+inline void cluster_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], int cs, int threads,
+                           size_t smem) {
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  pdl_attribute(attr[1]);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+}
+
+// Clusters of `cs` CTAs that run at once: fewer than SMs / cs, since a cluster
+// stays within one of the GPU's groups of SMs.
+template <typename Kernel>
+int clusters_at_once(Kernel kernel, int cs, int threads, size_t smem, int dev, KernelState *state) {
+  const int known = state->at_once[dev][cs].load(std::memory_order_relaxed);
+  if (known) return known - 1;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cluster_config(cfg, attr, cs, threads, smem);
+  cfg.gridDim = dim3(cs, 1, 1);
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 0) n = 0;
+  state->at_once[dev][cs].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
 // The tensor-core paths, bf16 only: rows along N (attn_kv4_tc.cu) and along M
 // (attn_kv4_rows.cu).
 int launch_kv4_tc(const Kv4AttnArgs &p, int max_prefix, void *stream);

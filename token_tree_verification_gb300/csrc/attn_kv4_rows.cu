@@ -528,7 +528,7 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
 
 int launch_kv4_rows(const Kv4AttnArgs &p, int max_prefix, void *stream) {
   const int blocks = (mean_nodes(p.a) * p.a.G + kRows - 1) / kRows;
-  static TileLaunch state[2];
+  static KernelState state[2];
   if (p.a.D == 128)
     return launch_kv4_tiles(tree_attn_kv4_rows_kernel<128>, p, kThreads, kLaunchRegs, Kv4Rows128<128>::kSmem, blocks,
                             max_prefix, &state[0], stream);

@@ -609,7 +609,7 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
 
 template <int D, int N>
 int launch_tc(const Kv4AttnArgs &p, int max_prefix, void *stream) {
-  static TileLaunch state;
+  static KernelState state;
   const int blocks = (mean_nodes(p.a) * p.a.G + N - 1) / N;
   return launch_kv4_tiles(tree_attn_kv4_tc_kernel<D, N>, p, kTcThreads, kLaunchRegs, Kv4Tc<D, N>::kSmem, blocks,
                           max_prefix, &state, stream);

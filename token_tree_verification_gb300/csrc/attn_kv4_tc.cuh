@@ -161,53 +161,15 @@ __device__ __forceinline__ void put_swizzled(uint32_t row, int g, const uint32_t
   st_shared_v4(at ^ (piece + 16), h[4], h[5], h[6], h[7]);
 }
 
-// What a launch keeps of its kernel, per device.
-struct TileLaunch {
-  std::atomic<size_t> granted[kMaxDevices];
-  std::atomic<bool> fits[kMaxDevices];
-  std::atomic<int> at_once[kMaxDevices][kMaxSplits + 1];    // clusters of each size that run at once, plus one
-};
-
 // Whether the kernel was compiled to launch with the registers that its roles
 // divide: with fewer, the roles that take more would wait for ever.
 template <typename Kernel>
-bool has_registers(Kernel kernel, int regs, int dev, TileLaunch *state) {
+bool has_registers(Kernel kernel, int regs, int dev, KernelState *state) {
   if (state->fits[dev].load(std::memory_order_acquire)) return true;
   cudaFuncAttributes f;
   if (cudaFuncGetAttributes(&f, kernel) != cudaSuccess || f.numRegs < regs) return false;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return false;
   state->fits[dev].store(true, std::memory_order_release);
   return true;
-}
-
-inline void cluster_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], int cs, int threads,
-                           size_t smem) {
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cs;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  pdl_attribute(attr[1]);
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-}
-
-// Clusters of `cs` CTAs that run at once: fewer than SMs / cs, since a cluster
-// stays within one of the GPU's groups of SMs.
-template <typename Kernel>
-int clusters_at_once(Kernel kernel, int cs, int threads, size_t smem, int dev, TileLaunch *state) {
-  const int known = state->at_once[dev][cs].load(std::memory_order_relaxed);
-  if (known) return known - 1;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
-  cluster_config(cfg, attr, cs, threads, smem);
-  cfg.gridDim = dim3(cs, 1, 1);
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 0) n = 0;
-  state->at_once[dev][cs].store(n + 1, std::memory_order_relaxed);
-  return n;
 }
 
 // Launch of a kernel that takes one CTA per SM: `blocks` row blocks (the grid's
@@ -219,10 +181,10 @@ int clusters_at_once(Kernel kernel, int cs, int threads, size_t smem, int dev, T
 // and 12.3 without.)
 template <typename Kernel>
 int launch_kv4_tiles(Kernel kernel, const Kv4AttnArgs &p, int threads, int regs, size_t smem, int blocks,
-                     int max_prefix, TileLaunch *state, void *stream) {
+                     int max_prefix, KernelState *state, void *stream) {
   const AttnArgs &a = p.a;
   const int dev = current_device();
-  if (dev < 0 || !has_registers(kernel, regs, dev, state) || !allow_dynamic_smem(kernel, smem, state->granted))
+  if (dev < 0 || !has_registers(kernel, regs, dev, state) || !allow_clusters(kernel, smem, dev, state))
     return SPEC_ERR_CUDA;
   const int nodes = mean_nodes(a);
   long long keys = static_cast<long long>(max_prefix) + nodes;
