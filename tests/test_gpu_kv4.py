@@ -1,6 +1,10 @@
 """The 4-bit KV cache on the GPU against its float64 oracle: writing and
 reading are exact, attention is held to bounds counted in half steps of the
 roundings it makes, and the calls run together as a step uses them."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -585,6 +589,39 @@ def test_decoding_steps_run_together(dtype):
         np.testing.assert_array_equal(lens.cpu().numpy(), L)
     assert sum(int(a.sum()) for _, a, _ in eager) > 0
     np.testing.assert_array_equal(cache, ref)
+
+
+FIRST_CALLS = """
+import torch, token_tree_verification_gb300 as ttv
+torch.manual_seed(0)
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+L, cap = 3000, 3200
+cache = ttv.make_kv4_cache(1, 2, cap, 128)
+k, v = torch.randn(2, L + 128, 2, 128, device="cuda").bfloat16()
+zero, st = i32([0]), i32([0])
+runs = [(torch.randn(n, 2 * g, 128, device="cuda").to(t), i32([L]), i32([0, n]), i32([-1] + [0] * (n - 1)))
+        for n, g, t in ((4, 1, torch.bfloat16), (24, 1, torch.bfloat16), (100, 2, torch.bfloat16), (20, 1, torch.float32))]
+everything = i32([0, L + 128])
+torch.cuda.synchronize()
+def calls():
+    ttv.kv4_write(k, v, cache, zero, everything, st)
+    out = [ttv.tree_attn_kv4(q, cache, l, off, None, L, st, parents=par) for q, l, off, par in runs]
+    return out + list(ttv.kv4_read(cache, zero, everything, st, rows=L + 128))
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    captured = calls()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(captured, calls())) and st.tolist() == [0]
+print("the same")
+"""
+
+
+def test_first_calls_inside_a_capture():
+    """A new process whose first calls are captured: what a launch asks of a kernel once is no stream operation."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "the same" in r.stdout, r.stderr[-2000:]
 
 
 def test_the_dense_attention_agrees_on_the_values_read_back():
