@@ -484,6 +484,7 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
             tid, CS, split, rows_here, timed_out, so, s_m, s_l, s_ml, reinterpret_cast<float4 *>(smem + C::kOffRecv),
             [] { cluster_wait(); }, out_row))
       return;
+    fence_proxy_async_smem();
     __syncthreads();    // all is read, before this CTA's next arrival says so and the ring is filled again
   }
 }

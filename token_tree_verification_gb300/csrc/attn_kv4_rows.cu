@@ -184,9 +184,10 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
       __syncthreads();
       tc::fence_after_sync();
       const bool done = finish(row0);
-      // (the next turn's operands take the staged rows' place)
-      __syncthreads();
+      // (the next turn's records and operands take the staged rows' place)
       if (!done) break;
+      fence_proxy_async_smem();
+      __syncthreads();
     }
   };
   // A split block's CTAs arrive twice at the cluster's barrier: when a thread's
