@@ -183,7 +183,9 @@ constexpr float kMoveLog2 = 7.f;
 constexpr int kMaxSplits = 16;
 
 // A row's query is taken as halves: scaled by 2^up so that its largest finite
-// element is near 2^13, which the score factor takes back.  (A row below
+// element is near 2^13, which the score factor takes back.  bf16 elements are
+// exact down to 2^-27 of the largest; below, the half's smallest step takes at
+// most 2^-38 of it, far under what the sums of the scores round.  (A row below
 // 2^-113 stays that much smaller: its scores vanish either way.)
 __device__ __forceinline__ int row_exponent(float top) {
   return top > 0.f && top < INFINITY ? min(13 + 127 - (__float_as_int(top) >> 23), 126) : 0;
