@@ -39,21 +39,33 @@ __device__ __forceinline__ uint32_t scale_of(uint32_t amax_bits) {
   return min(q < 0x38800000u ? small : normal, kKv4MaxScale);   // 2^-14 parts the two
 }
 
-// The codes of two elements, x / scale rounded to the nearest with ties to
+// The codes of eight elements, x / scale rounded to the nearest with ties to
 // even, exactly.  The boundaries are multiples of 1/4; an element (12
 // significant bits) that is on none stays 2^-14 away from it, so its quotient
 // may be rounded to multiples of 2^-14 first: adding and taking away 768 does
 // that, and removes the 2^-21 by which the product with 1 / scale can err.  (A
 // zero keeps the element's sign.)
-__device__ __forceinline__ uint32_t codes_of(float x0, float x1, float inv) {
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float inv) {
   constexpr float kGrid = 768.f;
-  float y0 = x0, y1 = x1;
-  fma2(y0, y1, inv, inv, kGrid, kGrid);
-  add2(y0, y1, -kGrid, -kGrid);
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    y[i] = x[i];
+    y[i + 1] = x[i + 1];
+    fma2(y[i], y[i + 1], inv, inv, kGrid, kGrid);
+    add2(y[i], y[i + 1], -kGrid, -kGrid);
+    y[i] = copysignf(y[i], x[i]);
+    y[i + 1] = copysignf(y[i + 1], x[i + 1]);
+  }
   uint32_t c;
-  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\tcvt.u32.u8 %0, t;\n\t}"
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
       : "=r"(c)
-      : "f"(copysignf(y0, x0)), "f"(copysignf(y1, x1)));
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
   return c;
 }
 
@@ -153,90 +165,76 @@ __device__ __forceinline__ void report_bad_rows(const Kv4Args &a) {
   }
 }
 
-// One row (key and value of one request, head and slot) is 2 x D / 8 lanes of
-// eight dimensions each: a whole warp for D = 128, half of one for D = 64.  A
-// warp walks `rounds` x U x (32 / lanes of a row) consecutive rows, U rounds of
-// loads under way at once, and for 16-bit rows the next ones too (kAhead; fp32
-// rows, twice the registers, are faster without: 43.8 us in place of 46.6 for
-// 220 MB).
+// One row (key and value of one request, head and slot) is D / 8 lanes when
+// written, a group of 16 dimensions each, and D / 4 when read, eight dimensions
+// each.  A warp walks `rounds` x U x (32 / lanes of a row) consecutive rows, U
+// rounds of loads under way at once; reading requests the next ones too.
 //
 // A short run (64 rows of 32 heads: 2.5 us) is bound by the chain of look-ups in
 // front of its first load.  A long one: 269 MB of bf16 rows and records (51200
-// rows of 8 heads, D = 128) take 59.8 us, 4.5 TB/s, 0.66 of what a copy reaches;
-// the conversions' instructions keep the issue slots three quarters and the
-// integer pipe two thirds busy.  Reading writes twice what it computes: 153 MB in 27.8 us, 5.5
-// TB/s, 0.81 of a copy.
+// rows of 8 heads, D = 128) are written in 46 us, 5.8 TB/s, 0.86 of what a copy
+// reaches; with eight dimensions a lane, and a group's scale found by both of its
+// lanes, 59 us, the conversions' instructions then filling the issue slots.
+// Reading writes twice what it computes: 153 MB in 27.8 us, 5.5 TB/s, 0.81 of a
+// copy.
 template <int D, int U, typename E>
 __global__ void __launch_bounds__(kRowThreads)
 kv4_write_kernel(const Kv4Args a, int rounds) {
-  constexpr int kLanes = D / 4;                 // lanes of a row
+  constexpr int kLanes = D / 8;                 // lanes of a row: a group of 16 each
   constexpr int kSide = 32 / kLanes;            // rows of a warp side by side
   constexpr int R = kv4_record_bytes(D);
-  constexpr bool kAhead = sizeof(E) == 2;
   const int tid = threadIdx.x, lane = tid & 31;
   const int sub = lane % kLanes;                // place within the row
   const bool is_v = sub >= kLanes / 2;
-  const E *base = static_cast<const E *>(is_v ? a.v : a.k) + sub % (kLanes / 2) * 8;
+  const E *base = static_cast<const E *>(is_v ? a.v : a.k) + sub % (kLanes / 2) * 16;
   pdl_trigger();
   pdl_wait();
   const uint32_t warp = (blockIdx.x * kRowThreads + tid) / 32;
   RowWalk<R> w(a, is_v ? a.v_st : a.k_st, is_v ? a.v_sh : a.k_sh,
                warp * static_cast<uint32_t>(rounds * U * kSide) + lane / kLanes);
-  Eight<E> next[U];
-  uint32_t *next_rec[U];
-  int next_req[U];
-  auto load = [&] {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      next_rec[u] = w.ok ? reinterpret_cast<uint32_t *>(w.rec) : nullptr;
-      next_req[u] = w.b;
-      if (w.ok) next[u].load(base + w.dense);
-      else next[u].clear();
-      w.advance(kSide);
-    }
-  };
-  if (kAhead) load();
   for (int round = 0; round < rounds; ++round) {
-    if (!kAhead) load();
-    Eight<E> in[U];
+    Eight<E> in[U][2];
     uint32_t *rec[U];
     int req[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      in[u] = next[u];
-      rec[u] = next_rec[u];
-      req[u] = next_req[u];
+      rec[u] = w.ok ? reinterpret_cast<uint32_t *>(w.rec) : nullptr;
+      req[u] = w.b;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (w.ok) in[u][e].load(base + w.dense + 8 * e);
+        else in[u][e].clear();
+      }
+      w.advance(kSide);
     }
-    if (kAhead && round + 1 < rounds) load();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      uint32_t top = in[u].top();
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      uint32_t top = max(in[u][0].top(), in[u][1].top());
       if (top >= 0x7F800000u) {                 // NaN or infinity: the group becomes zeros
         report(a.status, req[u], SPEC_ERR_NONFINITE);
         top = 0;
-        in[u].clear();
+        in[u][0].clear();
+        in[u][1].clear();
       }
       uint32_t byte = scale_of<E>(top);
       float inv = 0.f;
       if (byte) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(__half2float(__ushort_as_half(byte << 7))));
-      float x[8];
-      in[u].floats(x);
-      uint32_t codes = 0;
+      uint32_t codes[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float y[2];
+      for (int e = 0; e < 2; ++e) {
+        float x[8];
+        in[u][e].floats(x);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) y[e] = __uint_as_float(round_sticky<E>(__float_as_uint(x[2 * i + e])));
-        codes |= codes_of(y[0], y[1], inv) << (8 * i);
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(round_sticky<E>(__float_as_uint(x[i])));
+        codes[e] = codes_of(x, inv);
       }
       // scale bytes of four neighbouring groups to one word
-      byte |= __shfl_down_sync(0xffffffffu, byte, 2) << 8;
-      byte |= __shfl_down_sync(0xffffffffu, byte, 4) << 16;
+      byte |= __shfl_down_sync(0xffffffffu, byte, 1) << 8;
+      byte |= __shfl_down_sync(0xffffffffu, byte, 2) << 16;
       if (rec[u]) {
-        rec[u][sub] = codes;
-        if (sub % 8 == 0) rec[u][D / 4 + sub / 8] = byte;
-        if (D == 64 && sub % 8 == 4) rec[u][D / 4 + 2 + sub / 8] = 0u;
+        *reinterpret_cast<uint2 *>(rec[u] + 2 * sub) = make_uint2(codes[0], codes[1]);
+        if (sub % 4 == 0) rec[u][D / 4 + sub / 4] = byte;
+        if (D == 64 && sub % 4 == 2) rec[u][D / 4 + 2 + sub / 4] = 0u;
       }
     }
   }
@@ -345,11 +343,11 @@ int launch_rows(Kernel kernel, const Kv4Args &args, long long warps, int rounds,
 // that a tree's few rows spread over the GPU; beyond, U rounds at once, and as
 // many turns of them as make kWaves waves of 32 warps on every SM.  U by
 // registers: reading bf16 rows takes 27.8 us with 4 and 30.6 with 2, fp32 rows
-// 35.5 and 32.6; writing 69.7 and 59.9.
+// 35.5 and 32.6; writing 46.0 with 2 and 51.7 with 1.
 template <bool kWrite, int D, typename E>
 int rows_by_size(const Kv4Args &args, void *stream) {
   constexpr int U = !kWrite && sizeof(E) == 2 ? 4 : 2, kWaves = 4;
-  const long long rows = static_cast<long long>(args.T) * args.H, side = 32 / (D / 4);
+  const long long rows = static_cast<long long>(args.T) * args.H, side = 32 / (kWrite ? D / 8 : D / 4);
   if (rows == 0) return SPEC_OK;
   if (rows > 0x7FFFFFFFll) return SPEC_ERR_SHAPE;      // rows are counted in 32 bits
   const long long one = (rows + side - 1) / side, wave = 32ll * sm_count();
