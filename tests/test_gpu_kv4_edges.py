@@ -1,0 +1,84 @@
+"""The 4-bit cache's calls at the edges of what they take: scores and scales at
+the ends of fp32, and the calls that a batch or a caller makes rarely."""
+import numpy as np
+import pytest
+import torch
+
+import token_tree_verification_gb300 as ttv
+from oracle import kv4
+from test_gpu_kv4 import BF16, DTYPES, check_attn, i32, random_records, random_tree, zeros_status
+
+pytestmark = pytest.mark.gpu
+
+
+# Each form of the attention: up to 8, 16, 32 and 128 rows on a key.
+FORMS = pytest.mark.parametrize("Hq,n", [(1, 7), (2, 8), (2, 15), (2, 40)], ids=["8", "16", "32", "128"])
+
+
+@DTYPES
+@FORMS
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("size", [2.0 ** 20, 2.0 ** 24, 2.0 ** 26, 2.0 ** 29, 1e12, 1e25, 1e36])
+def test_scores_of_any_size(dtype, Hq, n, D, size):
+    """Scores so large that fp32 holds no fraction of them: the output lies between the values seen, and is
+    the best key's value where that key leads by more than the scores can be off."""
+    rng = np.random.default_rng(D + n)
+    L = 900
+    rec = random_records(rng, (1, 1, L + n + 2), D)
+    rec[..., L + n:, :] = 255
+    parents = random_tree(rng, n)
+    q = torch.from_numpy((rng.standard_normal((n, Hq, D)) * size).astype(np.float32)).to(dtype)
+    st = zeros_status(1)
+    o = ttv.tree_attn_kv4(q.cuda(), torch.from_numpy(rec).cuda(), i32([L]), i32([0, n]), None, L, st, parents=i32(parents))
+    got = o.double().cpu().numpy()
+    assert st.tolist() == [0] and np.isfinite(got).all()
+    k, v = kv4.values(rec[0, 0, :L + n], D)
+    ok = kv4.sees(parents, L)[:, None, :]
+    x, scale = q.double().numpy(), 1 / np.sqrt(D)
+    s = np.where(ok, np.einsum("ngd,sd->ngs", x, k) * scale, -np.inf)
+    big = np.where(ok, np.einsum("ngd,sd->ngs", np.abs(x), np.abs(k)) * scale, 0).max(-1)
+    # A score is off by at most (2^-21 + D 2^-24) sum |q||k| (query halves, sums of D products in fp32), and
+    # twice that by 2^-22 of itself (its rounding, and the reference's).  40 more make every other weight
+    # less than e^-40 of the best key's, 900 of them together less than 2^-47.
+    order = np.sort(s, -1)
+    clear = order[..., -1] - order[..., -2] > 2 * (2.0 ** -20 + D * 2.0 ** -24) * big + 40
+    assert clear.mean() > 0.5           # (the best two of 900 keys are seldom that close)
+    best = v[s.argmax(-1)]
+    # the weight enters the product as a half (2^-11, two of them 2^-22) and the sum as it is; then the output's rounding
+    tol = (2.0 ** -11 + 2.0 ** -8 if dtype == BF16 else 2.0 ** -21) * np.abs(best) * 1.01 + 2.0 ** -47 * np.abs(v).max()
+    assert (np.abs(got - best) <= tol)[clear].all()
+    seen = np.broadcast_to(ok[:, 0, :, None], (n, L + n, D))
+    low = np.where(seen, v[None], np.inf).min(1)[:, None]
+    high = np.where(seen, v[None], -np.inf).max(1)[:, None]
+    room = 2.0 ** -7 * np.abs(v).max()
+    assert (got >= low - room).all() and (got <= high + room).all()
+
+
+@DTYPES
+@FORMS
+@pytest.mark.parametrize("scale,size", [(1e-9, 1e-36), (1e-38, 1.0), (1e-42, 1e3), (1e-42, 1e-36)])
+def test_scales_so_small_that_all_keys_weigh_the_same(dtype, Hq, n, scale, size):
+    """The factor of a row's scores may fall below what fp32 holds; masked keys stay out."""
+    rng = np.random.default_rng(n)
+    L, D = [150, 0], 128
+    off = [0, n, 2 * n]
+    rec = random_records(rng, (2, 1, 200), D)
+    parents = random_tree(rng, n) + random_tree(rng, n)
+    q = torch.from_numpy((rng.standard_normal((2 * n, Hq, D)) * size).astype(np.float32)).to(dtype)
+    check_attn(q, rec, L, off, parents, scale=scale)
+
+
+@DTYPES
+@FORMS
+def test_a_query_with_an_infinity_gives_nan_in_its_row_alone(dtype, Hq, n):
+    rng = np.random.default_rng(n)
+    D, L = 128, 300
+    rec = torch.from_numpy(random_records(rng, (1, 1, L + n), D)).cuda()
+    q = torch.from_numpy(rng.standard_normal((n, Hq, D)).astype(np.float32)).to(dtype).cuda()
+    par, off, st = i32(random_tree(rng, n)), i32([0, n]), zeros_status(1)
+    ref = ttv.tree_attn_kv4(q, rec, i32([L]), off, None, L, st, parents=par)
+    q[n // 2, 0, 5] = float("inf")
+    got = ttv.tree_attn_kv4(q, rec, i32([L]), off, None, L, st, parents=par)
+    assert torch.isnan(got[n // 2, 0]).all()
+    got[n // 2, 0] = ref[n // 2, 0]
+    assert torch.equal(got, ref) and st.tolist() == [0]

@@ -204,7 +204,8 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int up = row_exponent(top);
       const float grow = power_of_two(up);
-      const float c = a.scale_log2 * power_of_two(-up);
+      // (a factor of zero would make NaN of a masked score; one this small hides all)
+      const float c = fmaxf(a.scale_log2 * power_of_two(-up), power_of_two(-126));
       c_row[nt][0] = __shfl_sync(0xffffffffu, c, 8 * t);
       c_row[nt][1] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
 #pragma unroll
@@ -245,7 +246,9 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
 
     // ---- the keys
     float o[NT][KS][4];
-    float m_ref[NT][2], nbase[NT][2], l_row[NT][2];
+    // a row's reference as 8 - reference, how large a score may come against it (-inf:
+    // there is no reference yet), and its sum of weights
+    float nbase[NT][2], limit[NT][2], l_row[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -254,8 +257,8 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
         for (int e = 0; e < 4; ++e) o[nt][j][e] = 0.f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        m_ref[nt][e] = -INFINITY;
         nbase[nt][e] = kWeightLog2;
+        limit[nt][e] = -INFINITY;
         l_row[nt][e] = 0.f;
       }
     }
@@ -339,28 +342,31 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
                 if (!row_sees(see, key0 + 16 * mt + kn + k, G.L, G.keys)) sc[mt][nt][2 * k + e] = -INFINITY;
           }
       }
+      // x = score - reference + 8, in powers of two, and whether a reference moves
+      float pw[2][NT][4], mx[NT][2];
       bool want = false;
-      float mx[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float m0 = fmaxf(sc[0][nt][e], sc[0][nt][2 + e]), m1 = fmaxf(sc[1][nt][e], sc[1][nt][2 + e]);
-          mx[nt][e] = fmaxf(m0, m1) * c_row[nt][e];
-          want |= mx[nt][e] > m_ref[nt][e] + kMoveLog2;
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              pw[mt][nt][2 * k + e] = fmaf(sc[mt][nt][2 * k + e], c_row[nt][e], nbase[nt][e]);
+          mx[nt][e] = fmaxf(fmaxf(pw[0][nt][e], pw[0][nt][2 + e]), fmaxf(pw[1][nt][e], pw[1][nt][2 + e]));
+          want |= mx[nt][e] > limit[nt][e];
         }
       // The weights, in fp32 calls at the present references, which hardly ever
       // move, before the vote on them (16 rows, 256 units behind 4096: 65.7 -> 62.8
       // us; bf16 calls have little to overlap: 178 -> 180 us on long prefixes)
-      float pw[2][NT][4];
       auto weigh = [&] {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              pw[mt][nt][e] = fast_exp2(fmaf(sc[mt][nt][e], c_row[nt][e & 1], nbase[nt][e & 1]));
+            for (int e = 0; e < 4; ++e) pw[mt][nt][e] = fast_exp2(pw[mt][nt][e]);
       };
       if (F32) weigh();
       if (__any_sync(0xffffffffu, want)) {
@@ -371,20 +377,25 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
             float m = mx[nt][e];
 #pragma unroll
             for (int x = 4; x < 32; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-            if (m > m_ref[nt][e] + kMoveLog2) {
-              m = ceilf(m);
-              const float alpha = exp2f(m_ref[nt][e] - m);    // 0 the first time
-              l_row[nt][e] *= alpha;
+            if (m > limit[nt][e]) {
+              const Move move(m, nbase[nt][e], limit[nt][e] == -INFINITY);
+              l_row[nt][e] *= move.factor;
 #pragma unroll
               for (int j = 0; j < KS; ++j) {
-                o[nt][j][e] *= alpha;
-                o[nt][j][2 + e] *= alpha;
+                o[nt][j][e] *= move.factor;
+                o[nt][j][2 + e] *= move.factor;
               }
-              m_ref[nt][e] = m;
-              nbase[nt][e] = kWeightLog2 - m;
+              nbase[nt][e] = move.next;
+              limit[nt][e] = kWeightLog2 + kMoveLog2;
+#pragma unroll
+              for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const float x = fmaf(sc[mt][nt][2 * k + e], c_row[nt][e], move.base) - move.less;
+                  pw[mt][nt][2 * k + e] = F32 ? fast_exp2(x) : x;
+                }
             }
           }
-        if (F32) weigh();
       }
       if (!F32) weigh();
       // ---- weights, and their product with V
@@ -465,7 +476,7 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
 #pragma unroll
           for (int x = 4; x < 32; x *= 2) l += __shfl_xor_sync(0xffffffffu, l, x);
           if (g == 0) {
-            s_m[warp][r] = m_ref[nt][e];
+            s_m[warp][r] = limit[nt][e] == -INFINITY ? -INFINITY : kWeightLog2 - nbase[nt][e];
             s_l[warp][r] = l;
           }
           float *dst = so + (warp * C::kRows + r) * C::kOStride + (D / 8) * g;

@@ -180,6 +180,30 @@ struct TileList {
 constexpr float kWeightLog2 = 8.f;
 constexpr float kMoveLog2 = 7.f;
 
+// A move of a row's reference: `most` is the row's largest x = score - reference
+// + 8 (score, all in powers of two, being s c) and `old` the present 8 -
+// reference.  From 2^24 on fp32 does not hold every whole number, and s c + (8 -
+// reference) may miss the range of halves either way: at 2^27 the steps are 16.
+// There x keeps its rounding at the old reference and is brought to the new one by
+// a subtraction, which leaves the largest score a weight of at least 1.
+constexpr float kWholeEnd = 16777216.f;
+__device__ __forceinline__ float reference_step(float most) {
+  return fabsf(most) < kWholeEnd ? ceilf(most - kWeightLog2) : most;
+}
+struct Move {
+  float factor, next;       // of what is summed; the new 8 - reference
+  float base, less;         // x = s c + base - less
+  __device__ __forceinline__ explicit Move(float old) : factor(1.f), next(old), base(old), less(0.f) {}   // none
+  __device__ __forceinline__ Move(float most, float old, bool fresh) {
+    const float by = reference_step(most);
+    factor = fresh ? 0.f : exp2f(-by);
+    next = old - by;
+    const bool steep = !(fabsf(next) < kWholeEnd);
+    base = steep ? old : next;
+    less = steep ? by : 0.f;
+  }
+};
+
 constexpr int kMaxSplits = 16;
 
 // A row's query is taken as halves: scaled by 2^up so that its largest finite

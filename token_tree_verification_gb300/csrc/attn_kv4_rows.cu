@@ -412,7 +412,7 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
         // the reference moves, which it hardly ever does.)
         uint32_t h[kHalf / 16][8];
         float tile_sum, most;
-        auto weigh = [&] {
+        auto weigh = [&](auto exponents) {
           float x[2][32];
           tc::ld32(s_col, x[0]);
           tc::ld32(s_col + 32, x[1]);
@@ -421,8 +421,7 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
           most = -INFINITY;
 #pragma unroll
           for (int part = 0; part < 2; ++part) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) fma2(x[part][j], x[part][j + 1], c, c, shift, shift);
+            exponents(x[part]);
             if (!whole) {
               const uint32_t sees = sees32(see, k0 + 32 * part, G.L, p.window);
 #pragma unroll
@@ -443,16 +442,18 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
           add2(s0, s1, s2, s3);
           tile_sum = s0 + s1;
         };
-        weigh();
+        weigh([&](float(&x)[32]) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) fma2(x[j], x[j + 1], c, c, shift, shift);
+        });
         const bool fresh = ref == -INFINITY;
         const bool moves = most > (fresh ? -INFINITY : kWeightLog2 + kMoveLog2);
         if (__any_sync(0xffffffffu, moves)) {
-          float factor = 1.f;
+          Move move(shift);
           if (moves) {
-            const float by = ceilf(most - kWeightLog2);
-            factor = fresh ? 0.f : exp2f(-by);
-            ref = (fresh ? 0.f : ref) + by;
-            shift -= by;
+            move = Move(most, shift, fresh);
+            shift = move.next;
+            ref = kWeightLog2 - shift;
           }
           if (i > 0) {
             // O holds the products of this turn's earlier tiles
@@ -465,13 +466,21 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
               tc::ld8(o_col + j, o);
               tc::wait_ld();
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] *= factor;
+              for (int e = 0; e < 8; ++e) o[e] *= move.factor;
               tmem_st(o_col + j, o);
             }
             tc::wait_st();
           }
-          sum *= factor;
-          weigh();
+          sum *= move.factor;
+          const bool steep = __any_sync(0xffffffffu, move.less != 0.f);
+          weigh([&](float(&x)[32]) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) fma2(x[j], x[j + 1], c, c, move.base, move.base);
+            if (steep) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] -= move.less;
+            }
+          });
         }
         tc::fence_before_sync();
         __syncwarp();

@@ -509,7 +509,7 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
             const bool fresh = ref == -INFINITY;
             float2 move = make_float2(1.f, 0.f);
             if (m > (fresh ? -INFINITY : kWeightLog2 + kMoveLog2)) {
-              const float by = ceilf(m - kWeightLog2);      // (0 stands for a reference that is not there)
+              const float by = reference_step(m);           // (0 stands for a reference that is not there)
               move = make_float2(fresh ? 0.f : exp2f(-by), -by);
               s_ref[par][r] = (fresh ? 0.f : ref) + by;
               s_n[par][r] -= by;
