@@ -82,3 +82,30 @@ def test_a_query_with_an_infinity_gives_nan_in_its_row_alone(dtype, Hq, n):
     assert torch.isnan(got[n // 2, 0]).all()
     got[n // 2, 0] = ref[n // 2, 0]
     assert torch.equal(got, ref) and st.tolist() == [0]
+
+
+# 9 to 16 rows on a key.  152 units (a request's rows on one KV head) are not split on this GPU's 152 SMs, so a
+# CTA takes all the tiles of 128 keys: 11 to 15 here.  Eight units are split.
+LONG = [  # D, Hq, Hkv, prefixes, nodes
+    (128, 38, 38, [1900, 1660, 1400, 1285], [16, 9, 12, 16]),       # 15, 14, 12 and 11 tiles
+    (64, 38, 38, [1900, 1660, 1400, 1285], [9, 16, 11, 13]),
+    (128, 114, 38, [1500, 1850, 1300, 1600], [5, 4, 5, 3]),         # three query heads on each key
+    # one request with many more rows than the mean, an odd and an even number of tiles in each turn
+    (128, 38, 38, [1600, 300, 1285, 20], [45, 1, 1, 2]), (64, 38, 38, [1600, 300, 1285, 20], [45, 1, 1, 2]),
+    (128, 38, 38, [40, 1400, 900, 20], [3, 58, 1, 1]), (64, 38, 38, [40, 1400, 900, 20], [3, 58, 1, 1]),
+    (128, 2, 2, [9000, 300, 2000, 20], [45, 1, 1, 2]), (64, 2, 2, [9000, 300, 2000, 20], [45, 1, 1, 2])]
+
+
+@DTYPES
+@pytest.mark.parametrize("D,Hq,Hkv,L,n", LONG)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1290, 300)], ids=["all", "window"])
+def test_nine_to_sixteen_rows_over_many_tiles_and_turns(dtype, D, Hq, Hkv, L, n, window, sinks):
+    rng = np.random.default_rng(D + Hq + n[0])
+    off = np.concatenate([[0], np.cumsum(n)])
+    assert 9 <= -(-off[-1] // len(n)) * (Hq // Hkv) <= 16
+    rec = random_records(rng, (len(L), Hkv, max(a + b for a, b in zip(L, n)) + 3), D)
+    for b, (a, c) in enumerate(zip(L, n)):
+        rec[b, :, a + c:] = 255
+    parents = sum((random_tree(rng, c) for c in n), [])
+    q = torch.from_numpy((2 * rng.standard_normal((off[-1], Hq, D))).astype(np.float32)).to(dtype)
+    check_attn(q, rec, L, off, parents, window, sinks)
