@@ -1,5 +1,9 @@
 """The 4-bit cache's calls at the edges of what they take: scores and scales at
 the ends of fp32, and the calls that a batch or a caller makes rarely."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -109,3 +113,52 @@ def test_nine_to_sixteen_rows_over_many_tiles_and_turns(dtype, D, Hq, Hkv, L, n,
     parents = sum((random_tree(rng, c) for c in n), [])
     q = torch.from_numpy((2 * rng.standard_normal((off[-1], Hq, D))).astype(np.float32)).to(dtype)
     check_attn(q, rec, L, off, parents, window, sinks)
+
+
+WITHOUT_GETTERS = """
+import torch
+torch.cuda.init()
+for owner, name in ((torch._C, "_cuda_getCurrentRawStream"), (torch._C._dynamo.guards, "_empty_strided_cuda")):
+    if hasattr(owner, name):
+        delattr(owner, name)
+import token_tree_verification_gb300 as ttv
+i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+cache, st = ttv.make_kv4_cache(1, 2, 20, 64), i32(0)
+k = torch.ones((4, 2, 64), dtype=torch.bfloat16, device="cuda")
+side = torch.cuda.Stream()
+side.wait_stream(torch.cuda.current_stream())
+with torch.cuda.stream(side):
+    ttv.kv4_write(k, k, cache, i32(0), i32(0, 4), st)
+    o = ttv.tree_attn_kv4(k[:1], cache, i32(3), i32(0, 1), None, 3, st, parents=i32(-1))
+    new = ttv.kv4_compact(cache, i32(3), i32(0, 1), i32(0), i32(0), st)
+    back, _ = ttv.kv4_read(cache, i32(0), i32(0, 4), st, rows=4)
+torch.cuda.synchronize()
+one = 6 * 0.171875          # 1 in the cache: 1/6 lies between the scales 0.15625 and 0.171875, nearer to the latter
+assert (back == one).all() and (o == one).all() and new.item() == 4 and st.item() == 0
+print("the same")
+"""
+
+
+def test_calls_without_the_private_getters_of_torch():
+    r = subprocess.run([sys.executable, "-c", WITHOUT_GETTERS], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "the same" in r.stdout, r.stderr[-2000:]
+
+
+@DTYPES
+def test_outputs_are_tensors_as_torch_makes_them(dtype):
+    """Under deterministic algorithms, what a call leaves of a new output is filled as torch fills it."""
+    cache, st, D = ttv.make_kv4_cache(2, 2, 30, 128), zeros_status(2), 128
+    q = torch.ones((6, 2, D), dtype=dtype, device="cuda")
+    parents, off = i32([-1, 0, -1, 0, 9, 9]), i32([0, 2, 4])
+    junk = [torch.ones(64 << 20, dtype=torch.uint8, device="cuda") for _ in range(3)]     # no NaN in what is reused
+    del junk
+    torch.use_deterministic_algorithms(True)
+    try:
+        k, v = ttv.kv4_read(cache, i32([0, 0]), off, st, rows=6, dtype=dtype)
+        o = ttv.tree_attn_kv4(q, cache, i32([5, 5]), off, None, 5, st, parents=parents)
+    finally:
+        torch.use_deterministic_algorithms(False)
+    for x in (k, v, o):       # two rows behind the last request
+        assert torch.isnan(x[4:]).all() and torch.isfinite(x[:4]).all()
+    assert st.tolist() == [0, 0]

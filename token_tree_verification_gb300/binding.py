@@ -275,12 +275,24 @@ def kv_compact(k_cache, v_cache, prefix_lens, offsets, path_nodes, accept_len, s
 # ---------------------------------------------------------------- 4-bit cache
 _KV4_DIMS = {144: 128, 80: 64}     # bytes of a slot record -> head dimension
 _U8, _I32 = torch.uint8, torch.int32
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
-# A new tensor (shape, strides, dtype) on the current device.  Outputs of a few
-# microseconds' work are made by it: torch.empty goes through the dispatcher,
-# 4.2 us beside a launch on a Grace core in place of 1.6 us.
-_empty = torch._C._dynamo.guards._empty_strided_cuda
+# Parts of torch that are not public, used where they are there: the getters of the
+# current device and stream, and a new tensor without the dispatcher (beside a
+# launch 1.6 us of host time against 4.2 on a Grace core, an output of a call whose
+# kernels take a few microseconds).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
+_empty_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+_deterministic = torch.are_deterministic_algorithms_enabled      # torch then fills new tensors
+
+
+def _empty(shape, strides, dtype):
+    """A new tensor on the current device."""
+    if _empty_cuda is None or _deterministic():
+        return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+    return _empty_cuda(shape, strides, dtype)
+
+
 _DTYPES = {torch.bfloat16: SPEC_BF16, torch.float32: SPEC_F32}
 
 
