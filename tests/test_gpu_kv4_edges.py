@@ -162,3 +162,84 @@ def test_outputs_are_tensors_as_torch_makes_them(dtype):
     for x in (k, v, o):       # two rows behind the last request
         assert torch.isnan(x[4:]).all() and torch.isfinite(x[:4]).all()
     assert st.tolist() == [0, 0]
+
+
+class Busy:
+    """Some milliseconds of copies, 2 GB each, queued on a stream."""
+
+    def __init__(self):
+        self.a, self.b = torch.zeros((2, 1 << 30), dtype=torch.uint8, device="cuda").unbind()
+
+    def queue(self, stream, copies=60):
+        with torch.cuda.stream(stream):
+            for _ in range(copies):
+                self.b.copy_(self.a)
+
+
+def test_outputs_on_another_stream_beside_work_in_flight():
+    """The caller's stream is busy with a tensor that it has dropped: the output of a call on another stream,
+    which does not wait, is not that tensor's memory.  Nor is an output that the caller's stream still reads
+    handed to the next call."""
+    rng = np.random.default_rng(31)
+    n, main, side, busy = 9000, torch.cuda.current_stream(), torch.cuda.Stream(), Busy()
+    cache = torch.from_numpy(random_records(rng, (1, 8, n), 128)).cuda()
+    start, off, st = i32([0]), i32([0, n]), zeros_status(1)
+    q, lens, one, par = torch.ones((1, 8, 128), dtype=BF16, device="cuda"), i32([n - 1]), i32([0, 1]), i32([-1])
+    want = ttv.kv4_read(cache, start, off, st, rows=n) + (ttv.tree_attn_kv4(q, cache, lens, one, None, n, st, parents=par),)
+    calls = lambda: (ttv.kv4_read(cache, start, off, st, rows=n, stream=side)  # noqa: E731
+                     + (ttv.tree_attn_kv4(q, cache, lens, one, None, n, st, parents=par, stream=side),))
+    kept = [torch.empty_like(x) for x in want]
+    for _ in range(3):
+        dropped = [torch.full_like(x, 3.0) for x in want]
+        torch.cuda.synchronize()
+        busy.queue(main)
+        for a, b in zip(kept, dropped):
+            a.copy_(b)
+        addresses = {x.data_ptr() for x in dropped}
+        del dropped, b
+        out = calls()
+        assert not addresses & {x.data_ptr() for x in out}
+        side.synchronize()
+        assert not main.query()            # (the side stream's calls were done long before)
+        torch.cuda.synchronize()
+        assert all((x == 3.0).all() for x in kept)
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    for _ in range(3):
+        out = calls()
+        main.wait_stream(side)
+        busy.queue(main)
+        for a, b in zip(kept, out):
+            a.copy_(b)
+        addresses = {x.data_ptr() for x in out}
+        del out, b
+        again = calls()
+        assert not main.query() and not addresses & {x.data_ptr() for x in again}
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(kept, want))
+        del again
+    assert st.tolist() == [0]
+
+
+def test_outputs_dropped_while_their_call_is_under_way():
+    """Work on the other stream keeps the calls from starting: what they will write is not given to anyone."""
+    rng = np.random.default_rng(32)
+    n, side, busy = 2000, torch.cuda.Stream(), Busy()
+    cache = torch.from_numpy(random_records(rng, (1, 8, n), 128)).cuda()
+    start, off, st = i32([0]), i32([0, n]), zeros_status(1)
+    path, acc = i32([[0]]), i32([0])
+    q, lens, one, par = torch.ones((1, 8, 128), dtype=BF16, device="cuda"), i32([n - 1]), i32([0, 1]), i32([-1])
+    for turn in range(4):            # (the first loads the kernels that it launches, which takes its time)
+        torch.cuda.synchronize()
+        busy.queue(side)
+        out = list(ttv.kv4_read(cache, start, off, st, rows=n, stream=side))
+        out.append(ttv.tree_attn_kv4(q, cache, lens, one, None, n, st, parents=par, stream=side))
+        out.append(ttv.kv4_compact(cache, lens, one, path, acc, st, stream=side))
+        addresses = {x.data_ptr() for x in out}
+        shapes = [(x.shape, x.dtype) for x in out]
+        del out
+        fresh = [torch.full(s, 5, dtype=t, device="cuda") for s, t in shapes]
+        assert turn == 0 or not side.query()
+        assert not addresses & {x.data_ptr() for x in fresh}
+        torch.cuda.synchronize()
+        assert all((x == 5).all() for x in fresh)
+    assert st.tolist() == [0]

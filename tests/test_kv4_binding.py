@@ -1,9 +1,13 @@
-"""The package imports wherever the public parts of torch are there."""
+"""The binding's own work on the host: what it needs of torch at import, and
+whose memory the outputs of the 4-bit cache's calls are."""
+import contextlib
 import os
 import subprocess
 import sys
+import types
 
 import pytest
+import torch
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -17,3 +21,60 @@ def test_the_package_imports_without_a_private_part_of_torch(missing):
             "assert ttv.tree_attn and ttv.kv4_write and synthetic.make_workload\n")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=ROOT)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+class FakeTensor:
+    """What the binding asks of a CUDA tensor."""
+
+    def __init__(self, shape, dtype, made_on=None):
+        self.shape, self.dtype, self.made_on, self.recorded = shape, dtype, made_on, []
+
+    def get_device(self):
+        return 0
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return int(torch.Size(self.shape).numel())
+
+    def data_ptr(self):
+        return 4096
+
+    def record_stream(self, stream):
+        self.recorded.append(stream)
+
+
+class FakeStream:
+    def __init__(self, name):
+        self.name, self.cuda_stream = name, 1
+
+
+def test_outputs_of_a_call_on_another_stream_are_memory_of_that_stream(monkeypatch):
+    """Allocated while it is current, so that the allocator orders them behind its work and not another's; kept
+    from reuse until the caller's stream is done with them too."""
+    from token_tree_verification_gb300 import binding
+    main, side = FakeStream("main"), FakeStream("side")
+    now = [main]
+
+    @contextlib.contextmanager
+    def stream(s):
+        now.append(s)
+        yield
+        now.pop()
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *_: now[-1])
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(binding, "_current_device", lambda: 0)
+    monkeypatch.setattr(binding, "_current_stream", lambda _: 1)
+    monkeypatch.setattr(binding, "_empty", lambda shape, strides, dtype: FakeTensor(shape, dtype, now[-1].name))
+    monkeypatch.setattr(binding, "_lib", types.SimpleNamespace(**{
+        name: lambda *_: 0 for name in ("spec_kv4_read", "spec_tree_attn_kv4", "spec_kv4_compact")}))
+    i32 = lambda *shape: FakeTensor(shape, torch.int32)  # noqa: E731
+    cache, q = FakeTensor((2, 4, 30, 144), torch.uint8), FakeTensor((6, 8, 128), torch.bfloat16)
+    for s, made_on, others in ((None, "main", []), (side, "side", [main])):
+        out = list(binding.kv4_read(cache, i32(2), i32(3), i32(2), rows=6, stream=s))
+        out.append(binding.tree_attn_kv4(q, cache, i32(2), i32(3), None, 20, i32(2), parents=i32(6), stream=s))
+        out.append(binding.kv4_compact(cache, i32(2), i32(3), i32(2, 4), i32(2), i32(2), stream=s))
+        assert [x.made_on for x in out] == [made_on] * 4
+        assert all(x.recorded == others for x in out)

@@ -293,6 +293,20 @@ def _empty(shape, strides, dtype):
     return _empty_cuda(shape, strides, dtype)
 
 
+def _new(stream, shape, strides, dtype):
+    """A new output of a call on ``stream`` (None: the current one).  It is memory
+    of that stream, so that nothing else in flight still uses what the call
+    writes, and once dropped it waits for the current stream's work too, which
+    may read it."""
+    if stream is None:
+        return _empty(shape, strides, dtype)
+    current = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = _empty(shape, strides, dtype)
+    t.record_stream(current)
+    return t
+
+
 _DTYPES = {torch.bfloat16: SPEC_BF16, torch.float32: SPEC_F32}
 
 
@@ -395,11 +409,8 @@ def kv4_read(kv_cache, start, offsets, status, rows=None, dtype=torch.bfloat16, 
             raise ValueError("kv4_read needs the number of rows, or out")
         T, ks0, ks1 = rows, Hkv * D, D
         vs0, vs1 = ks0, ks1
-        k = _empty((T, Hkv, D), (ks0, ks1, 1), dtype)
-        v = _empty((T, Hkv, D), (ks0, ks1, 1), dtype)
-        if stream is not None:       # made for the current stream, used on another
-            k.record_stream(stream)
-            v.record_stream(stream)
+        k = _new(stream, (T, Hkv, D), (ks0, ks1, 1), dtype)
+        v = _new(stream, (T, Hkv, D), (ks0, ks1, 1), dtype)
     else:
         k, v = out
         T = k.shape[0]
@@ -425,9 +436,7 @@ def kv4_compact(kv_cache, prefix_lens, offsets, path_nodes, accept_len, status,
     index, B, Hkv, S_cap, D = _kv4_cache(kv_cache)
     W = path_nodes.shape[-1]
     if new_prefix_lens is None:
-        new_prefix_lens = _empty((B,), (1,), _I32)
-        if stream is not None:
-            new_prefix_lens.record_stream(stream)
+        new_prefix_lens = _new(stream, (B,), (1,), _I32)
     prefix, offsets, status = _per_request(index, B, prefix_lens, offsets, status, "prefix_lens")
     rc = lib.spec_kv4_compact(kv_cache.data_ptr(), B, Hkv, D, S_cap, prefix, offsets,
                               _i32(index, B * W, path_nodes, "path_nodes"),
@@ -463,9 +472,7 @@ def tree_attn_kv4(q, kv_cache, prefix_lens, offsets, mask, max_prefix, status, o
     else:
         raise ValueError("tree_attn_kv4 needs a mask or the parent array")
     if o is None:
-        o = _empty((T, Hq, D), (Hq * D, D, 1), q.dtype)
-        if stream is not None:
-            o.record_stream(stream)
+        o = _new(stream, (T, Hq, D), (Hq * D, D, 1), q.dtype)
     elif o.dtype is not q.dtype or o.get_device() != index or o.shape != q.shape or not o.is_contiguous():
         raise ValueError("o must be like q")
     prefix, offsets, status = _per_request(index, B, prefix_lens, offsets, status, "prefix_lens")
