@@ -348,8 +348,9 @@ size_t spec_kv4_record_bytes(int D);   /* 0 when D is neither 64 nor 128 */
  *
  *   k, v      [T][Hkv][D]  dtype (SPEC_BF16 or SPEC_F32), 16-byte aligned, at
  *             the given strides in elements between rows and between heads
- *             (each a multiple of 16 bytes; the D elements of a head are
- *             contiguous), so that rows may lie inside a fused projection
+ *             (each a multiple of 16 bytes, unless there is only one row or
+ *             head to step between; the D elements of a head are contiguous),
+ *             so that rows may lie inside a fused projection
  *   start     [B] int32, offsets [B+1] int32 (a request may have no rows; it
  *             has no upper limit of rows)
  *   T         rows of k and v; rows at or behind offsets[B] are ignored, T = 0

@@ -243,3 +243,27 @@ def test_outputs_dropped_while_their_call_is_under_way():
         torch.cuda.synchronize()
         assert all((x == 5).all() for x in fresh)
     assert st.tolist() == [0]
+
+
+@DTYPES
+@pytest.mark.parametrize("D", [64, 128])
+def test_single_rows_and_heads_of_any_stride(dtype, D):
+    """torch reports anything as the stride of a dimension of one, an odd one too."""
+    rng = np.random.default_rng(D)
+    x = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).to(dtype).cuda()  # noqa: E731
+    single = x(D, 1).t()[:, None, :]
+    assert single.shape == (1, 1, D) and single.stride(0) == 1 and single.is_contiguous()
+    one_row, one_head = x(3 * D + 3)[:3 * D].view(3, D).as_strided((1, 3, D), (5, D, 1)), x(7, D).as_strided((7, 1, D), (D, 3, 1))
+    for rows in (single, one_row, one_head):
+        T, H, _ = rows.shape
+        cache, st = ttv.make_kv4_cache(1, H, 9, D), zeros_status(1)
+        ttv.kv4_write(rows, rows, cache, i32([1]), i32([0, T]), st)
+        want = np.zeros(cache.shape, np.uint8)
+        kv4.write(want, rows.float().cpu().numpy(), rows.float().cpu().numpy(), [1], [0, T])
+        np.testing.assert_array_equal(cache.cpu().numpy(), want)
+        out = torch.full((2, T * H * D), 7.0, dtype=dtype, device="cuda")
+        out = [y.as_strided((T, H, D), rows.stride(), y.storage_offset()) for y in out]
+        ttv.kv4_read(cache, i32([1]), i32([0, T]), st, out=out)
+        for got, ref in zip(out, kv4.read(want, D, [1], [0, T])):
+            np.testing.assert_array_equal(got.double().cpu().numpy(), ref)
+        assert st.tolist() == [0]

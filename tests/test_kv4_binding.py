@@ -1,6 +1,7 @@
 """The binding's own work on the host: what it needs of torch at import, and
 whose memory the outputs of the 4-bit cache's calls are."""
 import contextlib
+import ctypes
 import os
 import subprocess
 import sys
@@ -78,3 +79,18 @@ def test_outputs_of_a_call_on_another_stream_are_memory_of_that_stream(monkeypat
         out.append(binding.kv4_compact(cache, i32(2), i32(3), i32(2, 4), i32(2), i32(2), stream=s))
         assert [x.made_on for x in out] == [made_on] * 4
         assert all(x.recorded == others for x in out)
+
+
+@pytest.mark.parametrize("name", ["spec_kv4_write", "spec_kv4_read"])
+def test_strides_between_single_rows_and_heads_are_not_looked_at(name):
+    """What torch reports for a dimension of one may be anything."""
+    from token_tree_verification_gb300 import binding, build
+    build.build()
+    fake = ctypes.c_void_p(0x1000)       # never dereferenced: T = 0 launches nothing
+
+    def call(T, H, strides, dtype=1):
+        return getattr(binding.load(), name)(fake, fake, dtype, 1, T, H, 128, *strides, fake, 8, fake, fake, fake, None)
+
+    assert call(0, 2, (1, 128, -3, 128)) == 0
+    assert call(0, 1, (1, 7, -3, -9)) == 0
+    assert call(0, 2, (256, 1, 256, 128)) == -11 and call(0, 2, (256, -128, 256, 128)) == -2      # two heads

@@ -311,13 +311,16 @@ kv4_read_kernel(const Kv4Args a, int rounds) {
 }
 
 // Checks that both calls share.  Dense rows: 16-byte vectors, so every row
-// and head starts on a 16-byte boundary.
+// and head starts on a 16-byte boundary.  A stride between rows or heads of which
+// there is only one is never taken, whatever it is: it becomes 0.
 int check_rows(const void *k, const void *v, int dtype, int B, int T, int Hkv, int D,
-               long long k_st, long long k_sh, long long v_st, long long v_sh, const void *kv, int S_cap,
+               int64_t &k_st, int64_t &k_sh, int64_t &v_st, int64_t &v_sh, const void *kv, int S_cap,
                const int32_t *start, const int32_t *offsets, const int32_t *status) {
   if (((!k || !v) && T != 0) || !kv || !start || !offsets || !status) return SPEC_ERR_NULL;
   if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_DTYPE;
   if (B < 1 || T < 0 || Hkv < 1 || S_cap < 1 || (D != 64 && D != 128)) return SPEC_ERR_SHAPE;
+  if (T <= 1) k_st = v_st = 0;
+  if (Hkv == 1) k_sh = v_sh = 0;
   const int es = dtype == SPEC_F32 ? 4 : 2;
   if (k_st < 0 || k_sh < 0 || v_st < 0 || v_sh < 0) return SPEC_ERR_SHAPE;
   if (((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(kv)) & 15) ||
