@@ -103,8 +103,12 @@ __device__ __forceinline__ void store_row4(E *dst, float4 v) {
 }
 
 // mbar_wait for roles that wait long and often: the thread is suspended up to
-// 10 us a try instead of polling through the issue slots of the working warps.
-// (`bar` is a shared-memory address.)
+// 10 us a try (3.8 us, measured) instead of polling through the issue slots of the
+// working warps.  The limit is a number of tries, 3.8 s of them and at most 10 s,
+// never less than kWaitLimitNs while a try takes 2 us: a look at a clock, whichever
+// way, costs the loops that wait 1 to 2% (128-node trees 135.7 -> 137.5 us and
+// more).  (`bar` is a shared-memory address.)
+constexpr uint32_t kSleepTries = 1000000;
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
@@ -116,9 +120,9 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
-__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity, uint32_t tries = kSleepTries) {
 #pragma unroll 1
-  for (uint32_t it = 0; it < kWaitLimitNs / 10000; ++it)
+  for (uint32_t it = 0; it < tries; ++it)
     if (mbar_try(bar, parity)) return true;
   return false;
 }
