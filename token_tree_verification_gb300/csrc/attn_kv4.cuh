@@ -355,7 +355,8 @@ inline void cluster_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[
 }
 
 // Clusters of `cs` CTAs that run at once: fewer than SMs / cs, since a cluster
-// stays within one of the GPU's groups of SMs.
+// stays within one of the GPU's groups of SMs.  0 when it cannot be said now: the
+// next launch asks again (and no later call of the program meets the error).
 template <typename Kernel>
 int clusters_at_once(Kernel kernel, int cs, int threads, size_t smem, int dev, KernelState *state) {
   const int known = state->at_once[dev][cs].load(std::memory_order_relaxed);
@@ -366,7 +367,10 @@ int clusters_at_once(Kernel kernel, int cs, int threads, size_t smem, int dev, K
   cfg.gridDim = dim3(cs, 1, 1);
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 0) n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 0) {
+    cudaGetLastError();
+    return 0;
+  }
   state->at_once[dev][cs].store(n + 1, std::memory_order_relaxed);
   return n;
 }
