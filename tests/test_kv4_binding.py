@@ -42,8 +42,15 @@ class FakeTensor:
     def data_ptr(self):
         return 4096
 
+    def stride(self):
+        return tuple(int(torch.Size(self.shape[i + 1:]).numel()) for i in range(len(self.shape)))
+
     def record_stream(self, stream):
         self.recorded.append(stream)
+
+
+def i32(*shape):
+    return FakeTensor(shape, torch.int32)
 
 
 class FakeStream:
@@ -71,7 +78,6 @@ def test_outputs_of_a_call_on_another_stream_are_memory_of_that_stream(monkeypat
     monkeypatch.setattr(binding, "_empty", lambda shape, strides, dtype: FakeTensor(shape, dtype, now[-1].name))
     monkeypatch.setattr(binding, "_lib", types.SimpleNamespace(**{
         name: lambda *_: 0 for name in ("spec_kv4_read", "spec_tree_attn_kv4", "spec_kv4_compact")}))
-    i32 = lambda *shape: FakeTensor(shape, torch.int32)  # noqa: E731
     cache, q = FakeTensor((2, 4, 30, 144), torch.uint8), FakeTensor((6, 8, 128), torch.bfloat16)
     for s, made_on, others in ((None, "main", []), (side, "side", [main])):
         out = list(binding.kv4_read(cache, i32(2), i32(3), i32(2), rows=6, stream=s))
@@ -94,3 +100,31 @@ def test_strides_between_single_rows_and_heads_are_not_looked_at(name):
     assert call(0, 2, (1, 128, -3, 128)) == 0
     assert call(0, 1, (1, 7, -3, -9)) == 0
     assert call(0, 2, (256, 1, 256, 128)) == -11 and call(0, 2, (256, -128, 256, 128)) == -2      # two heads
+
+
+def test_numbers_beyond_a_c_int_are_limits_or_refused(monkeypatch):
+    """ctypes would pass 2^32 + 5 as 5."""
+    from token_tree_verification_gb300 import binding
+    seen = {}
+    monkeypatch.setattr(binding, "_current_device", lambda: 0)
+    monkeypatch.setattr(binding, "_current_stream", lambda _: 1)
+    monkeypatch.setattr(binding, "_lib", types.SimpleNamespace(
+        spec_tree_attn_kv4=lambda *a: seen.update(max_prefix=a[10], window=a[16], sinks=a[17]) or 0,
+        spec_kv4_write=lambda *a: 0))
+    cache, q = FakeTensor((2, 4, 30, 144), torch.uint8), FakeTensor((6, 8, 128), torch.bfloat16)
+
+    def attn(**kw):
+        args = dict(max_prefix=20, window=0, sinks=0)
+        args.update(kw)
+        binding.tree_attn_kv4(q, cache, i32(2), i32(3), None, status=i32(2), parents=i32(6), o=q, **args)
+        return seen["max_prefix"], seen["window"], seen["sinks"]
+
+    top = 2 ** 31 - 1
+    assert attn(max_prefix=2 ** 31, window=2 ** 32 + 5, sinks=2 ** 32) == (top, top, top)
+    assert attn(max_prefix=top, window=7, sinks=3) == (top, 7, 3)
+    assert attn(window=-1) == (20, -1, 0)          # (the library refuses it)
+    with pytest.raises(ValueError, match="rows"):
+        k = FakeTensor((2 ** 32 + 3, 4, 128), torch.bfloat16)
+        binding.kv4_write(k, k, cache, i32(2), i32(3), i32(2))
+    k = FakeTensor((6, 4, 128), torch.bfloat16)
+    binding.kv4_write(k, k, cache, i32(2), i32(3), i32(2))

@@ -307,6 +307,9 @@ def _new(stream, shape, strides, dtype):
     return t
 
 
+# The library takes C ints, to which ctypes cuts a number without a word.  What
+# limits something may be any number; what counts rows may not.
+_INT_MAX = 2 ** 31 - 1
 _DTYPES = {torch.bfloat16: SPEC_BF16, torch.float32: SPEC_F32}
 
 
@@ -372,8 +375,10 @@ def _dense_rows(index, t, T, Hkv, D, name):
         raise TypeError(f"{name} must be on cuda:{index}, got {t.device}")
     if t.shape == (T, Hkv, D):
         row, head, one = t.stride()
-        if one == 1:
+        if one == 1 and T <= _INT_MAX:
             return row, head
+    if T > _INT_MAX:
+        raise ValueError(f"{name} may have {_INT_MAX} rows, not {T}")
     raise ValueError(f"{name} must be [{T}, {Hkv}, {D}] with its last dimension contiguous")
 
 
@@ -477,8 +482,9 @@ def tree_attn_kv4(q, kv_cache, prefix_lens, offsets, mask, max_prefix, status, o
         raise ValueError("o must be like q")
     prefix, offsets, status = _per_request(index, B, prefix_lens, offsets, status, "prefix_lens")
     rc = lib.spec_tree_attn_kv4(q.data_ptr(), kv_cache.data_ptr(), o.data_ptr(), dt, B, T, Hq, Hkv, D, S_cap,
-                                max_prefix, prefix, offsets, mask_ptr, parents_ptr, softmax_scale, window, sinks,
-                                status, _current_stream(index) if stream is None else stream.cuda_stream)
+                                min(max_prefix, _INT_MAX), prefix, offsets, mask_ptr, parents_ptr, softmax_scale,
+                                min(window, _INT_MAX), min(sinks, _INT_MAX), status,
+                                _current_stream(index) if stream is None else stream.cuda_stream)
     if rc:
         raise SpecError(rc, "spec_tree_attn_kv4")
     return o
