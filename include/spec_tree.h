@@ -389,8 +389,11 @@ int spec_kv4_read(void *k, void *v, int dtype, int B, int T, int Hkv, int D, int
  * node.  With window > 0, node i at depth d sits at position L_b + d, a prefix
  * key j at position j and an ancestor at L_b + its depth; node i then sees a
  * key of K(i) only if it lies less than `window` positions behind it (itself
- * included), or at one of the first `sinks` positions.  window = 0 means no
- * window (sinks is then ignored).  Prefix slots that the window hides from
+ * included), or at one of the first `sinks` positions.  A node's depth is the
+ * size of its set less one, and its r-th lowest member the ancestor of depth r:
+ * with a window, a mask row is a path from the root to its node, as
+ * spec_build_tree_mask writes it.  window = 0 means no window (sinks is then
+ * ignored).  Prefix slots that the window hides from
  * every node may hold anything, like the slots behind the tree; tiles of such
  * slots are not read.  Every other slot holds a record as spec_kv4_write
  * stores them.
