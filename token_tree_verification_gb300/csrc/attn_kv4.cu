@@ -265,7 +265,12 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
     const int kn = key_of(g);                                 // this lane's K rows: kn, kn + 1
     const int kv0 = key_of(2 * t), kv1 = key_of(2 * t + 1);   // its V keys: these and the ones after
     for (int i = t_begin; i < t_end; i += kFewWarps) {
-      if (ok && !mbar_wait(&bar_full[warp][st], phase)) ok = false;
+      if (ok && !mbar_await(&bar_full[warp][st], phase)) {
+        ok = false;       // no more copies; those in flight get as long again to land
+#pragma unroll 1
+        for (int s = st; s < st + kFewStages && i + (s - st) * kFewWarps < t_end; ++s)
+          mbar_wait(&bar_full[warp][s % kFewStages], s < kFewStages ? phase : phase ^ 1);
+      }
       const int key0 = tiles.key0(i);
       uint8_t *tile = ring + st * C::kStageBytes;
       // keys that some row may not see: the tree, and the window's borders.  Those

@@ -120,12 +120,6 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
-__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity, uint32_t tries = kSleepTries) {
-#pragma unroll 1
-  for (uint32_t it = 0; it < tries; ++it)
-    if (mbar_try(bar, parity)) return true;
-  return false;
-}
 // Whether the phase is over, without waiting.
 __device__ __forceinline__ bool mbar_over(uint32_t bar, uint32_t parity) {
   uint32_t done;
@@ -137,6 +131,29 @@ __device__ __forceinline__ bool mbar_over(uint32_t bar, uint32_t parity) {
       : "r"(bar), "r"(parity)
       : "memory");
   return done != 0;
+}
+// -DSPEC_WAIT_POLLS=n (the failure test's build): waits give up after n looks.
+__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity, uint32_t tries = kSleepTries) {
+#ifdef SPEC_WAIT_POLLS
+  tries = SPEC_WAIT_POLLS;
+#endif
+#pragma unroll 1
+  for (uint32_t it = 0; it < tries; ++it) {
+#ifdef SPEC_WAIT_POLLS
+    if (mbar_over(bar, parity)) return true;
+#else
+    if (mbar_try(bar, parity)) return true;
+#endif
+  }
+  return false;
+}
+// For warps that are to go on at once: mbar_wait.
+__device__ __forceinline__ bool mbar_await(uint64_t *bar, uint32_t parity) {
+#ifdef SPEC_WAIT_POLLS
+  return mbar_sleep(smem_addr(bar), parity);
+#else
+  return mbar_wait(bar, parity);
+#endif
 }
 __device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");

@@ -114,7 +114,7 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
   __shared__ struct {
     uint64_t raw_full[kRaw], raw_empty[kRaw];
     uint64_t k_full[kOps], k_empty[kOps], v_full[kOps], v_empty[kOps];
-    uint64_t s_full[2], s_empty[2], p_full[2], o_done[2], q_full;
+    uint64_t s_full[2], s_empty[2], p_full[2], o_done[2], q_full, drained[2];
   } bars;
   __shared__ uint32_t s_tmem;
   __shared__ int s_timeout;
@@ -160,6 +160,7 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
       mbar_init(&bars.s_empty[s], kSoftWarps / 2);
       mbar_init(&bars.p_full[s], kSoftWarps / 2);
       mbar_init(&bars.o_done[s], 1);
+      mbar_init(&bars.drained[s], 1);
     }
     mbar_init(&bars.q_full, kSoftWarps);
     fence_barrier_init();
@@ -186,7 +187,9 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
   // Each role runs the turns (row blocks) of this CTA on its own, its places
   // in the rings going on from turn to turn, and meets the others at their
   // ends, where the softmax warps merge the rows.  A wait that runs out clears
-  // ok: the role stops waiting, and all return after the turn.
+  // ok: the role stops waiting, and all return after the turn.  (The
+  // products go on, on whatever is there: no lane leaves a loop in which its warp
+  // meets.)
   bool ok = true;
   auto turns = [&](auto &&work, auto &&finish) {
     for (int row0 = static_cast<int>(blockIdx.y) * N; row0 < rows_total; row0 += static_cast<int>(gridDim.y) * N) {
@@ -227,7 +230,9 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
       turns([&](int) {
         if (lane != 0) return;
         for (int i = 0; i < ntiles && ok; ++i, raw.next()) {
-          ok = mbar_sleep(raw_empty + 8 * raw.at, raw.phase);
+          // (decoders that gave up free a stage whose last copy has not landed: nothing
+          // may be announced on a barrier that still awaits bytes)
+          ok = mbar_sleep(raw_empty + 8 * raw.at, raw.phase) && mbar_over(raw_full + 8 * raw.at, raw.phase);
           if (!ok) break;
           const int key0 = tiles.key0(t0 + i), count = min(kTile, G.keys - key0);
           const uint32_t bytes = static_cast<uint32_t>(count * R);
@@ -240,6 +245,9 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
           }
         }
       }, wait_merge);
+      // (of a stage that has had no copy the phase before is over)
+      if (s_timeout != 0 && lane == 0)
+        for (uint32_t st = 0; st < kRaw; ++st) mbar_wait(&bars.raw_full[st], st < raw.at ? raw.phase ^ 1 : raw.phase);
     } else if (warp == 1) {
       // ---------------------------------------------------------- S^T = K Q^T
       constexpr uint32_t id = tc::idesc_f16_f32(128, N, 0, 0);
@@ -248,17 +256,17 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
       Ring<2> sr;
       Ring<kOps> kr;
       sr.phase = 1;
+      const bool leader = tc::elect_one();
       uint32_t q_phase = 0;
       turns([&](int) {
         if (ntiles == 0) return;
         ok = mbar_sleep(smem_addr(&bars.q_full), q_phase);
         q_phase ^= 1;
-        for (int i = 0; i < ntiles && ok; ++i, sr.next(), kr.next()) {
-          ok = mbar_sleep(s_empty + 8 * sr.at, sr.phase) && mbar_sleep(k_full + 8 * kr.at, kr.phase);
-          if (!ok) break;
+        for (int i = 0; i < ntiles; ++i, sr.next(), kr.next()) {
+          ok = ok && mbar_sleep(s_empty + 8 * sr.at, sr.phase) && mbar_sleep(k_full + 8 * kr.at, kr.phase);
           tc::fence_after_sync();
           const uint32_t kt = tmem + C::kColK + kr.at * (D / 2);
-          if (tc::elect_one()) {
+          if (leader) {
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
               const uint32_t qa = ((ks >> 2) * C::kQBoxBytes + (ks & 3) * 32) >> 4;
@@ -279,14 +287,14 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
       const uint32_t v_full = smem_addr(bars.v_full);
       Ring<2> pr;
       Ring<kOps> vr;
+      const bool leader = tc::elect_one();
       turns([&](int) {
-        for (int i = 0; i < ntiles && ok; ++i, pr.next(), vr.next()) {
-          ok = mbar_sleep(v_full + 8 * vr.at, vr.phase) && mbar_sleep(p_full + 8 * pr.at, pr.phase);
-          if (!ok) break;
+        for (int i = 0; i < ntiles; ++i, pr.next(), vr.next()) {
+          ok = ok && mbar_sleep(v_full + 8 * vr.at, vr.phase) && mbar_sleep(p_full + 8 * pr.at, pr.phase);
           tc::fence_after_sync();
           const uint64_t vd = vd0 + static_cast<uint64_t>(vr.at * C::kOpBytes >> 4);
           const uint64_t pd = pd0 + static_cast<uint64_t>(pr.at * C::kPBytes >> 4);
-          if (tc::elect_one()) {
+          if (leader) {
 #pragma unroll
             for (int kk = 0; kk < kTile / 16; ++kk)
               tc::mma_bf16(tmem + C::kColO + pr.at * N, vd + (kk * 16 * 128 >> 4), pd + (kk * 16 * C::kPPitch >> 4),
@@ -600,6 +608,14 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
     });
   }
   __syncwarp();
+  // A turn that was given up may leave products under way (and copies, see warp 0):
+  // the warps that issued them wait, with a limit, before the CTA gives up its memory.
+  if (s_timeout != 0 && (warp == 1 || warp == 2)) {
+    if (tc::elect_one()) tc::commit(&bars.drained[warp - 1]);
+    __syncwarp();
+    mbar_wait(&bars.drained[warp - 1], 0);
+    __syncwarp();
+  }
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 1) {
