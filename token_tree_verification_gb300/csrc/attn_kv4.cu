@@ -39,10 +39,12 @@ namespace {
 // What bounds it: every key is decoded by one warp, about 330 instructions per
 // tile of 32 keys at D = 128, so long prefixes run at the issue rate just below
 // the memory's.  8 requests x 32 heads x 6 rows behind 27000 to 32768 keys:
-// 1.10 GB in 179 us, 6.2 TB/s, 0.91 of what a copy reaches.  Short ones are bound
+// 1.10 GB in 181 us, 6.1 TB/s, 0.90 of what a copy reaches.  Short ones are bound
 // by latency: one token of 8 query heads x 4 requests x 8 KV heads behind 8192
-// keys (38 MB) 15.0 us, of which set-up, first tile and merge are about 10; 8
-// rows of one request behind 128 keys, fp32, 4.8 us.
+// keys (38 MB) 15.1 us, of which set-up, first tile and merge are about 10; 8
+// rows of one request behind 128 keys, fp32, 4.9 us.  fp32 calls of more rows
+// decode every key for each block of up to 32: 256 units behind 4096 keys take 46
+// us for 8 rows, 64 for 16, 118 for 32; 1024 rows of 32 units behind 8192 723 us.
 constexpr int kFewTile = 32;       // keys of a stage
 constexpr int kFewStages = 2;
 
@@ -614,10 +616,15 @@ int attn_few(const Kv4AttnArgs &p, int max_prefix, void *stream) {
 constexpr int kMaxSlots = 0x7FFFFFFF - 1024;
 
 // Which bf16 kernel: by the mean number of rows on each key (a request with
-// more takes more turns).  Measured, 32 heads x 8 requests behind 8192: 8 rows
-// take 59 us in mma.sync and 75 us on tcgen05 with the rows along N, 9 rows 75
-// us there; 32 rows 91 us along N and 121 us along M, 33 rows 121 us along M.  (A
-// form for 64 rows along N took 138 us for 64, 123 us along M.)
+// more takes more turns).  Measured, 256 units (32 heads x 8 requests) behind 8192
+// and 2048 keys, D = 128 | 64, us; in brackets the kernels not taken, of which
+// mma.sync takes 9 rows and along N 33 rows as two blocks:
+//    8 rows  mma.sync 62.4, 22.0 | 43.9, 15.2    (along N 81.1, 30.5 | 70.6, 27.4)
+//    9 rows  along N  81.2, 30.9 | 70.5, 27.4    (mma.sync 117, 39.0 | 79.3, 26.4)
+//   32 rows  along N  101, 36.7 | 94.1, 32.9     (along M 133, 45.9 | 120, 40.6)
+//   33 rows  along M  133, 46.0 | 121, 41.1      (along N 200, 70.2 | 183, 63.5)
+// Short calls at D = 64 are the exception: 9 rows behind 512 keys take 15.8 us along
+// N and 12.2 in mma.sync, in a window of 1024 21.6 and 17.2.
 template <int D>
 int attn_bf16(const Kv4AttnArgs &p, int max_prefix, void *stream) {
   const int rows = mean_nodes(p.a) * p.a.G;

@@ -33,7 +33,7 @@
 // of the keys, added 64 KB.)
 //
 // Measured, D = 128: 4 requests x 8 KV heads x 1024 rows behind 8192 keys take
-// 136 us, 1.03 PFLOP/s, 0.54 of the measured bf16 rate (256 CTAs are two waves on
+// 135 us, 1.04 PFLOP/s, 0.55 of the measured bf16 rate (256 CTAs are two waves on
 // 152 SMs, of which the second is two thirds full; with all arithmetic taken out
 // the copies, products and waits alone take 100 us), at D = 64 122 us.  A tree of
 // 64 nodes on 32 heads behind 2048 keys, five tiles a CTA: 13.9 us, nearly all

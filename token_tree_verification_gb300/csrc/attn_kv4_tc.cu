@@ -35,7 +35,7 @@
 // What bounds it, 32 rows, D = 128: about 1140 cycles a tile, of them 970 of
 // shared-memory traffic (records in and out, V's operand in and out, P), issue
 // slots 63% busy, the tensor pipe 15%.  8 requests x 32 heads behind 8192 keys:
-// 32 rows 91 us, 16 rows 74 us (278 MB, 3.8 TB/s); with a window of 4096 behind
+// 32 rows 101 us, 16 rows 81 us (302 MB, 3.7 TB/s); with a window of 4096 behind
 // 32768 61 us, in two waves of CTAs of which each spends about 10 us on its
 // set-up, first tile and output.
 #include <type_traits>
@@ -58,7 +58,7 @@ template <int D, int N>
 struct Kv4Tc {
   // 32 rows: the softmax bounds, so two groups share a tile's rows; 16: the
   // decoding does, and two sets of decoders take turns.  (32 heads x 8 requests
-  // behind 8192: 16 rows 84 -> 76 us with two sets; 32 rows 92 us with two
+  // behind 6759 to 8192: 16 rows 84 -> 76 us with two sets; 32 rows 92 us with two
   // softmax groups, 100 us with two sets.)
   static constexpr int kHalves = N == 16 ? 1 : 2;
   static constexpr int kSets = N == 16 ? 2 : 1;

@@ -345,8 +345,10 @@ int launch_rows(Kernel kernel, const Kv4Args &args, long long warps, int rounds,
 // One round of rows per warp while that leaves every SM at most 32 warps, so
 // that a tree's few rows spread over the GPU; beyond, U rounds at once, and as
 // many turns of them as make kWaves waves of 32 warps on every SM.  U by
-// registers: reading bf16 rows takes 27.8 us with 4 and 30.6 with 2, fp32 rows
-// 35.5 and 32.6; writing 46.0 with 2 and 51.7 with 1.
+// registers: reading 29081 rows of 8 heads, D = 128, takes 27.7 us with 4 and 30.5
+// with 2 for bf16, 64.3 and 59.7 for fp32 (272 MB, 4.6 TB/s); writing 51200 rows of
+// 8 heads 45.9 with 2 and 51.7 with 1 for bf16, 75.7 and 77.4 for fp32 (478 MB, 6.3
+// TB/s).
 template <bool kWrite, int D, typename E>
 int rows_by_size(const Kv4Args &args, void *stream) {
   constexpr int U = !kWrite && sizeof(E) == 2 ? 4 : 2, kWaves = 4;
