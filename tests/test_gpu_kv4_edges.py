@@ -267,3 +267,52 @@ def test_single_rows_and_heads_of_any_stride(dtype, D):
         for got, ref in zip(out, kv4.read(want, D, [1], [0, T])):
             np.testing.assert_array_equal(got.double().cpu().numpy(), ref)
         assert st.tolist() == [0]
+
+
+@DTYPES
+@FORMS
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("far", [1e2, 1e4, 1e6, 1e12, 1e28])
+@pytest.mark.parametrize("size", [2, 500])
+def test_keys_far_below_the_others_come_first(dtype, Hq, n, D, far, size):
+    """Runs of 256 keys whose scores are about -5000 x far, then 256 of ordinary ones, and so on: the softmax's
+    reference has to come all the way up without a trace."""
+    rng = np.random.default_rng(D + n)
+    L = 9000
+    rec = random_records(rng, (1, 1, L + n), D)
+    low = (np.arange(L + n) % 512 < 256) & (np.arange(L + n) < L)
+    rec[0, 0, :, 0] &= 0xF0                              # dimension 0 of the keys: 0, or -6 x 10240
+    rec[0, 0, low, 0] |= 0xF
+    rec[0, 0, low, D] = kv4.MAX_SCALE_BYTE
+    rec[0, 0, low, 1:8] = 0                              # (the others of its group would be as large)
+    rec[0, 0, low, 0] &= 0x0F
+    parents = random_tree(rng, n)
+    q = size * rng.standard_normal((n, Hq, D))
+    q[..., 0] = far
+    q = torch.from_numpy(q.astype(np.float32)).to(dtype)
+    st = zeros_status(1)
+    o = ttv.tree_attn_kv4(q.cuda(), torch.from_numpy(rec).cuda(), i32([L]), i32([0, n]), None, L, st, parents=i32(parents))
+    got = o.double().cpu().numpy()
+    k, v = kv4.values(rec[0, 0], D)
+    x, scale = q.double().numpy(), 1 / np.sqrt(D)
+    seen = kv4.sees(parents, L)[:, None, :]
+    near = seen & ~low                                   # the others' weights are 0: e^-300000 and less
+    s = np.where(near, np.einsum("ngd,sd->ngs", x, k) * scale, -np.inf)
+    assert np.where(seen & low, np.einsum("ngd,sd->ngs", x, k) * scale, -np.inf).max() < s.max(-1).min() - 1e5
+    p = np.exp(s - s.max(-1, keepdims=True))
+    p /= p.sum(-1, keepdims=True)
+    want, size = np.einsum("ngs,sd->ngd", p, v), np.einsum("ngs,sd->ngd", p, np.abs(v))
+    # As for any attention, from the near keys alone: their dimension 0 is 0, so `far` is no part of their scores.
+    # A query's elements beside it are halves of the row's scale: their smallest step is 2^-38 of the row's largest.
+    big = np.where(near, np.einsum("ngd,sd->ngs", np.abs(x), np.abs(k)) * scale, 0).max(-1)[..., None]
+    lost = 2.0 ** -38 * far * scale * np.where(near, np.abs(k).sum(-1), 0).max(-1)[..., None]
+    delta = (2.0 ** -21 + D * 2.0 ** -24) * big + lost + 2.0 ** -20
+    weight, last = (2.0 ** -11, 2.0 ** -8) if dtype == BF16 else (2.0 ** -22, 2.0 ** -24)
+    reach = np.einsum("ngs,sd->ngd", np.broadcast_to(near, s.shape).astype(np.float64), np.abs(v))
+    tol = size * (2 * delta + weight + 2.0 ** -18) + last * np.abs(want) * 1.01 + 2.0 ** -32 * reach
+    assert st.tolist() == [0] and np.isfinite(got).all()
+    if far <= 1e6:                       # (beyond, the elements beside `far` are lost, and the near keys' scores with them)
+        assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) / tol).max()
+    else:
+        top = np.where(near[..., None], np.abs(v)[None, None], 0).max((0, 1, 2))
+        assert (np.abs(got) <= 1.01 * top).all()

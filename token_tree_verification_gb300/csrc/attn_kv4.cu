@@ -377,6 +377,7 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
       };
       if (F32) weigh();
       if (__any_sync(0xffffffffu, want)) {
+        bool again = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -385,15 +386,17 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
 #pragma unroll
             for (int x = 4; x < 32; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
             if (m > limit[nt][e]) {
-              const Move move(m, nbase[nt][e], limit[nt][e] == -INFINITY);
+              const bool fresh = limit[nt][e] == -INFINITY, far = far_above(m, nbase[nt][e], fresh);
+              const Move move(m, nbase[nt][e], fresh);        // (far: a factor of 0)
               l_row[nt][e] *= move.factor;
 #pragma unroll
               for (int j = 0; j < KS; ++j) {
                 o[nt][j][e] *= move.factor;
                 o[nt][j][2 + e] *= move.factor;
               }
-              nbase[nt][e] = move.next;
-              limit[nt][e] = kWeightLog2 + kMoveLog2;
+              nbase[nt][e] = far ? kWeightLog2 : move.next;
+              limit[nt][e] = far ? -INFINITY : kWeightLog2 + kMoveLog2;
+              again |= far;
 #pragma unroll
               for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -403,6 +406,10 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
                 }
             }
           }
+        if (__any_sync(0xffffffffu, again)) {
+          i -= kFewWarps;
+          continue;
+        }
       }
       if (!F32) weigh();
       // ---- weights, and their product with V

@@ -207,9 +207,16 @@ constexpr float kMoveLog2 = 7.f;
 // reference) may miss the range of halves either way: at 2^27 the steps are 16.
 // There x keeps its rounding at the old reference and is brought to the new one by
 // a subtraction, which leaves the largest score a weight of at least 1.
-constexpr float kWholeEnd = 16777216.f;
+//
+// A score that far above a reference so low has lost its last places in x, and what
+// is summed is nothing beside it (2^-1024): the row starts again without a
+// reference, and its tile is taken once more (`far`).
+constexpr float kWholeEnd = 16777216.f, kFarStep = 1024.f, kFarBase = 4096.f;
 __device__ __forceinline__ float reference_step(float most) {
   return fabsf(most) < kWholeEnd ? ceilf(most - kWeightLog2) : most;
+}
+__device__ __forceinline__ bool far_above(float most, float old, bool fresh) {
+  return !fresh && most >= kFarStep && fabsf(old) >= kFarBase;
 }
 struct Move {
   float factor, next;       // of what is summed; the new 8 - reference

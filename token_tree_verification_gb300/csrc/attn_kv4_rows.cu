@@ -459,7 +459,12 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
         const bool moves = most > (fresh ? -INFINITY : kWeightLog2 + kMoveLog2);
         if (__any_sync(0xffffffffu, moves)) {
           Move move(shift);
-          if (moves) {
+          const bool far = moves && far_above(most, shift, fresh);
+          if (far) {
+            move.factor = 0.f;
+            shift = kWeightLog2;
+            ref = -INFINITY;
+          } else if (moves) {
             move = Move(most, shift, fresh);
             shift = move.next;
             ref = kWeightLog2 - shift;
@@ -481,6 +486,11 @@ tree_attn_kv4_rows_kernel(const Kv4AttnArgs p) {
             tc::wait_st();
           }
           sum *= move.factor;
+          if (__any_sync(0xffffffffu, far)) {
+            --i;
+            phase ^= 1;
+            continue;
+          }
           const bool steep = __any_sync(0xffffffffu, move.less != 0.f);
           weigh([&](float(&x)[32]) {
 #pragma unroll

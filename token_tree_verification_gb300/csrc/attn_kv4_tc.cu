@@ -34,7 +34,7 @@
 //
 // What bounds it, 32 rows, D = 128: about 1140 cycles a tile, of them 970 of
 // shared-memory traffic (records in and out, V's operand in and out, P), issue
-// slots 63% busy, the tensor pipe 15%.  8 requests x 32 heads behind 8192 keys:
+// slots 61% busy, the tensor pipe 15%.  8 requests x 32 heads behind 8192 keys:
 // 32 rows 101 us, 16 rows 81 us (302 MB, 3.7 TB/s); with a window of 4096 behind
 // 32768 61 us, in two waves of CTAs of which each spends about 10 us on its
 // set-up, first tile and output.
@@ -125,8 +125,9 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
   __shared__ int s_first[N];
   __shared__ __align__(16) float s_c[N];               // a row's score factor
   // per parity of the tiles: 8 - the row's reference, the last move of it
-  // (factor of the old sums, shift of the scores), the reference, the sum of
-  // weights, and the parts of maxima and sums that the four lane quarters hold
+  // (factor of the old sums, shift of the scores: infinite when the row starts
+  // again), the reference, the sum of weights, and the parts of maxima and sums
+  // that the four lane quarters hold
   __shared__ __align__(16) float s_n[2][N];
   __shared__ __align__(16) float2 s_move[2][N];
   __shared__ float s_ref[2][N], s_sum[2][N];
@@ -472,9 +473,6 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
         float x[RP];
         tc::ld16(s_col, x);
         tc::wait_ld();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_at(s_empty + 8 * par);
         // x = score - reference + 8, in powers of two
 #pragma unroll
         for (int j = 0; j < RP; j += 4) {
@@ -516,11 +514,15 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
             const float ref = s_ref[par][r];
             const bool fresh = ref == -INFINITY;
             float2 move = make_float2(1.f, 0.f);
-            if (m > (fresh ? -INFINITY : kWeightLog2 + kMoveLog2)) {
-              const float by = reference_step(m);           // (0 stands for a reference that is not there)
+            if (far_above(m, s_n[par][r], fresh)) {
+              move = make_float2(0.f, INFINITY);
+              s_ref[par][r] = -INFINITY;
+              s_n[par][r] = kWeightLog2;
+            } else if (m > (fresh ? -INFINITY : kWeightLog2 + kMoveLog2)) {
+              const float by = reference_step(m);
               move = make_float2(fresh ? 0.f : exp2f(-by), -by);
-              s_ref[par][r] = (fresh ? 0.f : ref) + by;
               s_n[par][r] -= by;
+              s_ref[par][r] = kWeightLog2 - s_n[par][r];
             }
             still = s_ref[par][r] == -INFINITY;
             s_move[par][r] = move;
@@ -542,13 +544,23 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
             }
             tc::wait_st();
           }
+          bool again = false;
 #pragma unroll
           for (int j = 0; j < RP; ++j) {
             const float2 move = s_move[par][r0 + j];
             sum[j] *= move.x;
             x[j] += move.y;
+            again |= move.y == INFINITY;
+          }
+          if (again) {           // (the same in the whole group)
+            i -= 2;
+            phase ^= 1;
+            continue;
           }
         }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(s_empty + 8 * par);
         // ---- weights; P's buffer is free once the parity's last product is done
         const bool room = mbar_over(o_done + 8 * par, phase ^ 1);
 #pragma unroll
