@@ -401,6 +401,8 @@ int spec_kv4_read(void *k, void *v, int dtype, int B, int T, int Hkv, int D, int
  *   dtype        of q and o.  SPEC_BF16: softmax weights enter the product
  *                with V as halves (11 significant bits), sums in fp32.
  *                SPEC_F32: queries and weights as two halves each (22 bits).
+ *                A row's queries share one power of two: what an element has
+ *                below 2^-38 of the row's largest is lost
  *   Hq % Hkv == 0, Hq / Hkv at most 128, D 64 or 128, B x Hkv at most 65535,
  *   S_cap at most 2^31 - 1025
  *   max_prefix   upper bound on every prefix_lens[b], sizes the key splits

@@ -39,12 +39,12 @@ namespace {
 // What bounds it: every key is decoded by one warp, about 330 instructions per
 // tile of 32 keys at D = 128, so long prefixes run at the issue rate just below
 // the memory's.  8 requests x 32 heads x 6 rows behind 27000 to 32768 keys:
-// 1.10 GB in 181 us, 6.1 TB/s, 0.90 of what a copy reaches.  Short ones are bound
+// 1.10 GB in 182 us, 6.1 TB/s, 0.89 of what a copy reaches.  Short ones are bound
 // by latency: one token of 8 query heads x 4 requests x 8 KV heads behind 8192
-// keys (38 MB) 15.1 us, of which set-up, first tile and merge are about 10; 8
+// keys (38 MB) 15.3 us, of which set-up, first tile and merge are about 10; 8
 // rows of one request behind 128 keys, fp32, 4.9 us.  fp32 calls of more rows
-// decode every key for each block of up to 32: 256 units behind 4096 keys take 46
-// us for 8 rows, 64 for 16, 118 for 32; 1024 rows of 32 units behind 8192 723 us.
+// decode every key for each block of up to 32: 256 units behind 4096 keys take 45
+// us for 8 rows, 66 for 16, 118 for 32; 1024 rows of 32 units behind 8192 718 us.
 constexpr int kFewTile = 32;       // keys of a stage
 constexpr int kFewStages = 2;
 
