@@ -79,7 +79,8 @@ typedef enum {
   SPEC_ERR_ALIGNMENT = -11,      /* a pointer is not 16-byte aligned */
   SPEC_ERR_INDEX = -12,          /* bounds-checked build only: a computed global index fell
                                     outside its buffer; the access was skipped */
-  SPEC_ERR_NONFINITE = -13       /* a row to be quantised holds NaN or infinity */
+  SPEC_ERR_NONFINITE = -13,      /* a row to be quantised holds NaN or infinity */
+  SPEC_ERR_PAGE = -14            /* a block table names a page outside the pool */
 } spec_status;
 
 typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
@@ -426,6 +427,168 @@ int spec_kv4_compact(void *kv_cache, int B, int Hkv, int D, int S_cap, const int
                      const int32_t *tree_offsets, const int32_t *path_nodes,
                      const int32_t *accept_len, int max_depth_plus1, int32_t *new_prefix_lens,
                      int32_t *status, void *stream);
+
+/*
+ * Rotary positions and the paged KV cache — spec_rope, spec_rope_write_paged,
+ * spec_tree_attn_paged and spec_kv_compact_paged: a step's rotation of
+ * queries and keys and its cache operations on a cache held in pages, so that
+ * requests of any length share one pool.
+ *
+ *   k_pages, v_pages  [num_pages][Hkv][page_size][D]  dtype, 16-byte aligned;
+ *                     page_size a power of two from 8 to 4096
+ *   block_table       [B][max_pages] int32: entry (b, i) is the page of request
+ *                     b's slots [i * page_size, (i + 1) * page_size).  Only the
+ *                     entries of slots that a call names are read (in use or
+ *                     about to be written); the others may hold anything.  A
+ *                     request has max_pages * page_size slots, 2^31 - 4097 at
+ *                     most.  A page may serve several requests (a shared
+ *                     prefix) as long as no call writes to a slot that another
+ *                     request uses
+ * An entry outside [0, num_pages) among those that are read is
+ * SPEC_ERR_PAGE, and the request's outputs stay as they were.
+ */
+
+/*
+ * spec_rope_table — frequencies of a rotation, computed on the host.
+ *
+ * Pair i of the first rotary_dim dims turns by theta_i = base^(-2i /
+ * rotary_dim) radians a position, scaled by `factor` >= 1 for contexts longer
+ * than the model was trained on (published methods):
+ *   SPEC_ROPE_NONE    theta_i (factor, original, low and high are ignored)
+ *   SPEC_ROPE_LINEAR  theta_i / factor
+ *   SPEC_ROPE_NTK     base multiplied by factor^(r / (r - 2)), r = rotary_dim >= 4
+ *   SPEC_ROPE_YARN    (Peng et al., 2023) theta_i k + theta_i / factor (1 - k),
+ *                     k falling from 1 at pair floor(d(high)) to 0 at pair
+ *                     ceil(d(low)) (both within [0, r - 1]), d(t) = r ln(original
+ *                     / (2 pi t)) / (2 ln base) the pair that makes t turns in
+ *                     `original` positions; cosines and sines are multiplied by
+ *                     0.1 ln(factor) + 1 (*scale).  low = 1, high = 32 usually
+ *   SPEC_ROPE_BANDS   the same mix with k = (original theta_i / 2 pi - low) /
+ *                     (high - low), cut to [0, 1]: pairs of more than `high`
+ *                     turns in the original context stay, those of fewer than
+ *                     `low` are divided.  low = 1, high = 4 usually
+ *   freqs   [rotary_dim / 2] uint64 HOST out: theta_i / 2 pi as a 64-bit fraction
+ *           of a turn; the caller copies it to the device for the calls below
+ *   scale   HOST out: the factor of cosines and sines, 1 but for YARN
+ * rotary_dim is even, from 2 to 512; base above 1.  Nothing is launched.
+ */
+typedef enum {
+  SPEC_ROPE_NONE = 0, SPEC_ROPE_LINEAR = 1, SPEC_ROPE_NTK = 2, SPEC_ROPE_YARN = 3, SPEC_ROPE_BANDS = 4
+} spec_rope_scaling;
+
+int spec_rope_table(int rotary_dim, double base, int scaling, double factor, double original,
+                    double low, double high, uint64_t *freqs, float *scale);
+
+/*
+ * spec_rope — rotary positions on dense rows.
+ *
+ * Row t of request b has position start[b] + depth[t] (a tree behind its
+ * prefix: start = prefix_lens, depth from spec_build_tree_mask), or start[b] +
+ * t - offsets[b] when depth is NULL (a run of tokens).  The pairs of its first
+ * rotary_dim dims, (i, i + rotary_dim / 2) or with `interleaved` (2i, 2i + 1),
+ * are turned by position x theta_i and multiplied by `scale`, in fp32; the
+ * other dims are copied.
+ *
+ *   x, y      [T][H][D] dtype, at the given strides in elements between rows
+ *             and heads (the D elements of a head are contiguous), so that rows
+ *             may lie inside a fused projection and x hold the heads of queries
+ *             and keys alike.  y may be x itself with the same strides (in
+ *             place); it may not overlap it otherwise.  Pointers and strides
+ *             of multiples of 16 bytes are fastest; any multiple of an element
+ *             is taken
+ *   D         a multiple of 8 up to 512; rotary_dim even, up to D (0: y is a copy)
+ *   freqs     [rotary_dim / 2] uint64 DEVICE, from spec_rope_table
+ *   start     [B] int32, depth [T] int32 or NULL, offsets [B+1] int32 (a
+ *             request may have no rows; it has no upper limit of rows)
+ *   T         rows; rows at or behind offsets[B] stay as they were, T = 0
+ *             enqueues nothing
+ * The angle is exact in 64-bit fixed point up to the table's own rounding, a
+ * double, so positions up to 2^32 keep fp32's accuracy.
+ * Errors on the device: SPEC_ERR_TREE_TOO_LARGE (offsets outside [0, T] or
+ * decreasing) and SPEC_ERR_PREFIX_RANGE (a start below zero; or a depth: then
+ * the row alone is left out), for which the request's rows of y stay as they
+ * were (with malformed offsets, rows of other requests may be left out too).
+ */
+int spec_rope(const void *x, void *y, int dtype, int B, int T, int H, int D, int64_t x_row_stride,
+              int64_t x_head_stride, int64_t y_row_stride, int64_t y_head_stride,
+              const uint64_t *freqs, int rotary_dim, float scale, int interleaved,
+              const int32_t *start, const int32_t *depth, const int32_t *offsets, int32_t *status,
+              void *stream);
+
+/*
+ * spec_rope_write_paged — new rows on their way into a paged cache.
+ *
+ * spec_rope on q into q_out and on k into the cache, in one call with the copy
+ * of v: row t of request b goes to slot prefix_lens[b] + t - offsets[b].  No
+ * other slot changes.  Positions start at `start`, or at prefix_lens when it is
+ * NULL (they differ in a cache that has lost slots, or whose prefix is shared).
+ *
+ *   q, k, v   [T][Hq | Hkv][D] at strides as in spec_rope; Hq = 0 writes k
+ *             and v alone (q and q_out are then ignored)
+ *   q_out     [T][Hq][D] contiguous; may be q when that is contiguous too
+ *   rotary_dim 0 (freqs NULL) rotates nothing
+ * Errors on the device: those of spec_rope, SPEC_ERR_PREFIX_RANGE also for
+ * rows that do not fit the request's slots, and SPEC_ERR_PAGE; the request's
+ * rows of q_out and its slots then stay as they were.
+ */
+int spec_rope_write_paged(const void *q, void *q_out, const void *k, const void *v, int dtype,
+                          int B, int T, int Hq, int Hkv, int D, int64_t q_row_stride,
+                          int64_t q_head_stride, int64_t k_row_stride, int64_t k_head_stride,
+                          int64_t v_row_stride, int64_t v_head_stride, const uint64_t *freqs,
+                          int rotary_dim, float scale, int interleaved, void *k_pages,
+                          void *v_pages, int num_pages, int page_size, const int32_t *block_table,
+                          int max_pages, const int32_t *prefix_lens, const int32_t *start,
+                          const int32_t *depth, const int32_t *offsets, int32_t *status,
+                          void *stream);
+
+/*
+ * spec_tree_attn_paged — attention of trees, or of chunks of tokens, over a
+ * paged cache.
+ *
+ * Trees (causal = 0): spec_tree_attn_ex on pages, with the mask or, when it is
+ * NULL, the parents; a single new token per request is a tree of one node.
+ * Chunks (causal != 0, mask and parents NULL): request b's rows are a run of
+ * any number of tokens behind its prefix, each of which sees the prefix, the
+ * run's earlier tokens and itself; a request may have no rows.  The rows' own
+ * keys and values must already sit in their slots, L_b and up.
+ *
+ *   q, o         [T][Hq][D] dtype, 16-byte aligned; Hq % Hkv == 0, Hq / Hkv at
+ *                most 128, D 64 or 128, Hkv at most 65535, T x Hq below 2^31
+ *   max_prefix   upper bound on every prefix_lens[b], sizes the key splits
+ *                (a larger value is safe, only slower)
+ * Slots at or behind L_b + n_b may hold anything, NaN included.  Rows of o at or
+ * behind offsets[B] stay as they were.  A row that sees no key (possible only
+ * with a mask that lacks the node itself) gets zeros.  Accumulation is fp32;
+ * the bf16 path splits every softmax weight into a bf16 high part and a bf16
+ * remainder (about 16 significant bits) and rounds o to bf16; SPEC_F32 computes
+ * in fp32 throughout.  Splits of the keys merge on chip; no workspace.
+ * Errors on the device: SPEC_ERR_TREE_TOO_LARGE (offsets outside [0, T] or
+ * decreasing; a tree without nodes or of more than SPEC_MAX_TREE_NODES),
+ * SPEC_ERR_PREFIX_RANGE (L_b < 0, or L_b + n_b beyond the request's slots),
+ * SPEC_ERR_BAD_PARENT as in spec_tree_attn_ex, SPEC_ERR_PAGE, SPEC_ERR_TIMEOUT.
+ * With malformed offsets, rows of other requests may be left out too.
+ */
+int spec_tree_attn_paged(const void *q, const void *k_pages, const void *v_pages, void *o,
+                         int dtype, int B, int T, int Hq, int Hkv, int D, int num_pages,
+                         int page_size, const int32_t *block_table, int max_pages, int max_prefix,
+                         const int32_t *prefix_lens, const int32_t *offsets, const uint32_t *mask,
+                         const int32_t *parents, int causal, float softmax_scale, int32_t *status,
+                         void *stream);
+
+/*
+ * spec_kv_compact_paged — spec_kv_compact on a paged cache: the accepted
+ * path's keys and values move behind the prefix, across pages where need be.
+ * The block table stays as it is (pages behind the new prefix are the
+ * caller's to reuse).  D is 64 or 128; new_prefix_lens must not be prefix_lens
+ * itself (SPEC_ERR_SHAPE).  Errors on the device: those of spec_kv_compact, and
+ * SPEC_ERR_PAGE for the pages of the slots that move.
+ */
+int spec_kv_compact_paged(void *k_pages, void *v_pages, int dtype, int B, int Hkv, int D,
+                          int num_pages, int page_size, const int32_t *block_table, int max_pages,
+                          const int32_t *prefix_lens, const int32_t *tree_offsets,
+                          const int32_t *path_nodes, const int32_t *accept_len,
+                          int max_depth_plus1, int32_t *new_prefix_lens, int32_t *status,
+                          void *stream);
 
 /*
  * spec_tree_expand — one level of draft token-tree construction.

@@ -11,4 +11,5 @@ from .binding import (  # noqa: F401
     tree_verify, tree_verify_workspace_size, make_verify_workspace, kv_compact, tree_expand, tree_prune, status_string,
     philox_uniforms, tree_merge, STATUS,
     kv4_record_bytes, make_kv4_cache, kv4_write, kv4_read, kv4_compact, tree_attn_kv4,
+    RopeTable, rope_table, rope, rope_write_paged, tree_attn_paged, kv_compact_paged,
 )

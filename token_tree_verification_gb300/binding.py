@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -25,7 +26,7 @@ STATUS = {
     -4: "SPEC_ERR_TREE_TOO_LARGE", -5: "SPEC_ERR_BAD_PARENT", -6: "SPEC_ERR_TOKEN_RANGE",
     -7: "SPEC_ERR_WORKSPACE", -8: "SPEC_ERR_CUDA", -9: "SPEC_ERR_TIMEOUT",
     -10: "SPEC_ERR_PREFIX_RANGE", -11: "SPEC_ERR_ALIGNMENT", -12: "SPEC_ERR_INDEX",
-    -13: "SPEC_ERR_NONFINITE",
+    -13: "SPEC_ERR_NONFINITE", -14: "SPEC_ERR_PAGE",
 }
 SPEC_F32, SPEC_BF16 = 0, 1
 MAX_TREE_NODES = 128
@@ -83,6 +84,18 @@ def load():
     lib.spec_kv4_compact.restype = I
     lib.spec_tree_attn_kv4.argtypes = [P, P, P, I, I, I, I, I, I, I, I, P, P, P, P, F, I, I, P, P]
     lib.spec_tree_attn_kv4.restype = I
+    DBL = ctypes.c_double
+    lib.spec_rope_table.argtypes = [I, DBL, I, DBL, DBL, DBL, DBL, P, P]
+    lib.spec_rope_table.restype = I
+    lib.spec_rope.argtypes = [P, P, I, I, I, I, I, I64, I64, I64, I64, P, I, F, I, P, P, P, P, P]
+    lib.spec_rope.restype = I
+    lib.spec_rope_write_paged.argtypes = [P, P, P, P, I, I, I, I, I, I, I64, I64, I64, I64, I64, I64, P, I, F, I,
+                                          P, P, I, I, P, I, P, P, P, P, P, P]
+    lib.spec_rope_write_paged.restype = I
+    lib.spec_tree_attn_paged.argtypes = [P, P, P, P, I, I, I, I, I, I, I, I, P, I, I, P, P, P, P, I, F, P, P]
+    lib.spec_tree_attn_paged.restype = I
+    lib.spec_kv_compact_paged.argtypes = [P, P, I, I, I, I, I, I, P, I, P, P, P, P, I, P, P, P]
+    lib.spec_kv_compact_paged.restype = I
     lib.spec_tree_expand.argtypes = [P, P, P, P, I, I, I, F, U64, P, P, P, P]
     lib.spec_tree_expand.restype = I
     lib.spec_tree_prune.argtypes = [P, P, P, P, I, I, P, P, P, P, P, P]
@@ -488,6 +501,222 @@ def tree_attn_kv4(q, kv_cache, prefix_lens, offsets, mask, max_prefix, status, o
     if rc:
         raise SpecError(rc, "spec_tree_attn_kv4")
     return o
+
+
+# ---------------------------------------------------------------- paged cache
+class RopeTable(NamedTuple):
+    """A rotation's frequencies: what rope and rope_write_paged take."""
+    freqs: torch.Tensor       # [rotary_dim / 2] int64 (the bits of uint64), on the device
+    scale: float              # of cosines and sines
+    rotary_dim: int
+
+
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+_I64 = torch.int64
+
+
+def rope_table(rotary_dim, base=10000.0, scaling="none", factor=1.0, original=0.0, low=1.0, high=None, device="cuda"):
+    """Frequencies of rotary positions over the first ``rotary_dim`` dims:
+    base^(-2i / rotary_dim), for contexts ``factor`` times the ``original`` one
+    scaled by "linear", "ntk", "yarn" or "bands" (spec_rope_table says how;
+    ``high`` is 32 for "yarn" and 4 for "bands" unless given).  Computed on the
+    host, once for a model."""
+    kind = _ROPE_SCALINGS.get(scaling)
+    if kind is None:
+        raise ValueError(f"scaling is one of {', '.join(_ROPE_SCALINGS)}, not {scaling!r}")
+    rotary_dim = int(rotary_dim)
+    if not 2 <= rotary_dim <= 512:
+        raise ValueError(f"rotary_dim is even and from 2 to 512, not {rotary_dim}")
+    host = torch.zeros(rotary_dim // 2, dtype=_I64)
+    scale = ctypes.c_float()
+    if high is None:
+        high = 32.0 if scaling == "yarn" else 4.0
+    rc = load().spec_rope_table(rotary_dim, float(base), kind, float(factor), float(original), float(low), float(high),
+                                host.data_ptr(), ctypes.byref(scale))
+    if rc:
+        raise SpecError(rc, "spec_rope_table")
+    return RopeTable(host.to(device), scale.value, rotary_dim)
+
+
+def _table(index, table):
+    """(pointer, rotated dims, scale) of a rotation; None rotates nothing."""
+    if table is None:
+        return None, 0, 1.0
+    freqs, scale, r = table
+    if freqs.dtype is not _I64 or freqs.get_device() != index or 2 * freqs.numel() != r or not freqs.is_contiguous():
+        raise ValueError(f"a rotation's frequencies are {r // 2} contiguous torch.int64 on cuda:{index}")
+    return freqs.data_ptr(), r, scale
+
+
+def _current(t, name):
+    """The device index of a tensor, which is the current device's."""
+    index = t.get_device()
+    if index < 0:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if index != _current_device():
+        raise ValueError(f"{name} is on cuda:{index}, the current device is cuda:{_current_device()}")
+    return index
+
+
+def _pool(k_pages, v_pages, block_table, B):
+    """Checks a paged cache; returns (device index, dtype code, pages, Hkv, page size, D, pages of a request)."""
+    index, shape = _current(k_pages, "k_pages"), k_pages.shape
+    dt = _DTYPES.get(k_pages.dtype)
+    if dt is None or v_pages.dtype is not k_pages.dtype:
+        raise TypeError("k_pages and v_pages must both be bfloat16 or float32")
+    if (len(shape) != 4 or v_pages.shape != shape or v_pages.get_device() != index or not k_pages.is_contiguous()
+            or not v_pages.is_contiguous()):
+        raise ValueError(f"k_pages and v_pages must be contiguous [pages, Hkv, page_size, D] on cuda:{index}")
+    if (block_table.dtype is not _I32 or block_table.get_device() != index or len(block_table.shape) != 2
+            or block_table.shape[0] != B or not block_table.is_contiguous()):
+        raise ValueError(f"block_table must be contiguous torch.int32 [{B}, max_pages] on cuda:{index}")
+    if shape[0] > _INT_MAX or block_table.shape[1] > _INT_MAX:
+        raise ValueError(f"a pool has at most {_INT_MAX} pages")
+    return index, dt, shape[0], shape[1], shape[2], shape[3], block_table.shape[1]
+
+
+def rope(x, table, start, offsets, status, depth=None, interleaved=False, out=None, stream=None):
+    """Rotary positions on dense rows x [T, H, D] (bf16 or fp32; rows and heads
+    at any stride): row t of request b at position start[b] + depth[t], or
+    start[b] + t - offsets[b] without ``depth``.  ``out`` may be x (in place).
+    Returns the rotated rows; a new tensor holds those of no request as they
+    happen to be."""
+    lib = _lib or load()
+    index, dt = _current(x, "x"), _DTYPES.get(x.dtype)
+    if dt is None:
+        raise TypeError("x must be bfloat16 or float32")
+    if len(x.shape) != 3:
+        raise ValueError("x must be [T, H, D]")
+    T, H, D = x.shape
+    xs0, xs1 = _dense_rows(index, x, T, H, D, "x")
+    freqs, r, scale = _table(index, table)
+    if out is None:
+        ys0, ys1 = H * D, D
+        out = _new(stream, (T, H, D), (ys0, ys1, 1), x.dtype)
+    else:
+        if out.dtype is not x.dtype:
+            raise TypeError(f"out must be {x.dtype}")
+        ys0, ys1 = _dense_rows(index, out, T, H, D, "out")
+    if depth is not None:
+        depth = _i32(index, T, depth, "depth")
+    B = status.numel()
+    start, offsets, status = _per_request(index, B, start, offsets, status, "start")
+    rc = lib.spec_rope(x.data_ptr(), out.data_ptr(), dt, B, T, H, D, xs0, xs1, ys0, ys1, freqs, r, scale,
+                       1 if interleaved else 0, start, depth, offsets, status,
+                       _current_stream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        raise SpecError(rc, "spec_rope")
+    return out
+
+
+def rope_write_paged(q, k, v, k_pages, v_pages, block_table, prefix_lens, offsets, status, table=None, depth=None,
+                     start=None, interleaved=False, q_out=None, stream=None):
+    """New rows q [T, Hq, D] (or None), k, v [T, Hkv, D] (rows and heads at any
+    stride) on their way into a paged cache: q rotated into a tensor of its
+    own, k rotated and v copied to slots prefix_lens[b] and up of request b.
+    Positions as in rope, from ``start`` or else prefix_lens on; without a
+    ``table`` nothing is rotated.  Returns the rotated q."""
+    lib = _lib or load()
+    B = status.numel()
+    index, dt, pages, Hkv, size, D, width = _pool(k_pages, v_pages, block_table, B)
+    if k.dtype is not k_pages.dtype or v.dtype is not k_pages.dtype or (q is not None and q.dtype is not k.dtype):
+        raise TypeError(f"rows must be of the cache's type, {k_pages.dtype}")
+    T = k.shape[0]
+    ks0, ks1 = _dense_rows(index, k, T, Hkv, D, "k")
+    vs0, vs1 = _dense_rows(index, v, T, Hkv, D, "v")
+    Hq = qs0 = qs1 = 0
+    q_ptr = out_ptr = None
+    if q is not None:
+        if len(q.shape) != 3 or q.shape[1] < 1:
+            raise ValueError(f"q must be [{T}, Hq, {D}]")
+        Hq = q.shape[1]
+        qs0, qs1 = _dense_rows(index, q, T, Hq, D, "q")
+        if q_out is None:
+            q_out = _new(stream, (T, Hq, D), (Hq * D, D, 1), q.dtype)
+        elif (q_out.dtype is not q.dtype or q_out.get_device() != index or q_out.shape != q.shape
+              or not q_out.is_contiguous()):
+            raise ValueError("q_out must be contiguous, of q's shape and type")
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    freqs, r, scale = _table(index, table)
+    if depth is not None:
+        depth = _i32(index, T, depth, "depth")
+    if start is not None:
+        start = _i32(index, B, start, "start")
+    prefix, offsets, status = _per_request(index, B, prefix_lens, offsets, status, "prefix_lens")
+    rc = lib.spec_rope_write_paged(q_ptr, out_ptr, k.data_ptr(), v.data_ptr(), dt, B, T, Hq, Hkv, D, qs0, qs1, ks0, ks1,
+                                   vs0, vs1, freqs, r, scale, 1 if interleaved else 0, k_pages.data_ptr(),
+                                   v_pages.data_ptr(), pages, size, block_table.data_ptr(), width, prefix, start,
+                                   depth, offsets, status,
+                                   _current_stream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        raise SpecError(rc, "spec_rope_write_paged")
+    return q_out
+
+
+def tree_attn_paged(q, k_pages, v_pages, block_table, prefix_lens, offsets, mask, max_prefix, status, o=None,
+                    softmax_scale: float = 0.0, stream=None, parents=None, causal=False):
+    """Attention over a paged cache.  q [T, Hq, D] bf16 or fp32; trees by
+    ``mask``, or by ``parents`` when it is None, as in tree_attn; with
+    ``causal`` (mask and parents None) request b's rows are a run of any
+    number of tokens behind its prefix, each seeing all before it.  Rows of
+    ``o`` behind the last request stay as they were."""
+    lib = _lib or load()
+    B = status.numel()
+    index, dt, pages, Hkv, size, D, width = _pool(k_pages, v_pages, block_table, B)
+    shape = q.shape
+    if q.dtype is not k_pages.dtype:
+        raise TypeError(f"q must be of the cache's type, {k_pages.dtype}")
+    if len(shape) != 3 or shape[2] != D or q.get_device() != index or not q.is_contiguous():
+        raise ValueError(f"q must be contiguous [T, Hq, {D}] on cuda:{index}")
+    T, Hq, _ = shape
+    if T > _INT_MAX or Hq > _INT_MAX:
+        raise ValueError(f"q may have {_INT_MAX} rows and heads")
+    mask_ptr = parents_ptr = None
+    if causal:
+        if mask is not None or parents is not None:
+            raise ValueError("a causal run takes neither mask nor parents")
+    elif mask is not None:
+        mask_ptr = _i32(index, 4 * T, mask, "mask")
+    elif parents is not None:
+        parents_ptr = _i32(index, T, parents, "parents")
+    else:
+        raise ValueError("tree_attn_paged needs a mask, the parent array or causal=True")
+    if o is None:
+        o = _new(stream, (T, Hq, D), (Hq * D, D, 1), q.dtype)
+    elif o.dtype is not q.dtype or o.get_device() != index or o.shape != q.shape or not o.is_contiguous():
+        raise ValueError("o must be like q")
+    prefix, offsets, status = _per_request(index, B, prefix_lens, offsets, status, "prefix_lens")
+    rc = lib.spec_tree_attn_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), o.data_ptr(), dt, B, T, Hq,
+                                  Hkv, D, pages, size, block_table.data_ptr(), width, min(max_prefix, _INT_MAX), prefix,
+                                  offsets, mask_ptr, parents_ptr, 1 if causal else 0, softmax_scale, status,
+                                  _current_stream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        raise SpecError(rc, "spec_tree_attn_paged")
+    return o
+
+
+def kv_compact_paged(k_pages, v_pages, block_table, prefix_lens, offsets, path_nodes, accept_len, status,
+                     new_prefix_lens=None, stream=None):
+    """kv_compact on a paged cache (in place).  Returns the new prefix lengths
+    (device int32 [B])."""
+    lib = _lib or load()
+    B = status.numel()
+    index, dt, pages, Hkv, size, D, width = _pool(k_pages, v_pages, block_table, B)
+    W = path_nodes.shape[-1]
+    if new_prefix_lens is None:
+        new_prefix_lens = _new(stream, (B,), (1,), _I32)
+    prefix, offsets, status = _per_request(index, B, prefix_lens, offsets, status, "prefix_lens")
+    rc = lib.spec_kv_compact_paged(k_pages.data_ptr(), v_pages.data_ptr(), dt, B, Hkv, D, pages, size,
+                                   block_table.data_ptr(), width, prefix, offsets,
+                                   _i32(index, B * W, path_nodes, "path_nodes"),
+                                   _i32(index, B, accept_len, "accept_len"), W,
+                                   _i32(index, B, new_prefix_lens, "new_prefix_lens"), status,
+                                   _current_stream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        raise SpecError(rc, "spec_kv_compact_paged")
+    return new_prefix_lens
 
 
 def tree_expand(draft_logits, parent_scores, node_ids, requests, width: int, temperature: float,

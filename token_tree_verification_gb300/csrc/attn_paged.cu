@@ -1,0 +1,594 @@
+// Attention of trees and chunks over a paged cache on the 5th-generation
+// tensor cores, bf16 in, fp32 accumulate.
+//
+// One CTA = one split of the keys x one block of 128 query rows (node-major,
+// head-minor) of one request and KV head, so that a tile of keys and values
+// serves every query head of its KV head.  Rows lie along M:
+//   S[rows][keys] = Q K^T   A = Q (TMEM),  B = K (keys x dims, shared memory, K-major)
+//   O[rows][dims] = P V     A = P (TMEM),  B = V (keys x dims, shared memory, MN-major)
+// P enters its product as a bf16 high part and a bf16 remainder, some 16
+// significant bits of each weight: with the high part alone elements of a
+// hundredth of the output's largest come out wrong by a tenth (their terms
+// cancel).  That makes a tile's tensor work 3/2 of the least: 512 cycles for S
+// and 1024 for O per 128 keys at D = 128.
+//
+// Warp roles:
+//   warp 0      brings tiles of 128 keys and of 128 values into rings of their
+//               own; a lane copies one box, 64 dims of one page's slots (of 128 at
+//               most), whose page it looked up a tile ahead
+//   warp 1      allocates TMEM and issues S_i as soon as K_i is there and the
+//               softmax has taken S_{i-1} into registers
+//   warp 2      issues O += P_i V_i
+//   warp 3      looks through the request's whole page table: a request that
+//               names a page outside the pool gets no output
+//   warps 4-11  softmax: a TMEM lane quarter's two warps hold the same 32 rows,
+//               each one half of a tile's keys.  A row has one reference; its two
+//               threads meet once a tile to learn whether either has a score that
+//               passes it by more than 2^8, which moves it (the tile's weights
+//               are then taken again from S, and O rescaled)
+// P has a place in TMEM beside S, so that the weights of a tile are worked out
+// while the last tile's are multiplied, and S of the next tile is multiplied
+// while they are stored.  A quarter without rows leaves the softmax out.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "attn_kv4_tc.cuh"
+#include "attn_paged.cuh"
+
+namespace spec {
+
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kSoftFirst = 4;         // warps: issuers and the page check, then the softmax
+constexpr int kSoftWarps = 8;
+constexpr int kSoftThreads = 32 * kSoftWarps;
+constexpr int kThreads = 32 * (kSoftFirst + kSoftWarps);
+constexpr int kHalf = kTile / 2;      // keys of one softmax thread
+constexpr float kPass = 8.f;          // powers of two by which a score may pass its row's reference
+
+template <int D>
+struct PagedCfg {
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kBoxBytes = kTile * 128;             // 128 slots of 64 dims
+  static constexpr int kTileBytes = kBoxes * kBoxBytes;
+  static constexpr int kStages = D == 128 ? 3 : 6;          // of keys, and as many of values
+  static constexpr int kOffK = 0, kOffV = kStages * kTileBytes;
+  static constexpr int kEnd = 2 * kStages * kTileBytes;
+  // after the loop: the rows, the ones received, and references and sums
+  static constexpr int kOffRecv = kRows * (D + 4) * 4;
+  static constexpr int kOffMl = kOffRecv + (kRows * D + 4 * kMaxSplits) * 4;
+  static constexpr int kMerge = kOffMl + kMaxSplits * kRows * 8;
+  static constexpr int kSmem = (kEnd > kMerge ? kEnd : kMerge) + 1024;
+  // TMEM: S, P (a pair of keys per column, remainders behind the high parts), O, Q
+  // (a pair of dims)
+  static constexpr uint32_t kColP = kTile, kColO = kColP + kTile, kColQ = kColO + 128, kTmemCols = 512;
+  static_assert(kSmem <= 227 * 1024 - 8192, "shared memory budget");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMap tmk,
+                       const __grid_constant__ CUtensorMap tmv, const int CS) {
+  using C = PagedCfg<D>;
+  constexpr int NS = C::kStages;
+  const AttnArgs &a = p.a;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ struct {
+    uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
+    uint64_t q_full, s_full, s_empty, p_full, o_done, drained[2];
+  } bars;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_timeout, s_bad_page;
+  __shared__ int s_par[SPEC_MAX_TREE_NODES];
+  __shared__ long long s_row[kRows];          // a row's first element of o
+  __shared__ float s_most[2][kRows];          // [half of the keys][row]
+  __shared__ float s_part[kRows];             // a row's sum over the second halves
+  __shared__ float s_ref[1][kRows], s_sum[1][kRows];
+
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  const uint32_t sb = smem_addr(smem);
+  const int split = static_cast<int>(blockIdx.x) % CS, block = static_cast<int>(blockIdx.x) / CS;
+  const int g_kv = static_cast<int>(blockIdx.y);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  pdl_trigger();
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&bars.k_full[s], 1);
+      mbar_init(&bars.k_empty[s], 1);
+      mbar_init(&bars.v_full[s], 1);
+      mbar_init(&bars.v_empty[s], 1);
+    }
+    mbar_init(&bars.q_full, kSoftWarps);
+    mbar_init(&bars.s_full, 1);
+    mbar_init(&bars.s_empty, kSoftWarps);
+    mbar_init(&bars.p_full, kSoftWarps);
+    mbar_init(&bars.o_done, 1);
+    mbar_init(&bars.drained[0], 1);
+    mbar_init(&bars.drained[1], 1);
+    fence_barrier_init();
+    s_timeout = 0;
+    s_bad_page = 0;
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmk);
+    tma_prefetch_desc(&tmv);
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(&s_tmem, C::kTmemCols);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = s_tmem;
+  pdl_wait();
+
+  const RowBlock w = find_block<kRows>(p, block, lane);
+  if (blockIdx.x == 0 && g_kv == 0 && warp == 3) report_bad_requests(p, lane);
+  if (w.b < 0 || w.R.err) {       // the same for every CTA of the cluster
+    if (warp == 1) {
+      __syncwarp();
+      tc::tmem_dealloc(tmem, C::kTmemCols);
+    }
+    return;
+  }
+  const int b = w.b, L = w.R.L;
+  const int all = (w.keys + kTile - 1) / kTile;
+  const int per = (all + CS - 1) / CS;
+  const int t0 = split * per;
+  const int ntiles = max(0, min(t0 + per, all) - t0);
+  bool ok = true;      // cleared by a wait that ran out: the role goes on without waiting, and no row is written
+
+  Ring<NS> kr, vr;     // warp 0's
+  if (warp == 0) {
+    // ------------------------------------------------------------ keys and values
+    const int shift = min(p.pages.shift, 7), box_rows = 1 << shift;      // slots of a box
+    const int place = lane / C::kBoxes, bx = lane % C::kBoxes;
+    const int in_page = (1 << p.pages.shift) - 1;
+    auto boxes = [&](int i) {      // of tile i that hold a key
+      return (min(kTile, w.keys - (t0 + i) * kTile) + box_rows - 1) >> shift;
+    };
+    auto look_up = [&](int i) {    // (an id outside the pool: any page will do, no row is written)
+      if (i >= ntiles || place >= boxes(i)) return 0;
+      return max(0, p.pages.page(b, ((t0 + i) * kTile + (place << shift)) >> p.pages.shift));
+    };
+    kr.phase = vr.phase = 1;       // every stage is free at first
+    int page = look_up(0);
+    for (int i = 0; i < ntiles && ok; ++i) {
+      const int next = look_up(i + 1);
+      const int n = boxes(i), slot = ((t0 + i) * kTile + (place << shift)) & in_page;
+      const uint32_t bytes = static_cast<uint32_t>(n * C::kBoxes * box_rows * 128);
+      auto bring = [&](uint64_t *full, uint64_t *empty, const CUtensorMap &map, int off, Ring<NS> &ring) {
+        // (a consumer that gave up frees a stage whose last copy has not landed: nothing
+        // may be announced on a barrier that still awaits bytes)
+        ok = ok && mbar_sleep(smem_addr(&empty[ring.at]), ring.phase) &&
+             mbar_over(smem_addr(&full[ring.at]), ring.phase);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        if (lane == 0) mbar_arrive_expect_tx(&full[ring.at], bytes);
+        __syncwarp();
+        if (place < n)
+          tma_load_4d(smem + off + ring.at * C::kTileBytes + bx * C::kBoxBytes + (place << shift) * 128, &map,
+                      &full[ring.at], bx * 64, slot, g_kv, page);
+        ring.next();
+      };
+      bring(bars.k_full, bars.k_empty, tmk, C::kOffK, kr);
+      bring(bars.v_full, bars.v_empty, tmv, C::kOffV, vr);
+      page = next;
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ S = Q K^T
+    constexpr uint32_t id = tc::idesc_bf16_f32(kRows, kTile, 0, 0);
+    const uint64_t kd0 = tc::smem_desc_sw128(sb + C::kOffK, 16, 1024);
+    Ring<NS> ring;
+    const bool leader = tc::elect_one();
+    if (ntiles > 0) ok = mbar_sleep(smem_addr(&bars.q_full), 0);
+    for (int i = 0; i < ntiles; ++i, ring.next()) {
+      ok = ok && mbar_sleep(smem_addr(&bars.k_full[ring.at]), ring.phase);
+      ok = ok && mbar_sleep(smem_addr(&bars.s_empty), (i & 1) ^ 1);
+      tc::fence_after_sync();
+      const uint64_t kd = kd0 + static_cast<uint64_t>((ring.at * C::kTileBytes) >> 4);
+      if (leader) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          tc::mma_bf16_ts(tmem, tmem + C::kColQ + ks * 8, kd + (((ks >> 2) * C::kBoxBytes + (ks & 3) * 32) >> 4), id,
+                          ks > 0);
+        tc::commit(&bars.s_full);
+        tc::commit(&bars.k_empty[ring.at]);
+      }
+      __syncwarp();
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ O += P V
+    constexpr uint32_t id = tc::idesc_bf16_f32(kRows, D, 0, 1);
+    const uint64_t vd0 = tc::smem_desc_sw128(sb + C::kOffV, C::kBoxBytes, 1024);
+    Ring<NS> ring;
+    const bool leader = tc::elect_one();
+    for (int i = 0; i < ntiles; ++i, ring.next()) {
+      ok = ok && mbar_sleep(smem_addr(&bars.v_full[ring.at]), ring.phase);
+      ok = ok && mbar_sleep(smem_addr(&bars.p_full), i & 1);
+      tc::fence_after_sync();
+      const uint64_t vd = vd0 + static_cast<uint64_t>((ring.at * C::kTileBytes) >> 4);
+      if (leader) {
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk) {
+          const uint32_t pt = tmem + C::kColP + kk * 8;
+          const uint64_t v = vd + (kk * 16 * 128 >> 4);
+          tc::mma_bf16_ts(tmem + C::kColO, pt, v, id, (i | kk) != 0);
+          tc::mma_bf16_ts(tmem + C::kColO, pt + kTile / 2, v, id, true);
+        }
+        tc::commit(&bars.o_done);
+        tc::commit(&bars.v_empty[ring.at]);
+      }
+      __syncwarp();
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ the page table
+    if (warp_finds_bad_page(p.pages, b, 0, w.R.keys, lane) && lane == 0) s_bad_page = 1;
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int quad = warp & 3, half = (warp - kSoftFirst) >> 2;
+    const int soft = tid - 32 * kSoftFirst;            // 0 .. 255
+    const int row = quad * 32 + lane;                  // and TMEM lane
+    const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t s_col = trow + half * kHalf, p_col = trow + C::kColP + half * (kHalf / 2);
+    const uint32_t o_col = trow + C::kColO + half * (D / 2);
+    const uint32_t s_full = smem_addr(&bars.s_full), s_empty = smem_addr(&bars.s_empty),
+                   p_full = smem_addr(&bars.p_full), o_done = smem_addr(&bars.o_done);
+    const bool busy = quad * 32 < w.rows;              // (a quarter without rows only keeps the barriers going)
+    const bool live = row < w.rows;
+    // ---- Q: this thread's row, half of its dims
+    const int node = (w.row0 + row) / a.G;
+    const bool mine = live && in_bounds(w.R.lo + node, a.T, a.status, b);
+    const long long first =
+        (static_cast<long long>(w.R.lo + node) * a.Hq + g_kv * a.G + (w.row0 + row) - node * a.G) * D;
+    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + first + half * (D / 2));
+    uint4 m = make_uint4(0u, 0u, 0u, 0u);
+    if (busy) {
+      uint4 x4[D / 16];
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) x4[c] = mine ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+      if (a.mask && mine) m = clip_mask(__ldg(a.mask + w.R.lo + node), w.R.n);
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) {
+        const uint4 x = x4[2 * q], y = x4[2 * q + 1];
+        const uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        tc::st8(trow + C::kColQ + half * (D / 4) + 8 * q, u);
+      }
+      tc::wait_st();
+    }
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_at(smem_addr(&bars.q_full));
+    if (half == 0) s_row[row] = mine ? first : -1;
+    // ---- what this thread's row sees
+    if (a.parents) {
+      for (int i = soft; i < w.R.n; i += kSoftThreads)
+        s_par[i] = in_bounds(w.R.lo + i, a.T, a.status, b) ? __ldg(a.parents + w.R.lo + i) : -2;
+      named_bar_sync(1, kSoftThreads);
+      bool bad = false;
+      if (live) m = ancestor_mask([&](int i) { return s_par[i]; }, node, &bad);
+      if (bad) report(a.status, b, SPEC_ERR_BAD_PARENT);
+    }
+    const RowSees see = {p.causal ? L + node + 1 : L, m};
+    const int all_see = p.causal ? L + w.row0 / a.G + 1 : L;       // what every row of the block sees: [0, all_see)
+    const float c = a.scale_log2;
+    float ref = -INFINITY, sum = 0.f;      // in powers of two; of the weights 2^(score - ref)
+    auto largest = [&](float mine_) {      // of the row's two threads
+      s_most[half][row] = mine_;
+      named_bar_sync(2 + quad, 64);
+      return fmaxf(s_most[0][row], s_most[1][row]);
+    };
+
+    for (int i = 0; i < ntiles; ++i) {
+      const int key0 = (t0 + i) * kTile, k0 = key0 + half * kHalf;
+      ok = ok && mbar_sleep(s_full, i & 1);
+      __syncwarp();
+      tc::fence_after_sync();
+      float x[2][32];
+      if (busy) {
+        tc::ld32(s_col, x[0]);
+        tc::ld32(s_col + 32, x[1]);
+        tc::wait_ld();
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_at(s_empty);
+      uint32_t hi[kHalf / 16][8], lo[kHalf / 16][8];
+      if (busy) {
+        if (k0 + kHalf > all_see) {
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            const uint32_t sees = sees_32(see, k0 + 32 * part, L);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!((sees >> j) & 1u)) x[part][j] = -INFINITY;
+          }
+        }
+        const float most = fmaxf(max_of(x[0]), max_of(x[1])) * c;
+        bool moves = i == 0;
+        if (i > 0) moves = named_bar_or(2 + quad, 64, most > ref + kPass);
+        if (moves) {
+          const float top = largest(most);
+          const bool mine_moves = i == 0 || top > ref + kPass;
+          const float factor = !mine_moves ? 1.f : ref == -INFINITY ? 0.f : exp2f(ref - top);
+          if (mine_moves) ref = top;
+          sum *= factor;
+          if (i > 0) {
+            // O holds the products of the earlier tiles
+            ok = ok && mbar_sleep(o_done, (i - 1) & 1);
+            __syncwarp();
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int j = 0; j < D / 2; j += 8) {
+              float o[8];
+              tc::ld8(o_col + j, o);
+              tc::wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] *= factor;
+              tmem_st(o_col + j, o);
+            }
+            tc::wait_st();
+          }
+        }
+        // weights 2^(s c - ref): one rounding of the difference, except where the
+        // reference has no places behind the point left; there the largest score's
+        // own rounding must cancel, or its weight could pass fp32's range
+        const float base = ref == -INFINITY ? 0.f : -ref;
+        const bool steep = !(fabsf(base) < kWholeEnd);
+        const float cs = steep ? 1.f : c;
+        if (__any_sync(0xffffffffu, steep)) {
+          const float pre = steep ? c : 1.f;
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[part][j] = __fmul_rn(x[part][j], pre);
+        }
+        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            float *y = &x[part][j];
+            fma2(y[0], y[1], cs, cs, base, base);
+            fma2(y[2], y[3], cs, cs, base, base);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = fast_exp2(y[e]);
+            add2(s0, s1, y[0], y[1]);
+            add2(s2, s3, y[2], y[3]);
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(y[e], y[e + 1]);
+              const uint32_t u = *reinterpret_cast<const uint32_t *>(&h);
+              float r0 = __uint_as_float(u << 16), r1 = __uint_as_float(u & 0xFFFF0000u);
+              fma2(r0, r1, -1.f, -1.f, y[e], y[e + 1]);
+              const __nv_bfloat162 l = __floats2bfloat162_rn(r0, r1);
+              hi[2 * part + j / 16][(j + e) / 2 % 8] = u;
+              lo[2 * part + j / 16][(j + e) / 2 % 8] = *reinterpret_cast<const uint32_t *>(&l);
+            }
+          }
+        add2(s0, s1, s2, s3);
+        sum += s0 + s1;
+      }
+      if (key0 + kTile > w.keys) {
+        // slots behind the last key may hold anything: a weight of zero does not
+        // hide a NaN
+        const int at = i % NS;
+        ok = ok && mbar_sleep(smem_addr(&bars.v_full[at]), (i / NS) & 1);
+        const int valid = w.keys - key0, pieces = (kTile - valid) * C::kBoxes * 8;
+        for (int z = soft; z < pieces; z += kSoftThreads) {
+          const int r = valid + z / (C::kBoxes * 8), rest = z % (C::kBoxes * 8);
+          st_shared_v4(sb + C::kOffV + at * C::kTileBytes + (rest >> 3) * C::kBoxBytes + r * 128 + (rest & 7) * 16, 0u,
+                       0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+      }
+      // ---- the weights' place is free once the last tile's product is done
+      if (i > 0) ok = ok && (mbar_over(o_done, (i - 1) & 1) || mbar_sleep(o_done, (i - 1) & 1));
+      __syncwarp();
+      tc::fence_after_sync();
+      if (busy) {
+#pragma unroll
+        for (int q = 0; q < kHalf / 16; ++q) {
+          tc::st8(p_col + 8 * q, hi[q]);
+          tc::st8(p_col + kTile / 2 + 8 * q, lo[q]);
+        }
+        tc::wait_st();
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_at(p_full);
+    }
+    // ---- the block's rows out of TMEM; their place in shared memory is free
+    //      once the last product is done
+    if (ntiles > 0) ok = ok && mbar_sleep(o_done, (ntiles - 1) & 1);
+    __syncwarp();
+    tc::fence_after_sync();
+    if (busy) {
+      if (half == 1) s_part[row] = sum;
+      named_bar_sync(2 + quad, 64);
+      if (half == 0) {
+        s_sum[0][row] = sum + s_part[row];
+        s_ref[0][row] = ref;
+      }
+      if (ok) {
+        const uint32_t so = sb + (row * (D + 4) + half * (D / 2)) * 4;
+#pragma unroll
+        for (int j = 0; j < D / 2; j += 32) {
+          float o[32] = {};
+          if (ntiles > 0) {
+            tc::ld32(o_col + j, o);
+            tc::wait_ld();
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            st_shared_v4(so + (j + e) * 4, __float_as_uint(o[e]), __float_as_uint(o[e + 1]), __float_as_uint(o[e + 2]),
+                         __float_as_uint(o[e + 3]));
+        }
+      }
+    }
+  }
+  if (!ok) s_timeout = 1;
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const bool timed_out = s_timeout != 0, bad_page = s_bad_page != 0;
+  if (timed_out) {
+    // What was given up may leave copies and products under way: the warps that
+    // issued them wait, with a limit.  (Of a stage that has had no copy the phase
+    // before is over.)
+    if (tid == 0) {
+      report(a.status, b, SPEC_ERR_TIMEOUT);
+      for (uint32_t st = 0; st < NS; ++st) {
+        mbar_wait(&bars.k_full[st], st < kr.at ? kr.phase ^ 1 : kr.phase);
+        mbar_wait(&bars.v_full[st], st < vr.at ? vr.phase ^ 1 : vr.phase);
+      }
+    }
+    if (warp == 1 || warp == 2) {
+      if (tc::elect_one()) tc::commit(&bars.drained[warp - 1]);
+      __syncwarp();
+      mbar_wait(&bars.drained[warp - 1], 0);
+    }
+    __syncthreads();
+  }
+  if (bad_page && tid == 0) report(a.status, b, SPEC_ERR_PAGE);
+  if (warp == 1) {
+    __syncwarp();
+    tc::tmem_dealloc(tmem, C::kTmemCols);
+  }
+  // (a page outside the pool is found by every CTA of the cluster)
+  auto out_row = [&](int r) { return s_row[r] < 0 ? nullptr : static_cast<__nv_bfloat16 *>(a.o) + s_row[r]; };
+  merge_rows<D, 1, kRows, kThreads, __nv_bfloat16>(
+      tid, CS, split, w.rows, timed_out || bad_page, reinterpret_cast<float *>(smem), s_ref, s_sum,
+      reinterpret_cast<float2 (*)[kRows]>(smem + C::kOffMl), reinterpret_cast<float4 *>(smem + C::kOffRecv),
+      [] { cluster_sync_all(); }, out_row);
+}
+
+// ---------------------------------------------------------------- host side
+using EncodeFn = PFN_cuTensorMapEncodeTiled_v12000;
+
+EncodeFn tensor_map_encoder() {
+  static EncodeFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeFn>(f);
+  });
+  return fn;
+}
+
+// 4-D map over a pool [pages][Hkv][slots][D]: a box is 64 dims of a page's
+// slots, 128 at most, loaded with 128-byte swizzle.  (Boxes of eight slots and
+// up start on the 1024 bytes over which the swizzle repeats.)
+bool encode_pool(CUtensorMap *m, const void *base, const PageTable &pages, int Hkv, int D) {
+  const EncodeFn enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t slots = 1ull << pages.shift;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), slots, static_cast<cuuint64_t>(Hkv),
+                              static_cast<cuuint64_t>(pages.pages)};
+  const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;
+  const cuuint64_t strides[3] = {row, slots * row, static_cast<cuuint64_t>(Hkv) * slots * row};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(slots < kTile ? slots : kTile), 1, 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// As many splits of the keys (a cluster) as make waves x (tiles of a CTA + its
+// set-up, first tile and merge, in half tiles) least.
+template <int D>
+int launch_bf16(const PagedAttnArgs &p, int max_prefix, void *stream) {
+  using C = PagedCfg<D>;
+  auto kernel = tree_attn_paged_kernel<D>;
+  static KernelState state;
+  const int dev = current_device();
+  if (dev < 0 || !allow_clusters(kernel, C::kSmem, dev, &state)) return SPEC_ERR_CUDA;
+  CUtensorMap tmk, tmv;
+  if (!encode_pool(&tmk, p.a.k, p.pages, p.a.Hkv, D) || !encode_pool(&tmv, p.a.v, p.pages, p.a.Hkv, D))
+    return SPEC_ERR_CUDA;
+  const long long blocks = most_blocks<kRows>(p.a), units = blocks * p.a.Hkv;
+  const long long keys = static_cast<long long>(max_prefix) + mean_nodes(p.a);
+  const long long tiles = (keys + kTile - 1) / kTile;
+  int cs = 1;
+  long long best = -1;
+  for (int n = 1; n <= kMaxSplits; n = n == 8 ? kMaxSplits : n + 1) {
+    if (n > 1 && tiles < 2 * n) break;
+    const int slots = clusters_at_once(kernel, n, kThreads, C::kSmem, dev, &state);
+    if (slots < 1) continue;
+    const long long waves = (units + slots - 1) / slots;
+    const long long cost = waves * (2 * ((tiles + n - 1) / n) + (n > 1 ? 12 : 8));
+    if (best < 0 || cost < best) {
+      best = cost;
+      cs = n;
+    }
+  }
+  if (blocks * cs > 0x7FFFFFFFll) return SPEC_ERR_SHAPE;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cluster_config(cfg, attr, cs, kThreads, C::kSmem);
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks * cs), static_cast<unsigned>(p.a.Hkv), 1);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  return cudaLaunchKernelEx(&cfg, kernel, p, tmk, tmv, cs) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+}  // namespace
+
+}  // namespace spec
+
+extern "C" int spec_tree_attn_paged(const void *q, const void *k_pages, const void *v_pages, void *o, int dtype, int B,
+                                    int T, int Hq, int Hkv, int D, int num_pages, int page_size,
+                                    const int32_t *block_table, int max_pages, int max_prefix,
+                                    const int32_t *prefix_lens, const int32_t *offsets, const uint32_t *mask,
+                                    const int32_t *parents, int causal, float softmax_scale, int32_t *status,
+                                    void *stream) {
+  using namespace spec;
+  if (((!q || !o) && T != 0) || !k_pages || !v_pages || !block_table || !prefix_lens || !offsets || !status ||
+      (!causal && !mask && !parents))
+    return SPEC_ERR_NULL;
+  if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_DTYPE;
+  PagedAttnArgs p = {};
+  const int rc = check_pages(num_pages, page_size, max_pages, &p.pages.shift);
+  if (rc != SPEC_OK) return rc;
+  if (causal && (mask || parents)) return SPEC_ERR_SHAPE;
+  if (B < 1 || T < 0 || Hq < 1 || Hkv < 1 || Hkv > 65535 || Hq % Hkv || Hq / Hkv > SPEC_MAX_TREE_NODES ||
+      (D != 64 && D != 128) || max_prefix < 0 || static_cast<long long>(T) * Hq > 0x7FFFFFFFll)
+    return SPEC_ERR_SHAPE;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_pages) | reinterpret_cast<uintptr_t>(v_pages) |
+       reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(mask)) & 15)
+    return SPEC_ERR_ALIGNMENT;
+  if (T == 0) return SPEC_OK;
+  AttnArgs &a = p.a;
+  a.q = q;
+  a.k = k_pages;
+  a.v = v_pages;
+  a.o = o;
+  a.prefix_lens = prefix_lens;
+  a.offsets = offsets;
+  a.mask = reinterpret_cast<const uint4 *>(mask);
+  a.parents = mask ? nullptr : parents;
+  a.status = status;
+  a.B = B;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.D = D;
+  p.pages.table = block_table;
+  p.pages.max_pages = max_pages;
+  p.pages.pages = num_pages;
+  p.causal = causal != 0;
+  const long long slots = static_cast<long long>(max_pages) << p.pages.shift;
+  a.S_cap = static_cast<int>(slots < 0x7FFFFFFFll - 4096 ? slots : 0x7FFFFFFFll - 4096);
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf(static_cast<float>(D));
+  a.scale_log2 = scale * 1.4426950408889634f;
+  if (dtype == SPEC_F32) return launch_attn_paged_f32(p, max_prefix, stream);
+  return D == 128 ? launch_bf16<128>(p, max_prefix, stream) : launch_bf16<64>(p, max_prefix, stream);
+}

@@ -1,0 +1,499 @@
+// Rotary positions, on dense rows and on the way into a paged cache.
+//
+// Pair i of a head's first r dims, (i, i + r/2) or (2i, 2i + 1), is turned by the
+// angle p theta_i of the row's position p:
+//   y_a = s (x_a cos - x_b sin),  y_b = s (x_a sin + x_b cos)
+// theta_i = base^(-2i/r), scaled for contexts longer than the model's (see
+// spec_rope_table); the other D - r dims stay as they are.
+//
+// Angles.  At position 2^20 an fp32 product p theta is off by up to 2^-5
+// radians, and fp64 arithmetic is slow here.  The table holds theta / 2 pi, the
+// turns a position, as a 64-bit fraction: p times it, modulo 2^64, is the
+// angle's fraction of a turn, off by less than p 2^-53 of a turn's unit in the
+// table (a double) and exact otherwise.  Its upper 32 bits go to sincospif as a
+// number of half turns in [-1, 1), which rounds to 2^-25.
+//
+// One CTA takes up to eight whole rows, or a part of one row's heads; a row's
+// cosines and sines are computed once for all of its heads.  An item is two
+// 16-byte vectors: both ends of eight (four, fp32) pairs, or two vectors of
+// dims that are copied.  The first items' loads need no look-up and are issued in
+// front of them: offsets, start and depth, page are a chain of three loads.
+#include <cuda_bf16.h>
+
+#include <cmath>
+
+#include "paged.cuh"
+
+namespace spec {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxRows = kThreads / 32;      // a warp looks up each row
+constexpr int kItems = 2;                    // of a thread, under way at once
+
+struct Rows {
+  const void *x;
+  long long st, sh;       // element strides of a row and of a head
+};
+
+struct RopeArgs {
+  Rows q, k, v;                      // v.x: null without a cache
+  void *y;                           // rotated q
+  long long y_st, y_sh;
+  void *k_pages, *v_pages;
+  PageTable pages;
+  const unsigned long long *freqs;   // [r / 2] turns a position, times 2^64
+  float scale;
+  const int32_t *slots, *start, *depth, *offsets;   // slots: prefix lengths (cache)
+  int32_t *status;
+  int B, T, Hq, Hkv, D, r;
+  int turn_items, copy_items;        // of a rotated and of a copied head
+  int row_items, span, rows;         // of a row, of a row in one CTA, and rows of a CTA
+};
+
+template <typename E>
+struct Vec;
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int n = 8;
+  static __device__ __forceinline__ void unpack(uint4 v, float (&f)[8]) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(u[i] << 16);
+      f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      u[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+};
+template <>
+struct Vec<float> {
+  static constexpr int n = 4;
+  static __device__ __forceinline__ void unpack(uint4 v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x);
+    f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z);
+    f[3] = __uint_as_float(v.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_float(float x, float *y) { *y = x; }
+__device__ __forceinline__ void from_float(float x, __nv_bfloat16 *y) { *y = __float2bfloat16_rn(x); }
+
+// (x_a, x_b) turned, in fp32.
+__device__ __forceinline__ void turn(float &xa, float &xb, float2 cs) {
+  const float a = xa * cs.x - xb * cs.y, b = xa * cs.y + xb * cs.x;
+  xa = a;
+  xb = b;
+}
+
+// One unit of a thread's work: where its elements lie in a head, and whether
+// they are turned.  Vectors (kVec): two of them at pa and pb (pb < 0: one).  Else
+// single elements: the two of a pair, or one that is copied.
+struct Item {
+  int row, head, pa, pb;      // head: q's, then k's, then v's
+  bool turn_a, turn_b;
+  int pair;                   // first pair of pa's cosines
+};
+
+template <typename E, bool kVec, bool kInter>
+__device__ __forceinline__ Item item_at(const RopeArgs &a, int idx, int first) {
+  Item it;
+  it.row = idx / a.span;
+  int i = first + idx - it.row * a.span;
+  constexpr int V = kVec ? Vec<E>::n : 1;
+  const int turned = (a.Hq + a.Hkv) * a.turn_items;
+  it.turn_a = it.turn_b = false;
+  it.pair = 0;
+  it.pb = -1;
+  if (i >= turned) {
+    i -= turned;
+    const int h = i / a.copy_items, j = i - h * a.copy_items;
+    it.head = a.Hq + a.Hkv + h;
+    it.pa = j * V;
+    if (kVec && j + a.copy_items < a.D / V) it.pb = (j + a.copy_items) * V;
+    return it;
+  }
+  it.head = i / a.turn_items;
+  const int j = i - it.head * a.turn_items;
+  if constexpr (kVec && kInter) {
+    it.pa = j * V;
+    it.turn_a = it.pa < a.r;
+    it.pair = it.pa / 2;
+    if (j + a.turn_items < a.D / V) it.pb = (j + a.turn_items) * V;
+    it.turn_b = it.pb >= 0 && it.pb < a.r;
+  } else {
+    const int half = a.r / 2 / V;
+    if (j < half) {
+      it.turn_a = it.turn_b = true;
+      it.pair = j * V;
+      it.pa = kInter ? 2 * j : j * V;
+      it.pb = kInter ? 2 * j + 1 : a.r / 2 + j * V;
+    } else if (kVec) {
+      it.pa = a.r + 2 * (j - half) * V;
+      if (it.pa + V < a.D) it.pb = it.pa + V;
+    } else {
+      it.pa = a.r + j - half;
+    }
+  }
+  return it;
+}
+
+template <typename E, bool kVec, bool kInter>
+__global__ void __launch_bounds__(kThreads)
+rope_kernel(const RopeArgs a) {
+  extern __shared__ __align__(16) float2 s_cs[];       // [rows][r / 2]
+  __shared__ int s_ok[kMaxRows], s_pos[kMaxRows];
+  __shared__ long long s_slot[kMaxRows];               // first element of the slot's head 0 in the pools
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int t0 = static_cast<int>(blockIdx.x) * a.rows;
+  const int rows = min(a.rows, a.T - t0);
+  const int first = static_cast<int>(blockIdx.y) * a.span;
+  const int total = rows * min(a.span, a.row_items - first);
+  using Load = typename std::conditional<kVec, uint4, E>::type;
+  pdl_trigger();
+  pdl_wait();
+
+  auto source = [&](const Item &it) -> const E * {
+    const bool is_q = it.head < a.Hq, is_k = it.head < a.Hq + a.Hkv;
+    const Rows &s = is_q ? a.q : is_k ? a.k : a.v;
+    const int h = is_q ? it.head : is_k ? it.head - a.Hq : it.head - a.Hq - a.Hkv;
+    return static_cast<const E *>(s.x) + (t0 + it.row) * s.st + h * s.sh;
+  };
+  Load la[kItems], lb[kItems];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < kItems; ++u) {
+      const int idx = i0 + u * kThreads;
+      if (idx >= total) continue;
+      const Item it = item_at<E, kVec, kInter>(a, idx, first);
+      const E *x = source(it);
+      la[u] = *reinterpret_cast<const Load *>(x + it.pa);
+      if (it.pb >= 0) lb[u] = *reinterpret_cast<const Load *>(x + it.pb);
+    }
+  };
+  load(tid);
+
+  // ---- each row's request, position and slot
+  if (warp < rows) {
+    const int t = t0 + warp;
+    const int b = warp_find_request(a.offsets, a.B, t, lane);
+    bool ok = b >= 0;
+    long long slot_at = 0;
+    int position = 0;
+    if (ok) {
+      const RowRange R = row_range(a.offsets, b, a.T);
+      const int start = __ldg(a.start + b), depth = a.depth ? __ldg(a.depth + t) : t - R.lo;
+      ok = !R.err && t >= R.lo && start >= 0;
+      if (ok && depth < 0) {
+        if (lane == 0) report(a.status, b, SPEC_ERR_PREFIX_RANGE);
+        ok = false;
+      }
+      position = static_cast<int>(static_cast<unsigned>(start) + static_cast<unsigned>(depth));
+      if (ok && a.v.x) {
+        const int L = __ldg(a.slots + b);
+        ok = L >= 0 && static_cast<long long>(L) + R.n <= a.pages.capacity();
+        if (ok) {
+          const int slot = L + t - R.lo;
+          const int page = a.pages.page(b, slot >> a.pages.shift);
+          if (warp_finds_bad_page(a.pages, b, L, L + R.n, lane)) {
+            if (lane == 0) report(a.status, b, SPEC_ERR_PAGE);
+            ok = false;
+          }
+          const int size = 1 << a.pages.shift;
+          slot_at = ((static_cast<long long>(page) * a.Hkv << a.pages.shift) + (slot & (size - 1))) * a.D;
+        }
+      }
+    }
+    if (lane == 0) {
+      s_ok[warp] = ok;
+      s_pos[warp] = position;
+      s_slot[warp] = slot_at;
+    }
+  }
+  // (whole batches are checked once, so that a request without rows here reports too)
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    for (int b = tid; b < a.B; b += kThreads) {
+      const RowRange R = row_range(a.offsets, b, a.T);
+      int err = R.err;
+      if (!err && __ldg(a.start + b) < 0) err = SPEC_ERR_PREFIX_RANGE;
+      if (!err && a.v.x) {
+        const int L = __ldg(a.slots + b);
+        if (L < 0 || static_cast<long long>(L) + R.n > a.pages.capacity()) err = SPEC_ERR_PREFIX_RANGE;
+      }
+      if (err) report(a.status, b, err);
+    }
+  }
+  __syncthreads();
+  const int pairs = a.r / 2;
+  for (int i = tid; i < rows * pairs; i += kThreads) {
+    const int row = i / pairs;
+    const unsigned long long turns = static_cast<unsigned long long>(static_cast<unsigned>(s_pos[row])) *
+                                     __ldg(a.freqs + i - row * pairs);
+    const float half_turns = static_cast<float>(static_cast<int>(turns >> 32)) * 4.656612873077393e-10f;   // 2^-31
+    float s, c;
+    sincospif(half_turns, &s, &c);
+    s_cs[i] = make_float2(c * a.scale, s * a.scale);
+  }
+  __syncthreads();
+
+  for (int i0 = tid; i0 < total; i0 += kItems * kThreads) {
+    if (i0 != tid) load(i0);
+#pragma unroll
+    for (int u = 0; u < kItems; ++u) {
+      const int idx = i0 + u * kThreads;
+      if (idx >= total) continue;
+      const Item it = item_at<E, kVec, kInter>(a, idx, first);
+      if (!s_ok[it.row]) continue;
+      const float2 *cs = s_cs + it.row * pairs + it.pair;
+      if constexpr (kVec) {
+        constexpr int V = Vec<E>::n;
+        if constexpr (kInter) {
+          auto turn_vec = [&](uint4 &x, const float2 *c) {
+            float f[V];
+            Vec<E>::unpack(x, f);
+#pragma unroll
+            for (int e = 0; e < V; e += 2) turn(f[e], f[e + 1], c[e / 2]);
+            x = Vec<E>::pack(f);
+          };
+          if (it.turn_a) turn_vec(la[u], cs);
+          if (it.turn_b) turn_vec(lb[u], cs + (it.pb - it.pa) / 2);
+        } else if (it.turn_a) {
+          float fa[V], fb[V];
+          Vec<E>::unpack(la[u], fa);
+          Vec<E>::unpack(lb[u], fb);
+#pragma unroll
+          for (int e = 0; e < V; ++e) turn(fa[e], fb[e], cs[e]);
+          la[u] = Vec<E>::pack(fa);
+          lb[u] = Vec<E>::pack(fb);
+        }
+      } else if (it.turn_a) {
+        float fa = to_float(la[u]), fb = to_float(lb[u]);
+        turn(fa, fb, *cs);
+        from_float(fa, &la[u]);
+        from_float(fb, &lb[u]);
+      }
+      E *y;
+      if (it.head < a.Hq) {
+        y = static_cast<E *>(a.y) + (t0 + it.row) * a.y_st + it.head * a.y_sh;
+      } else {
+        const bool is_k = it.head < a.Hq + a.Hkv;
+        const int h = it.head - a.Hq - (is_k ? 0 : a.Hkv);
+        y = static_cast<E *>(is_k ? a.k_pages : a.v_pages) + s_slot[it.row] +
+            (static_cast<long long>(h) << a.pages.shift) * a.D;
+      }
+      *reinterpret_cast<Load *>(y + it.pa) = la[u];
+      if (it.pb >= 0) *reinterpret_cast<Load *>(y + it.pb) = lb[u];
+    }
+  }
+}
+
+// Whole rows to a CTA, eight at most and about six items a thread, once that
+// makes four CTAs an SM; before that a row is split over CTAs of one item a
+// thread, so that a few tokens' heads spread over the GPU.
+template <typename E, bool kVec, bool kInter>
+int launch(RopeArgs &a, void *stream) {
+  constexpr int V = kVec ? Vec<E>::n : 1;
+  const int vecs = a.D / V;
+  a.copy_items = kVec ? (vecs + 1) / 2 : vecs;
+  a.turn_items = kVec ? (kInter ? (vecs + 1) / 2 : a.r / 2 / V + ((a.D - a.r) / V + 1) / 2) : a.r / 2 + a.D - a.r;
+  const long long items = static_cast<long long>(a.Hq + a.Hkv) * a.turn_items +
+                          (a.v.x ? static_cast<long long>(a.Hkv) * a.copy_items : 0);
+  if (items > 0x1000000) return SPEC_ERR_SHAPE;      // (a CTA counts its rows' items in 32 bits)
+  a.row_items = static_cast<int>(items);
+  const int whole = a.row_items >= 6 * kThreads ? 1 : 6 * kThreads / a.row_items;
+  const int rows = whole < kMaxRows ? whole : kMaxRows;
+  if (a.T / rows >= 4 * sm_count()) {
+    a.rows = rows;
+    a.span = a.row_items;
+  } else {
+    a.rows = 1;
+    a.span = a.row_items < kThreads ? a.row_items : kThreads;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((a.T + a.rows - 1) / a.rows),
+                     static_cast<unsigned>((a.row_items + a.span - 1) / a.span), 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(a.rows) * (a.r / 2) * sizeof(float2);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  pdl_attribute(attr[0]);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rope_kernel<E, kVec, kInter>, a) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+// 16-byte vectors where every pointer, stride and the pairs' ends allow them;
+// single elements otherwise.
+template <typename E>
+int launch_by_form(RopeArgs &a, bool interleaved, void *stream) {
+  constexpr int V = Vec<E>::n;
+  auto whole = [](const void *p, long long st, long long sh) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && st % V == 0 && sh % V == 0;
+  };
+  bool vec = a.D % V == 0 && (interleaved ? a.r % V == 0 : a.r / 2 % V == 0);
+  if (a.Hq) vec = vec && whole(a.q.x, a.q.st, a.q.sh) && whole(a.y, a.y_st, a.y_sh);
+  if (a.v.x) vec = vec && whole(a.k.x, a.k.st, a.k.sh) && whole(a.v.x, a.v.st, a.v.sh);
+  if (vec) return interleaved ? launch<E, true, true>(a, stream) : launch<E, true, false>(a, stream);
+  return interleaved ? launch<E, false, true>(a, stream) : launch<E, false, false>(a, stream);
+}
+
+// What both calls ask of the rotation and of the rows.
+int check(int dtype, int B, int T, int D, const void *freqs, int r, float scale) {
+  if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_DTYPE;
+  if (B < 1 || T < 0 || D < 8 || D > 512 || D % 8 || r < 0 || r > D || r % 2 || !(fabsf(scale) < INFINITY))
+    return SPEC_ERR_SHAPE;
+  if (r > 0 && !freqs) return SPEC_ERR_NULL;
+  if (reinterpret_cast<uintptr_t>(freqs) & 7) return SPEC_ERR_ALIGNMENT;
+  return SPEC_OK;
+}
+
+// A stride between rows or heads of which there is only one is never taken.
+bool bad_strides(int T, int H, int64_t &st, int64_t &sh) {
+  if (T <= 1) st = 0;
+  if (H <= 1) sh = 0;
+  return st < 0 || sh < 0;
+}
+
+}  // namespace
+
+}  // namespace spec
+
+extern "C" int spec_rope_table(int rotary_dim, double base, int scaling, double factor, double original, double low,
+                               double high, uint64_t *freqs, float *scale) {
+  const double kPi = 3.14159265358979323846;
+  const int r = rotary_dim;
+  if (!freqs || !scale) return SPEC_ERR_NULL;
+  if (r < 2 || r > 512 || r % 2 || !(base > 1.0 && base < 1e30) || scaling < SPEC_ROPE_NONE ||
+      scaling > SPEC_ROPE_BANDS)
+    return SPEC_ERR_SHAPE;
+  if (scaling == SPEC_ROPE_NONE) factor = 1.0;
+  if (!(factor >= 1.0 && factor < 1e9)) return SPEC_ERR_SHAPE;
+  if (scaling == SPEC_ROPE_NTK) {
+    if (r < 4) return SPEC_ERR_SHAPE;
+    base *= std::pow(factor, static_cast<double>(r) / (r - 2));
+  }
+  const bool ranged = scaling == SPEC_ROPE_YARN || scaling == SPEC_ROPE_BANDS;
+  if (ranged && !(original > 0.0 && original < 1e12 && low > 0.0 && high > low && high < 1e12)) return SPEC_ERR_SHAPE;
+  // the pair whose wavelength makes `turns` turns in the original context
+  auto pair_of = [&](double turns) { return r * std::log(original / (2.0 * kPi * turns)) / (2.0 * std::log(base)); };
+  double from = 0.0, width = 1.0;
+  if (scaling == SPEC_ROPE_YARN) {
+    from = std::fmax(0.0, std::floor(pair_of(high)));
+    const double to = std::fmin(r - 1.0, std::ceil(pair_of(low)));
+    width = std::fmax(to - from, 0.001);
+  }
+  for (int i = 0; i < r / 2; ++i) {
+    double theta = std::pow(base, -2.0 * i / r);
+    if (scaling == SPEC_ROPE_LINEAR) theta /= factor;
+    double keep = 1.0;      // how much of the unscaled frequency stays
+    if (scaling == SPEC_ROPE_YARN) keep = 1.0 - std::fmin(1.0, std::fmax(0.0, (i - from) / width));
+    if (scaling == SPEC_ROPE_BANDS)
+      keep = std::fmin(1.0, std::fmax(0.0, (original * theta / (2.0 * kPi) - low) / (high - low)));
+    theta = theta * keep + theta / factor * (1.0 - keep);
+    freqs[i] = static_cast<uint64_t>(std::ldexp(theta / (2.0 * kPi), 64));
+  }
+  *scale = scaling == SPEC_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
+  return SPEC_OK;
+}
+
+extern "C" int spec_rope(const void *x, void *y, int dtype, int B, int T, int H, int D, int64_t x_row_stride,
+                         int64_t x_head_stride, int64_t y_row_stride, int64_t y_head_stride, const uint64_t *freqs,
+                         int rotary_dim, float scale, int interleaved, const int32_t *start, const int32_t *depth,
+                         const int32_t *offsets, int32_t *status, void *stream) {
+  using namespace spec;
+  if (((!x || !y) && T != 0) || !start || !offsets || !status) return SPEC_ERR_NULL;
+  const int rc = check(dtype, B, T, D, freqs, rotary_dim, scale);
+  if (rc != SPEC_OK) return rc;
+  if (H < 1 || bad_strides(T, H, x_row_stride, x_head_stride) || bad_strides(T, H, y_row_stride, y_head_stride))
+    return SPEC_ERR_SHAPE;
+  if ((T > 1 && y_row_stride == 0) || (H > 1 && y_head_stride == 0)) return SPEC_ERR_SHAPE;
+  const uintptr_t es = dtype == SPEC_F32 ? 4 : 2;
+  if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) % es) return SPEC_ERR_ALIGNMENT;
+  if (T == 0) return SPEC_OK;
+  RopeArgs a = {};
+  a.q = {x, x_row_stride, x_head_stride};
+  a.y = y;
+  a.y_st = y_row_stride;
+  a.y_sh = y_head_stride;
+  a.freqs = reinterpret_cast<const unsigned long long *>(freqs);
+  a.scale = scale;
+  a.start = start;
+  a.depth = depth;
+  a.offsets = offsets;
+  a.status = status;
+  a.B = B;
+  a.T = T;
+  a.Hq = H;
+  a.D = D;
+  a.r = rotary_dim;
+  return dtype == SPEC_BF16 ? launch_by_form<__nv_bfloat16>(a, interleaved != 0, stream)
+                            : launch_by_form<float>(a, interleaved != 0, stream);
+}
+
+extern "C" int spec_rope_write_paged(const void *q, void *q_out, const void *k, const void *v, int dtype, int B, int T,
+                                     int Hq, int Hkv, int D, int64_t q_row_stride, int64_t q_head_stride,
+                                     int64_t k_row_stride, int64_t k_head_stride, int64_t v_row_stride,
+                                     int64_t v_head_stride, const uint64_t *freqs, int rotary_dim, float scale,
+                                     int interleaved, void *k_pages, void *v_pages, int num_pages, int page_size,
+                                     const int32_t *block_table, int max_pages, const int32_t *prefix_lens,
+                                     const int32_t *start, const int32_t *depth, const int32_t *offsets,
+                                     int32_t *status, void *stream) {
+  using namespace spec;
+  if (((!k || !v || (Hq && (!q || !q_out))) && T != 0) || !k_pages || !v_pages || !block_table || !prefix_lens ||
+      !offsets || !status)
+    return SPEC_ERR_NULL;
+  RopeArgs a = {};
+  int rc = check(dtype, B, T, D, freqs, rotary_dim, scale);
+  if (rc == SPEC_OK) rc = check_pages(num_pages, page_size, max_pages, &a.pages.shift);
+  if (rc != SPEC_OK) return rc;
+  if (Hq < 0 || Hkv < 1 || bad_strides(T, Hq, q_row_stride, q_head_stride) ||
+      bad_strides(T, Hkv, k_row_stride, k_head_stride) || bad_strides(T, Hkv, v_row_stride, v_head_stride))
+    return SPEC_ERR_SHAPE;
+  const uintptr_t es = dtype == SPEC_F32 ? 4 : 2;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(q_out) | reinterpret_cast<uintptr_t>(k) |
+       reinterpret_cast<uintptr_t>(v)) % es ||
+      ((reinterpret_cast<uintptr_t>(k_pages) | reinterpret_cast<uintptr_t>(v_pages)) & 15))
+    return SPEC_ERR_ALIGNMENT;
+  if (T == 0) return SPEC_OK;
+  a.q = {q, q_row_stride, q_head_stride};
+  a.k = {k, k_row_stride, k_head_stride};
+  a.v = {v, v_row_stride, v_head_stride};
+  a.y = q_out;
+  a.y_st = static_cast<long long>(Hq) * D;
+  a.y_sh = D;
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.pages.table = block_table;
+  a.pages.max_pages = max_pages;
+  a.pages.pages = num_pages;
+  a.freqs = reinterpret_cast<const unsigned long long *>(freqs);
+  a.scale = scale;
+  a.slots = prefix_lens;
+  a.start = start ? start : prefix_lens;
+  a.depth = depth;
+  a.offsets = offsets;
+  a.status = status;
+  a.B = B;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.r = rotary_dim;
+  return dtype == SPEC_BF16 ? launch_by_form<__nv_bfloat16>(a, interleaved != 0, stream)
+                            : launch_by_form<float>(a, interleaved != 0, stream);
+}

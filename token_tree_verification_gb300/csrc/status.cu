@@ -17,6 +17,7 @@ extern "C" const char *spec_status_string(int code) {
     case SPEC_ERR_ALIGNMENT: return "SPEC_ERR_ALIGNMENT: pointer not 16-byte aligned";
     case SPEC_ERR_INDEX: return "SPEC_ERR_INDEX: a computed index fell outside its buffer";
     case SPEC_ERR_NONFINITE: return "SPEC_ERR_NONFINITE: a row to be quantised holds NaN or infinity";
+    case SPEC_ERR_PAGE: return "SPEC_ERR_PAGE: a block table names a page outside the pool";
     default: return "unknown spec_status";
   }
 }
