@@ -16,19 +16,24 @@
 //   warp 0      brings tiles of 128 keys and of 128 values into rings of their
 //               own; a lane copies one box, 64 dims of one page's slots (of 128 at
 //               most), whose page it looked up a tile ahead
-//   warp 1      allocates TMEM and issues S_i as soon as K_i is there and the
-//               softmax has taken S_{i-1} into registers
-//   warp 2      issues O += P_i V_i
+//   warp 1      allocates TMEM and issues S_u, for 64 keys (half a tile) at a time
+//   warp 2      issues O += P_u V_u
 //   warp 3      looks through the request's whole page table: a request that
 //               names a page outside the pool gets no output
-//   warps 4-11  softmax: a TMEM lane quarter's two warps hold the same 32 rows,
-//               each one half of a tile's keys.  A row has one reference; its two
-//               threads meet once a tile to learn whether either has a score that
-//               passes it by more than 2^8, which moves it (the tile's weights
-//               are then taken again from S, and O rescaled)
-// P has a place in TMEM beside S, so that the weights of a tile are worked out
-// while the last tile's are multiplied, and S of the next tile is multiplied
-// while they are stored.  A quarter without rows leaves the softmax out.
+//   warps 4-11  softmax, in two groups that take the halves in turn; a thread
+//               has a row (a TMEM lane) and the 64 keys of a half
+// TMEM holds the scores of five halves, and P takes the place of S, so that the
+// products of one half run beside the softmax of two others.  A row's reference
+// is shared by the groups, which decide on it in the order of the halves (a
+// barrier per lane quarter and group passes the turn); it moves when a score passes
+// it by more than 2^8, which is rare behind the first keys, and O is then rescaled
+// in place.  A quarter without rows leaves the softmax out.
+//
+// The tensor cores' queue is short: what an issuing warp does between two batches
+// of products (tests of barriers at 36 cycles, waits at 70, descriptors) is time
+// lost unless the other issuing warp fills it.  Hence two of them; one that issued
+// both kinds took 2750 cycles a tile in place of 1900, 2350 with the tests placed
+// between its products.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -41,11 +46,18 @@ namespace {
 
 constexpr int kRows = 128;
 constexpr int kSoftFirst = 4;         // warps: issuers and the page check, then the softmax
-constexpr int kSoftWarps = 8;
+constexpr int kGroups = 2;            // of four softmax warps
+constexpr int kSoftWarps = 4 * kGroups;
 constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr int kThreads = 32 * (kSoftFirst + kSoftWarps);
-constexpr int kHalf = kTile / 2;      // keys of one softmax thread
+constexpr int kHalf = kTile / 2;      // keys of a product, and of one softmax thread
+constexpr int kBufs = 5;              // halves' scores and weights in TMEM
 constexpr float kPass = 8.f;          // powers of two by which a score may pass its row's reference
+
+// A wait that is over already, most often.
+__device__ __forceinline__ bool mbar_now(uint64_t *bar, uint32_t parity) {
+  return mbar_over(smem_addr(bar), parity) || mbar_sleep(smem_addr(bar), parity);
+}
 
 template <int D>
 struct PagedCfg {
@@ -60,11 +72,20 @@ struct PagedCfg {
   static constexpr int kOffMl = kOffRecv + (kRows * D + 4 * kMaxSplits) * 4;
   static constexpr int kMerge = kOffMl + kMaxSplits * kRows * 8;
   static constexpr int kSmem = (kEnd > kMerge ? kEnd : kMerge) + 1024;
-  // TMEM: S, P (a pair of keys per column, remainders behind the high parts), O, Q
-  // (a pair of dims)
-  static constexpr uint32_t kColP = kTile, kColO = kColP + kTile, kColQ = kColO + 128, kTmemCols = 512;
+  // TMEM: the halves' S, and P in their place (a pair of keys per column, remainders
+  // behind the high parts), Q (a pair of dims), O
+  static constexpr uint32_t kColQ = kBufs * kHalf, kColO = kColQ + 64, kTmemCols = 512;
   static_assert(kSmem <= 227 * 1024 - 8192, "shared memory budget");
 };
+
+// What rounding to bf16 took from y0 and y1 (`top` holds the two, y0's low), exactly.
+__device__ __forceinline__ void minus_bf16x2(float y0, float y1, uint32_t top, float &r0, float &r1) {
+  asm("{\n\t.reg .b16 t0, t1, m;\n\t"
+      "mov.b32 {t0, t1}, %2;\n\tmov.b16 m, 0xBF80;\n\t"
+      "fma.rn.f32.bf16 %0, t0, m, %3;\n\tfma.rn.f32.bf16 %1, t1, m, %4;\n\t}"
+      : "=f"(r0), "=f"(r1)
+      : "r"(top), "f"(y0), "f"(y1));
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -76,22 +97,23 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
   extern __shared__ uint8_t smem_raw[];
   __shared__ struct {
     uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
-    uint64_t q_full, s_full, s_empty, p_full, o_done, drained[2];
+    uint64_t q_full, s_full[kBufs], p_full[kBufs], o_done[kBufs], turn[4][kGroups], drained[2];
   } bars;
   __shared__ uint32_t s_tmem;
   __shared__ int s_timeout, s_bad_page;
   __shared__ int s_par[SPEC_MAX_TREE_NODES];
   __shared__ long long s_row[kRows];          // a row's first element of o
-  __shared__ float s_most[2][kRows];          // [half of the keys][row]
-  __shared__ float s_part[kRows];             // a row's sum over the second halves
-  __shared__ float s_ref[1][kRows], s_sum[1][kRows];
+  __shared__ float s_ref[1][kRows], s_sum[1][kRows], s_part[kGroups][kRows];
 
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
-  const uint32_t sb = smem_addr(smem);
+  const uint32_t sb = __shfl_sync(0xffffffffu, smem_addr(smem), 0);
   const int split = static_cast<int>(blockIdx.x) % CS, block = static_cast<int>(blockIdx.x) / CS;
   const int g_kv = static_cast<int>(blockIdx.y);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (a shuffle tells the compiler that a value is the same in all lanes: the products'
+  // operands then stay in uniform registers)
+  auto uniform = [](auto x) { return __shfl_sync(0xffffffffu, x, 0); };
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
   pdl_trigger();
   if (tid == 0) {
@@ -101,11 +123,13 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
       mbar_init(&bars.v_full[s], 1);
       mbar_init(&bars.v_empty[s], 1);
     }
-    mbar_init(&bars.q_full, kSoftWarps);
-    mbar_init(&bars.s_full, 1);
-    mbar_init(&bars.s_empty, kSoftWarps);
-    mbar_init(&bars.p_full, kSoftWarps);
-    mbar_init(&bars.o_done, 1);
+    mbar_init(&bars.q_full, 8);
+    for (int s = 0; s < kBufs; ++s) {
+      mbar_init(&bars.s_full[s], 1);
+      mbar_init(&bars.p_full[s], 4);
+      mbar_init(&bars.o_done[s], 1);
+    }
+    for (int s = 0; s < 4 * kGroups; ++s) mbar_init(&bars.turn[0][0] + s, 1);
     mbar_init(&bars.drained[0], 1);
     mbar_init(&bars.drained[1], 1);
     fence_barrier_init();
@@ -123,12 +147,13 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = uniform(s_tmem);
   pdl_wait();
 
+  if (warp == 0) touch_table(p, lane);
   const RowBlock w = find_block<kRows>(p, block, lane);
   if (blockIdx.x == 0 && g_kv == 0 && warp == 3) report_bad_requests(p, lane);
-  if (w.b < 0 || w.R.err) {       // the same for every CTA of the cluster
+  if (w.b < 0) {       // the same for every CTA of the cluster
     if (warp == 1) {
       __syncwarp();
       tc::tmem_dealloc(tmem, C::kTmemCols);
@@ -139,7 +164,8 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
   const int all = (w.keys + kTile - 1) / kTile;
   const int per = (all + CS - 1) / CS;
   const int t0 = split * per;
-  const int ntiles = max(0, min(t0 + per, all) - t0);
+  const int ntiles = uniform(max(0, min(t0 + per, all) - t0));
+  const int halves = uniform(max(0, min(2 * ntiles, (w.keys - t0 * kTile + kHalf - 1) / kHalf)));      // that hold a key
   bool ok = true;      // cleared by a wait that ran out: the role goes on without waiting, and no row is written
 
   Ring<NS> kr, vr;     // warp 0's
@@ -181,89 +207,97 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ S = Q K^T
-    constexpr uint32_t id = tc::idesc_bf16_f32(kRows, kTile, 0, 0);
+    constexpr uint32_t id = tc::idesc_bf16_f32(kRows, kHalf, 0, 0);
     const uint64_t kd0 = tc::smem_desc_sw128(sb + C::kOffK, 16, 1024);
     Ring<NS> ring;
+    Ring<kBufs> buf;
+    buf.phase = 1;             // free at first, then when what is in it has been multiplied
     const bool leader = tc::elect_one();
-    if (ntiles > 0) ok = mbar_sleep(smem_addr(&bars.q_full), 0);
-    for (int i = 0; i < ntiles; ++i, ring.next()) {
-      ok = ok && mbar_sleep(smem_addr(&bars.k_full[ring.at]), ring.phase);
-      ok = ok && mbar_sleep(smem_addr(&bars.s_empty), (i & 1) ^ 1);
+    if (halves > 0) ok = mbar_sleep(smem_addr(&bars.q_full), 0);
+    for (int u = 0; u < halves; ++u, buf.next()) {
+      const int h = u & 1;
+      if (h == 0) ok = ok && mbar_now(&bars.k_full[ring.at], ring.phase);
+      ok = ok && mbar_now(&bars.o_done[buf.at], buf.phase);
       tc::fence_after_sync();
-      const uint64_t kd = kd0 + static_cast<uint64_t>((ring.at * C::kTileBytes) >> 4);
+      const uint64_t kd = kd0 + static_cast<uint64_t>((ring.at * C::kTileBytes + h * (kHalf * 128)) >> 4);
       if (leader) {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
-          tc::mma_bf16_ts(tmem, tmem + C::kColQ + ks * 8, kd + (((ks >> 2) * C::kBoxBytes + (ks & 3) * 32) >> 4), id,
-                          ks > 0);
-        tc::commit(&bars.s_full);
-        tc::commit(&bars.k_empty[ring.at]);
+          tc::mma_bf16_ts(tmem + buf.at * kHalf, tmem + C::kColQ + ks * 8,
+                          kd + (((ks >> 2) * C::kBoxBytes + (ks & 3) * 32) >> 4), id, ks > 0);
+        tc::commit(&bars.s_full[buf.at]);
+        if (h) tc::commit(&bars.k_empty[ring.at]);
       }
       __syncwarp();
+      if (h) ring.next();
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ O += P V
     constexpr uint32_t id = tc::idesc_bf16_f32(kRows, D, 0, 1);
     const uint64_t vd0 = tc::smem_desc_sw128(sb + C::kOffV, C::kBoxBytes, 1024);
     Ring<NS> ring;
+    Ring<kBufs> buf;
     const bool leader = tc::elect_one();
-    for (int i = 0; i < ntiles; ++i, ring.next()) {
-      ok = ok && mbar_sleep(smem_addr(&bars.v_full[ring.at]), ring.phase);
-      ok = ok && mbar_sleep(smem_addr(&bars.p_full), i & 1);
+    for (int u = 0; u < halves; ++u, buf.next()) {
+      const int h = u & 1;
+      if (h == 0) ok = ok && mbar_now(&bars.v_full[ring.at], ring.phase);
+      ok = ok && mbar_now(&bars.p_full[buf.at], buf.phase);
       tc::fence_after_sync();
-      const uint64_t vd = vd0 + static_cast<uint64_t>((ring.at * C::kTileBytes) >> 4);
+      const uint64_t vd = vd0 + static_cast<uint64_t>((ring.at * C::kTileBytes + h * (kHalf * 128)) >> 4);
       if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk) {
-          const uint32_t pt = tmem + C::kColP + kk * 8;
+        for (int kk = 0; kk < kHalf / 16; ++kk) {
+          const uint32_t pt = tmem + buf.at * kHalf + kk * 8;
           const uint64_t v = vd + (kk * 16 * 128 >> 4);
-          tc::mma_bf16_ts(tmem + C::kColO, pt, v, id, (i | kk) != 0);
-          tc::mma_bf16_ts(tmem + C::kColO, pt + kTile / 2, v, id, true);
+          tc::mma_bf16_ts(tmem + C::kColO, pt, v, id, (u | kk) != 0);
+          tc::mma_bf16_ts(tmem + C::kColO, pt + kHalf / 2, v, id, true);
         }
-        tc::commit(&bars.o_done);
-        tc::commit(&bars.v_empty[ring.at]);
+        tc::commit(&bars.o_done[buf.at]);
+        if (h) tc::commit(&bars.v_empty[ring.at]);
       }
       __syncwarp();
+      if (h) ring.next();
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------ the page table
     if (warp_finds_bad_page(p.pages, b, 0, w.R.keys, lane) && lane == 0) s_bad_page = 1;
   } else {
     // ------------------------------------------------------------ softmax
-    const int quad = warp & 3, half = (warp - kSoftFirst) >> 2;
-    const int soft = tid - 32 * kSoftFirst;            // 0 .. 255
+    const int quad = warp & 3, group = (warp - kSoftFirst) >> 2;
+    const int soft = tid - 32 * kSoftFirst;
     const int row = quad * 32 + lane;                  // and TMEM lane
     const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t s_col = trow + half * kHalf, p_col = trow + C::kColP + half * (kHalf / 2);
-    const uint32_t o_col = trow + C::kColO + half * (D / 2);
-    const uint32_t s_full = smem_addr(&bars.s_full), s_empty = smem_addr(&bars.s_empty),
-                   p_full = smem_addr(&bars.p_full), o_done = smem_addr(&bars.o_done);
+    // decisions on the row's reference: this group's, and the one that goes before
+    const uint32_t turn = smem_addr(&bars.turn[quad][group]);
+    const uint32_t turn_before = smem_addr(&bars.turn[quad][(group + kGroups - 1) % kGroups]);
+    uint32_t round = group > 0 ? 0 : 1;      // of the one before, for the group's next half
     const bool busy = quad * 32 < w.rows;              // (a quarter without rows only keeps the barriers going)
     const bool live = row < w.rows;
-    // ---- Q: this thread's row, half of its dims
+    // ---- Q: this thread's row, half of its dims (two groups' work)
     const int node = (w.row0 + row) / a.G;
     const bool mine = live && in_bounds(w.R.lo + node, a.T, a.status, b);
     const long long first =
         (static_cast<long long>(w.R.lo + node) * a.Hq + g_kv * a.G + (w.row0 + row) - node * a.G) * D;
-    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + first + half * (D / 2));
+    const uint4 *src =
+        reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + first + group * (D / 2));
     uint4 m = make_uint4(0u, 0u, 0u, 0u);
-    if (busy) {
+    if (a.mask && mine) m = clip_mask(__ldg(a.mask + w.R.lo + node), w.R.n);
+    if (busy && group < 2) {
       uint4 x4[D / 16];
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) x4[c] = mine ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-      if (a.mask && mine) m = clip_mask(__ldg(a.mask + w.R.lo + node), w.R.n);
 #pragma unroll
       for (int q = 0; q < D / 32; ++q) {
         const uint4 x = x4[2 * q], y = x4[2 * q + 1];
         const uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        tc::st8(trow + C::kColQ + half * (D / 4) + 8 * q, u);
+        tc::st8(trow + C::kColQ + group * (D / 4) + 8 * q, u);
       }
       tc::wait_st();
     }
     tc::fence_before_sync();
     __syncwarp();
-    if (lane == 0) mbar_arrive_at(smem_addr(&bars.q_full));
-    if (half == 0) s_row[row] = mine ? first : -1;
+    if (lane == 0 && group < 2) mbar_arrive_at(smem_addr(&bars.q_full));
+    if (group == 0) s_row[row] = mine ? first : -1;
     // ---- what this thread's row sees
     if (a.parents) {
       for (int i = soft; i < w.R.n; i += kSoftThreads)
@@ -276,64 +310,69 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
     const RowSees see = {p.causal ? L + node + 1 : L, m};
     const int all_see = p.causal ? L + w.row0 / a.G + 1 : L;       // what every row of the block sees: [0, all_see)
     const float c = a.scale_log2;
-    float ref = -INFINITY, sum = 0.f;      // in powers of two; of the weights 2^(score - ref)
-    auto largest = [&](float mine_) {      // of the row's two threads
-      s_most[half][row] = mine_;
-      named_bar_sync(2 + quad, 64);
-      return fmaxf(s_most[0][row], s_most[1][row]);
-    };
+    float ref = -INFINITY, sum = 0.f;      // in powers of two; of this thread's weights 2^(score - ref)
+    if (group == 0) s_ref[0][row] = -INFINITY;
+    named_bar_sync(1, kSoftThreads);
 
-    for (int i = 0; i < ntiles; ++i) {
-      const int key0 = (t0 + i) * kTile, k0 = key0 + half * kHalf;
-      ok = ok && mbar_sleep(s_full, i & 1);
+    Ring<kBufs> buf, before;               // of this half, and of the one before
+    for (int v = 0; v < group; ++v) {
+      before = buf;
+      buf.next();
+    }
+    for (int u = group; u < halves; u += kGroups) {
+      const int k0 = t0 * kTile + u * kHalf;
+      const uint32_t s_col = trow + buf.at * kHalf;
+      ok = ok && mbar_now(&bars.s_full[buf.at], buf.phase);
       __syncwarp();
       tc::fence_after_sync();
-      float x[2][32];
       if (busy) {
+        float x[2][32];
         tc::ld32(s_col, x[0]);
         tc::ld32(s_col + 32, x[1]);
         tc::wait_ld();
-      }
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_at(s_empty);
-      uint32_t hi[kHalf / 16][8], lo[kHalf / 16][8];
-      if (busy) {
         if (k0 + kHalf > all_see) {
 #pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            const uint32_t sees = sees_32(see, k0 + 32 * part, L);
+          for (int v = 0; v < 2; ++v) {
+            const uint32_t sees = sees_32(see, k0 + 32 * v, L);
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (!((sees >> j) & 1u)) x[part][j] = -INFINITY;
+              if (!((sees >> j) & 1u)) x[v][j] = -INFINITY;
           }
         }
         const float most = fmaxf(max_of(x[0]), max_of(x[1])) * c;
-        bool moves = i == 0;
-        if (i > 0) moves = named_bar_or(2 + quad, 64, most > ref + kPass);
-        if (moves) {
-          const float top = largest(most);
-          const bool mine_moves = i == 0 || top > ref + kPass;
-          const float factor = !mine_moves ? 1.f : ref == -INFINITY ? 0.f : exp2f(ref - top);
-          if (mine_moves) ref = top;
-          sum *= factor;
-          if (i > 0) {
-            // O holds the products of the earlier tiles
-            ok = ok && mbar_sleep(o_done, (i - 1) & 1);
-            __syncwarp();
-            tc::fence_after_sync();
+        // The halves take turns at the row's reference: the other group's decision
+        // on the half before was long ago, most often.
+        if (u > 0) ok = ok && (mbar_over(turn_before, round) || mbar_sleep(turn_before, round));
+        round ^= 1;
+        __syncwarp();
+        const float now = s_ref[0][row];
+        if (__any_sync(0xffffffffu, now != ref || most > now + kPass)) {
+          const float next = most > now + kPass ? most : now;
+          if (__any_sync(0xffffffffu, next != now)) {
+            if (u > 0) {
+              // O holds the products of the halves before
+              const float factor = next == now ? 1.f : now == -INFINITY ? 0.f : exp2f(now - next);
+              ok = ok && mbar_sleep(smem_addr(&bars.o_done[before.at]), before.phase);
+              __syncwarp();
+              tc::fence_after_sync();
 #pragma unroll 1
-            for (int j = 0; j < D / 2; j += 8) {
-              float o[8];
-              tc::ld8(o_col + j, o);
-              tc::wait_ld();
+              for (int j = 0; j < D; j += 16) {
+                float o[16];
+                tc::ld16(trow + C::kColO + j, o);
+                tc::wait_ld();
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] *= factor;
-              tmem_st(o_col + j, o);
+                for (int e = 0; e < 16; ++e) o[e] *= factor;
+                tc::st16(trow + C::kColO + j, o);
+              }
+              tc::wait_st();
             }
-            tc::wait_st();
+            s_ref[0][row] = next;
           }
+          if (next != ref) sum *= ref == -INFINITY ? 0.f : exp2f(ref - next);
+          ref = next;
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(turn);
         // weights 2^(s c - ref): one rounding of the difference, except where the
         // reference has no places behind the point left; there the largest score's
         // own rounding must cancel, or its weight could pass fp32's range
@@ -343,94 +382,106 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
         if (__any_sync(0xffffffffu, steep)) {
           const float pre = steep ? c : 1.f;
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
+          for (int v = 0; v < 2; ++v)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[part][j] = __fmul_rn(x[part][j], pre);
+            for (int j = 0; j < 32; ++j) x[v][j] = __fmul_rn(x[v][j], pre);
         }
         float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+        for (int v = 0; v < 2; ++v)
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            float *y = &x[part][j];
-            fma2(y[0], y[1], cs, cs, base, base);
-            fma2(y[2], y[3], cs, cs, base, base);
+          for (int part = 0; part < 2; ++part) {
+            uint32_t hi[8], lo[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = fast_exp2(y[e]);
-            add2(s0, s1, y[0], y[1]);
-            add2(s2, s3, y[2], y[3]);
+            for (int j = 0; j < 16; j += 4) {
+              float *y = &x[v][16 * part + j];
+              fma2(y[0], y[1], cs, cs, base, base);
+              fma2(y[2], y[3], cs, cs, base, base);
 #pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(y[e], y[e + 1]);
-              const uint32_t u = *reinterpret_cast<const uint32_t *>(&h);
-              float r0 = __uint_as_float(u << 16), r1 = __uint_as_float(u & 0xFFFF0000u);
-              fma2(r0, r1, -1.f, -1.f, y[e], y[e + 1]);
-              const __nv_bfloat162 l = __floats2bfloat162_rn(r0, r1);
-              hi[2 * part + j / 16][(j + e) / 2 % 8] = u;
-              lo[2 * part + j / 16][(j + e) / 2 % 8] = *reinterpret_cast<const uint32_t *>(&l);
+              for (int e = 0; e < 4; ++e) y[e] = fast_exp2(y[e]);
+              add2(s0, s1, y[0], y[1]);
+              add2(s2, s3, y[2], y[3]);
+#pragma unroll
+              for (int e = 0; e < 4; e += 2) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(y[e], y[e + 1]);
+                const uint32_t top = *reinterpret_cast<const uint32_t *>(&h);
+                float r0, r1;
+                minus_bf16x2(y[e], y[e + 1], top, r0, r1);
+                const __nv_bfloat162 l = __floats2bfloat162_rn(r0, r1);
+                hi[(j + e) / 2] = top;
+                lo[(j + e) / 2] = *reinterpret_cast<const uint32_t *>(&l);
+              }
             }
+            tc::st8(s_col + 16 * v + 8 * part, hi);
+            tc::st8(s_col + kHalf / 2 + 16 * v + 8 * part, lo);
           }
         add2(s0, s1, s2, s3);
         sum += s0 + s1;
       }
-      if (key0 + kTile > w.keys) {
+      if (k0 + kHalf > w.keys) {
         // slots behind the last key may hold anything: a weight of zero does not
         // hide a NaN
-        const int at = i % NS;
-        ok = ok && mbar_sleep(smem_addr(&bars.v_full[at]), (i / NS) & 1);
-        const int valid = w.keys - key0, pieces = (kTile - valid) * C::kBoxes * 8;
-        for (int z = soft; z < pieces; z += kSoftThreads) {
-          const int r = valid + z / (C::kBoxes * 8), rest = z % (C::kBoxes * 8);
+        const int at = (u >> 1) % NS;
+        ok = ok && mbar_sleep(smem_addr(&bars.v_full[at]), ((u >> 1) / NS) & 1);
+        const int valid = w.keys - k0, pieces = (kHalf - valid) * C::kBoxes * 8;
+        for (int z = soft & 127; z < pieces; z += 128) {
+          const int r = (u & 1) * kHalf + valid + z / (C::kBoxes * 8), rest = z % (C::kBoxes * 8);
           st_shared_v4(sb + C::kOffV + at * C::kTileBytes + (rest >> 3) * C::kBoxBytes + r * 128 + (rest & 7) * 16, 0u,
                        0u, 0u, 0u);
         }
         fence_proxy_async_smem();
       }
-      // ---- the weights' place is free once the last tile's product is done
-      if (i > 0) ok = ok && (mbar_over(o_done, (i - 1) & 1) || mbar_sleep(o_done, (i - 1) & 1));
-      __syncwarp();
-      tc::fence_after_sync();
-      if (busy) {
-#pragma unroll
-        for (int q = 0; q < kHalf / 16; ++q) {
-          tc::st8(p_col + 8 * q, hi[q]);
-          tc::st8(p_col + kTile / 2 + 8 * q, lo[q]);
-        }
-        tc::wait_st();
-      }
+      if (busy) tc::wait_st();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive_at(p_full);
+      if (lane == 0) mbar_arrive_at(smem_addr(&bars.p_full[buf.at]));
+#pragma unroll
+      for (int v = 0; v < kGroups; ++v) {
+        before = buf;
+        buf.next();
+      }
     }
-    // ---- the block's rows out of TMEM; their place in shared memory is free
-    //      once the last product is done
-    if (ntiles > 0) ok = ok && mbar_sleep(o_done, (ntiles - 1) & 1);
+    // ---- the block's rows out of TMEM.  Their place in shared memory is free
+    //      once the last products of both groups are done.
+    //      (One after the other from the group's own last half on: a barrier that is
+    //      two phases behind looks done.)
+    int u = halves > group ? halves - 1 - (halves - 1 - group) % kGroups : 0;
+    buf = Ring<kBufs>();
+    for (int v = 0; v < u; ++v) buf.next();
+    for (; u < halves; ++u, buf.next()) ok = ok && mbar_sleep(smem_addr(&bars.o_done[buf.at]), buf.phase);
+    if (CS > 1) cluster_arrive_relaxed();
     __syncwarp();
     tc::fence_after_sync();
-    if (busy) {
-      if (half == 1) s_part[row] = sum;
-      named_bar_sync(2 + quad, 64);
-      if (half == 0) {
-        s_sum[0][row] = sum + s_part[row];
-        s_ref[0][row] = ref;
+    if (busy && halves > 0)
+      ok = ok && mbar_sleep(smem_addr(&bars.turn[quad][(halves - 1) % kGroups]), (halves - 1) / kGroups & 1);
+    __syncwarp();
+    const float now = s_ref[0][row];
+    if (now != ref) sum *= ref == -INFINITY ? 0.f : exp2f(ref - now);
+    s_part[group][row] = sum;
+    if (!ok) s_timeout = 1;
+    named_bar_sync(1, kSoftThreads);
+    if (busy && group < 2 && s_timeout == 0) {
+      if (group == 0) {
+        for (int q = 1; q < kGroups; ++q) sum += s_part[q][row];
+        s_sum[0][row] = sum;
       }
-      if (ok) {
-        const uint32_t so = sb + (row * (D + 4) + half * (D / 2)) * 4;
+      const uint32_t so = sb + (row * (D + 4) + group * (D / 2)) * 4;
 #pragma unroll
-        for (int j = 0; j < D / 2; j += 32) {
-          float o[32] = {};
-          if (ntiles > 0) {
-            tc::ld32(o_col + j, o);
-            tc::wait_ld();
-          }
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            st_shared_v4(so + (j + e) * 4, __float_as_uint(o[e]), __float_as_uint(o[e + 1]), __float_as_uint(o[e + 2]),
-                         __float_as_uint(o[e + 3]));
+      for (int j = 0; j < D / 2; j += 32) {
+        float o[32] = {};
+        if (halves > 0) {
+          tc::ld32(trow + C::kColO + group * (D / 2) + j, o);
+          tc::wait_ld();
         }
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          st_shared_v4(so + (j + e) * 4, __float_as_uint(o[e]), __float_as_uint(o[e + 1]), __float_as_uint(o[e + 2]),
+                       __float_as_uint(o[e + 3]));
       }
     }
   }
+  // (a CTA has arrived, for its peers to write here, once its products are done)
+  if (CS > 1 && warp < kSoftFirst) cluster_arrive_relaxed();
   if (!ok) s_timeout = 1;
   __syncwarp();
   tc::fence_before_sync();
@@ -461,11 +512,13 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
     tc::tmem_dealloc(tmem, C::kTmemCols);
   }
   // (a page outside the pool is found by every CTA of the cluster)
-  auto out_row = [&](int r) { return s_row[r] < 0 ? nullptr : static_cast<__nv_bfloat16 *>(a.o) + s_row[r]; };
+  // (a peer's rows may have landed where this CTA's last copies did: no row is
+  // written after a time-out)
+  auto out_row = [&](int r) { return timed_out || s_row[r] < 0 ? nullptr : static_cast<__nv_bfloat16 *>(a.o) + s_row[r]; };
   merge_rows<D, 1, kRows, kThreads, __nv_bfloat16>(
       tid, CS, split, w.rows, timed_out || bad_page, reinterpret_cast<float *>(smem), s_ref, s_sum,
       reinterpret_cast<float2 (*)[kRows]>(smem + C::kOffMl), reinterpret_cast<float4 *>(smem + C::kOffRecv),
-      [] { cluster_sync_all(); }, out_row);
+      [] { cluster_wait(); }, out_row);
 }
 
 // ---------------------------------------------------------------- host side

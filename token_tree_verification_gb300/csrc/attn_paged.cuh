@@ -15,11 +15,11 @@ struct PagedAttnArgs {
 
 // Rows, prefix and errors of request b.
 __device__ __forceinline__ ReqGeom paged_geometry(const PagedAttnArgs &p, int b) {
-  const RowRange r = row_range(p.a.offsets, b, p.a.T);
   ReqGeom g;
+  g.L = __ldg(p.a.prefix_lens + b);
+  const RowRange r = row_range(p.a.offsets, b, p.a.T);
   g.lo = r.lo;
   g.n = r.n;
-  g.L = __ldg(p.a.prefix_lens + b);
   g.err = r.err;
   if (!g.err && !p.causal && (g.n < 1 || g.n > SPEC_MAX_TREE_NODES)) g.err = SPEC_ERR_TREE_TOO_LARGE;
   if (!g.err && (g.L < 0 || g.L > p.a.S_cap - g.n)) g.err = SPEC_ERR_PREFIX_RANGE;
@@ -35,10 +35,11 @@ struct RowBlock {
   ReqGeom R;
 };
 
-// The j-th block of the batch; by one warp, 32 requests a step.  The host knows
-// only how many rows there are in all, so a launch has blocks for the worst
-// split of them over the requests; those left over find none.  The last blocks of
-// a run of tokens, which see most, come first.
+// The j-th block of the batch; by one warp, 32 requests a step, whose three
+// loads are under way at once.  The host knows only how many rows there are in
+// all, so a launch has blocks for the worst split of them over the requests;
+// those left over find none, and requests in error have none.  The last blocks
+// of a run of tokens, which see most, come first.
 template <int ROWS>
 __device__ __forceinline__ RowBlock find_block(const PagedAttnArgs &p, int j, int lane) {
   const int G = p.a.G;
@@ -47,12 +48,9 @@ __device__ __forceinline__ RowBlock find_block(const PagedAttnArgs &p, int j, in
   w.row0 = w.rows = w.keys = 0;
   w.R = {0, 0, 0, 0, 0};
   for (int b0 = 0; b0 < p.a.B; b0 += 32) {
-    int blocks = 0;
-    if (b0 + lane < p.a.B) {
-      const RowRange r = row_range(p.a.offsets, b0 + lane, p.a.T);
-      const bool rows = !r.err && (p.causal || r.n <= SPEC_MAX_TREE_NODES);
-      blocks = rows ? (r.n * G + ROWS - 1) / ROWS : 0;
-    }
+    ReqGeom mine = {0, 0, 0, 0, 0};
+    if (b0 + lane < p.a.B) mine = paged_geometry(p, b0 + lane);
+    const int blocks = mine.err ? 0 : (mine.n * G + ROWS - 1) / ROWS;
     int up_to = blocks;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -69,14 +67,24 @@ __device__ __forceinline__ RowBlock find_block(const PagedAttnArgs &p, int j, in
     int i = j - (__shfl_sync(0xffffffffu, up_to, at) - count);
     if (p.causal) i = count - 1 - i;
     w.b = b0 + at;
-    w.R = paged_geometry(p, w.b);
+    w.R.lo = __shfl_sync(0xffffffffu, mine.lo, at);
+    w.R.n = __shfl_sync(0xffffffffu, mine.n, at);
+    w.R.L = __shfl_sync(0xffffffffu, mine.L, at);
+    w.R.keys = w.R.L + w.R.n;
     w.row0 = i * ROWS;
     w.rows = min(ROWS, w.R.n * G - w.row0);
-    w.keys = w.R.keys;
-    if (p.causal && !w.R.err) w.keys = w.R.L + (w.row0 + w.rows - 1) / G + 1;
+    w.keys = p.causal ? w.R.L + (w.row0 + w.rows - 1) / G + 1 : w.R.keys;
     break;
   }
   return w;
+}
+
+// The first 4 KB of the block table on their way into L1 before it is known
+// which entries are wanted: that takes a load of its own.  By one warp.
+__device__ __forceinline__ void touch_table(const PagedAttnArgs &p, int lane) {
+  if (32ll * lane >= static_cast<long long>(p.a.B) * p.pages.max_pages) return;
+  int unused;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(unused) : "l"(p.pages.table + 32 * lane));
 }
 
 // Blocks that find_block may have to tell apart.
@@ -85,8 +93,8 @@ inline long long most_blocks(const AttnArgs &a) {
   return (static_cast<long long>(a.T) * a.G - (a.B < a.T ? a.B : a.T)) / ROWS + (a.B < a.T ? a.B : a.T);
 }
 
-// Every request's error, reported once (some have no block, or one that stops
-// at its page table); by one warp of the launch's first CTA.
+// Every request's error, reported once (those in error have no block); by one
+// warp of the launch's first CTA.
 __device__ __forceinline__ void report_bad_requests(const PagedAttnArgs &p, int lane) {
   for (int b = lane; b < p.a.B; b += 32) {
     const ReqGeom g = paged_geometry(p, b);
