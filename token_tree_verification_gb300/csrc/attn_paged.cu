@@ -13,13 +13,14 @@
 // and 1024 for O per 128 keys at D = 128.
 //
 // Warp roles:
-//   warp 0      brings tiles of 128 keys and of 128 values into rings of their
-//               own; a lane copies one box, 64 dims of one page's slots (of 128 at
-//               most), whose page it looked up a tile ahead
+//   warps 0, 3  bring tiles of 128 keys and of 128 values into rings of their own;
+//               a lane copies one box, 64 dims of one page's slots (of 128 at most),
+//               whose page it looked up a tile ahead.  (A box is some 60 cycles of
+//               the warp's time; with one warp for both, pages of 16 slots took 3000
+//               a tile.)  Warp 3 then looks through the request's whole page table:
+//               a request that names a page outside the pool gets no output
 //   warp 1      allocates TMEM and issues S_u, for 64 keys (half a tile) at a time
 //   warp 2      issues O += P_u V_u
-//   warp 3      looks through the request's whole page table: a request that
-//               names a page outside the pool gets no output
 //   warps 4-11  softmax, in two groups that take the halves in turn; a thread
 //               has a row (a TMEM lane) and the 64 keys of a half
 // TMEM holds the scores of five halves, and P takes the place of S, so that the
@@ -67,11 +68,8 @@ struct PagedCfg {
   static constexpr int kStages = D == 128 ? 3 : 6;          // of keys, and as many of values
   static constexpr int kOffK = 0, kOffV = kStages * kTileBytes;
   static constexpr int kEnd = 2 * kStages * kTileBytes;
-  // after the loop: the rows, the ones received, and references and sums
-  static constexpr int kOffRecv = kRows * (D + 4) * 4;
-  static constexpr int kOffMl = kOffRecv + (kRows * D + 4 * kMaxSplits) * 4;
-  static constexpr int kMerge = kOffMl + kMaxSplits * kRows * 8;
-  static constexpr int kSmem = (kEnd > kMerge ? kEnd : kMerge) + 1024;
+  static_assert(merge_bytes<D>(kRows) <= kEnd, "the rows take the rings' place after the loop");
+  static constexpr int kSmem = kEnd + 1024;
   // TMEM: the halves' S, and P in their place (a pair of keys per column, remainders
   // behind the high parts), Q (a pair of dims), O
   static constexpr uint32_t kColQ = kBufs * kHalf, kColO = kColQ + 64, kTmemCols = 512;
@@ -97,13 +95,13 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
   extern __shared__ uint8_t smem_raw[];
   __shared__ struct {
     uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
-    uint64_t q_full, s_full[kBufs], p_full[kBufs], o_done[kBufs], turn[4][kGroups], drained[2];
+    uint64_t q_full, s_full[kBufs], p_full[kBufs], o_done[kBufs], turn[4][kGroups], drained[2], merge;
   } bars;
   __shared__ uint32_t s_tmem;
   __shared__ int s_timeout, s_bad_page;
   __shared__ int s_par[SPEC_MAX_TREE_NODES];
   __shared__ long long s_row[kRows];          // a row's first element of o
-  __shared__ float s_ref[1][kRows], s_sum[1][kRows], s_part[kGroups][kRows];
+  __shared__ float s_ref[kRows], s_part[kGroups][kRows];
 
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -130,6 +128,7 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
       mbar_init(&bars.o_done[s], 1);
     }
     for (int s = 0; s < 4 * kGroups; ++s) mbar_init(&bars.turn[0][0] + s, 1);
+    mbar_init(&bars.merge, 1);
     mbar_init(&bars.drained[0], 1);
     mbar_init(&bars.drained[1], 1);
     fence_barrier_init();
@@ -168,43 +167,42 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
   const int halves = uniform(max(0, min(2 * ntiles, (w.keys - t0 * kTile + kHalf - 1) / kHalf)));      // that hold a key
   bool ok = true;      // cleared by a wait that ran out: the role goes on without waiting, and no row is written
 
-  Ring<NS> kr, vr;     // warp 0's
-  if (warp == 0) {
+  Ring<NS> copies;     // of the copying warps
+  copies.phase = 1;    // every stage is free at first
+  if (warp == 0 || warp == 3) {
     // ------------------------------------------------------------ keys and values
-    const int shift = min(p.pages.shift, 7), box_rows = 1 << shift;      // slots of a box
-    const int place = lane / C::kBoxes, bx = lane % C::kBoxes;
+    const bool of_v = warp == 3;
+    uint64_t *full = of_v ? bars.v_full : bars.k_full, *empty = of_v ? bars.v_empty : bars.k_empty;
+    const CUtensorMap *map = of_v ? &tmv : &tmk;
+    uint8_t *ring = smem + (of_v ? C::kOffV : C::kOffK);
+    const int shift = min(p.pages.shift, 7), box_slots = 1 << shift;
+    const int place = lane / C::kBoxes, bx = lane % C::kBoxes;           // a lane's box: page and half of D
     const int in_page = (1 << p.pages.shift) - 1;
     auto boxes = [&](int i) {      // of tile i that hold a key
-      return (min(kTile, w.keys - (t0 + i) * kTile) + box_rows - 1) >> shift;
+      return (min(kTile, w.keys - (t0 + i) * kTile) + box_slots - 1) >> shift;
     };
     auto look_up = [&](int i) {    // (an id outside the pool: any page will do, no row is written)
       if (i >= ntiles || place >= boxes(i)) return 0;
       return max(0, p.pages.page(b, ((t0 + i) * kTile + (place << shift)) >> p.pages.shift));
     };
-    kr.phase = vr.phase = 1;       // every stage is free at first
     int page = look_up(0);
-    for (int i = 0; i < ntiles && ok; ++i) {
+    for (int i = 0; i < ntiles; ++i) {
       const int next = look_up(i + 1);
       const int n = boxes(i), slot = ((t0 + i) * kTile + (place << shift)) & in_page;
-      const uint32_t bytes = static_cast<uint32_t>(n * C::kBoxes * box_rows * 128);
-      auto bring = [&](uint64_t *full, uint64_t *empty, const CUtensorMap &map, int off, Ring<NS> &ring) {
-        // (a consumer that gave up frees a stage whose last copy has not landed: nothing
-        // may be announced on a barrier that still awaits bytes)
-        ok = ok && mbar_sleep(smem_addr(&empty[ring.at]), ring.phase) &&
-             mbar_over(smem_addr(&full[ring.at]), ring.phase);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return;
-        if (lane == 0) mbar_arrive_expect_tx(&full[ring.at], bytes);
-        __syncwarp();
-        if (place < n)
-          tma_load_4d(smem + off + ring.at * C::kTileBytes + bx * C::kBoxBytes + (place << shift) * 128, &map,
-                      &full[ring.at], bx * 64, slot, g_kv, page);
-        ring.next();
-      };
-      bring(bars.k_full, bars.k_empty, tmk, C::kOffK, kr);
-      bring(bars.v_full, bars.v_empty, tmv, C::kOffV, vr);
+      // (a consumer that gave up frees a stage whose last copy has not landed: nothing
+      // may be announced on a barrier that still awaits bytes)
+      ok = ok && mbar_now(&empty[copies.at], copies.phase) && mbar_over(smem_addr(&full[copies.at]), copies.phase);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&full[copies.at], static_cast<uint32_t>(n * C::kBoxes * box_slots * 128));
+      __syncwarp();
+      if (place < n)
+        tma_load_4d(ring + copies.at * C::kTileBytes + bx * C::kBoxBytes + (place << shift) * 128, map, &full[copies.at],
+                    bx * 64, slot, g_kv, page);
+      copies.next();
       page = next;
     }
+    if (of_v && warp_finds_bad_page(p.pages, b, 0, w.R.keys, lane) && lane == 0) s_bad_page = 1;
   } else if (warp == 1) {
     // ------------------------------------------------------------ S = Q K^T
     constexpr uint32_t id = tc::idesc_bf16_f32(kRows, kHalf, 0, 0);
@@ -258,9 +256,6 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
       __syncwarp();
       if (h) ring.next();
     }
-  } else if (warp == 3) {
-    // ------------------------------------------------------------ the page table
-    if (warp_finds_bad_page(p.pages, b, 0, w.R.keys, lane) && lane == 0) s_bad_page = 1;
   } else {
     // ------------------------------------------------------------ softmax
     const int quad = warp & 3, group = (warp - kSoftFirst) >> 2;
@@ -311,7 +306,7 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
     const int all_see = p.causal ? L + w.row0 / a.G + 1 : L;       // what every row of the block sees: [0, all_see)
     const float c = a.scale_log2;
     float ref = -INFINITY, sum = 0.f;      // in powers of two; of this thread's weights 2^(score - ref)
-    if (group == 0) s_ref[0][row] = -INFINITY;
+    if (group == 0) s_ref[row] = -INFINITY;
     named_bar_sync(1, kSoftThreads);
 
     Ring<kBufs> buf, before;               // of this half, and of the one before
@@ -345,7 +340,7 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
         if (u > 0) ok = ok && (mbar_over(turn_before, round) || mbar_sleep(turn_before, round));
         round ^= 1;
         __syncwarp();
-        const float now = s_ref[0][row];
+        const float now = s_ref[row];
         if (__any_sync(0xffffffffu, now != ref || most > now + kPass)) {
           const float next = most > now + kPass ? most : now;
           if (__any_sync(0xffffffffu, next != now)) {
@@ -366,7 +361,7 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
               }
               tc::wait_st();
             }
-            s_ref[0][row] = next;
+            s_ref[row] = next;
           }
           if (next != ref) sum *= ref == -INFINITY ? 0.f : exp2f(ref - next);
           ref = next;
@@ -449,23 +444,23 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
     buf = Ring<kBufs>();
     for (int v = 0; v < u; ++v) buf.next();
     for (; u < halves; ++u, buf.next()) ok = ok && mbar_sleep(smem_addr(&bars.o_done[buf.at]), buf.phase);
-    if (CS > 1) cluster_arrive_relaxed();
     __syncwarp();
     tc::fence_after_sync();
     if (busy && halves > 0)
       ok = ok && mbar_sleep(smem_addr(&bars.turn[quad][(halves - 1) % kGroups]), (halves - 1) / kGroups & 1);
     __syncwarp();
-    const float now = s_ref[0][row];
+    const float now = s_ref[row];
     if (now != ref) sum *= ref == -INFINITY ? 0.f : exp2f(ref - now);
     s_part[group][row] = sum;
     if (!ok) s_timeout = 1;
     named_bar_sync(1, kSoftThreads);
     if (busy && group < 2 && s_timeout == 0) {
+      float *staged = reinterpret_cast<float *>(smem) + row * (D + 4);
       if (group == 0) {
         for (int q = 1; q < kGroups; ++q) sum += s_part[q][row];
-        s_sum[0][row] = sum;
+        *reinterpret_cast<float2 *>(staged + D) = make_float2(now, sum);
       }
-      const uint32_t so = sb + (row * (D + 4) + group * (D / 2)) * 4;
+      const uint32_t so = smem_addr(staged + group * (D / 2));
 #pragma unroll
       for (int j = 0; j < D / 2; j += 32) {
         float o[32] = {};
@@ -480,8 +475,6 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
       }
     }
   }
-  // (a CTA has arrived, for its peers to write here, once its products are done)
-  if (CS > 1 && warp < kSoftFirst) cluster_arrive_relaxed();
   if (!ok) s_timeout = 1;
   __syncwarp();
   tc::fence_before_sync();
@@ -492,13 +485,10 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
     // What was given up may leave copies and products under way: the warps that
     // issued them wait, with a limit.  (Of a stage that has had no copy the phase
     // before is over.)
-    if (tid == 0) {
-      report(a.status, b, SPEC_ERR_TIMEOUT);
-      for (uint32_t st = 0; st < NS; ++st) {
-        mbar_wait(&bars.k_full[st], st < kr.at ? kr.phase ^ 1 : kr.phase);
-        mbar_wait(&bars.v_full[st], st < vr.at ? vr.phase ^ 1 : vr.phase);
-      }
-    }
+    if (tid == 0) report(a.status, b, SPEC_ERR_TIMEOUT);
+    if (lane == 0 && (warp == 0 || warp == 3))
+      for (uint32_t st = 0; st < NS; ++st)
+        mbar_wait(warp == 3 ? &bars.v_full[st] : &bars.k_full[st], st < copies.at ? copies.phase ^ 1 : copies.phase);
     if (warp == 1 || warp == 2) {
       if (tc::elect_one()) tc::commit(&bars.drained[warp - 1]);
       __syncwarp();
@@ -511,14 +501,11 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
     __syncwarp();
     tc::tmem_dealloc(tmem, C::kTmemCols);
   }
-  // (a page outside the pool is found by every CTA of the cluster)
-  // (a peer's rows may have landed where this CTA's last copies did: no row is
-  // written after a time-out)
-  auto out_row = [&](int r) { return timed_out || s_row[r] < 0 ? nullptr : static_cast<__nv_bfloat16 *>(a.o) + s_row[r]; };
-  merge_rows<D, 1, kRows, kThreads, __nv_bfloat16>(
-      tid, CS, split, w.rows, timed_out || bad_page, reinterpret_cast<float *>(smem), s_ref, s_sum,
-      reinterpret_cast<float2 (*)[kRows]>(smem + C::kOffMl), reinterpret_cast<float4 *>(smem + C::kOffRecv),
-      [] { cluster_wait(); }, out_row);
+  float *so = reinterpret_cast<float *>(smem);
+  if ((timed_out || bad_page) && tid < kRows) so[tid * (D + 4) + D + 1] = -1.f;
+  auto out_row = [&](int r) { return s_row[r] < 0 ? nullptr : static_cast<__nv_bfloat16 *>(a.o) + s_row[r]; };
+  if (!merge_splits<D, kThreads, __nv_bfloat16>(tid, CS, split, w.rows, so, &bars.merge, out_row) && tid == 0)
+    report(a.status, b, SPEC_ERR_TIMEOUT);
 }
 
 // ---------------------------------------------------------------- host side

@@ -2,7 +2,7 @@
 // rows a CTA has, and what a row sees.
 #pragma once
 
-#include "attn_common.cuh"
+#include "attn_kv4.cuh"
 #include "paged.cuh"
 
 namespace spec {
@@ -122,6 +122,79 @@ __device__ __forceinline__ uint32_t sees_32(const RowSees &r, int k0, int L) {
   const uint32_t lo = w == 0 ? m.x : w == 1 ? m.y : w == 2 ? m.z : w == 3 ? m.w : 0u;
   const uint32_t hi = w == 0 ? m.y : w == 1 ? m.z : w == 2 ? m.w : 0u;
   return near | __funnelshift_r(lo, hi, o & 31);
+}
+
+// Merge of a block's rows over the splits of its keys, and the output, by all
+// THREADS threads of the CTA.  Each CTA of the cluster has its rows in
+// so[rows][D + 4] (shared memory, at the same place in all): the weighted sum,
+// the reference, the sum of weights (below zero: this CTA's are not to be used).
+// CTA q merges rows [q share, (q + 1) share): every CTA sends it those, in one
+// copy that completes on its barrier, to recv[split][share][D + 4] behind `so`.
+// (Pieces read from the peers, or stored to them, by the threads themselves: 1000
+// cycles and more for each round of them.)  Code that runs once costs more in
+// instruction fetches than in work here, so the loop is one for all splits, and
+// kept small: factors worked out once a row, unrolled, took 1000 cycles longer.
+template <int D>
+constexpr int merge_bytes(int rows) { return (2 * rows + kMaxSplits) * (D + 4) * 4; }      // so and recv
+
+// False: a peer's rows did not arrive in time, and none are written.
+template <int D, int THREADS, typename E, typename OutRow>
+__device__ __forceinline__ bool merge_splits(int tid, int CS, int split, int rows, float *so, uint64_t *bar,
+                                             OutRow out_row) {
+  constexpr int kStride = D + 4;
+  const int share = CS == 1 ? rows : (rows + CS - 1) / CS;
+  const int from = min(rows, split * share), n = min(rows, from + share) - from;
+  const float *part0 = so;
+  bool ok = true;
+  if (CS > 1) {
+    float *recv = so + rows * kStride;
+    fence_proxy_async_smem();
+    cluster_sync_all();      // every CTA's rows are there, and room for its peers'
+    if (tid < CS) {
+      const int r0 = min(rows, tid * share), rn = min(rows, r0 + share) - r0;
+      if (rn > 0)
+        bulk_copy_s2s(peer_addr(recv + split * share * kStride, tid), smem_addr(so + r0 * kStride),
+                      static_cast<uint32_t>(rn * kStride * 4), peer_addr(bar, tid));
+    }
+    if (n > 0) {
+      if (tid == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(CS * n * kStride * 4));
+      ok = mbar_await(bar, 0);
+    }
+    part0 = recv;
+  } else {
+    __syncthreads();
+  }
+#pragma unroll 1
+  for (int idx = tid; idx < n * (D / 4) && ok; idx += THREADS) {
+    const int r = idx / (D / 4), c = idx % (D / 4) * 4;
+    const float *part = part0 + r * kStride;
+    float top = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool void_part = false;
+#pragma unroll 1
+    for (int q = 0; q < CS; ++q, part += share * kStride) {
+      const float2 m = *reinterpret_cast<const float2 *>(part + D);
+      const float4 v = *reinterpret_cast<const float4 *>(part + c);
+      const float next = fmaxf(top, m.x), zero = next == -INFINITY ? 0.f : next;
+      const float f0 = fast_exp2(top - zero), f1 = fast_exp2(m.x - zero);
+      top = next;
+      void_part |= m.y < 0.f;
+      sum = fmaf(f1, m.y, sum * f0);
+      acc.x = fmaf(f1, v.x, acc.x * f0);
+      acc.y = fmaf(f1, v.y, acc.y * f0);
+      acc.z = fmaf(f1, v.z, acc.z * f0);
+      acc.w = fmaf(f1, v.w, acc.w * f0);
+    }
+    E *dst = out_row(from + r);
+    if (void_part || !dst) continue;
+    const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
+    store_row4(dst + c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+  }
+  if (CS > 1) {      // no CTA leaves while a copy may still read its rows
+    cluster_arrive_relaxed();
+    cluster_wait();
+  }
+  return ok;
 }
 
 int launch_attn_paged_f32(const PagedAttnArgs &p, int max_prefix, void *stream);

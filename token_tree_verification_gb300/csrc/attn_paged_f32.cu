@@ -10,7 +10,6 @@
 // keys of the next tile beside the output's products and its values beside the
 // scores'.  R = 16 for few rows, where what 64 would multiply in vain costs more
 // than reading the keys.
-#include "attn_kv4.cuh"
 #include "attn_paged.cuh"
 
 namespace spec {
@@ -35,10 +34,8 @@ struct F32Cfg {
   static constexpr int kP = kKeys + 4;
   static constexpr int kOffK = R * kRow, kOffV = kOffK + kKeys * kRow, kOffP = kOffV + kKeys * D;
   static constexpr int kEnd = kOffP + R * kP;
-  // after the loop: the rows, the ones received, and references and sums
-  static constexpr int kOffRecv = R * kRow, kOffMl = kOffRecv + R * D + 4 * kMaxSplits;
-  static constexpr int kMerge = kOffMl + kMaxSplits * R * 2;
-  static constexpr int kSmem = (kEnd > kMerge ? kEnd : kMerge) * 4;
+  // (the result's rows take the place of all)
+  static constexpr int kSmem = kEnd * 4 > merge_bytes<D>(R) ? kEnd * 4 : merge_bytes<D>(R);
 };
 
 template <int D, int R>
@@ -48,13 +45,17 @@ tree_attn_paged_f32_kernel(const PagedAttnArgs p, const int CS) {
   constexpr int kDims = D / 16;               // of a thread: kDims / 4 groups of four
   const AttnArgs &a = p.a;
   extern __shared__ __align__(16) float sm[];
-  __shared__ float s_ref[1][R], s_sum[1][R];
+  __shared__ uint64_t s_bar;
   __shared__ long long s_row[R];
   __shared__ int s_par[SPEC_MAX_TREE_NODES];
   const int split = static_cast<int>(blockIdx.x) % CS, block = static_cast<int>(blockIdx.x) / CS;
   const int g_kv = static_cast<int>(blockIdx.y), tid = threadIdx.x, lane = tid & 31;
   const int tx = tid & 15, r0 = (tid >> 4) * 4;        // this thread's keys tx and tx + 16, and rows r0 .. r0 + 3
   pdl_trigger();
+  if (tid == 0) {
+    mbar_init(&s_bar, 1);
+    fence_barrier_init();
+  }
   pdl_wait();
   if (tid < 32) touch_table(p, lane);
   const RowBlock w = find_block<R>(p, block, lane);
@@ -208,28 +209,22 @@ tree_attn_paged_f32_kernel(const PagedAttnArgs p, const int CS) {
     bring(i + 1, a.v, C::kOffV, D);
   }
   copies_wait<0>();
-  __syncthreads();
+  bad = __syncthreads_or(bad);
+  if (bad && tid == 0) report(a.status, b, SPEC_ERR_PAGE);
   // ---- the rows take q's place
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
 #pragma unroll
     for (int d = 8; d; d /= 2) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], d);
-    if (tx == 0) {
-      s_ref[0][r0 + r] = ref[r];
-      s_sum[0][r0 + r] = sum[r];
-    }
+    if (tx == 0) *reinterpret_cast<float2 *>(sm + (r0 + r) * C::kRow + D) = make_float2(ref[r], bad ? -1.f : sum[r]);
 #pragma unroll
     for (int g = 0; g < kDims / 4; ++g)
       *reinterpret_cast<float4 *>(sm + (r0 + r) * C::kRow + 64 * g + 4 * tx) =
           make_float4(o[r][4 * g], o[r][4 * g + 1], o[r][4 * g + 2], o[r][4 * g + 3]);
   }
-  bad = __syncthreads_or(bad);
-  if (bad && tid == 0) report(a.status, b, SPEC_ERR_PAGE);
   auto out_row = [&](int r) { return s_row[r] < 0 ? nullptr : static_cast<float *>(a.o) + s_row[r]; };
-  merge_rows<D, 1, R, C::kThreads, float>(tid, CS, split, w.rows, bad, sm, s_ref, s_sum,
-                                          reinterpret_cast<float2 (*)[R]>(sm + C::kOffMl),
-                                          reinterpret_cast<float4 *>(sm + C::kOffRecv), [] { cluster_sync_all(); },
-                                          out_row);
+  if (!merge_splits<D, C::kThreads, float>(tid, CS, split, w.rows, sm, &s_bar, out_row) && tid == 0)
+    report(a.status, b, SPEC_ERR_TIMEOUT);
 }
 
 // As many splits of the keys as make waves x (tiles of a CTA + its set-up and
