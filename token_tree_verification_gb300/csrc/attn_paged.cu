@@ -543,7 +543,10 @@ bool encode_pool(CUtensorMap *m, const void *base, const PageTable &pages, int H
 }
 
 // As many splits of the keys (a cluster) as make waves x (tiles of a CTA + its
-// set-up, first tile and merge, in half tiles) least.
+// set-up, first tile and merge, which grows with the rows, in half tiles) least.
+// (Device us by splits 1, 2, 3, 4, 5 and 8: 32 rows of 8 heads behind 500 keys 9.5,
+// 9.1, 8.1, 8.1, 7.5 and 7.6; 128 rows of 32 heads behind 300 12.3, 13.2, 13.2, 13.5;
+// one token x 4 x 8 heads behind 8192 58, 34, 26.9, 26.2, 39 and 45.)
 template <int D>
 int launch_bf16(const PagedAttnArgs &p, int max_prefix, void *stream) {
   using C = PagedCfg<D>;
@@ -554,17 +557,18 @@ int launch_bf16(const PagedAttnArgs &p, int max_prefix, void *stream) {
   CUtensorMap tmk, tmv;
   if (!encode_pool(&tmk, p.a.k, p.pages, p.a.Hkv, D) || !encode_pool(&tmv, p.a.v, p.pages, p.a.Hkv, D))
     return SPEC_ERR_CUDA;
-  const long long blocks = most_blocks<kRows>(p.a), units = blocks * p.a.Hkv;
+  const long long blocks = most_blocks<kRows>(p.a), units = likely_blocks<kRows>(p.a) * p.a.Hkv;
   const long long keys = static_cast<long long>(max_prefix) + mean_nodes(p.a);
   const long long tiles = (keys + kTile - 1) / kTile;
+  const long long rows = static_cast<long long>(mean_nodes(p.a)) * p.a.G, merge = 2 + (rows < kRows ? rows : kRows) / 32;
   int cs = 1;
   long long best = -1;
   for (int n = 1; n <= kMaxSplits; n = n == 8 ? kMaxSplits : n + 1) {
-    if (n > 1 && tiles < 2 * n) break;
+    if (n > 1 && tiles < n) break;
     const int slots = clusters_at_once(kernel, n, kThreads, C::kSmem, dev, &state);
     if (slots < 1) continue;
     const long long waves = (units + slots - 1) / slots;
-    const long long cost = waves * (2 * ((tiles + n - 1) / n) + (n > 1 ? 12 : 8));
+    const long long cost = waves * (2 * ((tiles + n - 1) / n) + 8 + (n > 1 ? merge : 0));
     if (best < 0 || cost < best) {
       best = cost;
       cs = n;

@@ -93,6 +93,12 @@ inline long long most_blocks(const AttnArgs &a) {
   return (static_cast<long long>(a.T) * a.G - (a.B < a.T ? a.B : a.T)) / ROWS + (a.B < a.T ? a.B : a.T);
 }
 
+// Blocks of requests alike, by which launches are planned.
+template <int ROWS>
+inline long long likely_blocks(const AttnArgs &a) {
+  return (static_cast<long long>(mean_nodes(a)) * a.G + ROWS - 1) / ROWS * (a.B < a.T ? a.B : a.T);
+}
+
 // Every request's error, reported once (those in error have no block); by one
 // warp of the launch's first CTA.
 __device__ __forceinline__ void report_bad_requests(const PagedAttnArgs &p, int lane) {
