@@ -13,11 +13,19 @@
 // table (a double) and exact otherwise.  Its upper 32 bits go to sincospif as a
 // number of half turns in [-1, 1), which rounds to 2^-25.
 //
-// One CTA takes up to eight whole rows, or a part of one row's heads; a row's
-// cosines and sines are computed once for all of its heads.  An item is two
-// 16-byte vectors: both ends of eight (four, fp32) pairs, or two vectors of
-// dims that are copied.  The first items' loads need no look-up and are issued in
-// front of them: offsets, start and depth, page are a chain of three loads.
+// A thread has one item of a row, two 16-byte vectors: both ends of eight (four,
+// fp32) pairs, or two vectors of dims that are copied; it keeps it along a run of
+// rows, so that what an item is (head, place, source, destination) is worked out
+// once, and rows differ by a stride, a slot and the angles, which one CTA computes
+// once for all heads.  (With an item worked out for every row and head the
+// instructions bound it: 112 us where this takes 101.)  The first rows' loads need
+// no look-up and are issued in front of them: offsets, start and depth, page are a
+// chain of three loads.
+//
+// Memory bounds long runs: 50000 rows of 40 heads, D = 128, 1.05 GB in 164 us, 6.4
+// TB/s, 0.94 of a copy's rate; 14000 rows of 80 heads into pages of 64 slots, 583 MB
+// in 101 us, 5.8 TB/s.  A few tokens (2.9 us) and a 64-node tree of 96 heads (3.6
+// us) are the chain of loads.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -28,9 +36,11 @@ namespace spec {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxRows = kThreads / 32;      // a warp looks up each row
-constexpr int kItems = 2;                    // of a thread, under way at once
+constexpr int kMaxThreads = 384;
+constexpr int kMaxRows = 32;                 // of a CTA
+constexpr int kLong = 4;                     // rows of a thread whose loads are under way, along a run
+constexpr int kRun = 8;                      // rows of a run
+constexpr int kAngleBytes = 32 * 1024;
 
 struct Rows {
   const void *x;
@@ -49,7 +59,8 @@ struct RopeArgs {
   int32_t *status;
   int B, T, Hq, Hkv, D, r;
   int turn_items, copy_items;        // of a rotated and of a copied head
-  int row_items, span, rows;         // of a row, of a row in one CTA, and rows of a CTA
+  int row_items, span;               // of a row, and of a row in one CTA
+  int rows, side;                    // of a CTA, and how many side by side
 };
 
 template <typename E>
@@ -105,16 +116,14 @@ __device__ __forceinline__ void turn(float &xa, float &xb, float2 cs) {
 // they are turned.  Vectors (kVec): two of them at pa and pb (pb < 0: one).  Else
 // single elements: the two of a pair, or one that is copied.
 struct Item {
-  int row, head, pa, pb;      // head: q's, then k's, then v's
+  int head, pa, pb;           // head: q's, then k's, then v's
   bool turn_a, turn_b;
   int pair;                   // first pair of pa's cosines
 };
 
 template <typename E, bool kVec, bool kInter>
-__device__ __forceinline__ Item item_at(const RopeArgs &a, int idx, int first) {
+__device__ __forceinline__ Item item_at(const RopeArgs &a, int i) {
   Item it;
-  it.row = idx / a.span;
-  int i = first + idx - it.row * a.span;
   constexpr int V = kVec ? Vec<E>::n : 1;
   const int turned = (a.Hq + a.Hkv) * a.turn_items;
   it.turn_a = it.turn_b = false;
@@ -153,44 +162,42 @@ __device__ __forceinline__ Item item_at(const RopeArgs &a, int idx, int first) {
   return it;
 }
 
-template <typename E, bool kVec, bool kInter>
-__global__ void __launch_bounds__(kThreads)
+template <typename E, bool kVec, bool kInter, int kAhead>
+__global__ void __launch_bounds__(kMaxThreads, kAhead == 1 ? 1 : 3)
 rope_kernel(const RopeArgs a) {
-  extern __shared__ __align__(16) float2 s_cs[];       // [rows][r / 2]
+  extern __shared__ __align__(16) float s_angle[];     // [rows][cosines, sines][r / 2]
   __shared__ int s_ok[kMaxRows], s_pos[kMaxRows];
   __shared__ long long s_slot[kMaxRows];               // first element of the slot's head 0 in the pools
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, threads = blockDim.x, warp = tid >> 5, lane = tid & 31;
   const int t0 = static_cast<int>(blockIdx.x) * a.rows;
-  const int rows = min(a.rows, a.T - t0);
-  const int first = static_cast<int>(blockIdx.y) * a.span;
-  const int total = rows * min(a.span, a.row_items - first);
+  const int rows = min(a.rows, a.T - t0), pairs = a.r / 2;
   using Load = typename std::conditional<kVec, uint4, E>::type;
   pdl_trigger();
   pdl_wait();
 
-  auto source = [&](const Item &it) -> const E * {
-    const bool is_q = it.head < a.Hq, is_k = it.head < a.Hq + a.Hkv;
-    const Rows &s = is_q ? a.q : is_k ? a.k : a.v;
-    const int h = is_q ? it.head : is_k ? it.head - a.Hq : it.head - a.Hq - a.Hkv;
-    return static_cast<const E *>(s.x) + (t0 + it.row) * s.st + h * s.sh;
+  // ---- this thread's item, and the first of its rows
+  const int sub = tid / a.span, i = static_cast<int>(blockIdx.y) * a.span + tid - sub * a.span;
+  const bool busy = sub < a.side && i < a.row_items;
+  const Item it = item_at<E, kVec, kInter>(a, busy ? i : 0);
+  const bool is_q = it.head < a.Hq, is_k = !is_q && it.head < a.Hq + a.Hkv;
+  const int head = is_q ? it.head : it.head - a.Hq - (is_k ? 0 : a.Hkv);
+  const long long x_st = is_q ? a.q.st : is_k ? a.k.st : a.v.st;
+  const E *x = static_cast<const E *>(is_q ? a.q.x : is_k ? a.k.x : a.v.x) +
+               head * (is_q ? a.q.sh : is_k ? a.k.sh : a.v.sh) + it.pa + t0 * x_st;
+  const int to_b = it.pb - it.pa;
+  const bool two = it.pb >= 0;
+  Load la[kAhead], lb[kAhead];
+  auto load = [&](int u, int row) {
+    if (!busy || row >= rows) return;
+    la[u] = *reinterpret_cast<const Load *>(x + row * x_st);
+    if (two) lb[u] = *reinterpret_cast<const Load *>(x + row * x_st + to_b);
   };
-  Load la[kItems], lb[kItems];
-  auto load = [&](int i0) {
 #pragma unroll
-    for (int u = 0; u < kItems; ++u) {
-      const int idx = i0 + u * kThreads;
-      if (idx >= total) continue;
-      const Item it = item_at<E, kVec, kInter>(a, idx, first);
-      const E *x = source(it);
-      la[u] = *reinterpret_cast<const Load *>(x + it.pa);
-      if (it.pb >= 0) lb[u] = *reinterpret_cast<const Load *>(x + it.pb);
-    }
-  };
-  load(tid);
+  for (int u = 0; u < kAhead; ++u) load(u, sub + u * a.side);
 
-  // ---- each row's request, position and slot
-  if (warp < rows) {
-    const int t = t0 + warp;
+  // ---- each row's request, position and slot, by a warp
+  for (int row = warp; row < rows; row += threads / 32) {
+    const int t = t0 + row;
     const int b = warp_find_request(a.offsets, a.B, t, lane);
     bool ok = b >= 0;
     long long slot_at = 0;
@@ -220,14 +227,14 @@ rope_kernel(const RopeArgs a) {
       }
     }
     if (lane == 0) {
-      s_ok[warp] = ok;
-      s_pos[warp] = position;
-      s_slot[warp] = slot_at;
+      s_ok[row] = ok;
+      s_pos[row] = position;
+      s_slot[row] = slot_at;
     }
   }
   // (whole batches are checked once, so that a request without rows here reports too)
   if (blockIdx.x == 0 && blockIdx.y == 0) {
-    for (int b = tid; b < a.B; b += kThreads) {
+    for (int b = tid; b < a.B; b += threads) {
       const RowRange R = row_range(a.offsets, b, a.T);
       int err = R.err;
       if (!err && __ldg(a.start + b) < 0) err = SPEC_ERR_PREFIX_RANGE;
@@ -239,72 +246,80 @@ rope_kernel(const RopeArgs a) {
     }
   }
   __syncthreads();
-  const int pairs = a.r / 2;
-  for (int i = tid; i < rows * pairs; i += kThreads) {
-    const int row = i / pairs;
-    const unsigned long long turns = static_cast<unsigned long long>(static_cast<unsigned>(s_pos[row])) *
-                                     __ldg(a.freqs + i - row * pairs);
+  for (int p = tid; p < rows * pairs; p += threads) {
+    const int row = p / pairs, at = p - row * pairs;
+    const unsigned long long turns =
+        static_cast<unsigned long long>(static_cast<unsigned>(s_pos[row])) * __ldg(a.freqs + at);
     const float half_turns = static_cast<float>(static_cast<int>(turns >> 32)) * 4.656612873077393e-10f;   // 2^-31
     float s, c;
     sincospif(half_turns, &s, &c);
-    s_cs[i] = make_float2(c * a.scale, s * a.scale);
+    s_angle[row * a.r + at] = c * a.scale;
+    s_angle[row * a.r + pairs + at] = s * a.scale;
   }
   __syncthreads();
+  if (!busy) return;
 
-  for (int i0 = tid; i0 < total; i0 += kItems * kThreads) {
-    if (i0 != tid) load(i0);
+  E *y = static_cast<E *>(is_q ? a.y : is_k ? a.k_pages : a.v_pages) + it.pa +
+         (is_q ? head * a.y_sh + t0 * a.y_st : (static_cast<long long>(head) << a.pages.shift) * a.D);
+  auto store = [&](int u, int row) {
+    if (!s_ok[row]) return;
+    const float *cosine = s_angle + row * a.r + it.pair, *sine = cosine + pairs;
+    if constexpr (kVec) {
+      constexpr int V = Vec<E>::n;
+      if constexpr (kInter) {
+        auto turn_vec = [&](uint4 &x, int from) {
+          float f[V];
+          Vec<E>::unpack(x, f);
 #pragma unroll
-    for (int u = 0; u < kItems; ++u) {
-      const int idx = i0 + u * kThreads;
-      if (idx >= total) continue;
-      const Item it = item_at<E, kVec, kInter>(a, idx, first);
-      if (!s_ok[it.row]) continue;
-      const float2 *cs = s_cs + it.row * pairs + it.pair;
-      if constexpr (kVec) {
-        constexpr int V = Vec<E>::n;
-        if constexpr (kInter) {
-          auto turn_vec = [&](uint4 &x, const float2 *c) {
-            float f[V];
-            Vec<E>::unpack(x, f);
-#pragma unroll
-            for (int e = 0; e < V; e += 2) turn(f[e], f[e + 1], c[e / 2]);
-            x = Vec<E>::pack(f);
-          };
-          if (it.turn_a) turn_vec(la[u], cs);
-          if (it.turn_b) turn_vec(lb[u], cs + (it.pb - it.pa) / 2);
-        } else if (it.turn_a) {
-          float fa[V], fb[V];
-          Vec<E>::unpack(la[u], fa);
-          Vec<E>::unpack(lb[u], fb);
-#pragma unroll
-          for (int e = 0; e < V; ++e) turn(fa[e], fb[e], cs[e]);
-          la[u] = Vec<E>::pack(fa);
-          lb[u] = Vec<E>::pack(fb);
-        }
+          for (int e = 0; e < V; e += 2) turn(f[e], f[e + 1], make_float2(cosine[from + e / 2], sine[from + e / 2]));
+          x = Vec<E>::pack(f);
+        };
+        if (it.turn_a) turn_vec(la[u], 0);
+        if (it.turn_b) turn_vec(lb[u], to_b / 2);
       } else if (it.turn_a) {
-        float fa = to_float(la[u]), fb = to_float(lb[u]);
-        turn(fa, fb, *cs);
-        from_float(fa, &la[u]);
-        from_float(fb, &lb[u]);
+        float fa[V], fb[V];
+        Vec<E>::unpack(la[u], fa);
+        Vec<E>::unpack(lb[u], fb);
+        // (pairs of eight, four in fp32: whole vectors of angles)
+        float c[V], s[V];
+#pragma unroll
+        for (int e = 0; e < V; e += 4) {
+          *reinterpret_cast<float4 *>(c + e) = *reinterpret_cast<const float4 *>(cosine + e);
+          *reinterpret_cast<float4 *>(s + e) = *reinterpret_cast<const float4 *>(sine + e);
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) turn(fa[e], fb[e], make_float2(c[e], s[e]));
+        la[u] = Vec<E>::pack(fa);
+        lb[u] = Vec<E>::pack(fb);
       }
-      E *y;
-      if (it.head < a.Hq) {
-        y = static_cast<E *>(a.y) + (t0 + it.row) * a.y_st + it.head * a.y_sh;
-      } else {
-        const bool is_k = it.head < a.Hq + a.Hkv;
-        const int h = it.head - a.Hq - (is_k ? 0 : a.Hkv);
-        y = static_cast<E *>(is_k ? a.k_pages : a.v_pages) + s_slot[it.row] +
-            (static_cast<long long>(h) << a.pages.shift) * a.D;
-      }
-      *reinterpret_cast<Load *>(y + it.pa) = la[u];
-      if (it.pb >= 0) *reinterpret_cast<Load *>(y + it.pb) = lb[u];
+    } else if (it.turn_a) {
+      float fa = to_float(la[u]), fb = to_float(lb[u]);
+      turn(fa, fb, make_float2(*cosine, *sine));
+      from_float(fa, &la[u]);
+      from_float(fb, &lb[u]);
+    }
+    E *dst = y + (is_q ? row * a.y_st : s_slot[row]);
+    *reinterpret_cast<Load *>(dst) = la[u];
+    if (two) *reinterpret_cast<Load *>(dst + to_b) = lb[u];
+  };
+  for (int row0 = sub; row0 < rows; row0 += kAhead * a.side) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int row = row0 + u * a.side;
+      if (row >= rows) break;
+      store(u, row);
+      load(u, row + kAhead * a.side);
     }
   }
 }
 
-// Whole rows to a CTA, eight at most and about six items a thread, once that
-// makes four CTAs an SM; before that a row is split over CTAs of one item a
-// thread, so that a few tokens' heads spread over the GPU.
+// An item a thread, a row's items in as few CTAs as take them in kMaxThreads, or
+// several rows side by side where a row has few; and rows in a run up to kRun (32
+// side by side) while that leaves sixteen CTAs an SM.  (Runs of 4, 8, 16 and 32 rows:
+// 160, 164, 177 and 190 us for the 50000 rows above, 109, 101, 111 and 124 for the
+// rows into pages; two loads ahead in place of four, 48 warps an SM: 160 and 104.)
+// A single row a thread takes no registers for a run: 3.6 in place of 4.4 us for the
+// tree.
 template <typename E, bool kVec, bool kInter>
 int launch(RopeArgs &a, void *stream) {
   constexpr int V = kVec ? Vec<E>::n : 1;
@@ -313,28 +328,35 @@ int launch(RopeArgs &a, void *stream) {
   a.turn_items = kVec ? (kInter ? (vecs + 1) / 2 : a.r / 2 / V + ((a.D - a.r) / V + 1) / 2) : a.r / 2 + a.D - a.r;
   const long long items = static_cast<long long>(a.Hq + a.Hkv) * a.turn_items +
                           (a.v.x ? static_cast<long long>(a.Hkv) * a.copy_items : 0);
-  if (items > 0x1000000) return SPEC_ERR_SHAPE;      // (a CTA counts its rows' items in 32 bits)
+  if (items > 0xFFFFll * kMaxThreads) return SPEC_ERR_SHAPE;      // (the grid's second dimension)
   a.row_items = static_cast<int>(items);
-  const int whole = a.row_items >= 6 * kThreads ? 1 : 6 * kThreads / a.row_items;
-  const int rows = whole < kMaxRows ? whole : kMaxRows;
-  if (a.T / rows >= 4 * sm_count()) {
-    a.rows = rows;
-    a.span = a.row_items;
-  } else {
-    a.rows = 1;
-    a.span = a.row_items < kThreads ? a.row_items : kThreads;
+  const int parts = (a.row_items + kMaxThreads - 1) / kMaxThreads;
+  a.span = (a.row_items + parts - 1) / parts;
+  a.side = 1;
+  if (a.span > 32) a.span = (a.span + 31) / 32 * 32;
+  const long long runs = static_cast<long long>(a.T) * parts / (16ll * sm_count());
+  int most = kRun;
+  if (a.span < 128) {
+    a.side = 128 / a.span < a.T ? 128 / a.span : a.T;
+    if (a.side > 16) a.side = 16;
+    most = kMaxRows;
   }
+  a.rows = runs < a.side ? a.side : runs < most ? static_cast<int>(runs) : most;
+  if (a.rows > a.side) a.rows -= a.rows % a.side;
+  while (a.rows > 1 && a.rows * a.r * 4 > kAngleBytes) a.rows = a.rows / 2;
+  if (a.side > a.rows) a.side = a.rows;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((a.T + a.rows - 1) / a.rows),
                      static_cast<unsigned>((a.row_items + a.span - 1) / a.span), 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(a.rows) * (a.r / 2) * sizeof(float2);
+  cfg.blockDim = dim3((a.span * a.side + 31) / 32 * 32, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(a.rows) * a.r * sizeof(float);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   pdl_attribute(attr[0]);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rope_kernel<E, kVec, kInter>, a) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  const auto kernel = a.rows > a.side ? rope_kernel<E, kVec, kInter, kLong> : rope_kernel<E, kVec, kInter, 1>;
+  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 // 16-byte vectors where every pointer, stride and the pairs' ends allow them;
