@@ -2,6 +2,9 @@
 Copies are exact; rotation and attention are held to bounds counted from the
 roundings they make."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -649,3 +652,107 @@ def test_no_rows_at_all(gpu_lib):
     assert ttv.tree_attn_paged(empty(4), cache.k, cache.v, cache.block_table, i32([0, 0]), none, None, 0, status,
                                causal=True).shape == (0, 4, 64)
     assert status.eq(0).all()
+
+
+def test_first_calls_inside_a_capture(gpu_lib):
+    """A fresh process whose first calls of every kind are captured, replayed twice."""
+    code = """
+import torch, token_tree_verification_gb300 as ttv
+i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+for dt, D in ((torch.bfloat16, 128), (torch.float32, 64)):
+    kp, vp = (torch.zeros((20, 2, 16, D), dtype=dt, device="cuda") for _ in range(2))
+    table = torch.arange(19, -1, -1, dtype=torch.int32, device="cuda").reshape(1, 20)
+    rows = [torch.randn((150, h, D), device="cuda").to(dt) for h in (4, 2, 2)]
+    off, lens, status, rope = i32(0, 150), i32(0), i32(0), ttv.rope_table(D)
+    path, acc, at, tree = i32(0, 2).reshape(1, 2), i32(1), i32(10), i32(0, 64)
+    torch.cuda.synchronize()
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=side):
+        t = ttv.rope_write_paged(*rows, kp, vp, table, lens, off, status, rope)
+        r = ttv.rope(rows[0], rope, lens, off, status)
+        o = ttv.tree_attn_paged(t, kp, vp, table, lens, off, None, 0, status, causal=True)
+        m = ttv.kv_compact_paged(kp, vp, table, at, tree, path, acc, status)
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    kept = kp.clone()
+    t2 = ttv.rope_write_paged(*rows, kp, vp, table, lens, off, status, rope)
+    assert torch.equal(t, t2) and torch.equal(r, t2) and m.item() == 12
+    assert torch.equal(o, ttv.tree_attn_paged(t2, kp, vp, table, lens, off, None, 0, status, causal=True))
+    assert not torch.equal(kept, kp) and status.item() == 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=root)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+@DTYPES
+def test_pools_beyond_32_bits(gpu_lib, dtype):
+    """Pages whose elements lie past 2^32 of the pool: written, attended to, moved."""
+    rng = np.random.default_rng(16)
+    H, P, D = 2, 4096, 128
+    pages = 2 ** 32 // (H * P * D) + 3
+    pools = [torch.empty((pages, H, P, D), dtype=dtype, device="cuda") for _ in range(2)]
+    table = np.array([[pages - 1, 1], [2, pages - 2]])
+    n, L = [20, 30], [4090, 4090]
+    off = [0, 20, 50]
+    q, k, v = (gpu(rng.standard_normal((50, h, D)), dtype) for h in (4, 2, 2))
+    small = [torch.empty((4, H, P, D), dtype=dtype, device="cuda") for _ in range(2)]
+    where = [pages - 1, 1, 2, pages - 2]
+    for x, y in zip(pools, small):
+        for i, page in enumerate(where):
+            y[i] = gpu(rng.standard_normal((H, P, D)), dtype)
+            x[page] = y[i]
+    near = np.array([[0, 1], [2, 3]])
+    path, acc = [[0, 3, 9]] * 2, [2, 2]
+    got = []
+    for kp, vp, t in ((*pools, table), (*small, near)):
+        status = zeros_status(2)
+        turned = ttv.rope_write_paged(q, k, v, kp, vp, i32(t), i32(L), i32(off), status, ttv.rope_table(D))
+        o = ttv.tree_attn_paged(turned, kp, vp, i32(t), i32(L), i32(off), None, 4090, status, causal=True)
+        lens = ttv.kv_compact_paged(kp, vp, i32(t), i32(L), i32(off), i32(path), i32(acc), status)
+        assert status.eq(0).all() and lens.tolist() == [4093, 4093]
+        got.append((turned, o))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    for x, y in zip(pools, small):
+        for i, page in enumerate(where):
+            assert torch.equal(x[page], y[i])
+
+
+def test_tensors_the_calls_refuse(gpu_lib):
+    q, k, pool = (torch.zeros(s, dtype=BF16, device="cuda") for s in ((3, 4, 64), (3, 2, 64), (5, 2, 16, 64)))
+    table, lens, off, st = i32([[0, 1]]), i32([0]), i32([0, 3]), zeros_status(1)
+    rope = ttv.rope_table(64)
+    attn = lambda q=q, kp=pool, vp=pool, t=table, lens=lens, off=off, st=st, **kw: ttv.tree_attn_paged(  # noqa: E731
+        q, kp, vp, t, lens, off, None, 0, st, **({"causal": True} | kw))
+    attn()
+    for wrong in (dict(q=q.float()), dict(vp=pool.float()), dict(st=st.long()), dict(lens=lens.cpu()), dict(kp=pool.half(), vp=pool.half()),
+                  dict(off=off.float())):
+        with pytest.raises(TypeError):
+            attn(**wrong)
+    for wrong in (dict(q=q[:, :, :32]), dict(q=q.transpose(0, 1)), dict(t=table[0]), dict(t=i32([[0, 1], [2, 3]])), dict(kp=pool[0]),
+                  dict(vp=pool[:4]), dict(causal=False), dict(parents=i32([0, 0, 0])), dict(o=q.float()), dict(off=i32([0])),
+                  dict(t=table.long())):
+        with pytest.raises(ValueError):
+            attn(**wrong)
+    with pytest.raises(ttv.SpecError):
+        attn(kp=pool[:, :, :12].contiguous(), vp=pool[:, :, :12].contiguous())
+    with pytest.raises(ValueError):
+        ttv.rope(q, ttv.RopeTable(rope.freqs[:5], 1.0, 64), lens, off, st)
+    with pytest.raises(TypeError):
+        ttv.rope(q, rope, lens, off, st, out=q.float())
+    with pytest.raises(ValueError):
+        ttv.rope(q, rope, lens, off, st, depth=i32([0]))
+    with pytest.raises(ttv.SpecError):
+        ttv.rope(q, ttv.rope_table(128), lens, off, st)
+    with pytest.raises(ttv.SpecError):                       # rows of the output on one another
+        ttv.rope(q, rope, lens, off, st, out=torch.zeros((4, 64), dtype=BF16, device="cuda").expand(3, 4, 64))
+    with pytest.raises(TypeError):
+        ttv.rope_write_paged(q, k.float(), k, pool, pool.clone(), table, lens, off, st, rope)
+    with pytest.raises(ValueError):
+        ttv.rope_write_paged(q, k[:, :1], k, pool, pool.clone(), table, lens, off, st, rope)
+    with pytest.raises(ValueError):
+        ttv.rope_write_paged(None, k, k, pool, pool.clone(), table, lens, off, st, rope, q_out=q)
+    with pytest.raises(ttv.SpecError):                       # the lengths may not be written where they are read
+        ttv.kv_compact_paged(pool, pool.clone(), table, lens, off, i32([[0, 1]]), i32([1]), st, new_prefix_lens=lens)
+    assert st.eq(0).all()

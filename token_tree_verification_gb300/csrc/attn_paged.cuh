@@ -164,7 +164,7 @@ __device__ __forceinline__ bool merge_splits(int tid, int CS, int split, int row
     }
     if (n > 0) {
       if (tid == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(CS * n * kStride * 4));
-      ok = mbar_await(bar, 0);
+      ok = mbar_wait(bar, 0);      // (every CTA sends, also after a time-out: none may leave before)
     }
     part0 = recv;
   } else {
