@@ -145,3 +145,21 @@ def test_the_oracle_attends_like_a_dense_one():
             w = np.exp(s) * see[i]
             assert np.allclose(got[i, h], w @ v[0, h // G, :L + n] / w.sum())
 
+
+
+def test_the_module_of_the_host_work(lib):
+    """Built and bound here too; without a GPU it leaves every call to binding.py."""
+    import torch
+    from token_tree_verification_gb300 import binding
+    assert binding._marshal is not None
+    x, one = torch.zeros((2, 3, 64)), torch.zeros(1, dtype=torch.int32)
+    assert binding._marshal.rope(x, None, one, one, one, None, False) is None
+    assert binding._marshal.kv_compact_paged(x, x, x, x, x, x, x, x) is None
+    assert binding._marshal.tree_attn_paged(*[None] * 12) is None
+    assert binding._marshal.rope_write_paged(1, 2) is None
+    with pytest.raises(TypeError):
+        binding._marshal.bind(1, 2, 3)
+    with pytest.raises(ValueError):
+        binding._marshal.bind(1, 2, 3, 0)
+    with pytest.raises(TypeError):
+        ttv.rope(x, None, one, one, one)

@@ -20,6 +20,10 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lib = None
+# The module of csrc/marshal.cpp once the library is loaded, where it was built:
+# the paged calls go through it, and it leaves what is not as it should be (it
+# then returns None) to the functions here.
+_marshal = None
 
 STATUS = {
     0: "SPEC_OK", -1: "SPEC_ERR_NULL", -2: "SPEC_ERR_SHAPE", -3: "SPEC_ERR_DTYPE",
@@ -109,7 +113,19 @@ def load():
     lib.spec_build_checked.argtypes = []
     lib.spec_build_checked.restype = I
     _lib = lib
+    _load_marshal(lib)
     return lib
+
+
+def _load_marshal(lib):
+    global _marshal
+    try:
+        from . import _marshal as module
+        module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (lib.spec_rope, lib.spec_rope_write_paged, lib.spec_tree_attn_paged,
+                                                        lib.spec_kv_compact_paged)))
+        _marshal = module
+    except ImportError:
+        _marshal = None
 
 
 def status_string(code: int) -> str:
@@ -581,6 +597,10 @@ def rope(x, table, start, offsets, status, depth=None, interleaved=False, out=No
     start[b] + t - offsets[b] without ``depth``.  ``out`` may be x (in place).
     Returns the rotated rows; a new tensor holds those of no request as they
     happen to be."""
+    if _marshal is not None and out is None and stream is None:
+        out = _marshal.rope(x, table, start, offsets, status, depth, interleaved)
+        if out is not None:
+            return out
     lib = _lib or load()
     index, dt = _current(x, "x"), _DTYPES.get(x.dtype)
     if dt is None:
@@ -616,6 +636,11 @@ def rope_write_paged(q, k, v, k_pages, v_pages, block_table, prefix_lens, offset
     own, k rotated and v copied to slots prefix_lens[b] and up of request b.
     Positions as in rope, from ``start`` or else prefix_lens on; without a
     ``table`` nothing is rotated.  Returns the rotated q."""
+    if _marshal is not None and q_out is None and stream is None:
+        q_out = _marshal.rope_write_paged(q, k, v, k_pages, v_pages, block_table, prefix_lens, offsets, status, table, depth,
+                                          start, interleaved)
+        if q_out is not None:
+            return q_out
     lib = _lib or load()
     B = status.numel()
     index, dt, pages, Hkv, size, D, width = _pool(k_pages, v_pages, block_table, B)
@@ -662,6 +687,11 @@ def tree_attn_paged(q, k_pages, v_pages, block_table, prefix_lens, offsets, mask
     ``causal`` (mask and parents None) request b's rows are a run of any
     number of tokens behind its prefix, each seeing all before it.  Rows of
     ``o`` behind the last request stay as they were."""
+    if _marshal is not None and o is None and stream is None:
+        o = _marshal.tree_attn_paged(q, k_pages, v_pages, block_table, prefix_lens, offsets, mask, max_prefix, status,
+                                     softmax_scale, parents, causal)
+        if o is not None:
+            return o
     lib = _lib or load()
     B = status.numel()
     index, dt, pages, Hkv, size, D, width = _pool(k_pages, v_pages, block_table, B)
@@ -701,6 +731,11 @@ def kv_compact_paged(k_pages, v_pages, block_table, prefix_lens, offsets, path_n
                      new_prefix_lens=None, stream=None):
     """kv_compact on a paged cache (in place).  Returns the new prefix lengths
     (device int32 [B])."""
+    if _marshal is not None and new_prefix_lens is None and stream is None:
+        new_prefix_lens = _marshal.kv_compact_paged(k_pages, v_pages, block_table, prefix_lens, offsets, path_nodes,
+                                                    accept_len, status)
+        if new_prefix_lens is not None:
+            return new_prefix_lens
     lib = _lib or load()
     B = status.numel()
     index, dt, pages, Hkv, size, D, width = _pool(k_pages, v_pages, block_table, B)

@@ -8,6 +8,10 @@ linked statically, so the library needs only the driver at run time.
 (``-DSPEC_CHECKED``, objects under ``_build/spec_tree_checked``, output
 ``libspec_tree_checked.so``); ``binding.load()`` opens it when the
 environment sets ``SPEC_TREE_CHECKED=1``.
+
+``csrc/marshal.cpp`` becomes the module ``_marshal`` beside them (g++, torch's
+headers): the paged calls' checks and launches from C++, which only saves
+host time.  Where it cannot be built, ``binding.py`` does that work.
 """
 from __future__ import annotations
 
@@ -15,6 +19,8 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -24,6 +30,34 @@ OUT_CHECKED = os.path.join(HERE, "libspec_tree_checked.so")
 BUILD_DIR_CHECKED = os.path.join(os.path.dirname(HERE), "_build", "spec_tree_checked")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
+
+
+OUT_MARSHAL = os.path.join(HERE, "_marshal.so")
+
+
+def build_marshal(force: bool = False) -> bool:
+    """Builds the module ``_marshal``; False (and a line on stderr) if that fails."""
+    src = os.path.join(CSRC, "marshal.cpp")
+    if not (force or _stale(OUT_MARSHAL, [src] + [h for h in _headers() if h.endswith("spec_tree.h")])):
+        return True
+    try:
+        import torch
+        root = os.path.dirname(torch.__file__)
+        cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+        inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+        lib = os.path.join(root, "lib")
+        tmp = OUT_MARSHAL + f".tmp{os.getpid()}"
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", *(f"-I{i}" for i in inc), src, "-o", tmp,
+               f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(r.stderr[-2000:])
+        os.replace(tmp, OUT_MARSHAL)
+        return True
+    except Exception as e:
+        print(f"_marshal was not built (calls take longer on the host): {e}", file=sys.stderr)
+        return False
 
 
 def _nvcc() -> str:
@@ -71,8 +105,10 @@ def build(force: bool = False, verbose: bool = False, checked: bool = False) -> 
                 print(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        marshal = ex.submit(build_marshal, force)
         list(ex.map(lambda p: compile_one(*p), zip(srcs, objs)))
+        marshal.result()
     if force or _stale(out, objs):
         tmp = out + f".tmp{os.getpid()}"
         cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
