@@ -442,8 +442,8 @@ int spec_kv4_compact(void *kv_cache, int B, int Hkv, int D, int S_cap, const int
  *                     about to be written); the others may hold anything.  A
  *                     request has max_pages * page_size slots, 2^31 - 4097 at
  *                     most.  A page may serve several requests (a shared
- *                     prefix) as long as no call writes to a slot that another
- *                     request uses
+ *                     prefix), or one request twice, as long as no call writes
+ *                     to a slot that is in use under another place
  * An entry outside [0, num_pages) among those that are read is
  * SPEC_ERR_PAGE, and the request's outputs stay as they were.
  */
@@ -556,8 +556,10 @@ int spec_rope_write_paged(const void *q, void *q_out, const void *k, const void 
  *                most 128, D 64 or 128, Hkv at most 65535, T x Hq below 2^31
  *   max_prefix   upper bound on every prefix_lens[b], sizes the key splits
  *                (a larger value is safe, only slower)
- * Slots at or behind L_b + n_b may hold anything, NaN included.  Rows of o at or
- * behind offsets[B] stay as they were.  A row that sees no key (possible only
+ * Slots at or behind L_b + n_b may hold anything, NaN included; so may the key of
+ * a slot in the eyes of a row that does not see it.  A value that is not finite
+ * may reach rows of its request that do not see its slot (as zero times it).
+ * Rows of o at or behind offsets[B] stay as they were.  A row that sees no key (possible only
  * with a mask that lacks the node itself) gets zeros.  Accumulation is fp32;
  * the bf16 path splits every softmax weight into a bf16 high part and a bf16
  * remainder (about 16 significant bits) and rounds o to bf16; SPEC_F32 computes
@@ -579,8 +581,8 @@ int spec_tree_attn_paged(const void *q, const void *k_pages, const void *v_pages
  * spec_kv_compact_paged — spec_kv_compact on a paged cache: the accepted
  * path's keys and values move behind the prefix, across pages where need be.
  * The block table stays as it is (pages behind the new prefix are the
- * caller's to reuse).  D is 64 or 128; new_prefix_lens must not be prefix_lens
- * itself (SPEC_ERR_SHAPE).  Errors on the device: those of spec_kv_compact, and
+ * caller's to reuse).  D is 64 or 128; new_prefix_lens must not overlap prefix_lens
+ * (SPEC_ERR_SHAPE).  Errors on the device: those of spec_kv_compact, and
  * SPEC_ERR_PAGE for the pages of the slots that move.
  */
 int spec_kv_compact_paged(void *k_pages, void *v_pages, int dtype, int B, int Hkv, int D,

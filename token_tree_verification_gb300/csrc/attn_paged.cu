@@ -151,7 +151,7 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
 
   if (warp == 0) touch_table(p, lane);
   const RowBlock w = find_block<kRows>(p, block, lane);
-  if (blockIdx.x == 0 && g_kv == 0 && warp == 3) report_bad_requests(p, lane);
+  if (g_kv == 0 && warp == 3) report_bad_requests(p, lane);
   if (w.b < 0) {       // the same for every CTA of the cluster
     if (warp == 1) {
       __syncwarp();

@@ -71,7 +71,7 @@ tree_attn_paged_f32_kernel(const PagedAttnArgs p, const int CS) {
   pdl_wait();
   if (tid < 32) touch_table(p, lane);
   const RowBlock w = find_block<R>(p, block, lane);
-  if (blockIdx.x == 0 && g_kv == 0 && tid < 32) report_bad_requests(p, lane);
+  if (g_kv == 0 && tid < 32) report_bad_requests(p, lane);
   if (w.b < 0) return;       // the same for every CTA of the cluster
   const int b = w.b, L = w.R.L;
   const int all = (w.keys + kKeys - 1) / kKeys, per = (all + CS - 1) / CS, t0 = split * per;
