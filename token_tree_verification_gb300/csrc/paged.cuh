@@ -24,13 +24,14 @@ struct PageTable {
 };
 
 // Whether one of the pages of slots [from, to) of request b lies outside the
-// pool; by one warp.
-__device__ __forceinline__ bool warp_finds_bad_page(const PageTable &p, int b, int from, int to, int lane) {
+// pool; by one warp, which looks at the `part`-th of `parts` shares of them.
+__device__ __forceinline__ bool warp_finds_bad_page(const PageTable &p, int b, int from, int to, int lane,
+                                                    int part = 0, int parts = 1) {
   if (to <= from) return false;
   const int end = static_cast<int>((static_cast<unsigned>(to) - 1u) >> p.shift) + 1;
   bool bad = false;
 #pragma unroll 8
-  for (int i = (from >> p.shift) + lane; i < end; i += 32) bad |= p.page(b, i) < 0;
+  for (int i = (from >> p.shift) + 32 * part + lane; i < end; i += 32 * parts) bad |= p.page(b, i) < 0;
   return __any_sync(0xffffffffu, bad);
 }
 

@@ -18,14 +18,15 @@
 // rows, so that what an item is (head, place, source, destination) is worked out
 // once, and rows differ by a stride, a slot and the angles, which one CTA computes
 // once for all heads.  (With an item worked out for every row and head the
-// instructions bound it: 112 us where this takes 101.)  The first rows' loads need
+// instructions bound it: 112 us where this takes 102.)  The first rows' loads need
 // no look-up and are issued in front of them: offsets, start and depth, page are a
 // chain of three loads.
 //
-// Memory bounds long runs: 50000 rows of 40 heads, D = 128, 1.05 GB in 164 us, 6.4
-// TB/s, 0.94 of a copy's rate; 14000 rows of 80 heads into pages of 64 slots, 583 MB
-// in 101 us, 5.8 TB/s.  A few tokens (2.9 us) and a 64-node tree of 96 heads (3.6
-// us) are the chain of loads.
+// Memory bounds long runs: 50000 rows of 40 heads, D = 128, 1.05 GB in 162 us, 6.5
+// TB/s, 0.95 of a copy's rate; 14000 rows of 80 heads into pages of 64 slots, 583 MB
+// in 102 us, 5.7 TB/s; single tokens of 4096 requests, 48 heads, 101 MB in 21 us, 4.8
+// TB/s.  A few tokens (2.9 us) and a 64-node tree of 96 heads (3.6 us) are the chain
+// of loads.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -36,9 +37,9 @@ namespace spec {
 
 namespace {
 
-constexpr int kMaxThreads = 384;
+constexpr int kMaxThreads = 192;
 constexpr int kMaxRows = 32;                 // of a CTA
-constexpr int kLong = 4;                     // rows of a thread whose loads are under way, along a run
+constexpr int kLong = 2;                     // rows of a thread whose loads are under way, along a run
 constexpr int kRun = 8;                      // rows of a run
 constexpr int kAngleBytes = 32 * 1024;
 
@@ -163,7 +164,7 @@ __device__ __forceinline__ Item item_at(const RopeArgs &a, int i) {
 }
 
 template <typename E, bool kVec, bool kInter, int kAhead>
-__global__ void __launch_bounds__(kMaxThreads, kAhead == 1 ? 1 : 3)
+__global__ void __launch_bounds__(kMaxThreads, kAhead == 1 ? 1 : 6)
 rope_kernel(const RopeArgs a) {
   extern __shared__ __align__(16) float s_angle[];     // [rows][cosines, sines][r / 2]
   __shared__ int s_ok[kMaxRows], s_pos[kMaxRows];
@@ -196,20 +197,18 @@ rope_kernel(const RopeArgs a) {
   for (int u = 0; u < kAhead; ++u) load(u, sub + u * a.side);
 
   // ---- each row's request, position and slot, by a warp
+  bool none = false;      // no row is to be written
   for (int row = warp; row < rows; row += threads / 32) {
     const int t = t0 + row;
     const int b = warp_find_request(a.offsets, a.B, t, lane);
     bool ok = b >= 0;
     long long slot_at = 0;
-    int position = 0;
+    int position = 0, depth = 0;
     if (ok) {
       const RowRange R = row_range(a.offsets, b, a.T);
-      const int start = __ldg(a.start + b), depth = a.depth ? __ldg(a.depth + t) : t - R.lo;
+      const int start = __ldg(a.start + b);
+      depth = a.depth ? __ldg(a.depth + t) : t - R.lo;
       ok = !R.err && t >= R.lo && start >= 0;
-      if (ok && depth < 0) {
-        if (lane == 0) report(a.status, b, SPEC_ERR_PREFIX_RANGE);
-        ok = false;
-      }
       position = static_cast<int>(static_cast<unsigned>(start) + static_cast<unsigned>(depth));
       if (ok && a.v.x) {
         const int L = __ldg(a.slots + b);
@@ -217,14 +216,22 @@ rope_kernel(const RopeArgs a) {
         if (ok) {
           const int slot = L + t - R.lo;
           const int page = a.pages.page(b, slot >> a.pages.shift);
-          if (warp_finds_bad_page(a.pages, b, L, L + R.n, lane)) {
+          // rows that are all of one request share its pages out (65536 rows of 12 heads
+          // into pages of 8: 145 us; with all of them looked at for every row 247)
+          const bool alone = R.lo <= t0 && R.lo + R.n >= t0 + rows;
+          if (warp_finds_bad_page(a.pages, b, L, L + R.n, lane, alone ? row : 0, alone ? rows : 1) || page < 0) {
             if (lane == 0) report(a.status, b, SPEC_ERR_PAGE);
             ok = false;
+            none |= alone;
           }
           const int size = 1 << a.pages.shift;
           slot_at = ((static_cast<long long>(page) * a.Hkv << a.pages.shift) + (slot & (size - 1))) * a.D;
         }
       }
+    }
+    if (ok && depth < 0) {
+      if (lane == 0) report(a.status, b, SPEC_ERR_PREFIX_RANGE);
+      ok = false;
     }
     if (lane == 0) {
       s_ok[row] = ok;
@@ -245,7 +252,7 @@ rope_kernel(const RopeArgs a) {
       if (err) report(a.status, b, err);
     }
   }
-  __syncthreads();
+  if (__syncthreads_or(none)) return;
   for (int p = tid; p < rows * pairs; p += threads) {
     const int row = p / pairs, at = p - row * pairs;
     const unsigned long long turns =
@@ -314,10 +321,14 @@ rope_kernel(const RopeArgs a) {
 }
 
 // An item a thread, a row's items in as few CTAs as take them in kMaxThreads, or
-// several rows side by side where a row has few; and rows in a run up to kRun (32
-// side by side) while that leaves sixteen CTAs an SM.  (Runs of 4, 8, 16 and 32 rows:
-// 160, 164, 177 and 190 us for the 50000 rows above, 109, 101, 111 and 124 for the
-// rows into pages; two loads ahead in place of four, 48 warps an SM: 160 and 104.)
+// several rows side by side where a row has few; and rows in a run up to kRun (32 in
+// all) while that leaves sixteen CTAs an SM.  Device us for the 50000 rows, the 14000,
+// the 4096 above and a run of 8192 rows of 48 heads:
+//   192 threads, 2 rows ahead of the stores, runs of 8 and 6: 162, 102, 21, 36
+//   runs of 16 and 4: 169, 111, 21, 36 and 164, 103, 21, 38
+//   192 threads, 3 rows ahead: 165, 105, 22, 38
+//   256 threads, 2 ahead: 168, 106, 22, 37; 320 threads, 2 ahead: 167, 100, 22, 37
+//   384 threads, 4 ahead: 165, 101, 50, 43 (its registers spill, or do not, at a touch)
 // A single row a thread takes no registers for a run: 3.6 in place of 4.4 us for the
 // tree.
 template <typename E, bool kVec, bool kInter>
@@ -339,7 +350,7 @@ int launch(RopeArgs &a, void *stream) {
   if (a.span < 128) {
     a.side = 128 / a.span < a.T ? 128 / a.span : a.T;
     if (a.side > 16) a.side = 16;
-    most = kMaxRows;
+    most = kRun * a.side < kMaxRows ? kRun * a.side : kMaxRows;
   }
   a.rows = runs < a.side ? a.side : runs < most ? static_cast<int>(runs) : most;
   if (a.rows > a.side) a.rows -= a.rows % a.side;
@@ -377,7 +388,7 @@ int launch_by_form(RopeArgs &a, bool interleaved, void *stream) {
 // What both calls ask of the rotation and of the rows.
 int check(int dtype, int B, int T, int D, const void *freqs, int r, float scale) {
   if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_DTYPE;
-  if (B < 1 || T < 0 || D < 8 || D > 512 || D % 8 || r < 0 || r > D || r % 2 || !(fabsf(scale) < INFINITY))
+  if (B < 1 || T < 0 || T > 0x7FFFFFFF - kMaxRows || D < 8 || D > 512 || D % 8 || r < 0 || r > D || r % 2 || !(fabsf(scale) < INFINITY))
     return SPEC_ERR_SHAPE;
   if (r > 0 && !freqs) return SPEC_ERR_NULL;
   if (reinterpret_cast<uintptr_t>(freqs) & 7) return SPEC_ERR_ALIGNMENT;
