@@ -272,6 +272,47 @@ def test_rows_into_pages_errors(gpu_lib):
     assert status == [0, 0, 0]
 
 
+@pytest.mark.parametrize("n", [[3000, 40], [4, 3, 5, 1, 8, 2], [70, 1, 600]])
+def test_every_page_of_a_run_is_looked_at(gpu_lib, n):
+    """A page that is not there, anywhere in a run, keeps every row of the run from being written; a wrong
+    depth beside it changes nothing."""
+    rng = np.random.default_rng(sum(n))
+    P, D, B = 8, 64, len(n)
+    L = [3] * B
+    off = np.concatenate([[0], np.cumsum(n)])
+    T = int(off[-1])
+    q, k, v = (torch.randn((T, h, D), device="cuda") for h in (2, 1, 1))
+    rope = ttv.rope_table(64)
+    depth = np.concatenate([np.arange(m) for m in n])
+    kept = Cache(rng, [a + b for a, b in zip(n, L)], 1, P, D, F32, fill=5.0)
+
+    def call(table, depth):
+        cache = [torch.full_like(kept.k, 5.0) for _ in range(2)]
+        out, status = torch.full_like(q, 7.0), zeros_status(B)
+        ttv.rope_write_paged(q, k, v, *cache, i32(table), i32(L), i32(off), status, rope, depth=i32(depth), q_out=out)
+        return status.tolist(), out, cache
+
+    status, good, written = call(kept.table, depth)
+    assert status == [0] * B
+    for b in range(B):
+        last = (n[b] + L[b] - 1) // P
+        for page in sorted({0, last, last // 2, last // 3, max(0, last - 1)}):
+            for row in (None, 0, n[b] // 2, n[b] - 1):
+                table, deep = kept.table.copy(), depth.copy()
+                table[b, page] = -1 if page % 2 else kept.total
+                if row is not None:
+                    deep[off[b] + row] = -1
+                status, out, cache = call(table, deep)
+                assert status[b] in ((-14,) if row is None else (-14, -10)) and sum(map(bool, status)) == 1
+                assert out[off[b]:off[b + 1]].eq(7).all()
+                for x, y in zip(cache, written):
+                    mine = torch.from_numpy(kept.table[b][:last + 1]).cuda()
+                    assert x[mine].eq(5).all()
+                    for other in set(range(B)) - {b}:
+                        theirs = torch.from_numpy(kept.table[other][kept.table[other] >= 0]).cuda()
+                        assert torch.equal(x[theirs], y[theirs])
+
+
 # ------------------------------------------------------------------ attention
 def attn_bound(o, size, big, count, D, dtype):
     """Scores: D products summed in fp32, the scale; weights: the exponential's
@@ -365,6 +406,34 @@ def test_many_requests_among_them_empty_ones(gpu_lib):
     o = ttv.tree_attn_paged(q, cache.k, cache.v, cache.block_table, i32(L), i32(off), None, 70, status, causal=True)
     assert status.eq(0).all()
     check_attn(o, q, cache, L, off)
+
+
+@DTYPES
+@pytest.mark.parametrize("B,causal", [(64, False), (65, False), (65, True), (1100, False), (1100, True)])
+def test_hundreds_of_requests(gpu_lib, dtype, B, causal):
+    """Runs that fill blocks of rows exactly (32 x 4), end inside one or are empty; some are wrong."""
+    rng = np.random.default_rng(B + causal)
+    n = rng.choice([0, 1, 4, 5, 32, 33] if causal else [1, 4, 5, 32, 33], B)
+    n[[0, 7, B - 1]] = 96, 128, 32
+    L = rng.integers(0, 40, B)
+    q, cache, off = batch(rng, n.tolist(), L.tolist(), 4, 1, 8, 64, dtype, extra=200)
+    parents = np.concatenate([random_tree(rng, k) for k in n] + [np.full(200, -1)])
+    T, wrong_page, wrong_prefix = int(off[-1]), 7, B - 2
+    table, lens = cache.table.copy(), L.copy()
+    table[wrong_page, -(-(n[7] + L[7]) // 8) - 1] = cache.total
+    lens[wrong_prefix] = -1
+    for split in (70, 100000):
+        status, o = zeros_status(B), torch.full_like(q, 7.0)
+        ttv.tree_attn_paged(q, cache.k, cache.v, i32(table), i32(lens), i32(off), None, split, status, o=o, causal=causal,
+                            parents=None if causal else i32(parents))
+        assert np.flatnonzero(status.cpu().numpy()).tolist() == [wrong_page, wrong_prefix]
+        assert status[wrong_page] == -14 and status[wrong_prefix] == -10
+        left = np.zeros(T + 200, dtype=bool)
+        left[T:] = True
+        for b in (wrong_page, wrong_prefix):
+            left[off[b]:off[b + 1]] = True
+        assert o[torch.from_numpy(left).cuda()].eq(7).all()
+        check_attn(o, q, cache, L, off, None if causal else parents, rows=np.flatnonzero(~left[:T]))
 
 
 @DTYPES

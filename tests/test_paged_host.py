@@ -114,6 +114,18 @@ def test_moves_within_pages_are_refused(lib):
                 dict(width=0), dict(new=FAKE)):
         assert move(**bad) == -2, bad
 
+def test_lengths_that_overlap_are_refused(lib):
+    def move(old, new, B):
+        return lib.spec_kv_compact_paged(FAKE, FAKE, 1, B, 2, 64, 10, 16, FAKE, 4, P(old), FAKE, FAKE, FAKE, 4, P(new), FAKE, None)
+    for old, new, B in ((0x2000, 0x2004, 2), (0x2004, 0x2000, 2), (0x2000, 0x2000 + 4 * 99, 100)):
+        assert move(old, new, B) == -2
+
+
+def test_rows_beyond_the_grid_are_refused(lib):
+    assert lib.spec_rope(FAKE, FAKE, 1, 1, 2 ** 31 - 1, 1, 8, I64(8), I64(8), I64(8), I64(8), FAKE, 8, F32(1.0), 0, FAKE, None,
+                         FAKE, FAKE, None) == -2
+
+
 def test_the_oracle_rotates_whole_and_quarter_turns():
     """Positions of quarter turns, by hand."""
     x = np.array([[[1.0, 2.0, 3.0, 4.0]]])

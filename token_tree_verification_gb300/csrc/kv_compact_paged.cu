@@ -108,7 +108,7 @@ extern "C" int spec_kv_compact_paged(void *k_pages, void *v_pages, int dtype, in
   if (rc != SPEC_OK) return rc;
   // (the CTAs of a request read its length while one of them writes the new one)
   if (B < 1 || B > 65535 || Hkv < 1 || (D != 64 && D != 128) || max_depth_plus1 < 1 ||
-      max_depth_plus1 > SPEC_MAX_TREE_NODES || new_prefix_lens == prefix_lens)
+      max_depth_plus1 > SPEC_MAX_TREE_NODES || (new_prefix_lens < prefix_lens + B && prefix_lens < new_prefix_lens + B))
     return SPEC_ERR_SHAPE;
   if ((reinterpret_cast<uintptr_t>(k_pages) | reinterpret_cast<uintptr_t>(v_pages)) & 15) return SPEC_ERR_ALIGNMENT;
   a.k = static_cast<uint8_t *>(k_pages);
