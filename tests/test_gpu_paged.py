@@ -436,6 +436,81 @@ def test_hundreds_of_requests(gpu_lib, dtype, B, causal):
         check_attn(o, q, cache, L, off, None if causal else parents, rows=np.flatnonzero(~left[:T]))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("form", ["mask", "parents", "causal"])
+def test_many_requests_behind_few_keys(gpu_lib, form, D):
+    """More blocks of rows than SMs, a few tiles of keys each."""
+    rng = np.random.default_rng(D + len(form))
+    B, causal = 150, form == "causal"
+    n = rng.choice([0, 1, 40, 130] if causal else [1, 2, 31, 64, 70], B)
+    L = rng.choice([0, 1, 63, 64, 127, 128, 129, 200, 383, 512], B)
+    q, cache, off = batch(rng, n.tolist(), L.tolist(), 16, 8, 16, D, BF16, extra=5)
+    T = int(off[-1])
+    parents = None if causal else np.concatenate([random_tree(rng, k) for k in n] + [[-1] * 5])
+    status, o, mask = zeros_status(B), torch.full_like(q, 7.0), None
+    if form == "mask":
+        mask = ttv.build_tree_mask(i32(parents[:T]), i32(off), status)[0]
+        mask = torch.cat([mask, mask[:1].expand(5, 4)])
+    ttv.tree_attn_paged(q, cache.k, cache.v, cache.block_table, i32(L), i32(off), mask, 512, status, o=o, causal=causal,
+                        parents=i32(parents) if form == "parents" else None)
+    assert status.eq(0).all() and o[T:].eq(7).all()
+    check_attn(o, q, cache, L, off, parents)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("size", [0.01, 6.0, 40.0])
+def test_scores_of_every_size_of_many_requests(gpu_lib, size, D):
+    rng = np.random.default_rng(5)
+    B = 160
+    n, L = [2] * B, rng.integers(300, 500, B).tolist()
+    q, cache, off = batch(rng, n, L, 8, 8, 64, D, BF16, size=size)
+    status = zeros_status(B)
+    o = ttv.tree_attn_paged(q, cache.k, cache.v, cache.block_table, i32(L), i32(off), None, 500, status, causal=True)
+    assert status.eq(0).all()
+    check_attn(o, q, cache, L, off)
+
+
+def test_calls_of_both_kinds_in_turn(gpu_lib):
+    """Launches for many requests and for one long one, and the dense call, each of which may begin while the
+    one before it ends; on two streams, captured and not."""
+    rng = np.random.default_rng(6)
+    B, D, H = 150, 128, 8
+    n, L = [2] * B, rng.integers(50, 300, B).tolist()
+    many = batch(rng, n, L, H, H, 16, D, BF16)
+    one = batch(rng, [64], [1500], H, H, 16, D, BF16)
+    parents = i32(random_tree(rng, 64))
+    dense = [torch.randn((1, H, 600, D), device="cuda").to(BF16) for _ in range(2)]
+    lens, offs, s1, s2 = i32(L), i32(many[2]), zeros_status(B), zeros_status(1)
+    tables = many[1].block_table, one[1].block_table
+    other = i32([1500]), i32([0, 64]), i32([500])
+
+    def calls():
+        out = []
+        for _ in range(3):
+            out.append(ttv.tree_attn_paged(many[0], many[1].k, many[1].v, tables[0], lens, offs, None, 300, s1, causal=True))
+            out.append(ttv.tree_attn_paged(one[0], one[1].k, one[1].v, tables[1], other[0], other[1], None, 1500, s2,
+                                           parents=parents))
+            out.append(ttv.tree_attn(one[0], *dense, other[2], other[1], None, 500, s2, parents=parents))
+            out.append(ttv.tree_attn_paged(many[0], many[1].k, many[1].v, tables[0], lens, offs, None, 300, s1, causal=True))
+        return out
+
+    want = calls()
+    check_attn(want[0], many[0], many[1], L, many[2])
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = calls()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        with torch.cuda.stream(side):
+            beside = calls()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b, c in zip(want, beside, captured):
+            assert torch.equal(a, b) and torch.equal(a, c)
+    assert s1.eq(0).all() and s2.eq(0).all()
+
+
 @DTYPES
 def test_scores_of_every_size(gpu_lib, dtype):
     """Scores that rise along the keys by far more than a reference's slack, negative ones,

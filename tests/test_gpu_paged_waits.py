@@ -82,3 +82,30 @@ def test_waits_that_run_out_end_the_call(libs, polls, form, D):
             assert (same | ((got == 9.0).all(-1) & (code != 0))).all()
     st = zeros_status(3)
     assert torch.equal(call(st), ref) and st.tolist() == [0, 0, 0]
+
+
+@pytest.mark.parametrize("polls", POLLS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_waits_that_run_out_in_launches_for_many_requests(libs, polls, D):
+    rng = np.random.default_rng(7)
+    B = 150
+    n, L = rng.integers(1, 9, B).tolist(), rng.integers(0, 300, B).tolist()
+    q, cache, off = batch(rng, n, L, 4, 2, 16, D, BF16)
+    lens, offs, table = i32(L), i32(off), cache.block_table
+    call = lambda st: ttv.tree_attn_paged(q, cache.k, cache.v, table, lens, offs, None, 300, st, causal=True)  # noqa: E731
+    ref = call(zeros_status(B))
+    for _ in range(3):
+        o, st = torch.full_like(ref, 9.0), zeros_status(B)
+        rc = libs[polls](q.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(), o.data_ptr(), 1, B, int(off[-1]), 4, 2, D,
+                         cache.total, 16, table.data_ptr(), table.shape[1], 300, lens.data_ptr(), offs.data_ptr(), None, None, 1,
+                         0.0, st.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        torch.cuda.synchronize()
+        codes = st.tolist()
+        assert all(c in (0, SPEC_ERR_TIMEOUT) for c in codes)
+        for b, code in enumerate(codes):
+            assert polls > 0 or code == SPEC_ERR_TIMEOUT
+            got, want = o[off[b]:off[b + 1]], ref[off[b]:off[b + 1]]
+            assert ((got == want).all(-1) | ((got == 9.0).all(-1) & (code != 0))).all()
+    st = zeros_status(B)
+    assert torch.equal(call(st), ref) and st.eq(0).all()

@@ -23,6 +23,11 @@
 //   warp 2      issues O += P_u V_u
 //   warps 4-11  softmax, in two groups that take the halves in turn; a thread
 //               has a row (a TMEM lane) and the 64 keys of a half
+// That is the whole form, which has an SM to itself.  A launch of many blocks with
+// few keys each is set-up for the most part (offsets, page, keys: three loads one
+// behind the other; output), and takes the small form: half an SM, one softmax group,
+// one tile of keys and one of values, so that a CTA's set-up hides behind another's
+// tiles.  launch_bf16 says which and what both take.
 // TMEM holds the scores of five halves, and P takes the place of S, so that the
 // products of one half run beside the softmax of two others.  A row's reference
 // is shared by the groups, which decide on it in the order of the halves (a
@@ -35,6 +40,16 @@
 // lost unless the other issuing warp fills it.  Hence two of them; one that issued
 // both kinds took 2750 cycles a tile in place of 1900, 2350 with the tests placed
 // between its products.
+//
+// Measured, device times: 128-node trees of 4 requests, 64 heads on 8, behind 8192
+// keys: 141 us, 0.98 PFLOP/s and with the remainders' products 1.46; the tensor pipe
+// is busy for 0.79 of it, and of its two waves of CTAs the second is part full.  A
+// chunk of 2048 tokens behind 16384, 64 heads on 8: 1.0 ms, 1.17 PFLOP/s, with the
+// remainders' 1.75, near what a library product sustains.  6-node chains of 8
+// requests, 32 heads, behind 26000 to 32768 keys: 563 us, 7.0 TB/s, a copy's rate.
+// One token of 4 requests behind 8192 keys, 64 heads on 8: 27 us, 5 TB/s; 64-node
+// tree, 32 heads, behind 2048: 14.9 us, of them 2.5 to the first key tile, 7 of tiles
+// and 4 of output and merge.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -47,12 +62,7 @@ namespace {
 
 constexpr int kRows = 128;
 constexpr int kSoftFirst = 4;         // warps: issuers and the page check, then the softmax
-constexpr int kGroups = 2;            // of four softmax warps
-constexpr int kSoftWarps = 4 * kGroups;
-constexpr int kSoftThreads = 32 * kSoftWarps;
-constexpr int kThreads = 32 * (kSoftFirst + kSoftWarps);
 constexpr int kHalf = kTile / 2;      // keys of a product, and of one softmax thread
-constexpr int kBufs = 5;              // halves' scores and weights in TMEM
 constexpr float kPass = 8.f;          // powers of two by which a score may pass its row's reference
 
 // A wait that is over already, most often.
@@ -60,20 +70,28 @@ __device__ __forceinline__ bool mbar_now(uint64_t *bar, uint32_t parity) {
   return mbar_over(smem_addr(bar), parity) || mbar_sleep(smem_addr(bar), parity);
 }
 
-template <int D>
+// The whole form has an SM to itself; the small one (kSmall) half of it: one softmax
+// group, a stage of keys and of values, half of TMEM, and no splits.
+template <int D, bool kSmall>
 struct PagedCfg {
+  static constexpr int kGroups = kSmall ? 1 : 2;            // of four softmax warps
+  static constexpr int kSoftThreads = 128 * kGroups;
+  static constexpr int kThreads = 32 * kSoftFirst + kSoftThreads;
+  static constexpr int kCtas = kSmall ? 2 : 1;              // of an SM
+  static constexpr int kBufs = kSmall ? (D == 128 ? 1 : 2) : 5;       // halves' scores and weights in TMEM
   static constexpr int kBoxes = D / 64;
   static constexpr int kBoxBytes = kTile * 128;             // 128 slots of 64 dims
   static constexpr int kTileBytes = kBoxes * kBoxBytes;
-  static constexpr int kStages = D == 128 ? 3 : 6;          // of keys, and as many of values
+  static constexpr int kStages = (kSmall ? 1 : 3) * 128 / D;      // of keys, and as many of values
   static constexpr int kOffK = 0, kOffV = kStages * kTileBytes;
-  static constexpr int kEnd = 2 * kStages * kTileBytes;
-  static_assert(merge_bytes<D>(kRows) <= kEnd, "the rows take the rings' place after the loop");
-  static constexpr int kSmem = kEnd + 1024;
+  static constexpr int kRings = 2 * kStages * kTileBytes, kMerge = kSmall ? kRows * (D + 4) * 4 : merge_bytes<D>(kRows);
+  // (the rows take the rings' place after the loop)
+  static constexpr int kSmem = (kRings > kMerge ? kRings : kMerge) + 1024;
   // TMEM: the halves' S, and P in their place (a pair of keys per column, remainders
   // behind the high parts), Q (a pair of dims), O
-  static constexpr uint32_t kColQ = kBufs * kHalf, kColO = kColQ + 64, kTmemCols = 512;
-  static_assert(kSmem <= 227 * 1024 - 8192, "shared memory budget");
+  static constexpr uint32_t kColQ = kBufs * kHalf, kColO = kColQ + 64, kTmemCols = 512 / kCtas;
+  static_assert(kColO + D <= kTmemCols, "tensor memory");
+  static_assert(kCtas * (kSmem + 8192) <= 227 * 1024, "shared memory budget");
 };
 
 // What rounding to bf16 took from y0 and y1 (`top` holds the two, y0's low), exactly.
@@ -85,12 +103,13 @@ __device__ __forceinline__ void minus_bf16x2(float y0, float y1, uint32_t top, f
       : "r"(top), "f"(y0), "f"(y1));
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, bool kSmall>
+__global__ void __launch_bounds__(PagedCfg<D, kSmall>::kThreads, PagedCfg<D, kSmall>::kCtas)
 tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMap tmk,
-                       const __grid_constant__ CUtensorMap tmv, const int CS) {
-  using C = PagedCfg<D>;
-  constexpr int NS = C::kStages;
+                       const __grid_constant__ CUtensorMap tmv, const int splits) {
+  using C = PagedCfg<D, kSmall>;
+  constexpr int NS = C::kStages, kGroups = C::kGroups, kBufs = C::kBufs, kSoftThreads = C::kSoftThreads;
+  const int CS = kSmall ? 1 : splits;
   const AttnArgs &a = p.a;
   extern __shared__ uint8_t smem_raw[];
   __shared__ struct {
@@ -113,7 +132,7 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
   auto uniform = [](auto x) { return __shfl_sync(0xffffffffu, x, 0); };
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
-  pdl_trigger();
+  if (!kSmall) pdl_trigger();
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&bars.k_full[s], 1);
@@ -121,7 +140,7 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
       mbar_init(&bars.v_full[s], 1);
       mbar_init(&bars.v_empty[s], 1);
     }
-    mbar_init(&bars.q_full, 8);
+    mbar_init(&bars.q_full, 4 * kGroups);
     for (int s = 0; s < kBufs; ++s) {
       mbar_init(&bars.s_full[s], 1);
       mbar_init(&bars.p_full[s], 4);
@@ -139,6 +158,10 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
     tma_prefetch_desc(&tmk);
     tma_prefetch_desc(&tmv);
   }
+  // The small form leaves room for CTAs of the launches before and after: it must
+  // take its TMEM neither before those in front have done with theirs, nor after
+  // those behind, which would wait for it with TMEM in hand.
+  if (kSmall) pdl_wait();
   if (warp == 1) {
     tc::tmem_alloc(&s_tmem, C::kTmemCols);
     tc::tmem_relinquish();
@@ -147,7 +170,8 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = uniform(s_tmem);
-  pdl_wait();
+  if (kSmall) pdl_trigger();
+  else pdl_wait();
 
   if (warp == 0) touch_table(p, lane);
   const RowBlock w = find_block<kRows>(p, block, lane);
@@ -268,30 +292,31 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
     uint32_t round = group > 0 ? 0 : 1;      // of the one before, for the group's next half
     const bool busy = quad * 32 < w.rows;              // (a quarter without rows only keeps the barriers going)
     const bool live = row < w.rows;
-    // ---- Q: this thread's row, half of its dims (two groups' work)
+    // ---- Q: this thread's row, its group's share of the dims
+    constexpr int kDims = D / kGroups;
     const int node = (w.row0 + row) / a.G;
     const bool mine = live && in_bounds(w.R.lo + node, a.T, a.status, b);
     const long long first =
         (static_cast<long long>(w.R.lo + node) * a.Hq + g_kv * a.G + (w.row0 + row) - node * a.G) * D;
     const uint4 *src =
-        reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + first + group * (D / 2));
+        reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + first + group * kDims);
     uint4 m = make_uint4(0u, 0u, 0u, 0u);
     if (a.mask && mine) m = clip_mask(__ldg(a.mask + w.R.lo + node), w.R.n);
-    if (busy && group < 2) {
-      uint4 x4[D / 16];
+    if (busy) {
+      uint4 x4[kDims / 8];
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) x4[c] = mine ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+      for (int c = 0; c < kDims / 8; ++c) x4[c] = mine ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int q = 0; q < D / 32; ++q) {
+      for (int q = 0; q < kDims / 16; ++q) {
         const uint4 x = x4[2 * q], y = x4[2 * q + 1];
         const uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        tc::st8(trow + C::kColQ + group * (D / 4) + 8 * q, u);
+        tc::st8(trow + C::kColQ + group * (kDims / 2) + 8 * q, u);
       }
       tc::wait_st();
     }
     tc::fence_before_sync();
     __syncwarp();
-    if (lane == 0 && group < 2) mbar_arrive_at(smem_addr(&bars.q_full));
+    if (lane == 0) mbar_arrive_at(smem_addr(&bars.q_full));
     if (group == 0) s_row[row] = mine ? first : -1;
     // ---- what this thread's row sees
     if (a.parents) {
@@ -454,18 +479,18 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
     s_part[group][row] = sum;
     if (!ok) s_timeout = 1;
     named_bar_sync(1, kSoftThreads);
-    if (busy && group < 2 && s_timeout == 0) {
+    if (busy && s_timeout == 0) {
       float *staged = reinterpret_cast<float *>(smem) + row * (D + 4);
       if (group == 0) {
         for (int q = 1; q < kGroups; ++q) sum += s_part[q][row];
         *reinterpret_cast<float2 *>(staged + D) = make_float2(now, sum);
       }
-      const uint32_t so = smem_addr(staged + group * (D / 2));
+      const uint32_t so = smem_addr(staged + group * kDims);
 #pragma unroll
-      for (int j = 0; j < D / 2; j += 32) {
+      for (int j = 0; j < kDims; j += 32) {
         float o[32] = {};
         if (halves > 0) {
-          tc::ld32(trow + C::kColO + group * (D / 2) + j, o);
+          tc::ld32(trow + C::kColO + group * kDims + j, o);
           tc::wait_ld();
         }
 #pragma unroll
@@ -504,7 +529,7 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
   float *so = reinterpret_cast<float *>(smem);
   if ((timed_out || bad_page) && tid < kRows) so[tid * (D + 4) + D + 1] = -1.f;
   auto out_row = [&](int r) { return s_row[r] < 0 ? nullptr : static_cast<__nv_bfloat16 *>(a.o) + s_row[r]; };
-  if (!merge_splits<D, kThreads, __nv_bfloat16>(tid, CS, split, w.rows, so, &bars.merge, out_row) && tid == 0)
+  if (!merge_splits<D, C::kThreads, __nv_bfloat16>(tid, CS, split, w.rows, so, &bars.merge, out_row) && tid == 0)
     report(a.status, b, SPEC_ERR_TIMEOUT);
 }
 
@@ -543,14 +568,20 @@ bool encode_pool(CUtensorMap *m, const void *base, const PageTable &pages, int H
 }
 
 // As many splits of the keys (a cluster) as make waves x (tiles of a CTA + its
-// set-up, first tile and merge, which grows with the rows, in half tiles) least.
+// set-up, first tile and merge, which grows with the rows, in half tiles) least; or
+// the small form, whose tiles, two CTAs side by side, cost 5 half tiles (3 at D = 64).
 // (Device us by splits 1, 2, 3, 4, 5 and 8: 32 rows of 8 heads behind 500 keys 9.5,
 // 9.1, 8.1, 8.1, 7.5 and 7.6; 128 rows of 32 heads behind 300 12.3, 13.2, 13.2, 13.5;
-// one token x 4 x 8 heads behind 8192 58, 34, 26.9, 26.2, 39 and 45.)
+// one token x 4 x 8 heads behind 8192 58, 34, 26.9, 26.2, 39 and 45.  Whole and small
+// form, 8 heads of 4 query heads each: a token of 256 requests behind 60, 500, 1000 and
+// 1500 keys 77 and 37, 144 and 121, 215 and 208, 283 and 296; at D = 64 72 and 34, 118
+// and 71, 163 and 108, 210 and 147; of 16 requests behind 200, 7.5 and 10.1; prompts of
+// 512 tokens x 8, 80 and 57.  The occupancy calculator says one CTA an SM for the small
+// form; two run: 128 units behind 200 keys take 10.1 us, 256 take 10.9.)
 template <int D>
 int launch_bf16(const PagedAttnArgs &p, int max_prefix, void *stream) {
-  using C = PagedCfg<D>;
-  auto kernel = tree_attn_paged_kernel<D>;
+  using C = PagedCfg<D, false>;
+  auto kernel = tree_attn_paged_kernel<D, false>;
   static KernelState state;
   const int dev = current_device();
   if (dev < 0 || !allow_clusters(kernel, C::kSmem, dev, &state)) return SPEC_ERR_CUDA;
@@ -560,12 +591,13 @@ int launch_bf16(const PagedAttnArgs &p, int max_prefix, void *stream) {
   const long long blocks = most_blocks<kRows>(p.a), units = likely_blocks<kRows>(p.a) * p.a.Hkv;
   const long long keys = static_cast<long long>(max_prefix) + mean_nodes(p.a);
   const long long tiles = (keys + kTile - 1) / kTile;
+  const long long mean_tiles = (keys - (p.causal ? mean_nodes(p.a) / 2 : 0) + kTile - 1) / kTile;
   const long long rows = static_cast<long long>(mean_nodes(p.a)) * p.a.G, merge = 2 + (rows < kRows ? rows : kRows) / 32;
   int cs = 1;
   long long best = -1;
   for (int n = 1; n <= kMaxSplits; n = n == 8 ? kMaxSplits : n + 1) {
     if (n > 1 && tiles < n) break;
-    const int slots = clusters_at_once(kernel, n, kThreads, C::kSmem, dev, &state);
+    const int slots = clusters_at_once(kernel, n, C::kThreads, C::kSmem, dev, &state);
     if (slots < 1) continue;
     const long long waves = (units + slots - 1) / slots;
     const long long cost = waves * (2 * ((tiles + n - 1) / n) + 8 + (n > 1 ? merge : 0));
@@ -575,12 +607,21 @@ int launch_bf16(const PagedAttnArgs &p, int max_prefix, void *stream) {
     }
   }
   if (blocks * cs > 0x7FFFFFFFll) return SPEC_ERR_SHAPE;
+  using S = PagedCfg<D, true>;
+  auto small_kernel = tree_attn_paged_kernel<D, true>;
+  static KernelState small_state;
+  const long long small_waves = (units + S::kCtas * sm_count() - 1) / (S::kCtas * sm_count());
+  const bool small = small_waves * (D == 128 ? 5 * mean_tiles + 6 : 3 * mean_tiles + 7) < best;
+  if (small) {
+    if (!allow_dynamic_smem(small_kernel, S::kSmem, small_state.granted)) return SPEC_ERR_CUDA;
+    cs = 1;
+  }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  cluster_config(cfg, attr, cs, kThreads, C::kSmem);
+  cluster_config(cfg, attr, cs, small ? S::kThreads : C::kThreads, small ? S::kSmem : C::kSmem);
   cfg.gridDim = dim3(static_cast<unsigned>(blocks * cs), static_cast<unsigned>(p.a.Hkv), 1);
   cfg.stream = static_cast<cudaStream_t>(stream);
-  return cudaLaunchKernelEx(&cfg, kernel, p, tmk, tmv, cs) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, small ? small_kernel : kernel, p, tmk, tmv, cs) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 }  // namespace
