@@ -46,7 +46,7 @@
 // is busy for 0.79 of it, and of its two waves of CTAs the second is part full.  A
 // chunk of 2048 tokens behind 16384, 64 heads on 8: 1.0 ms, 1.17 PFLOP/s, with the
 // remainders' 1.75, near what a library product sustains.  6-node chains of 8
-// requests, 32 heads, behind 26000 to 32768 keys: 563 us, 7.0 TB/s, a copy's rate.
+// requests, 32 heads, behind 27000 to 32768 keys: 563 us, 7.0 TB/s, a copy's rate.
 // One token of 4 requests behind 8192 keys, 64 heads on 8: 27 us, 5 TB/s; 64-node
 // tree, 32 heads, behind 2048: 14.9 us, of them 2.5 to the first key tile, 7 of tiles
 // and 4 of output and merge.

@@ -38,7 +38,8 @@ struct RowBlock {
 // Up to this many requests their blocks are counted 32 requests a step, which leaves
 // none without rows in between; beyond, a request's first block follows from its
 // offset alone.  (bf16, a token each of 256, 1024 and 4096 requests behind 200 slots,
-// 8 heads: 106, 420 and 1711 us; counted, 114, 628 and 6365.)
+// 8 heads, the form with an SM to itself: 106, 420 and 1711 us; counted, 114, 628 and
+// 6365.)
 constexpr int kCounted = 64;
 
 // What block i of a request with geometry R, of `count`, has.

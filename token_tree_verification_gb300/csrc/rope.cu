@@ -22,8 +22,8 @@
 // no look-up and are issued in front of them: offsets, start and depth, page are a
 // chain of three loads.
 //
-// Memory bounds long runs: 50000 rows of 40 heads, D = 128, 1.05 GB in 162 us, 6.5
-// TB/s, 0.95 of a copy's rate; 14000 rows of 80 heads into pages of 64 slots, 583 MB
+// Memory bounds long runs: 51200 rows of 40 heads, D = 128, 1.05 GB in 162 us, 6.5
+// TB/s, 0.95 of a copy's rate; 14237 rows of 80 heads into pages of 64 slots, 583 MB
 // in 102 us, 5.7 TB/s; single tokens of 4096 requests, 48 heads, 101 MB in 21 us, 4.8
 // TB/s.  A few tokens (2.9 us) and a 64-node tree of 96 heads (3.6 us) are the chain
 // of loads.
@@ -322,7 +322,7 @@ rope_kernel(const RopeArgs a) {
 
 // An item a thread, a row's items in as few CTAs as take them in kMaxThreads, or
 // several rows side by side where a row has few; and rows in a run up to kRun (32 in
-// all) while that leaves sixteen CTAs an SM.  Device us for the 50000 rows, the 14000,
+// all) while that leaves sixteen CTAs an SM.  Device us for the 51200 rows, the 14237,
 // the 4096 above and a run of 8192 rows of 48 heads:
 //   192 threads, 2 rows ahead of the stores, runs of 8 and 6: 162, 102, 21, 36
 //   runs of 16 and 4: 169, 111, 21, 36 and 164, 103, 21, 38
