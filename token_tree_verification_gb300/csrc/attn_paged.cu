@@ -27,7 +27,10 @@
 // few keys each is set-up for the most part (offsets, page, keys: three loads one
 // behind the other; output), and takes the small form: half an SM, one softmax group,
 // one tile of keys and one of values, so that a CTA's set-up hides behind another's
-// tiles.  launch_bf16 says which and what both take.
+// tiles.  At D = 128 its Q lies in shared memory, which leaves TMEM for the scores of
+// two halves (one: 121 in place of 107 us for single tokens of 256 requests behind 500
+// keys; at D = 64 there is room for both and it gains nothing).  launch_bf16 says which
+// form is taken and what both take.
 // TMEM holds the scores of five halves, and P takes the place of S, so that the
 // products of one half run beside the softmax of two others.  A row's reference
 // is shared by the groups, which decide on it in the order of the halves (a
@@ -78,18 +81,20 @@ struct PagedCfg {
   static constexpr int kSoftThreads = 128 * kGroups;
   static constexpr int kThreads = 32 * kSoftFirst + kSoftThreads;
   static constexpr int kCtas = kSmall ? 2 : 1;              // of an SM
-  static constexpr int kBufs = kSmall ? (D == 128 ? 1 : 2) : 5;       // halves' scores and weights in TMEM
+  static constexpr int kBufs = kSmall ? 2 : 5;             // halves' scores and weights in TMEM
   static constexpr int kBoxes = D / 64;
   static constexpr int kBoxBytes = kTile * 128;             // 128 slots of 64 dims
   static constexpr int kTileBytes = kBoxes * kBoxBytes;
   static constexpr int kStages = (kSmall ? 1 : 3) * 128 / D;      // of keys, and as many of values
   static constexpr int kOffK = 0, kOffV = kStages * kTileBytes;
-  static constexpr int kRings = 2 * kStages * kTileBytes, kMerge = kSmall ? kRows * (D + 4) * 4 : merge_bytes<D>(kRows);
+  static constexpr bool kQSmem = kSmall && D == 128;        // Q lies in shared memory, as keys do
+  static constexpr int kOffQ = 2 * kStages * kTileBytes;
+  static constexpr int kRings = kOffQ + (kQSmem ? D / 64 * kRows * 128 : 0), kMerge = kSmall ? kRows * (D + 4) * 4 : merge_bytes<D>(kRows);
   // (the rows take the rings' place after the loop)
   static constexpr int kSmem = (kRings > kMerge ? kRings : kMerge) + 1024;
   // TMEM: the halves' S, and P in their place (a pair of keys per column, remainders
   // behind the high parts), Q (a pair of dims), O
-  static constexpr uint32_t kColQ = kBufs * kHalf, kColO = kColQ + 64, kTmemCols = 512 / kCtas;
+  static constexpr uint32_t kColQ = kBufs * kHalf, kColO = kColQ + (kQSmem ? 0 : 64), kTmemCols = 512 / kCtas;
   static_assert(kColO + D <= kTmemCols, "tensor memory");
   static_assert(kCtas * (kSmem + 8192) <= 227 * 1024, "shared memory budget");
 };
@@ -231,6 +236,7 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
     // ------------------------------------------------------------ S = Q K^T
     constexpr uint32_t id = tc::idesc_bf16_f32(kRows, kHalf, 0, 0);
     const uint64_t kd0 = tc::smem_desc_sw128(sb + C::kOffK, 16, 1024);
+    [[maybe_unused]] const uint64_t qd = tc::smem_desc_sw128(sb + C::kOffQ, 16, 1024);
     Ring<NS> ring;
     Ring<kBufs> buf;
     buf.phase = 1;             // free at first, then when what is in it has been multiplied
@@ -244,9 +250,13 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
       const uint64_t kd = kd0 + static_cast<uint64_t>((ring.at * C::kTileBytes + h * (kHalf * 128)) >> 4);
       if (leader) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          tc::mma_bf16_ts(tmem + buf.at * kHalf, tmem + C::kColQ + ks * 8,
-                          kd + (((ks >> 2) * C::kBoxBytes + (ks & 3) * 32) >> 4), id, ks > 0);
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t at = ((ks >> 2) * C::kBoxBytes + (ks & 3) * 32) >> 4;
+          if constexpr (C::kQSmem)
+            tc::mma_bf16(tmem + buf.at * kHalf, qd + at, kd + at, id, ks > 0);
+          else
+            tc::mma_bf16_ts(tmem + buf.at * kHalf, tmem + C::kColQ + ks * 8, kd + at, id, ks > 0);
+        }
         tc::commit(&bars.s_full[buf.at]);
         if (h) tc::commit(&bars.k_empty[ring.at]);
       }
@@ -306,13 +316,21 @@ tree_attn_paged_kernel(const PagedAttnArgs p, const __grid_constant__ CUtensorMa
       uint4 x4[kDims / 8];
 #pragma unroll
       for (int c = 0; c < kDims / 8; ++c) x4[c] = mine ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+      if constexpr (C::kQSmem) {
 #pragma unroll
-      for (int q = 0; q < kDims / 16; ++q) {
-        const uint4 x = x4[2 * q], y = x4[2 * q + 1];
-        const uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        tc::st8(trow + C::kColQ + group * (kDims / 2) + 8 * q, u);
+        for (int q = 0; q < kDims / 8; ++q)
+          st_shared_v4(sb + C::kOffQ + (q >> 3) * C::kBoxBytes + row * 128 + ((q ^ row) & 7) * 16, x4[q].x, x4[q].y,
+                       x4[q].z, x4[q].w);
+        fence_proxy_async_smem();
+      } else {
+#pragma unroll
+        for (int q = 0; q < kDims / 16; ++q) {
+          const uint4 x = x4[2 * q], y = x4[2 * q + 1];
+          const uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+          tc::st8(trow + C::kColQ + group * (kDims / 2) + 8 * q, u);
+        }
+        tc::wait_st();
       }
-      tc::wait_st();
     }
     tc::fence_before_sync();
     __syncwarp();
@@ -569,15 +587,17 @@ bool encode_pool(CUtensorMap *m, const void *base, const PageTable &pages, int H
 
 // As many splits of the keys (a cluster) as make waves x (tiles of a CTA + its
 // set-up, first tile and merge, which grows with the rows, in half tiles) least; or
-// the small form, whose tiles, two CTAs side by side, cost 5 half tiles (3 at D = 64).
+// the small form, whose tiles, two CTAs side by side, cost 4.5 half tiles (3 at D = 64).
 // (Device us by splits 1, 2, 3, 4, 5 and 8: 32 rows of 8 heads behind 500 keys 9.5,
 // 9.1, 8.1, 8.1, 7.5 and 7.6; 128 rows of 32 heads behind 300 12.3, 13.2, 13.2, 13.5;
 // one token x 4 x 8 heads behind 8192 58, 34, 26.9, 26.2, 39 and 45.  Whole and small
-// form, 8 heads of 4 query heads each: a token of 256 requests behind 60, 500, 1000 and
-// 1500 keys 77 and 37, 144 and 121, 215 and 208, 283 and 296; at D = 64 72 and 34, 118
-// and 71, 163 and 108, 210 and 147; of 16 requests behind 200, 7.5 and 10.1; prompts of
-// 512 tokens x 8, 80 and 57.  The occupancy calculator says one CTA an SM for the small
-// form; two run: 128 units behind 200 keys take 10.1 us, 256 take 10.9.)
+// form, 8 heads of 4 query heads each: a token of 256 requests behind 60, 500, 1000,
+// 1500, 2000 and 3000 keys 77 and 39, 144 and 107, 215 and 187, 283 and 261, 350 and
+// 338, 486 and 484; at D = 64 behind 60, 500, 1500 and 3000 72 and 34, 118 and 71, 210
+// and 147, 336 and 256; prompts of 512 tokens x 8, 80 and 54.  128-node trees x 4, 64
+// heads on 8, behind 8192: 142 and 149, at D = 64 118 and 112; chains of 6 x 8, 32
+// heads, behind 27000 to 32768: 562 and 610.  The occupancy calculator says one CTA an
+// SM for the small form, but two run.)
 template <int D>
 int launch_bf16(const PagedAttnArgs &p, int max_prefix, void *stream) {
   using C = PagedCfg<D, false>;
@@ -611,7 +631,7 @@ int launch_bf16(const PagedAttnArgs &p, int max_prefix, void *stream) {
   auto small_kernel = tree_attn_paged_kernel<D, true>;
   static KernelState small_state;
   const long long small_waves = (units + S::kCtas * sm_count() - 1) / (S::kCtas * sm_count());
-  const bool small = small_waves * (D == 128 ? 5 * mean_tiles + 6 : 3 * mean_tiles + 7) < best;
+  const bool small = small_waves * (D == 128 ? 9 * mean_tiles + 8 : 6 * mean_tiles + 14) < 2 * best;
   if (small) {
     if (!allow_dynamic_smem(small_kernel, S::kSmem, small_state.granted)) return SPEC_ERR_CUDA;
     cs = 1;
