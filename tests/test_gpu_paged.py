@@ -470,6 +470,23 @@ def test_scores_of_every_size_of_many_requests(gpu_lib, size, D):
     check_attn(o, q, cache, L, off)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,L,Hq,Hkv,P,causal", [
+    ([1] * 3, [5000, 0, 4097], 4, 1, 8, True), ([1, 1], [9000, 1], 2, 2, 16, False), ([1] * 70, list(range(0, 700, 10)), 8, 2, 32, True),
+    ([8], [2047], 3, 3, 64, False), ([2, 0, 1, 3], [300, 5, 31, 32], 5, 1, 8, True), ([16, 1], [1000, 3], 8, 1, 128, False),
+    ([33, 2, 128], [100, 64, 200], 2, 1, 16, False), ([300], [700], 6, 2, 16, True), ([3] * 90, [90] * 90, 1, 1, 4096, False)])
+def test_fp32_rows_from_one_to_many(gpu_lib, n, L, Hq, Hkv, P, causal, D):
+    rng = np.random.default_rng(sum(n) + sum(L) + D)
+    q, cache, off = batch(rng, n, L, Hq, Hkv, P, D, F32, extra=4)
+    T, B = int(off[-1]), len(n)
+    parents = None if causal else np.concatenate([random_tree(rng, k) for k in n] + [[-1] * 4])
+    status, o = zeros_status(B), torch.full_like(q, 7.0)
+    ttv.tree_attn_paged(q, cache.k, cache.v, cache.block_table, i32(L), i32(off), None, max(L), status, o=o, causal=causal,
+                        parents=None if causal else i32(parents))
+    assert status.eq(0).all() and o[T:].eq(7).all()
+    check_attn(o, q, cache, L, off, parents)
+
+
 def test_calls_of_both_kinds_in_turn(gpu_lib):
     """Launches for many requests and for one long one, and the dense call, each of which may begin while the
     one before it ends; on two streams, captured and not."""
