@@ -495,7 +495,8 @@ int spec_rope_table(int rotary_dim, double base, int scaling, double factor, dou
  *             and keys alike.  y may be x itself with the same strides (in
  *             place); it may not overlap it otherwise.  Pointers and strides
  *             of multiples of 16 bytes are fastest; any multiple of an element
- *             is taken
+ *             is taken, and rotary_dim / 2 with few factors of two costs
+ *             likewise
  *   D         a multiple of 8 up to 512; rotary_dim even, up to D (0: y is a copy)
  *   freqs     [rotary_dim / 2] uint64 DEVICE, from spec_rope_table
  *   start     [B] int32, depth [T] int32 or NULL, offsets [B+1] int32 (a

@@ -148,6 +148,32 @@ def test_rope_at_every_launch_shape(gpu_lib, T):
     assert_rotated(y, x, paged.positions([17], [0, T]), theta, scale, False)
 
 
+@DTYPES
+@LAYOUTS
+@pytest.mark.parametrize("D,r,shift", [(128, 24, 0), (80, 20, 0), (64, 36, 0), (72, 18, 0), (128, 64, 4), (128, 64, 2), (96, 8, 6), (64, 64, 5)])
+@pytest.mark.parametrize("T", [9, 3000])
+def test_rope_in_narrow_pieces(gpu_lib, dtype, interleaved, D, r, shift, T):
+    """Pairs' ends and rows that do not start on 16 bytes."""
+    rng = np.random.default_rng(D + r + shift)
+    H, off = 24, [0, 2, 2, T]
+    start = [3, 0, 100]
+    theta, scale = paged.frequencies(r)
+    x = strided(rng, T, H, D, dtype, 1, shift)
+    y = ttv.rope(x, ttv.rope_table(r), i32(start), i32(off), zeros_status(3), interleaved=interleaved)
+    assert_rotated(y, x, paged.positions(start, off), theta, scale, interleaved)
+    assert torch.equal(y[:, :, r:], x[:, :, r:])
+    # on the way into pages, keys and values at other alignments than the queries'
+    k, v = strided(rng, T, 2, D, dtype, 0, 0), strided(rng, T, 2, D, dtype, 1, shift)
+    cache, status = Cache(rng, [T + 3, 1, T + 100], 2, 64, D, dtype, fill=5.0), zeros_status(3)
+    q_out = ttv.rope_write_paged(x, k, v, cache.k, cache.v, cache.block_table, i32(start), i32(off), status, ttv.rope_table(r),
+                                 interleaved=interleaved)
+    assert status.eq(0).all() and torch.equal(bits(q_out), bits(y))
+    turned = ttv.rope(k, ttv.rope_table(r), i32(start), i32(off), status, interleaved=interleaved)
+    for pool, rows in ((cache.k, turned), (cache.v, v)):
+        want = paged.write(np.full(pool.shape, 5.0), f64(rows), cache.table, start, off)
+        assert (f64(pool) == want).all()
+
+
 def test_rope_errors_leave_rows_alone(gpu_lib):
     table = ttv.rope_table(64)
     x = torch.randn((12, 2, 64), device="cuda")

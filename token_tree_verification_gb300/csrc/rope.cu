@@ -13,8 +13,9 @@
 // table (a double) and exact otherwise.  Its upper 32 bits go to sincospif as a
 // number of half turns in [-1, 1), which rounds to 2^-25.
 //
-// A thread has one item of a row, two 16-byte vectors: both ends of eight (four,
-// fp32) pairs, or two vectors of dims that are copied; it keeps it along a run of
+// A thread has one item of a row, two vectors of 16 bytes (fewer where alignment or the
+// pairs' ends ask for it): both ends of eight (four, fp32) pairs, or two vectors of dims
+// that are copied; it keeps it along a run of
 // rows, so that what an item is (head, place, source, destination) is worked out
 // once, and rows differ by a stride, a slot and the angles, which one CTA computes
 // once for all heads.  (With an item worked out for every row and head the
@@ -64,57 +65,77 @@ struct RopeArgs {
   int rows, side;                    // of a CTA, and how many side by side
 };
 
-template <typename E>
-struct Vec;
-template <>
-struct Vec<__nv_bfloat16> {
-  static constexpr int n = 8;
-  static __device__ __forceinline__ void unpack(uint4 v, float (&f)[8]) {
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+// V elements as one load, of 16, 8 or 4 bytes; V = 1: a single element.
+template <typename E, int V>
+struct Vec {
+  using Load = E;
+};
+template <int V>
+struct Words {
+  uint32_t w[V];
+};
+template <int V>
+struct BfVec {
+  using Load = typename std::conditional<V == 8, uint4, typename std::conditional<V == 4, uint2, uint32_t>::type>::type;
+  static __device__ __forceinline__ void unpack(Load v, float (&f)[V]) {
+    const Words<V / 2> u = *reinterpret_cast<const Words<V / 2> *>(&v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(u[i] << 16);
-      f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    for (int i = 0; i < V / 2; ++i) {
+      f[2 * i] = __uint_as_float(u.w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(u.w[i] & 0xFFFF0000u);
     }
   }
-  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
-    uint32_t u[4];
+  static __device__ __forceinline__ Load pack(const float (&f)[V]) {
+    Words<V / 2> u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < V / 2; ++i) {
       const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      u[i] = *reinterpret_cast<const uint32_t *>(&h);
+      u.w[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
-    return make_uint4(u[0], u[1], u[2], u[3]);
+    return *reinterpret_cast<const Load *>(&u);
   }
 };
 template <>
-struct Vec<float> {
-  static constexpr int n = 4;
-  static __device__ __forceinline__ void unpack(uint4 v, float (&f)[4]) {
-    f[0] = __uint_as_float(v.x);
-    f[1] = __uint_as_float(v.y);
-    f[2] = __uint_as_float(v.z);
-    f[3] = __uint_as_float(v.w);
+struct Vec<__nv_bfloat16, 8> : BfVec<8> {};
+template <>
+struct Vec<__nv_bfloat16, 4> : BfVec<4> {};
+template <>
+struct Vec<__nv_bfloat16, 2> : BfVec<2> {};
+template <int V>
+struct FloatVec {
+  using Load = typename std::conditional<V == 4, uint4, uint2>::type;
+  static __device__ __forceinline__ void unpack(Load v, float (&f)[V]) {
+    const Words<V> u = *reinterpret_cast<const Words<V> *>(&v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = __uint_as_float(u.w[i]);
   }
-  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  static __device__ __forceinline__ Load pack(const float (&f)[V]) {
+    Words<V> u;
+#pragma unroll
+    for (int i = 0; i < V; ++i) u.w[i] = __float_as_uint(f[i]);
+    return *reinterpret_cast<const Load *>(&u);
   }
 };
+template <>
+struct Vec<float, 4> : FloatVec<4> {};
+template <>
+struct Vec<float, 2> : FloatVec<2> {};
 
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void from_float(float x, float *y) { *y = x; }
 __device__ __forceinline__ void from_float(float x, __nv_bfloat16 *y) { *y = __float2bfloat16_rn(x); }
 
-// (x_a, x_b) turned, in fp32.
+// (x_a, x_b) turned, in fp32; which product is rounded is said, so that every form
+// gives the same bits.
 __device__ __forceinline__ void turn(float &xa, float &xb, float2 cs) {
-  const float a = xa * cs.x - xb * cs.y, b = xa * cs.y + xb * cs.x;
+  const float a = __fmaf_rn(xa, cs.x, -__fmul_rn(xb, cs.y)), b = __fmaf_rn(xa, cs.y, __fmul_rn(xb, cs.x));
   xa = a;
   xb = b;
 }
 
 // One unit of a thread's work: where its elements lie in a head, and whether
-// they are turned.  Vectors (kVec): two of them at pa and pb (pb < 0: one).  Else
+// they are turned.  Vectors (V > 1): two of them at pa and pb (pb < 0: one).  Else
 // single elements: the two of a pair, or one that is copied.
 struct Item {
   int head, pa, pb;           // head: q's, then k's, then v's
@@ -122,10 +143,10 @@ struct Item {
   int pair;                   // first pair of pa's cosines
 };
 
-template <typename E, bool kVec, bool kInter>
+template <int V, bool kInter>
 __device__ __forceinline__ Item item_at(const RopeArgs &a, int i) {
   Item it;
-  constexpr int V = kVec ? Vec<E>::n : 1;
+  constexpr bool kVec = V > 1;
   const int turned = (a.Hq + a.Hkv) * a.turn_items;
   it.turn_a = it.turn_b = false;
   it.pair = 0;
@@ -163,7 +184,7 @@ __device__ __forceinline__ Item item_at(const RopeArgs &a, int i) {
   return it;
 }
 
-template <typename E, bool kVec, bool kInter, int kAhead>
+template <typename E, int V, bool kInter, int kAhead>
 __global__ void __launch_bounds__(kMaxThreads, kAhead == 1 ? 1 : 6)
 rope_kernel(const RopeArgs a) {
   extern __shared__ __align__(16) float s_angle[];     // [rows][cosines, sines][r / 2]
@@ -172,14 +193,14 @@ rope_kernel(const RopeArgs a) {
   const int tid = threadIdx.x, threads = blockDim.x, warp = tid >> 5, lane = tid & 31;
   const int t0 = static_cast<int>(blockIdx.x) * a.rows;
   const int rows = min(a.rows, a.T - t0), pairs = a.r / 2;
-  using Load = typename std::conditional<kVec, uint4, E>::type;
+  using Load = typename Vec<E, V>::Load;
   pdl_trigger();
   pdl_wait();
 
   // ---- this thread's item, and the first of its rows
   const int sub = tid / a.span, i = static_cast<int>(blockIdx.y) * a.span + tid - sub * a.span;
   const bool busy = sub < a.side && i < a.row_items;
-  const Item it = item_at<E, kVec, kInter>(a, busy ? i : 0);
+  const Item it = item_at<V, kInter>(a, busy ? i : 0);
   const bool is_q = it.head < a.Hq, is_k = !is_q && it.head < a.Hq + a.Hkv;
   const int head = is_q ? it.head : it.head - a.Hq - (is_k ? 0 : a.Hkv);
   const long long x_st = is_q ? a.q.st : is_k ? a.k.st : a.v.st;
@@ -271,33 +292,34 @@ rope_kernel(const RopeArgs a) {
   auto store = [&](int u, int row) {
     if (!s_ok[row]) return;
     const float *cosine = s_angle + row * a.r + it.pair, *sine = cosine + pairs;
-    if constexpr (kVec) {
-      constexpr int V = Vec<E>::n;
+    if constexpr (V > 1) {
       if constexpr (kInter) {
-        auto turn_vec = [&](uint4 &x, int from) {
+        auto turn_vec = [&](Load &x, int from) {
           float f[V];
-          Vec<E>::unpack(x, f);
+          Vec<E, V>::unpack(x, f);
 #pragma unroll
           for (int e = 0; e < V; e += 2) turn(f[e], f[e + 1], make_float2(cosine[from + e / 2], sine[from + e / 2]));
-          x = Vec<E>::pack(f);
+          x = Vec<E, V>::pack(f);
         };
         if (it.turn_a) turn_vec(la[u], 0);
         if (it.turn_b) turn_vec(lb[u], to_b / 2);
       } else if (it.turn_a) {
         float fa[V], fb[V];
-        Vec<E>::unpack(la[u], fa);
-        Vec<E>::unpack(lb[u], fb);
-        // (pairs of eight, four in fp32: whole vectors of angles)
+        Vec<E, V>::unpack(la[u], fa);
+        Vec<E, V>::unpack(lb[u], fb);
+        // (pairs in multiples of V: whole vectors of angles)
+        using Angles = typename std::conditional<V == 2, float2, float4>::type;
+        constexpr int kStep = V == 2 ? 2 : 4;
         float c[V], s[V];
 #pragma unroll
-        for (int e = 0; e < V; e += 4) {
-          *reinterpret_cast<float4 *>(c + e) = *reinterpret_cast<const float4 *>(cosine + e);
-          *reinterpret_cast<float4 *>(s + e) = *reinterpret_cast<const float4 *>(sine + e);
+        for (int e = 0; e < V; e += kStep) {
+          *reinterpret_cast<Angles *>(c + e) = *reinterpret_cast<const Angles *>(cosine + e);
+          *reinterpret_cast<Angles *>(s + e) = *reinterpret_cast<const Angles *>(sine + e);
         }
 #pragma unroll
         for (int e = 0; e < V; ++e) turn(fa[e], fb[e], make_float2(c[e], s[e]));
-        la[u] = Vec<E>::pack(fa);
-        lb[u] = Vec<E>::pack(fb);
+        la[u] = Vec<E, V>::pack(fa);
+        lb[u] = Vec<E, V>::pack(fb);
       }
     } else if (it.turn_a) {
       float fa = to_float(la[u]), fb = to_float(lb[u]);
@@ -331,9 +353,9 @@ rope_kernel(const RopeArgs a) {
 //   384 threads, 4 ahead: 165, 101, 50, 43 (its registers spill, or do not, at a touch)
 // A single row a thread takes no registers for a run: 3.6 in place of 4.4 us for the
 // tree.
-template <typename E, bool kVec, bool kInter>
+template <typename E, int V, bool kInter>
 int launch(RopeArgs &a, void *stream) {
-  constexpr int V = kVec ? Vec<E>::n : 1;
+  constexpr bool kVec = V > 1;
   const int vecs = a.D / V;
   a.copy_items = kVec ? (vecs + 1) / 2 : vecs;
   a.turn_items = kVec ? (kInter ? (vecs + 1) / 2 : a.r / 2 / V + ((a.D - a.r) / V + 1) / 2) : a.r / 2 + a.D - a.r;
@@ -366,23 +388,28 @@ int launch(RopeArgs &a, void *stream) {
   pdl_attribute(attr[0]);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const auto kernel = a.rows > a.side ? rope_kernel<E, kVec, kInter, kLong> : rope_kernel<E, kVec, kInter, 1>;
+  const auto kernel = a.rows > a.side ? rope_kernel<E, V, kInter, kLong> : rope_kernel<E, V, kInter, 1>;
   return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
-// 16-byte vectors where every pointer, stride and the pairs' ends allow them;
-// single elements otherwise.
-template <typename E>
-int launch_by_form(RopeArgs &a, bool interleaved, void *stream) {
-  constexpr int V = Vec<E>::n;
+// The widest vectors that every pointer, stride and the pairs' ends allow, of 16 bytes
+// and less; single elements otherwise.  (12000 rows of 80 heads into pages, D = 128, the
+// first 128, 24 and 20 dims turned, bf16, 16, 8 and 4 bytes: 87, 114 and 183 us; by
+// single elements 470 and 475.)
+template <typename E, int V>
+bool fits(const RopeArgs &a, bool interleaved) {
   auto whole = [](const void *p, long long st, long long sh) {
-    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && st % V == 0 && sh % V == 0;
+    return reinterpret_cast<uintptr_t>(p) % (V * sizeof(E)) == 0 && st % V == 0 && sh % V == 0;
   };
-  bool vec = a.D % V == 0 && (interleaved ? a.r % V == 0 : a.r / 2 % V == 0);
-  if (a.Hq) vec = vec && whole(a.q.x, a.q.st, a.q.sh) && whole(a.y, a.y_st, a.y_sh);
-  if (a.v.x) vec = vec && whole(a.k.x, a.k.st, a.k.sh) && whole(a.v.x, a.v.st, a.v.sh);
-  if (vec) return interleaved ? launch<E, true, true>(a, stream) : launch<E, true, false>(a, stream);
-  return interleaved ? launch<E, false, true>(a, stream) : launch<E, false, false>(a, stream);
+  return a.D % V == 0 && (interleaved ? a.r % V == 0 : a.r / 2 % V == 0) &&
+         (!a.Hq || (whole(a.q.x, a.q.st, a.q.sh) && whole(a.y, a.y_st, a.y_sh))) &&
+         (!a.v.x || (whole(a.k.x, a.k.st, a.k.sh) && whole(a.v.x, a.v.st, a.v.sh)));
+}
+template <typename E, int V>
+int launch_by_form(RopeArgs &a, bool interleaved, void *stream) {
+  if constexpr (V > 1)
+    if (!fits<E, V>(a, interleaved)) return launch_by_form<E, V / 2>(a, interleaved, stream);
+  return interleaved ? launch<E, V, true>(a, stream) : launch<E, V, false>(a, stream);
 }
 
 // What both calls ask of the rotation and of the rows.
@@ -474,8 +501,8 @@ extern "C" int spec_rope(const void *x, void *y, int dtype, int B, int T, int H,
   a.Hq = H;
   a.D = D;
   a.r = rotary_dim;
-  return dtype == SPEC_BF16 ? launch_by_form<__nv_bfloat16>(a, interleaved != 0, stream)
-                            : launch_by_form<float>(a, interleaved != 0, stream);
+  return dtype == SPEC_BF16 ? launch_by_form<__nv_bfloat16, 8>(a, interleaved != 0, stream)
+                            : launch_by_form<float, 4>(a, interleaved != 0, stream);
 }
 
 extern "C" int spec_rope_write_paged(const void *q, void *q_out, const void *k, const void *v, int dtype, int B, int T,
@@ -527,6 +554,6 @@ extern "C" int spec_rope_write_paged(const void *q, void *q_out, const void *k, 
   a.Hkv = Hkv;
   a.D = D;
   a.r = rotary_dim;
-  return dtype == SPEC_BF16 ? launch_by_form<__nv_bfloat16>(a, interleaved != 0, stream)
-                            : launch_by_form<float>(a, interleaved != 0, stream);
+  return dtype == SPEC_BF16 ? launch_by_form<__nv_bfloat16, 8>(a, interleaved != 0, stream)
+                            : launch_by_form<float, 4>(a, interleaved != 0, stream);
 }
