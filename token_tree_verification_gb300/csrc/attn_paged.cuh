@@ -179,6 +179,33 @@ __device__ __forceinline__ uint32_t sees_32(const RowSees &r, int k0, int L) {
   return near | __funnelshift_r(lo, hi, o & 31);
 }
 
+// The output of a block whose keys are not split: rows as merge_splits takes them,
+// eight dims a thread.  (128-node trees x 4, 64 heads on 8, behind 8192 keys: 137
+// us, with the merge's loop 143; prompts of 128 tokens x 64, 74 and 81.)
+template <int D, int THREADS, typename E, typename OutRow>
+__device__ __forceinline__ void write_rows(int tid, int rows, const float *so, OutRow out_row) {
+  __syncthreads();
+#pragma unroll 4
+  for (int idx = tid; idx < rows * (D / 8); idx += THREADS) {
+    const int r = idx / (D / 8), c = idx % (D / 8) * 8;
+    const float *from = so + r * (D + 4);
+    const float total = from[D + 1];
+    const float4 x = *reinterpret_cast<const float4 *>(from + c), y = *reinterpret_cast<const float4 *>(from + c + 4);
+    E *dst = out_row(r);
+    if (total < 0.f || !dst) continue;
+    const float inv = total == 0.f ? 0.f : __fdividef(1.f, total);
+    if constexpr (sizeof(E) == 4) {
+      *reinterpret_cast<float4 *>(dst + c) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+      *reinterpret_cast<float4 *>(dst + c + 4) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+    } else {
+      const __nv_bfloat162 h[4] = {__floats2bfloat162_rn(x.x * inv, x.y * inv), __floats2bfloat162_rn(x.z * inv, x.w * inv),
+                                   __floats2bfloat162_rn(y.x * inv, y.y * inv), __floats2bfloat162_rn(y.z * inv, y.w * inv)};
+      const uint32_t *u = reinterpret_cast<const uint32_t *>(h);
+      *reinterpret_cast<uint4 *>(dst + c) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+  }
+}
+
 // Merge of a block's rows over the splits of its keys, and the output, by all
 // THREADS threads of the CTA.  Each CTA of the cluster has its rows in
 // so[rows][D + 4] (shared memory, at the same place in all): the weighted sum,
@@ -196,33 +223,31 @@ constexpr int merge_bytes(int rows) { return (2 * rows + kMaxSplits) * (D + 4) *
 template <int D, int THREADS, typename E, typename OutRow>
 __device__ __forceinline__ bool merge_splits(int tid, int CS, int split, int rows, float *so, uint64_t *bar,
                                              OutRow out_row) {
+  if (CS == 1) {
+    write_rows<D, THREADS, E>(tid, rows, so, out_row);
+    return true;
+  }
   constexpr int kStride = D + 4;
-  const int share = CS == 1 ? rows : (rows + CS - 1) / CS;
+  const int share = (rows + CS - 1) / CS;
   const int from = min(rows, split * share), n = min(rows, from + share) - from;
-  const float *part0 = so;
+  float *recv = so + rows * kStride;
   bool ok = true;
-  if (CS > 1) {
-    float *recv = so + rows * kStride;
-    fence_proxy_async_smem();
-    cluster_sync_all();      // every CTA's rows are there, and room for its peers'
-    if (tid < CS) {
-      const int r0 = min(rows, tid * share), rn = min(rows, r0 + share) - r0;
-      if (rn > 0)
-        bulk_copy_s2s(peer_addr(recv + split * share * kStride, tid), smem_addr(so + r0 * kStride),
-                      static_cast<uint32_t>(rn * kStride * 4), peer_addr(bar, tid));
-    }
-    if (n > 0) {
-      if (tid == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(CS * n * kStride * 4));
-      ok = mbar_wait(bar, 0);      // (every CTA sends, also after a time-out: none may leave before)
-    }
-    part0 = recv;
-  } else {
-    __syncthreads();
+  fence_proxy_async_smem();
+  cluster_sync_all();      // every CTA's rows are there, and room for its peers'
+  if (tid < CS) {
+    const int r0 = min(rows, tid * share), rn = min(rows, r0 + share) - r0;
+    if (rn > 0)
+      bulk_copy_s2s(peer_addr(recv + split * share * kStride, tid), smem_addr(so + r0 * kStride),
+                    static_cast<uint32_t>(rn * kStride * 4), peer_addr(bar, tid));
+  }
+  if (n > 0) {
+    if (tid == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(CS * n * kStride * 4));
+    ok = mbar_wait(bar, 0);      // (every CTA sends, also after a time-out: none may leave before)
   }
 #pragma unroll 1
   for (int idx = tid; idx < n * (D / 4) && ok; idx += THREADS) {
     const int r = idx / (D / 4), c = idx % (D / 4) * 4;
-    const float *part = part0 + r * kStride;
+    const float *part = recv + r * kStride;
     float top = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     bool void_part = false;
@@ -245,10 +270,8 @@ __device__ __forceinline__ bool merge_splits(int tid, int CS, int split, int row
     const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
     store_row4(dst + c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
   }
-  if (CS > 1) {      // no CTA leaves while a copy may still read its rows
-    cluster_arrive_relaxed();
-    cluster_wait();
-  }
+  cluster_arrive_relaxed();      // no CTA leaves while a copy may still read its rows
+  cluster_wait();
   return ok;
 }
 
