@@ -462,6 +462,33 @@ def test_hundreds_of_requests(gpu_lib, dtype, B, causal):
         check_attn(o, q, cache, L, off, None if causal else parents, rows=np.flatnonzero(~left[:T]))
 
 
+@DTYPES
+@pytest.mark.parametrize("wrong", [-2 ** 31, -1, 2 ** 31 - 1, 10 ** 6])
+@pytest.mark.parametrize("B", [3, 70, 600])
+def test_offsets_that_are_anything(gpu_lib, dtype, wrong, B):
+    """The request behind a wrong offset and the one before it report it; others are right or left out."""
+    rng = np.random.default_rng(B)
+    n, L = [3] * B, [20] * B
+    q, cache, off = batch(rng, n, L, 16, 1, 16, 64, dtype)
+    args = (q, cache.k, cache.v, cache.block_table, i32(L))
+    good, status = torch.full_like(q, 7.0), zeros_status(B)
+    ttv.tree_attn_paged(*args, i32(off), None, 20, status, o=good, causal=True)
+    assert status.eq(0).all()
+    for at in sorted({0, 1, B // 2, B}):
+        bad = off.copy()
+        bad[at] = wrong
+        o, status = torch.full_like(q, 7.0), zeros_status(B)
+        ttv.tree_attn_paged(*args, i32(bad), None, 20, status, o=o, causal=True)
+        codes = status.cpu().numpy()
+        assert set(np.flatnonzero(codes).tolist()) == {b for b in (at - 1, at) if 0 <= b < B} and set(codes[codes != 0]) == {-4}
+        same = (bits(o) == bits(good)).flatten(1).all(1) | (o == 7).flatten(1).all(1)
+        assert same.all()
+        left = (o == 7).flatten(1).all(1).cpu().numpy()
+        for b in (at - 1, at):
+            if 0 <= b < B:
+                assert left[off[b]:off[b + 1]].all()
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("form", ["mask", "parents", "causal"])
 def test_many_requests_behind_few_keys(gpu_lib, form, D):

@@ -45,7 +45,7 @@
 // between its products.
 //
 // Measured, device times: 128-node trees of 4 requests, 64 heads on 8, behind 8192
-// keys: 137 us, 1.0 PFLOP/s and with the remainders' products 1.5; the tensor pipe
+// keys: 137 to 141 us, 1.0 PFLOP/s and with the remainders' products 1.5; the tensor pipe
 // is busy for 0.8 of it, and of its two waves of CTAs the second is part full.  A
 // chunk of 2048 tokens behind 16384, 64 heads on 8: 1.0 ms, 1.17 PFLOP/s, with the
 // remainders' 1.75, near what a library product sustains.  6-node chains of 8

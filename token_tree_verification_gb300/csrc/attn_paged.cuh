@@ -77,10 +77,11 @@ __device__ __forceinline__ RowBlock find_block_of_many(const PagedAttnArgs &p, i
   if (!who) return w;
   const int b = lo + __ffs(static_cast<int>(who)) - 1;
   w.R = paged_geometry(p, b);
-  const int i = j - static_cast<int>(first(b)), count = w.R.err ? 0 : (w.R.n * p.a.G + ROWS - 1) / ROWS;
+  const long long i = j - first(b);      // from 0 on; beyond 32 bits where offsets are anything
+  const int count = w.R.err ? 0 : (w.R.n * p.a.G + ROWS - 1) / ROWS;
   if (i >= count) return w;
   w.b = b;
-  set_block<ROWS>(p, w, i, count);
+  set_block<ROWS>(p, w, static_cast<int>(i), count);
   return w;
 }
 
@@ -150,7 +151,7 @@ inline long long likely_blocks(const AttnArgs &a) {
 // Every request's error, reported once (those in error have no block); by one
 // warp each of the first head's CTAs.
 __device__ __forceinline__ void report_bad_requests(const PagedAttnArgs &p, int lane) {
-  const int step = 32 * static_cast<int>(gridDim.x);
+  const long long step = 32ll * gridDim.x;
   for (long long b = 32ll * blockIdx.x + lane; b < p.a.B; b += step) {
     const ReqGeom g = paged_geometry(p, static_cast<int>(b));
     if (g.err) report(p.a.status, static_cast<int>(b), g.err);
@@ -181,7 +182,7 @@ __device__ __forceinline__ uint32_t sees_32(const RowSees &r, int k0, int L) {
 
 // The output of a block whose keys are not split: rows as merge_splits takes them,
 // eight dims a thread.  (128-node trees x 4, 64 heads on 8, behind 8192 keys: 137
-// us, with the merge's loop 143; prompts of 128 tokens x 64, 74 and 81.)
+// to 141 us, with the merge's loop 143; prompts of 128 tokens x 64, 74 and 81.)
 template <int D, int THREADS, typename E, typename OutRow>
 __device__ __forceinline__ void write_rows(int tid, int rows, const float *so, OutRow out_row) {
   __syncthreads();
