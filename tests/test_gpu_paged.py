@@ -736,6 +736,36 @@ def test_compaction_errors_leave_the_cache_alone(gpu_lib):
             assert torch.equal(bits(x[cache.table[b].tolist()]), bits(y[cache.table[b].tolist()])), b
 
 
+@DTYPES
+@pytest.mark.parametrize("bad", [[0, -2 ** 31, -2 ** 31 + 1, 3], [0, -2, -1, 3], [0, 2 ** 31 - 1, -5, -4], [-1, 0, 1, 2],
+                                 [0, 1, 1, 2], [0, 0, 1, 2], [-2 ** 31, -2 ** 31 + 1, -9, -8], [2 ** 31 - 1] * 4])
+def test_compaction_of_paths_that_are_anything(gpu_lib, dtype, bad):
+    """Entries that increase from below zero: each looks like a node behind its neighbour, its slot lies far outside."""
+    rng = np.random.default_rng(4)
+    n, L = [4, 4, 4], [0, 12, 5]
+    cache = Cache(rng, [4, 16, 9], 2, 8, 64, dtype).fill(rng, [4, 16, 9])
+    path = np.array([bad, [0, 2, 3, -1], bad])
+    want = [paged.compact(f64(x), cache.table, L, path, [0, 2, 0]) for x in (cache.k, cache.v)]
+    status = zeros_status(3)
+    lens = ttv.kv_compact_paged(cache.k, cache.v, cache.block_table, i32(L), i32([0, 4, 8, 12]), i32(path), i32([3, 2, 3]), status)
+    assert status.tolist() == [-5, 0, -5] and lens.tolist() == [0, 15, 5]
+    for x, y in zip((cache.k, cache.v), want):
+        assert np.array_equal(f64(x), y, equal_nan=True)
+
+
+def test_compaction_of_a_long_path_of_a_small_tree(gpu_lib):
+    """128 entries that increase up to node 1 of two, at the end of the request's slots: their places lie behind the table."""
+    rng = np.random.default_rng(4)
+    cache = Cache(rng, [16], 2, 8, 64, F32).fill(rng, [16])
+    path = [[0] + list(range(-125, 2))]
+    before = [cache.k.clone(), cache.v.clone()]
+    status = zeros_status(1)
+    lens = ttv.kv_compact_paged(cache.k, cache.v, cache.block_table, i32([14]), i32([0, 2]), i32(path), i32([127]), status)
+    assert status.tolist() == [-5] and lens.tolist() == [14]
+    for x, y in zip((cache.k, cache.v), before):
+        assert torch.equal(bits(x), bits(y))
+
+
 # ------------------------------------------------------------------ together
 def step(q, k, v, cache, rope, depth, parents, off, lens, path, accept, max_prefix, status, stream=None):
     """One step as a program runs it: rows into pages, attention, the accepted path."""

@@ -45,9 +45,11 @@ kv_compact_paged_kernel(const CompactArgs a) {
     err = n < 1 || n > SPEC_MAX_TREE_NODES || lo < 0 ? SPEC_ERR_TREE_TOO_LARGE : SPEC_ERR_PREFIX_RANGE;
   else if (accepted < 0 || accepted + 1 > a.W)
     err = SPEC_ERR_TREE_TOO_LARGE;
-  // each thread's path entry: the root first, then increasing nodes of the tree
+  // each thread's path entry: the root first, then increasing nodes of the tree.  Entry
+  // j of such a path is node j or a later one; asked of every entry by itself, that
+  // keeps the slots that a thread looks up within [L, L + n) whatever the others hold.
   if (!skipped && !err && tid <= accepted) {
-    if (tid == 0 ? x != 0 : x <= before || x >= n) {
+    if (tid == 0 ? x != 0 : x <= before || x < tid || x >= n) {
       err = SPEC_ERR_BAD_PARENT;
     } else {
       const int src = L + x, dst = L + tid, size = 1 << a.pages.shift;
