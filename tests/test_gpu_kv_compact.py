@@ -94,3 +94,20 @@ def test_errors_and_skipped_requests():
     status = np.array([0, 0, 0, -9], np.int32)
     npg = _check(k, v, L, off, pn, acc, status)
     assert npg.tolist() == L.tolist()
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("acc", [4, 2 ** 31 - 1, -1, -2 ** 31])
+def test_accepted_lengths_that_are_anything(acc, paged):
+    """A length plus one that passes 2^31; the dense and the paged call."""
+    cache = [torch.randn((3, 2, 16, 64), device="cuda") for _ in range(2)]
+    before = [x.clone() for x in cache]
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    status, path = i32(0, 0, 0), i32(*[[0, 2, 5, 7]] * 3)
+    # (paged: a page a request, laid out as the dense cache)
+    call, args = (ttv.kv_compact_paged, (*cache, i32([0], [1], [2]))) if paged else (ttv.kv_compact, cache)
+    lens = call(*args, i32(3, 4, 5), i32(0, 8, 16, 24), path, i32(acc, 1, acc), status)
+    assert status.tolist() == [-4, 0, -4] and lens.tolist() == [3, 6, 5]
+    for x, y in zip(cache, before):
+        y[1, :, 5] = y[1, :, 6]
+        assert torch.equal(x, y)

@@ -44,7 +44,7 @@ kv_compact_kernel(const KvArgs a) {
       int err = 0;
       if (L < 0 || static_cast<long long>(L) + n > a.S_cap) {
         err = SPEC_ERR_PREFIX_RANGE;
-      } else if (acc < 0 || acc + 1 > a.W) {
+      } else if (acc < 0 || acc >= a.W) {
         err = SPEC_ERR_TREE_TOO_LARGE;
       } else {
         int prev = __ldg(pn);

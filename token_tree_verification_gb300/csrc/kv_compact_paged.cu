@@ -43,7 +43,7 @@ kv_compact_paged_kernel(const CompactArgs a) {
   int err = 0;
   if (L < 0 || lo < 0 || n < 1 || n > SPEC_MAX_TREE_NODES || static_cast<long long>(L) + n > a.pages.capacity())
     err = n < 1 || n > SPEC_MAX_TREE_NODES || lo < 0 ? SPEC_ERR_TREE_TOO_LARGE : SPEC_ERR_PREFIX_RANGE;
-  else if (accepted < 0 || accepted + 1 > a.W)
+  else if (accepted < 0 || accepted >= a.W)
     err = SPEC_ERR_TREE_TOO_LARGE;
   // each thread's path entry: the root first, then increasing nodes of the tree.  Entry
   // j of such a path is node j or a later one; asked of every entry by itself, that
