@@ -13,16 +13,20 @@ around calls on another GPU).
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 from typing import NamedTuple
 
 import torch
 
+from . import build
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lib = None
-# The module of csrc/marshal.cpp once the library is loaded, where it was built:
-# the paged calls go through it, and it leaves what is not as it should be (it
-# then returns None) to the functions here.
+# The module of csrc/marshal.cpp once the library is loaded, where it was built (for
+# this torch and Python): the paged calls go through it, and it leaves what is not as
+# it should be (it then returns None) to the functions here.
 _marshal = None
 
 STATUS = {
@@ -119,13 +123,19 @@ def load():
 
 def _load_marshal(lib):
     global _marshal
+    _marshal = None
     try:
-        from . import _marshal as module
+        path = build.marshal_path()
+        if not os.path.exists(path):
+            return
+        loader = importlib.machinery.ExtensionFileLoader(f"{__package__}._marshal", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_file_location(loader.name, path, loader=loader))
+        loader.exec_module(module)
         module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (lib.spec_rope, lib.spec_rope_write_paged, lib.spec_tree_attn_paged,
                                                         lib.spec_kv_compact_paged)))
         _marshal = module
-    except ImportError:
-        _marshal = None
+    except (ImportError, OSError):
+        pass
 
 
 def status_string(code: int) -> str:

@@ -11,11 +11,15 @@ environment sets ``SPEC_TREE_CHECKED=1``.
 
 ``csrc/marshal.cpp`` becomes the module ``_marshal`` beside them (g++, torch's
 headers): the paged calls' checks and launches from C++, which only saves
-host time.  Where it cannot be built, ``binding.py`` does that work.
+host time.  Its file is named after what it was compiled against (torch, this
+Python, its source and the C header), and only a file of the right name is
+loaded.  Where there is none, ``binding.py`` does that work.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import glob
+import hashlib
 import os
 import shutil
 import subprocess
@@ -32,28 +36,48 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 
 
-OUT_MARSHAL = os.path.join(HERE, "_marshal.so")
+MARSHAL_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-shared"]
+
+
+def _marshal_sources() -> list[str]:
+    return [os.path.join(CSRC, "marshal.cpp"), os.path.join(os.path.dirname(HERE), "include", "spec_tree.h")]
+
+
+def marshal_path() -> str:
+    """The file of the module ``_marshal`` for the present torch, Python and sources, whose layouts and
+    signatures are compiled into it."""
+    import torch
+    key = hashlib.sha256(repr((torch.__version__, torch.version.git_version, sys.version, sysconfig.get_config_var("SOABI"),
+                               MARSHAL_FLAGS)).encode())
+    for path in _marshal_sources():
+        with open(path, "rb") as f:
+            key.update(hashlib.sha256(f.read()).digest())
+    return os.path.join(HERE, f"_marshal_{key.hexdigest()[:16]}.so")
 
 
 def build_marshal(force: bool = False) -> bool:
-    """Builds the module ``_marshal``; False (and a line on stderr) if that fails."""
-    src = os.path.join(CSRC, "marshal.cpp")
-    if not (force or _stale(OUT_MARSHAL, [src] + [h for h in _headers() if h.endswith("spec_tree.h")])):
-        return True
+    """Builds the module ``_marshal``; False (and a line on stderr) if that fails.  Modules of
+    other versions are removed, also when it fails."""
     try:
         import torch
+        out = marshal_path()
+        for old in glob.glob(os.path.join(HERE, "_marshal*.so")):
+            if force or old != out:
+                os.unlink(old)
+        if os.path.exists(out):
+            return True
         root = os.path.dirname(torch.__file__)
         cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
         inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
         lib = os.path.join(root, "lib")
-        tmp = OUT_MARSHAL + f".tmp{os.getpid()}"
-        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", *(f"-I{i}" for i in inc), src, "-o", tmp,
+        tmp = out + f".tmp{os.getpid()}"
+        cmd = [os.environ.get("CXX", "g++"), *MARSHAL_FLAGS, *(f"-I{i}" for i in inc), _marshal_sources()[0], "-o", tmp,
                f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(r.stderr[-2000:])
-        os.replace(tmp, OUT_MARSHAL)
+        os.replace(tmp, out)
         return True
     except Exception as e:
         print(f"_marshal was not built (calls take longer on the host): {e}", file=sys.stderr)
