@@ -468,7 +468,8 @@ int spec_kv4_compact(void *kv_cache, int B, int Hkv, int D, int S_cap, const int
  *                     turns in the original context stay, those of fewer than
  *                     `low` are divided.  low = 1, high = 4 usually
  *   freqs   [rotary_dim / 2] uint64 HOST out: theta_i / 2 pi as a 64-bit fraction
- *           of a turn; the caller copies it to the device for the calls below
+ *           of a turn, right to its last place; the caller copies it to the device
+ *           for the calls below
  *   scale   HOST out: the factor of cosines and sines, 1 but for YARN
  * rotary_dim is even, from 2 to 512; base above 1.  Nothing is launched.
  */
@@ -503,8 +504,10 @@ int spec_rope_table(int rotary_dim, double base, int scaling, double factor, dou
  *             request may have no rows; it has no upper limit of rows)
  *   T         rows; rows at or behind offsets[B] stay as they were, T = 0
  *             enqueues nothing
- * The angle is exact in 64-bit fixed point up to the table's own rounding, a
- * double, so positions up to 2^32 keep fp32's accuracy.
+ * The angle is an exact product in 64-bit fixed point, so positions up to 2^32 keep
+ * fp32's accuracy: the table's rounding is 2^-33 of a turn there.  Its upper 32 bits
+ * (the others are cut, 2^-32 of a turn) are rounded to fp32 as a number of half turns
+ * (2^-25), whose cosine and sine are fp32's to an ulp; all is within 2^-20 of |x_a| + |x_b|.
  * Errors on the device: SPEC_ERR_TREE_TOO_LARGE (offsets outside [0, T] or
  * decreasing) and SPEC_ERR_PREFIX_RANGE (a start below zero; or a depth: then
  * the row alone is left out), for which the request's rows of y stay as they

@@ -123,6 +123,30 @@ def test_rope_far_away(gpu_lib):
             assert abs(y[t, 0, i + 4].item() - (c + s)) <= 2.0 ** -19
 
 
+@LAYOUTS
+def test_rope_far_away_by_the_formula(gpu_lib, interleaved):
+    """Positions up to 2^31 + 6 against angles of 60 digits, without the table."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    pi = Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803")
+    x = torch.zeros((3, 1, 128), dtype=F32, device="cuda")
+    x[:, :, 0::2 if interleaved else 1] = 1.0
+    if not interleaved:
+        x[:, :, 64:] = 0.0
+    start, depth = 2 ** 31 - 3, [0, 2, 9]
+    y = ttv.rope(x, ttv.rope_table(128, 500000.0), i32([start]), i32([0, 3]), zeros_status(1), depth=i32(depth),
+                 interleaved=interleaved)[:, 0].double().cpu().numpy()
+    for t in range(3):
+        for i in range(64):
+            turns = (start + depth[t]) * Decimal(500000) ** (Decimal(-2 * i) / 128) / (2 * pi)
+            angle = 2 * math.pi * float(turns % 1)
+            a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + 64)
+            # half turns rounded to 2^-25 (times pi), the turn's lower bits cut (2^-32), the table's half unit 2^31
+            # times over; an ulp of cosine and sine (2^-24); times one and plus zero are exact
+            bound = math.pi * 2.0 ** -25 + 2 * math.pi * (2.0 ** -32 + 2.0 ** -34) + 2.0 ** -24
+            assert abs(y[t, a] - math.cos(angle)) <= bound and abs(y[t, b] - math.sin(angle)) <= bound, (t, i)
+
+
 def test_rope_of_trees_and_of_many_requests(gpu_lib):
     rng = np.random.default_rng(9)
     B = 1500

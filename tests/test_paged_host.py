@@ -175,3 +175,42 @@ def test_the_module_of_the_host_work(lib):
         binding._marshal.bind(1, 2, 3, 0)
     with pytest.raises(TypeError):
         ttv.rope(x, None, one, one, one)
+
+
+def _theta_exactly(r, base, scaling, factor, original, low, high):
+    """Turns a position of each pair, to 60 digits, from the formulas (Python's decimal); the ramp's ends as in the oracle."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    pi = Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803")
+    base, factor, original, low, high = (Decimal(x) for x in (base, factor, original, low, high))
+    if scaling == "ntk":
+        base *= factor ** (Decimal(r) / (r - 2))
+    if scaling == "yarn":
+        d = [r * (original / (2 * pi * t)).ln() / (2 * base.ln()) for t in (high, low)]
+        first, last = max(0, math.floor(d[0])), min(r - 1, math.ceil(d[1]))
+    out = []
+    for i in range(r // 2):
+        t = base ** (Decimal(-2 * i) / r)
+        keep = Decimal(1)
+        if scaling == "linear":
+            keep = Decimal(0)
+        elif scaling == "yarn":
+            keep = 1 - min(Decimal(1), max(Decimal(0), Decimal(i - first) / max(Decimal(last - first), Decimal(0.001))))
+        elif scaling == "bands":
+            keep = min(Decimal(1), max(Decimal(0), (original * t / (2 * pi) - low) / (high - low)))
+        out.append((t * keep + t / factor * (1 - keep)) / (2 * pi))
+    return out
+
+@pytest.mark.parametrize("r,base", [(128, 10000.0), (64, 500000.0), (2, 10.0), (4, 1.001), (24, 1e6), (512, 10000.0), (512, 9e29), (256, 1.5)])
+@pytest.mark.parametrize("scaling,factor,original,low,high", [
+    ("none", 1.0, 1.0, 1.0, 4.0), ("linear", 3.0, 1.0, 1.0, 4.0), ("linear", 9e8, 1.0, 1.0, 4.0), ("ntk", 8.0, 1.0, 1.0, 4.0),
+    ("ntk", 1.7e6, 1.0, 1.0, 4.0), ("yarn", 16.0, 4096.0, 1.0, 32.0), ("yarn", 2.3, 64.0, 2.0, 5.0), ("yarn", 1.0, 4096.0, 1.0, 32.0),
+    ("bands", 8.0, 8192.0, 1.0, 4.0), ("bands", 4.1, 100.0, 3.0, 3.5)])
+def test_frequencies_to_the_last_place(lib, r, base, scaling, factor, original, low, high):
+    """What a position multiplies, up to 2^32 times: half a unit of 2^-64 turns, and the two-double sums' own error,
+    some 2^-100 for each of 256 products (beside it a ramp's or band's quotient)."""
+    if scaling == "ntk" and r == 2:
+        pytest.skip("refused, see above")
+    table = ttv.rope_table(r, base, scaling, factor, original=original, low=low, high=high, device="cpu")
+    for i, turns in enumerate(_theta_exactly(r, base, scaling, factor, original, low, high)):
+        assert abs(float(table.freqs[i].item() % 2 ** 64 - turns * 2 ** 64)) <= 0.5 + 2.0 ** -20, i

@@ -8,9 +8,9 @@
 //
 // Angles.  At position 2^20 an fp32 product p theta is off by up to 2^-5
 // radians, and fp64 arithmetic is slow here.  The table holds theta / 2 pi, the
-// turns a position, as a 64-bit fraction: p times it, modulo 2^64, is the
-// angle's fraction of a turn, off by less than p 2^-53 of a turn's unit in the
-// table (a double) and exact otherwise.  Its upper 32 bits go to sincospif as a
+// turns a position, as a 64-bit fraction rounded to its last place: p times it,
+// modulo 2^64, is the angle's fraction of a turn, off by at most p 2^-65 turns.
+// Its upper 32 bits (the others, 2^-32 turns, are cut) go to sincospif as a
 // number of half turns in [-1, 1), which rounds to 2^-25.
 //
 // A thread has one item of a row, two vectors of 16 bytes (fewer where alignment or the
@@ -422,6 +422,45 @@ int check(int dtype, int B, int T, int D, const void *freqs, int r, float scale)
   return SPEC_OK;
 }
 
+// Sums of two doubles, about 105 bits: the table's fractions have 64, and the error of
+// one is multiplied by the position.  (Frequencies in double were off by 2^-55 of a turn,
+// at position 2^31 the angle by 3e-7.)  The sums of Knuth (1969) and Dekker (1971); a
+// product is kept from being fused with what follows, which its error term presumes.
+struct Two {
+  double hi, lo;
+};
+Two sum_of(double a, double b) {
+  const double s = a + b, x = s - a;
+  return {s, (a - (s - x)) + (b - x)};
+}
+Two sum(Two a, Two b) {
+  const Two s = sum_of(a.hi, b.hi), t = sum_of(a.lo, b.lo), u = sum_of(s.hi, s.lo + t.hi);
+  return sum_of(u.hi, u.lo + t.lo);
+}
+Two mul(Two a, Two b) {
+  const volatile double p = a.hi * b.hi;
+  return sum_of(p, std::fma(a.lo, b.hi, std::fma(a.hi, b.lo, std::fma(a.hi, b.hi, -p))));
+}
+Two div(Two a, Two b) {
+  const double q = a.hi / b.hi;
+  const Two rest = mul(b, {-q, 0.0});
+  return sum_of(q, sum(a, rest).hi / b.hi);
+}
+// x^(1/n): one step of Newton's method squares the double's error.
+Two root(double x, int n) {
+  const Two g = {std::pow(x, 1.0 / n), 0.0};
+  Two power = {1.0, 0.0};
+  for (int i = 0; i < n; ++i) power = mul(power, g);
+  const Two off = sum(div({x, 0.0}, power), {-1.0, 0.0});
+  return sum(g, mul(g, div(off, {static_cast<double>(n), 0.0})));
+}
+// 2^64 x to the nearest whole number, x in [0, 1/4).
+uint64_t turns_of(Two x) {
+  const double hi = std::ldexp(x.hi, 64), whole = std::floor(hi);
+  return static_cast<uint64_t>(whole) +
+         static_cast<uint64_t>(static_cast<int64_t>(std::floor((hi - whole) + std::ldexp(x.lo, 64) + 0.5)));
+}
+
 // A stride between rows or heads of which there is only one is never taken.
 bool bad_strides(int T, int H, int64_t &st, int64_t &sh) {
   if (T <= 1) st = 0;
@@ -435,6 +474,7 @@ bool bad_strides(int T, int H, int64_t &st, int64_t &sh) {
 
 extern "C" int spec_rope_table(int rotary_dim, double base, int scaling, double factor, double original, double low,
                                double high, uint64_t *freqs, float *scale) {
+  using namespace spec;
   const double kPi = 3.14159265358979323846;
   const int r = rotary_dim;
   if (!freqs || !scale) return SPEC_ERR_NULL;
@@ -443,10 +483,7 @@ extern "C" int spec_rope_table(int rotary_dim, double base, int scaling, double 
     return SPEC_ERR_SHAPE;
   if (scaling == SPEC_ROPE_NONE) factor = 1.0;
   if (!(factor >= 1.0 && factor < 1e9)) return SPEC_ERR_SHAPE;
-  if (scaling == SPEC_ROPE_NTK) {
-    if (r < 4) return SPEC_ERR_SHAPE;
-    base *= std::pow(factor, static_cast<double>(r) / (r - 2));
-  }
+  if (scaling == SPEC_ROPE_NTK && r < 4) return SPEC_ERR_SHAPE;
   const bool ranged = scaling == SPEC_ROPE_YARN || scaling == SPEC_ROPE_BANDS;
   if (ranged && !(original > 0.0 && original < 1e12 && low > 0.0 && high > low && high < 1e12)) return SPEC_ERR_SHAPE;
   // the pair whose wavelength makes `turns` turns in the original context
@@ -457,15 +494,22 @@ extern "C" int spec_rope_table(int rotary_dim, double base, int scaling, double 
     const double to = std::fmin(r - 1.0, std::ceil(pair_of(low)));
     width = std::fmax(to - from, 0.001);
   }
-  for (int i = 0; i < r / 2; ++i) {
-    double theta = std::pow(base, -2.0 * i / r);
-    if (scaling == SPEC_ROPE_LINEAR) theta /= factor;
-    double keep = 1.0;      // how much of the unscaled frequency stays
-    if (scaling == SPEC_ROPE_YARN) keep = 1.0 - std::fmin(1.0, std::fmax(0.0, (i - from) / width));
-    if (scaling == SPEC_ROPE_BANDS)
-      keep = std::fmin(1.0, std::fmax(0.0, (original * theta / (2.0 * kPi) - low) / (high - low)));
-    theta = theta * keep + theta / factor * (1.0 - keep);
-    freqs[i] = static_cast<uint64_t>(std::ldexp(theta / (2.0 * kPi), 64));
+  const Two one = {1.0, 0.0}, per_turn = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};      // 1 / 2 pi
+  Two step = div(one, root(base, r / 2)), theta = one;
+  // (base factor^(r / (r - 2)))^(-2 / r) = base^(-2 / r) factor^(-2 / (r - 2))
+  if (scaling == SPEC_ROPE_NTK) step = div(step, root(factor, r / 2 - 1));
+  for (int i = 0; i < r / 2; ++i, theta = mul(theta, step)) {
+    Two keep = one;      // how much of the unscaled frequency stays
+    if (scaling == SPEC_ROPE_LINEAR) keep = {0.0, 0.0};
+    if (scaling == SPEC_ROPE_YARN && i > from)
+      keep = i - from < width ? sum(one, div({from - i, 0.0}, {width, 0.0})) : Two{0.0, 0.0};
+    if (scaling == SPEC_ROPE_BANDS) {
+      const Two over = sum(mul(mul(theta, per_turn), {original, 0.0}), {-low, 0.0}), all = sum_of(high, -low);
+      if (over.hi <= 0.0) keep = {0.0, 0.0};
+      else if (sum(over, {-all.hi, -all.lo}).hi < 0.0) keep = div(over, all);
+    }
+    const Two less = mul(div(theta, {factor, 0.0}), sum(one, {-keep.hi, -keep.lo}));
+    freqs[i] = turns_of(mul(sum(mul(theta, keep), less), per_turn));
   }
   *scale = scaling == SPEC_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
   return SPEC_OK;
