@@ -208,3 +208,20 @@ def test_parents_path_bad_parent(gpu_lib, kernel):
     for b in (0, 2):
         a, z = w.offsets[b], w.offsets[b + 1]
         assert np.array_equal(got[a:z], ref_good[a:z])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_requests_without_rows_of_their_own_report(gpu_lib, kernel, dtype):
+    """A tree without nodes, offsets below zero and beyond the batch; rows of no sound request stay as they were."""
+    import token_tree_verification_gb300 as ttv
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    q = torch.randn((12, 2, 64), device="cuda").to(dtype)
+    k, v = (torch.randn((3, 2, 40, 64), device="cuda").to(dtype) for _ in range(2))
+    three = [-1, 0, 0, 1] * 3
+    for offsets, parents, codes, kept in (
+            ([0, 4, 4, 12], three[:4] + [-1, 0, 0, 1, 2, 2, 3, 0], [0, -4, 0], []), ([-1, 4, 8, 12], three, [-4, 0, 0], [0, 1, 2, 3]),
+            ([0, 4, 8, 13], three, [0, 0, -4], [8, 9, 10, 11]), ([0, 4, -1, 12], three, [0, -4, -4], list(range(4, 12)))):
+        status, o = i32(0, 0, 0), torch.full_like(q, 7.0)
+        ttv.tree_attn(q, k, v, i32(20, 30, 5), i32(*offsets), None, 40, status, o=o, parents=i32(*parents))
+        same = o.eq(7).flatten(1).all(1).tolist()
+        assert status.tolist() == codes and [i for i in range(12) if same[i]] == kept, offsets

@@ -396,13 +396,16 @@ tree_attn_f32_kernel(const AttnArgs a) {
   __shared__ float red[kF32Threads / 32];
   const int h = blockIdx.x, t = blockIdx.y, tid = threadIdx.x;
   const int D = a.D;
+  if (h == 0 && t == 0) {      // every request once: one in error may have no row
+    for (int i = tid; i < a.B; i += kF32Threads) {
+      const ReqGeom any = request_geometry(a, i);
+      if (any.err) report(a.status, i, any.err);
+    }
+  }
   const int b = find_request(a.offsets, a.B, t);
   if (b < 0) return;
   const ReqGeom R = request_geometry(a, b);
-  if (R.err) {
-    if (tid == 0 && h == 0 && t == R.lo) report(a.status, b, R.err);
-    return;
-  }
+  if (R.err) return;
   const int g = h / a.G;
   const uint4 m = node_mask(a, R, b, t);
   const float *q = static_cast<const float *>(a.q) + (static_cast<size_t>(t) * a.Hq + h) * D;
