@@ -225,3 +225,30 @@ def test_requests_without_rows_of_their_own_report(gpu_lib, kernel, dtype):
         ttv.tree_attn(q, k, v, i32(20, 30, 5), i32(*offsets), None, 40, status, o=o, parents=i32(*parents))
         same = o.eq(7).flatten(1).all(1).tolist()
         assert status.tolist() == codes and [i for i in range(12) if same[i]] == kept, offsets
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("by_parents", [False, True])
+def test_prefixes_and_offsets_whose_sums_pass_31_bits(gpu_lib, kernel, dtype, by_parents):
+    """A prefix that passes 2^31 with its tree, and offsets whose difference does and looks like a few nodes: errors,
+    and rows that stay as they were."""
+    import token_tree_verification_gb300 as ttv
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    q = torch.randn((12, 2, 64), device="cuda").to(dtype)
+    k, v = (torch.randn((3, 2, 40, 64), device="cuda").to(dtype) for _ in range(2))
+    parents = i32(*[-1, 0, 0, 1] * 3)
+    mask, _ = ttv.build_tree_mask(parents, i32(0, 4, 8, 12), i32(0, 0, 0))
+
+    def call(lens, offsets):
+        status, o = i32(0, 0, 0), torch.full_like(q, 7.0)
+        ttv.tree_attn(q, k, v, i32(*lens), i32(*offsets), None if by_parents else mask, 40, status, o=o,
+                      parents=parents if by_parents else None)
+        return o, status.tolist()
+
+    good, status = call([20, 36, 5], [0, 4, 8, 12])
+    assert status == [0, 0, 0]
+    o, status = call([20, 2 ** 31 - 1, 5], [0, 4, 8, 12])
+    assert status == [0, -10, 0] and o[4:8].eq(7).all() and torch.equal(o[:4], good[:4]) and torch.equal(o[8:], good[8:])
+    assert call([2 ** 31 - 4, 37, 2 ** 31 - 2], [0, 4, 8, 12])[1] == [-10, -10, -10]
+    o, status = call([20, 20, 20], [0, 2 ** 31 - 1, -2 ** 31 + 3, 12])
+    assert status == [-4, -4, -4] and o.eq(7).all()

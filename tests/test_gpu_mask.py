@@ -44,3 +44,13 @@ def test_errors_reported_per_request(gpu_lib):
     mo, do, _ = oracle.build_mask(*pack([good]))
     for b in (0, 2, 4):
         np.testing.assert_array_equal(m[off[b]:off[b + 1]], mo)
+
+
+def test_offsets_whose_difference_passes_31_bits(gpu_lib):
+    """2^31 - 1 to -2^31 + 3 looks like four nodes."""
+    import torch
+    import token_tree_verification_gb300 as ttv
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    status = i32(0, 0, 0)
+    ttv.build_tree_mask(i32(-1, 0, 0, 1), i32(0, 2 ** 31 - 1, -2 ** 31 + 3, 4), status)
+    assert status.tolist() == [-4, -4, -4]

@@ -55,3 +55,13 @@ def test_merge_errors(gpu_lib):
     g, o = _both(pairs)
     assert g["status"].tolist() == [-4, -5, 0] == o["status"].tolist()
     np.testing.assert_array_equal(g["parents"][2], o["parents"][2])
+
+
+def test_offsets_whose_difference_passes_31_bits():
+    """2^31 - 1 to -2^31 + 3 looks like four nodes, in either tree."""
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    parents, tokens, good, bad = i32(*[-1, 0, 0, 1] * 3), i32(*range(12)), i32(0, 4, 8, 12), i32(0, 2 ** 31 - 1, -2 ** 31 + 3, 12)
+    for a, b in ((bad, good), (good, bad)):
+        status = i32(0, 0, 0)
+        ttv.tree_merge(parents, tokens, a, parents, tokens, b, status)
+        assert status.tolist() == [-4, -4, -4]

@@ -29,7 +29,8 @@ struct AttnArgs {
 };
 
 // Geometry of request b as one CTA sees it.  Keys [0, L) are the prefix,
-// keys [L, L + n) the tree slots in node order.
+// keys [L, L + n) the tree slots in node order.  Offsets and prefix lengths may be
+// any numbers: no difference or sum of them passes 2^31 before it has been ruled out.
 struct ReqGeom {
   int lo, n, L, keys, err;
 };
@@ -41,8 +42,8 @@ __device__ __forceinline__ ReqGeom request_geometry(const AttnArgs &a, int b) {
   r.n = hi - r.lo;
   r.L = __ldg(a.prefix_lens + b);
   r.err = 0;
-  if (r.lo < 0 || hi > a.T || r.n < 1 || r.n > SPEC_MAX_TREE_NODES) r.err = SPEC_ERR_TREE_TOO_LARGE;
-  else if (r.L < 0 || r.L + r.n > a.S_cap) r.err = SPEC_ERR_PREFIX_RANGE;
+  if (r.lo < 0 || hi > a.T || hi <= r.lo || r.n > SPEC_MAX_TREE_NODES) r.err = SPEC_ERR_TREE_TOO_LARGE;
+  else if (r.L < 0 || r.L > a.S_cap - r.n) r.err = SPEC_ERR_PREFIX_RANGE;
   r.keys = r.err ? 0 : r.L + r.n;
   return r;
 }

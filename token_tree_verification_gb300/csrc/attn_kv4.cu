@@ -127,7 +127,7 @@ tree_attn_kv4_few_kernel(const Kv4AttnArgs p) {
   __syncwarp();
   pdl_wait();
 
-  const ReqGeom G = kv4_geometry(a, b);
+  const ReqGeom G = request_geometry(a, b);
   if (G.err) {      // the same for the whole cluster
     if (tid == 0 && split == 0 && blockIdx.y == 0 && g_kv == 0) report(a.status, b, G.err);
     return;

@@ -177,7 +177,7 @@ tree_attn_kv4_tc_kernel(const Kv4AttnArgs p) {
   const uint32_t tmem = s_tmem;
   pdl_wait();
 
-  const ReqGeom G = kv4_geometry(a, b);
+  const ReqGeom G = request_geometry(a, b);
   const int rows_total = G.err ? 0 : G.n * a.G;
   if (G.err && tid == 0 && split == 0 && blockIdx.y == 0 && g_kv == 0) report(a.status, b, G.err);
   const TileList<kTile> tiles(G.L, G.keys, p.window, p.sinks);

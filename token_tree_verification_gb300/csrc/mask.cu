@@ -28,7 +28,7 @@ build_tree_mask_kernel(const int32_t *__restrict__ parents, const int32_t *__res
   pdl_wait();
   const int lo = __ldg(offsets + b), hi = __ldg(offsets + b + 1);
   const int n = hi - lo;
-  if (lo < 0 || hi > T || n < 1 || n > SPEC_MAX_TREE_NODES) {
+  if (lo < 0 || hi > T || hi <= lo || n > SPEC_MAX_TREE_NODES) {
     if (i == 0) report(status, b, SPEC_ERR_TREE_TOO_LARGE);
     return;
   }

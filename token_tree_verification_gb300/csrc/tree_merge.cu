@@ -40,7 +40,7 @@ tree_merge_kernel(const int32_t *parents_a, const int32_t *tokens_a, const int32
   const int lo_a = __ldg(off_a + b), hi_a = __ldg(off_a + b + 1);
   const int lo_b = __ldg(off_b + b), hi_b = __ldg(off_b + b + 1);
   const int na = hi_a - lo_a, nb = hi_b - lo_b;
-  if (na < 1 || na > kMergeCap || nb < 1 || nb > kMergeCap || lo_a < 0 || hi_a > Ta || lo_b < 0 ||
+  if (hi_a <= lo_a || na > kMergeCap || hi_b <= lo_b || nb > kMergeCap || lo_a < 0 || hi_a > Ta || lo_b < 0 ||
       hi_b > Tb) {
     if (tid == 0) report(status, b, SPEC_ERR_TREE_TOO_LARGE);
     return;
