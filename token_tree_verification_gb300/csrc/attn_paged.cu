@@ -689,6 +689,7 @@ extern "C" int spec_tree_attn_paged(const void *q, const void *k_pages, const vo
   p.pages.table = block_table;
   p.pages.max_pages = max_pages;
   p.pages.pages = num_pages;
+  p.pages.status = status;
   p.causal = causal != 0;
   const long long slots = static_cast<long long>(max_pages) << p.pages.shift;
   a.S_cap = static_cast<int>(slots < 0x7FFFFFFFll - 4096 ? slots : 0x7FFFFFFFll - 4096);

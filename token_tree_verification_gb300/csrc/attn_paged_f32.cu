@@ -98,7 +98,8 @@ tree_attn_paged_f32_kernel(const PagedAttnArgs p, const int CS) {
     long long at = -1;
     if (i < ntiles && key < w.keys) {
       const int page = max(0, p.pages.page(b, key >> p.pages.shift));
-      at = (((static_cast<long long>(page) * a.Hkv + g_kv) << p.pages.shift) + (key & ((1 << p.pages.shift) - 1))) * D;
+      at = ((static_cast<long long>(page) * a.Hkv + g_kv) << p.pages.shift) + (key & ((1 << p.pages.shift) - 1));
+      at = p.pages.holds(at, 1, a.Hkv, b) ? at * D : -1;
     }
     s_slot[i & 1][tid] = at;
   };
@@ -333,7 +334,8 @@ tree_attn_paged_f32_few_kernel(const PagedAttnArgs p, const int CS) {
     const int key = (t0 + i) * C::kTile + warp * K;
     if (i >= ntiles || key >= w.keys) return 0;
     const long long page = max(0, p.pages.page(b, key >> p.pages.shift));
-    return (((page * a.Hkv + g_kv) << p.pages.shift) + (key & ((1 << p.pages.shift) - 1))) * D + lane * V;
+    const long long row = ((page * a.Hkv + g_kv) << p.pages.shift) + (key & ((1 << p.pages.shift) - 1));
+    return (p.pages.holds(row, min(K, w.keys - key), a.Hkv, b) ? row * D : 0) + lane * V;
   };
   long long at = look_up(0);
 

@@ -57,6 +57,7 @@ kv_compact_paged_kernel(const CompactArgs a) {
       if (ps < 0 || pd < 0) err = SPEC_ERR_PAGE;
       s_src[tid] = (static_cast<long long>(ps) * a.H + h) * size + (src & (size - 1));
       s_dst[tid] = (static_cast<long long>(pd) * a.H + h) * size + (dst & (size - 1));
+      if (!err && !(a.pages.holds(s_src[tid], 1, a.H, b) && a.pages.holds(s_dst[tid], 1, a.H, b))) err = SPEC_ERR_INDEX;
     }
   }
   // every thread has the same view of what does not depend on its entry; entries
@@ -119,6 +120,7 @@ extern "C" int spec_kv_compact_paged(void *k_pages, void *v_pages, int dtype, in
   a.pages.table = block_table;
   a.pages.max_pages = max_pages;
   a.pages.pages = num_pages;
+  a.pages.status = status;
   a.row_bytes = D * (dtype == SPEC_F32 ? 4 : 2);
   a.H = Hkv;
   a.W = max_depth_plus1;

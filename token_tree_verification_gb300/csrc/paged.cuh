@@ -10,6 +10,7 @@ namespace spec {
 struct PageTable {
   const int32_t *table;    // [B][max_pages]
   int max_pages, pages, shift;
+  int32_t *status;         // the call's, for the bounds-checked build
 
   // Slots of a request, which are counted in 32 bits (with room for a tile).
   __device__ __forceinline__ int capacity() const {
@@ -18,8 +19,14 @@ struct PageTable {
   // The page of request b's slots [i << shift, (i + 1) << shift), or -1 for an id
   // outside the pool (i below max_pages).
   __device__ __forceinline__ int page(int b, int i) const {
+    if (!in_bounds(i, max_pages, status, b)) return -1;
     const int id = __ldg(table + static_cast<size_t>(b) * max_pages + i);
     return static_cast<unsigned>(id) < static_cast<unsigned>(pages) ? id : -1;
+  }
+  // Whether `n` rows from `row` on lie in a pool of `heads` KV heads (bounds-checked
+  // build; true in the normal one).
+  __device__ __forceinline__ bool holds(long long row, long long n, int heads, int b) const {
+    return range_in_bounds(row, n, static_cast<long long>(pages) * heads << shift, status, b);
   }
 };
 

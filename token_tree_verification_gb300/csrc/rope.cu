@@ -188,7 +188,7 @@ template <typename E, int V, bool kInter, int kAhead>
 __global__ void __launch_bounds__(kMaxThreads, kAhead == 1 ? 1 : 6)
 rope_kernel(const RopeArgs a) {
   extern __shared__ __align__(16) float s_angle[];     // [rows][cosines, sines][r / 2]
-  __shared__ int s_ok[kMaxRows], s_pos[kMaxRows];
+  __shared__ int s_ok[kMaxRows], s_pos[kMaxRows];      // request + 1 (0: not to be written), position
   __shared__ long long s_slot[kMaxRows];               // first element of the slot's head 0 in the pools
   const int tid = threadIdx.x, threads = blockDim.x, warp = tid >> 5, lane = tid & 31;
   const int t0 = static_cast<int>(blockIdx.x) * a.rows;
@@ -222,7 +222,7 @@ rope_kernel(const RopeArgs a) {
   for (int row = warp; row < rows; row += threads / 32) {
     const int t = t0 + row;
     const int b = warp_find_request(a.offsets, a.B, t, lane);
-    bool ok = b >= 0;
+    bool ok = b >= 0 && in_bounds(b, a.B, a.status, 0);
     long long slot_at = 0;
     int position = 0, depth = 0;
     if (ok) {
@@ -255,7 +255,7 @@ rope_kernel(const RopeArgs a) {
       ok = false;
     }
     if (lane == 0) {
-      s_ok[row] = ok;
+      s_ok[row] = ok ? b + 1 : 0;
       s_pos[row] = position;
       s_slot[row] = slot_at;
     }
@@ -327,6 +327,9 @@ rope_kernel(const RopeArgs a) {
       from_float(fa, &la[u]);
       from_float(fb, &lb[u]);
     }
+    if (kChecked && !is_q &&
+        !a.pages.holds((s_slot[row] + (static_cast<long long>(head) << a.pages.shift) * a.D) / a.D, 1, a.Hkv, s_ok[row] - 1))
+      return;
     E *dst = y + (is_q ? row * a.y_st : s_slot[row]);
     *reinterpret_cast<Load *>(dst) = la[u];
     if (two) *reinterpret_cast<Load *>(dst + to_b) = lb[u];
@@ -585,6 +588,7 @@ extern "C" int spec_rope_write_paged(const void *q, void *q_out, const void *k, 
   a.pages.table = block_table;
   a.pages.max_pages = max_pages;
   a.pages.pages = num_pages;
+  a.pages.status = status;
   a.freqs = reinterpret_cast<const unsigned long long *>(freqs);
   a.scale = scale;
   a.slots = prefix_lens;
