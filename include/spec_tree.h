@@ -298,6 +298,7 @@ int spec_tree_verify_top_p(const float *target_logits, const float *draft_logits
  *   tree_offsets     [B+1] int32
  *   path_nodes       [B][max_depth_plus1] int32, accept_len [B] int32
  *   new_prefix_lens  [B] int32 out (L_b for a skipped request)
+ *   B                at most 65535 (SPEC_ERR_SHAPE beyond)
  *   status           [B] int32 in/out: requests whose status is already
  *                    non-zero are skipped (caches untouched)
  * Errors on the device: SPEC_ERR_PREFIX_RANGE (L_b + N_b > S_cap),
@@ -421,7 +422,7 @@ int spec_tree_attn_kv4(const void *q, const void *kv_cache, void *o, int dtype, 
 /*
  * spec_kv4_compact — spec_kv_compact on the 4-bit cache: the accepted path's
  * records move behind the prefix as they are.  new_prefix_lens must not be
- * prefix_lens itself (SPEC_ERR_SHAPE).
+ * prefix_lens itself (SPEC_ERR_SHAPE); B at most 65535.
  */
 int spec_kv4_compact(void *kv_cache, int B, int Hkv, int D, int S_cap, const int32_t *prefix_lens,
                      const int32_t *tree_offsets, const int32_t *path_nodes,
@@ -462,7 +463,9 @@ int spec_kv4_compact(void *kv_cache, int B, int Hkv, int D, int S_cap, const int
  *                     ceil(d(low)) (both within [0, r - 1]), d(t) = r ln(original
  *                     / (2 pi t)) / (2 ln base) the pair that makes t turns in
  *                     `original` positions; cosines and sines are multiplied by
- *                     0.1 ln(factor) + 1 (*scale).  low = 1, high = 32 usually
+ *                     0.1 ln(factor) + 1 (*scale).  low = 1, high = 32 usually.
+ *                     k is linear in the pair, between whole pairs, as models in
+ *                     use are trained with; the paper's is linear in the turns
  *   SPEC_ROPE_BANDS   the same mix with k = (original theta_i / 2 pi - low) /
  *                     (high - low), cut to [0, 1]: pairs of more than `high`
  *                     turns in the original context stay, those of fewer than
@@ -502,8 +505,8 @@ int spec_rope_table(int rotary_dim, double base, int scaling, double factor, dou
  *   freqs     [rotary_dim / 2] uint64 DEVICE, from spec_rope_table
  *   start     [B] int32, depth [T] int32 or NULL, offsets [B+1] int32 (a
  *             request may have no rows; it has no upper limit of rows)
- *   T         rows; rows at or behind offsets[B] stay as they were, T = 0
- *             enqueues nothing
+ *   T         rows, at most 2^31 - 33; rows at or behind offsets[B] stay as they
+ *             were, T = 0 enqueues nothing
  * The angle is an exact product in 64-bit fixed point, so positions up to 2^32 keep
  * fp32's accuracy: the table's rounding is 2^-33 of a turn there.  Its upper 32 bits
  * (the others are cut, 2^-32 of a turn) are rounded to fp32 as a number of half turns
@@ -526,6 +529,7 @@ int spec_rope(const void *x, void *y, int dtype, int B, int T, int H, int D, int
  * of v: row t of request b goes to slot prefix_lens[b] + t - offsets[b].  No
  * other slot changes.  Positions start at `start`, or at prefix_lens when it is
  * NULL (they differ in a cache that has lost slots, or whose prefix is shared).
+ * D as in spec_rope; attention and compaction take caches of D 64 and 128 alone.
  *
  *   q, k, v   [T][Hq | Hkv][D] at strides as in spec_rope; Hq = 0 writes k
  *             and v alone (q and q_out are then ignored)
@@ -554,7 +558,8 @@ int spec_rope_write_paged(const void *q, void *q_out, const void *k, const void 
  * Chunks (causal != 0, mask and parents NULL): request b's rows are a run of
  * any number of tokens behind its prefix, each of which sees the prefix, the
  * run's earlier tokens and itself; a request may have no rows.  The rows' own
- * keys and values must already sit in their slots, L_b and up.
+ * keys and values must already sit in their slots, L_b and up.  Every row sees the
+ * whole prefix: there is no sliding window here (spec_tree_attn_kv4 has one).
  *
  *   q, o         [T][Hq][D] dtype, 16-byte aligned; Hq % Hkv == 0, Hq / Hkv at
  *                most 128, D 64 or 128, Hkv at most 65535, T x Hq below 2^31
@@ -586,7 +591,9 @@ int spec_tree_attn_paged(const void *q, const void *k_pages, const void *v_pages
  * path's keys and values move behind the prefix, across pages where need be.
  * The block table stays as it is (pages behind the new prefix are the
  * caller's to reuse).  D is 64 or 128; new_prefix_lens must not overlap prefix_lens
- * (SPEC_ERR_SHAPE).  Errors on the device: those of spec_kv_compact, and
+ * (SPEC_ERR_SHAPE); B is at most 65535, which the other calls on pages are not: a
+ * larger batch's paths move in several calls, each on its own requests' rows of the
+ * arrays.  Errors on the device: those of spec_kv_compact, and
  * SPEC_ERR_PAGE for the pages of the slots that move.
  */
 int spec_kv_compact_paged(void *k_pages, void *v_pages, int dtype, int B, int Hkv, int D,

@@ -790,6 +790,30 @@ def test_compaction_of_a_long_path_of_a_small_tree(gpu_lib):
         assert torch.equal(bits(x), bits(y))
 
 
+def test_paths_of_more_requests_than_a_call_takes(gpu_lib):
+    """65540 requests write and attend in one call each; their paths move in two, on slices of the arrays."""
+    B, n, D = 65540, 3, 64
+    rows, off, lens = torch.randn((B * n, 1, D), device="cuda"), i32(np.arange(B + 1) * n), i32(np.arange(B) % 5)
+    kp, vp = (torch.zeros((B, 1, 8, D), device="cuda") for _ in range(2))
+    table, status = i32(np.random.default_rng(0).permutation(B)[:, None]), zeros_status(B)
+    ttv.rope_write_paged(None, rows, rows, kp, vp, table, lens, off, status)
+    o = ttv.tree_attn_paged(rows, kp, vp, table, lens, off, None, 4, status, parents=i32(np.tile([-1, 0, 0], B)))
+    assert o.isfinite().all()
+    path, accept = i32(np.tile([0, 2], (B, 1))), i32(np.ones(B))
+    want = [x[table[:, 0].long(), 0].clone() for x in (kp, vp)]
+    at, row = lens.long(), torch.arange(B, device="cuda")
+    for x in want:
+        x[row, at + 1] = x[row, at + 2]
+    with pytest.raises(ttv.SpecError, match="SHAPE"):
+        ttv.kv_compact_paged(kp, vp, table, lens, off, path, accept, status)
+    for b in (slice(0, 65535), slice(65535, B)):
+        new = ttv.kv_compact_paged(kp, vp, table[b], lens[b], off[b.start:b.stop + 1], path[b], accept[b], status[b])
+        assert torch.equal(new, lens[b] + 2)
+    assert status.eq(0).all()
+    for x, y in zip((kp, vp), want):
+        assert torch.equal(x[table[:, 0].long(), 0], y)
+
+
 # ------------------------------------------------------------------ together
 def step(q, k, v, cache, rope, depth, parents, off, lens, path, accept, max_prefix, status, stream=None):
     """One step as a program runs it: rows into pages, attention, the accepted path."""

@@ -214,3 +214,10 @@ def test_frequencies_to_the_last_place(lib, r, base, scaling, factor, original, 
     table = ttv.rope_table(r, base, scaling, factor, original=original, low=low, high=high, device="cpu")
     for i, turns in enumerate(_theta_exactly(r, base, scaling, factor, original, low, high)):
         assert abs(float(table.freqs[i].item() % 2 ** 64 - turns * 2 ** 64)) <= 0.5 + 2.0 ** -20, i
+
+
+def test_more_requests_than_a_compaction_takes_are_refused(lib):
+    """The dense and the 4-bit call, as the paged one above."""
+    for B, rc in ((65536, -2), (2 ** 31 - 1, -2)):
+        assert lib.spec_kv_compact(FAKE, FAKE, 1, B, 2, 64, 40, FAKE, FAKE, FAKE, FAKE, 4, P(0x2000), FAKE, None) == rc
+        assert lib.spec_kv4_compact(FAKE, B, 2, 64, 40, FAKE, FAKE, FAKE, FAKE, 4, P(0x2000), FAKE, None) == rc
