@@ -252,3 +252,15 @@ def test_prefixes_and_offsets_whose_sums_pass_31_bits(gpu_lib, kernel, dtype, by
     assert call([2 ** 31 - 4, 37, 2 ** 31 - 2], [0, 4, 8, 12])[1] == [-10, -10, -10]
     o, status = call([20, 20, 20], [0, 2 ** 31 - 1, -2 ** 31 + 3, 12])
     assert status == [-4, -4, -4] and o.eq(7).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,mine", [(300, 299), (300, 0), (128, 127), (129, 5)])
+def test_hundreds_of_requests_without_rows_report(gpu_lib, kernel, dtype, B, mine):
+    """One node in all, of request `mine`; every other request is a tree without nodes."""
+    import token_tree_verification_gb300 as ttv
+    i32 = lambda x: torch.as_tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    q, v = torch.ones((1, 2, 64), device="cuda").to(dtype), torch.full((B, 1, 3, 64), 0.5, device="cuda").to(dtype)
+    status = i32([0] * B)
+    o = ttv.tree_attn(q, v, v, i32([2] * B), i32([0] * (mine + 1) + [1] * (B - mine)), None, 2, status, parents=i32([-1]))
+    assert status.tolist() == [0 if b == mine else -4 for b in range(B)] and o.eq(0.5).all()

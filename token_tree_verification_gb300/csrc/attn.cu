@@ -396,11 +396,14 @@ tree_attn_f32_kernel(const AttnArgs a) {
   __shared__ float red[kF32Threads / 32];
   const int h = blockIdx.x, t = blockIdx.y, tid = threadIdx.x;
   const int D = a.D;
-  if (h == 0 && t == 0) {      // every request once: one in error may have no row
-    for (int i = tid; i < a.B; i += kF32Threads) {
-      const ReqGeom any = request_geometry(a, i);
-      if (any.err) report(a.status, i, any.err);
+  if (h >= a.Hq) {      // CTAs behind the last head look at every request: one in error may have no row
+    // (a thread each: with a loop over them in the kernel a small tree took 24 in place of 18 us)
+    const long long i = (static_cast<long long>(h - a.Hq) * gridDim.y + t) * kF32Threads + tid;
+    if (i < a.B) {
+      const ReqGeom any = request_geometry(a, static_cast<int>(i));
+      if (any.err) report(a.status, static_cast<int>(i), any.err);
     }
+    return;
   }
   const int b = find_request(a.offsets, a.B, t);
   if (b < 0) return;
@@ -633,7 +636,8 @@ extern "C" int spec_tree_attn_ex(const void *q, const void *k_cache, const void 
   args.prefetch_keys = B == 1 ? max_prefix + T : 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == SPEC_F32) {
-    spec::tree_attn_f32_kernel<<<dim3(Hq, T), spec::kF32Threads, 0, st>>>(args);
+    const int looking = static_cast<int>((B - 1) / (static_cast<long long>(spec::kF32Threads) * T)) + 1;      // columns of CTAs that have a request each thread
+    spec::tree_attn_f32_kernel<<<dim3(Hq + looking, T), spec::kF32Threads, 0, st>>>(args);
     return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
   }
   if (use_mma_kernel())
