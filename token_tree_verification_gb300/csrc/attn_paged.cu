@@ -45,11 +45,12 @@
 // between its products.
 //
 // Measured, device times: 128-node trees of 4 requests, 64 heads on 8, behind 8192
-// keys: 137 to 141 us, 1.0 PFLOP/s and with the remainders' products 1.5; the tensor pipe
-// is busy for 0.8 of it, and of its two waves of CTAs the second is part full.  A
-// chunk of 2048 tokens behind 16384, 64 heads on 8: 1.0 ms, 1.17 PFLOP/s, with the
-// remainders' 1.75, near what a library product sustains.  6-node chains of 8
-// requests, 32 heads, behind 27000 to 32768 keys: 563 us, 7.0 TB/s, a copy's rate.
+// keys: 138 to 141 us, 1.0 PFLOP/s and with the remainders' products 1.5; the tensor pipe
+// is busy for 0.8 of an SM's time, for all but 0.04 of the busiest's, which has two of
+// 256 CTAs where an even share is 1.7.  A
+// chunk of 2048 tokens behind 16384, 64 heads on 8: 0.97 to 1.02 ms, 1.17 PFLOP/s, with
+// the remainders' 1.75, near what a library product sustains.  6-node chains of 8
+// requests, 32 heads, behind 27000 to 32768 keys: 564 us, 7.0 TB/s, a copy's rate.
 // One token of 4 requests behind 8192 keys, 64 heads on 8: 27 us, 5 TB/s; 64-node
 // tree, 32 heads, behind 2048: 14.9 us, of them 2.5 to the first key tile, 7 of tiles
 // and 4 of output and merge.
@@ -594,7 +595,8 @@ bool encode_pool(CUtensorMap *m, const void *base, const PageTable &pages, int H
 // form, 8 heads of 4 query heads each: a token of 256 requests behind 60, 500, 1000,
 // 1500, 2000 and 3000 keys 77 and 39, 144 and 107, 215 and 187, 283 and 261, 350 and
 // 338, 486 and 484; at D = 64 behind 60, 500, 1500 and 3000 72 and 34, 118 and 71, 210
-// and 147, 336 and 256; prompts of 512 tokens x 8, 80 and 50.  128-node trees x 4, 64
+// and 147, 336 and 256 (60 keys of all lie in L2; from memory the small form takes 43
+// and, at D = 64, 38); prompts of 512 tokens x 8, 80 and 50.  128-node trees x 4, 64
 // heads on 8, behind 8192: 137 and 149, at D = 64 118 and 112; chains of 6 x 8, 32
 // heads, behind 27000 to 32768: 562 and 610.  The occupancy calculator says one CTA an
 // SM for the small form, but two run.)

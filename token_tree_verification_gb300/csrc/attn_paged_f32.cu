@@ -6,7 +6,7 @@
 // Blocks of 4 or 8 rows: a warp takes 8 or 4 keys at a time, straight from memory into
 // registers, and nothing but the weights passes through shared memory.  Memory bounds
 // it: a token of 4 query heads each, D = 128, of 64 requests x 8 heads behind 1000 keys
-// 86 us (6.1 TB/s, 0.9 of a copy), of 1024 behind 200 319; of 4 requests behind 4096
+// 87 us (6.1 TB/s, 0.9 of a copy), of 1024 behind 200 323; of 4 requests behind 4096
 // 27.  (Tiles of 32 keys in shared memory for 16 rows, whose products read their
 // operands there: 248, 620 and 77.)
 //

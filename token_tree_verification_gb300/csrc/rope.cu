@@ -25,8 +25,9 @@
 //
 // Memory bounds long runs: 51200 rows of 40 heads, D = 128, 1.05 GB in 162 us, 6.5
 // TB/s, 0.95 of a copy's rate; 14237 rows of 80 heads into pages of 64 slots, 583 MB
-// in 102 us, 5.7 TB/s; single tokens of 4096 requests, 48 heads, 101 MB in 21 us, 4.8
-// TB/s.  A few tokens (2.9 us) and a 64-node tree of 96 heads (3.6 us) are the chain
+// in 103 us, 5.7 TB/s; single tokens of 4096 requests, 48 heads, 101 MB in 24 us, 4.1
+// TB/s.  fp32: 25600 rows of 40 heads, 1.05 GB in 160 us; 14237 of 80 into pages, 1.17
+// GB in 184.  A few tokens (2.9 us) and a 64-node tree of 96 heads (3.6 us) are the chain
 // of loads.
 #include <cuda_bf16.h>
 
@@ -238,7 +239,7 @@ rope_kernel(const RopeArgs a) {
           const int slot = L + t - R.lo;
           const int page = a.pages.page(b, slot >> a.pages.shift);
           // rows that are all of one request share its pages out (65536 rows of 12 heads
-          // into pages of 8: 145 us; with all of them looked at for every row 247)
+          // into pages of 8: 147 us; with all of them looked at for every row 247)
           const bool alone = R.lo <= t0 && R.lo + R.n >= t0 + rows;
           if (warp_finds_bad_page(a.pages, b, L, L + R.n, lane, alone ? row : 0, alone ? rows : 1) || page < 0) {
             if (lane == 0) report(a.status, b, SPEC_ERR_PAGE);
@@ -348,7 +349,7 @@ rope_kernel(const RopeArgs a) {
 // An item a thread, a row's items in as few CTAs as take them in kMaxThreads, or
 // several rows side by side where a row has few; and rows in a run up to kRun (32 in
 // all) while that leaves sixteen CTAs an SM.  Device us for the 51200 rows, the 14237,
-// the 4096 above and a run of 8192 rows of 48 heads:
+// the 4096 above (in L2 here) and a run of 8192 rows of 48 heads:
 //   192 threads, 2 rows ahead of the stores, runs of 8 and 6: 162, 102, 21, 36
 //   runs of 16 and 4: 169, 111, 21, 36 and 164, 103, 21, 38
 //   192 threads, 3 rows ahead: 165, 105, 22, 38
@@ -397,7 +398,7 @@ int launch(RopeArgs &a, void *stream) {
 
 // The widest vectors that every pointer, stride and the pairs' ends allow, of 16 bytes
 // and less; single elements otherwise.  (12000 rows of 80 heads into pages, D = 128, the
-// first 128, 24 and 20 dims turned, bf16, 16, 8 and 4 bytes: 87, 114 and 183 us; by
+// first 128, 24 and 20 dims turned, bf16, 16, 8 and 4 bytes: 85, 110 and 177 us; by
 // single elements 470 and 475.)
 template <typename E, int V>
 bool fits(const RopeArgs &a, bool interleaved) {
