@@ -27,8 +27,8 @@ build_tree_mask_kernel(const int32_t *__restrict__ parents, const int32_t *__res
   pdl_trigger();
   pdl_wait();
   const int lo = __ldg(offsets + b), hi = __ldg(offsets + b + 1);
-  const int n = hi - lo;
-  if (lo < 0 || hi > T || hi <= lo || n > SPEC_MAX_TREE_NODES) {
+  const int n = static_cast<int>(static_cast<uint32_t>(hi) - static_cast<uint32_t>(lo));
+  if (static_cast<uint32_t>(lo) > static_cast<uint32_t>(T) || hi > T || n < 1 || n > SPEC_MAX_TREE_NODES) {
     if (i == 0) report(status, b, SPEC_ERR_TREE_TOO_LARGE);
     return;
   }
