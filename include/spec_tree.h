@@ -297,7 +297,8 @@ int spec_tree_verify_top_p(const float *target_logits, const float *draft_logits
  *   prefix_lens      [B] int32 (L_b, before the update)
  *   tree_offsets     [B+1] int32
  *   path_nodes       [B][max_depth_plus1] int32, accept_len [B] int32
- *   new_prefix_lens  [B] int32 out (L_b for a skipped request)
+ *   new_prefix_lens  [B] int32 out (L_b for a skipped request); must not overlap
+ *                    prefix_lens where Hkv > 1 (SPEC_ERR_SHAPE)
  *   B                at most 65535 (SPEC_ERR_SHAPE beyond)
  *   status           [B] int32 in/out: requests whose status is already
  *                    non-zero are skipped (caches untouched)
@@ -421,8 +422,8 @@ int spec_tree_attn_kv4(const void *q, const void *kv_cache, void *o, int dtype, 
 
 /*
  * spec_kv4_compact — spec_kv_compact on the 4-bit cache: the accepted path's
- * records move behind the prefix as they are.  new_prefix_lens must not be
- * prefix_lens itself (SPEC_ERR_SHAPE); B at most 65535.
+ * records move behind the prefix as they are.  new_prefix_lens must not overlap
+ * prefix_lens (SPEC_ERR_SHAPE); B at most 65535.
  */
 int spec_kv4_compact(void *kv_cache, int B, int Hkv, int D, int S_cap, const int32_t *prefix_lens,
                      const int32_t *tree_offsets, const int32_t *path_nodes,

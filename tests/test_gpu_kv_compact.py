@@ -111,3 +111,16 @@ def test_accepted_lengths_that_are_anything(acc, paged):
     for x, y in zip(cache, before):
         y[1, :, 5] = y[1, :, 6]
         assert torch.equal(x, y)
+
+
+def test_one_head_may_update_its_lengths_in_place():
+    k = torch.randn((2, 1, 16, 64), device="cuda")
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    lens, status, want = i32(3, 5), i32(0, 0), k.clone()
+    want[0, :, 4], want[1, :, 6] = k[0, :, 5], k[1, :, 8]
+    args = (k, k.clone(), lens, i32(0, 4, 8), i32([0, 2], [0, 3]), i32(1, 1), status)
+    assert ttv.kv_compact(*args, new_prefix_lens=lens) is lens and lens.tolist() == [5, 7]
+    assert torch.equal(k, want) and status.eq(0).all()
+    two = torch.zeros((2, 2, 16, 64), device="cuda")
+    with pytest.raises(ttv.SpecError, match="SHAPE"):
+        ttv.kv_compact(two, two.clone(), *args[2:], new_prefix_lens=lens)

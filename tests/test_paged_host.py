@@ -221,3 +221,10 @@ def test_more_requests_than_a_compaction_takes_are_refused(lib):
     for B, rc in ((65536, -2), (2 ** 31 - 1, -2)):
         assert lib.spec_kv_compact(FAKE, FAKE, 1, B, 2, 64, 40, FAKE, FAKE, FAKE, FAKE, 4, P(0x2000), FAKE, None) == rc
         assert lib.spec_kv4_compact(FAKE, B, 2, 64, 40, FAKE, FAKE, FAKE, FAKE, 4, P(0x2000), FAKE, None) == rc
+
+
+def test_lengths_written_over_those_that_are_read_are_refused(lib):
+    """The dense and the 4-bit call: a request's heads read its length while one of them writes the new one."""
+    for old, new, B in ((0x2000, 0x2000, 1), (0x2000, 0x2004, 2), (0x2004, 0x2000, 2), (0x2000, 0x2000 + 4 * 99, 100)):
+        assert lib.spec_kv_compact(FAKE, FAKE, 1, B, 2, 64, 40, P(old), FAKE, FAKE, FAKE, 4, P(new), FAKE, None) == -2
+        assert lib.spec_kv4_compact(FAKE, B, 2, 64, 40, P(old), FAKE, FAKE, FAKE, 4, P(new), FAKE, None) == -2

@@ -100,6 +100,8 @@ int compact_rows(KvArgs args, int max_depth_plus1, void *stream) {
     return SPEC_ERR_SHAPE;
   if ((reinterpret_cast<uintptr_t>(args.k) & 15) || (reinterpret_cast<uintptr_t>(args.v) & 15))
     return SPEC_ERR_ALIGNMENT;
+  // (the CTAs of a request read its length while the first of them writes the new one)
+  if (args.H > 1 && args.new_prefix < args.prefix + args.B && args.prefix < args.new_prefix + args.B) return SPEC_ERR_SHAPE;
   // room for every row an accepted path can move (acc <= max_depth_plus1 - 1)
   const size_t smem = static_cast<size_t>(args.arrays) * (max_depth_plus1 - 1) * args.row_bytes;
   if (smem > 200 * 1024) return SPEC_ERR_SHAPE;
@@ -146,8 +148,7 @@ extern "C" int spec_kv4_compact(void *kv_cache, int B, int Hkv, int D, int S_cap
   using namespace spec;
   if (!kv_cache) return SPEC_ERR_NULL;
   if (D != 64 && D != 128) return SPEC_ERR_SHAPE;
-  // the CTAs of a request read its length while one of them writes the new one
-  if (new_prefix_lens && new_prefix_lens == prefix_lens) return SPEC_ERR_SHAPE;
+  if (new_prefix_lens && new_prefix_lens == prefix_lens) return SPEC_ERR_SHAPE;      // (with one head too)
   const KvArgs args = {static_cast<uint8_t *>(kv_cache), nullptr, 1, kv4_record_bytes(D), B, Hkv, S_cap,
                        max_depth_plus1, prefix_lens, tree_offsets, path_nodes, accept_len, new_prefix_lens, status};
   return compact_rows(args, max_depth_plus1, stream);
